@@ -19,17 +19,22 @@ Operand encodings (contiguous; K-major unless la / lb say MN_MAJOR):
 MN-major operands (gemm_bf16, gemm_mx) are stored transposed: A (K, M), B
 (K, N), E2M1 packing two consecutive M (N) per byte, (K, M/2); scales keep
 their (M, K/32) layout.
-Each returns D: (M, N) torch.bfloat16 (or writes into ``out``).
+The mixture-of-experts operators (moe_route ... moe_combine_backward) are
+described at their functions.
+Each GEMM returns D: (M, N) torch.bfloat16 (or writes into ``out``).
 """
 from __future__ import annotations
 
 import contextlib
 import ctypes
 from pathlib import Path
+from typing import NamedTuple
 
 import torch
 
-__all__ = ["gemm_bf16", "gemm_bf16_decoupled", "gemm_mx", "gemm_mx_mixed", "gemm_nvfp4", "gemm_nvfp4_fp8", "gemm_nvfp4_fp8_noalloc", "nvfp4_fp8_workspace_bytes", "gemm_nvfp4_fp6", "nvfp4_fp6_workspace_bytes", "gemm_grouped_bf16", "gemm_grouped_mx", "gemm_grouped_nvfp4", "quant_mx", "quant_nvfp4", "quant_bf16", "lib", "LIB_PATH", "DbsError", "load_poison_library", "using_library",
+__all__ = ["gemm_bf16", "gemm_bf16_decoupled", "gemm_mx", "gemm_mx_mixed", "gemm_nvfp4", "gemm_nvfp4_fp8", "gemm_nvfp4_fp8_noalloc", "nvfp4_fp8_workspace_bytes", "gemm_nvfp4_fp6", "nvfp4_fp6_workspace_bytes", "gemm_grouped_bf16", "gemm_grouped_mx", "gemm_grouped_nvfp4", "quant_mx", "quant_nvfp4", "quant_bf16",
+           "MoeRouting", "moe_route", "moe_route_backward", "gemm_moe_bf16", "gemm_moe_swiglu_bf16", "gemm_moe_dw_bf16",
+           "swiglu", "swiglu_backward", "moe_combine", "moe_combine_backward", "lib", "LIB_PATH", "DbsError", "load_poison_library", "using_library",
            "DBS_OK", "DBS_EINVAL", "DBS_EUNSUPPORTED", "DBS_EHIP", "K_MAJOR", "MN_MAJOR",
            "E4M3", "E5M2", "E2M3", "E3M2", "E2M1", "status_str"]
 
@@ -124,6 +129,27 @@ def _declare(L: ctypes.CDLL) -> None:
     L.quant_nvfp4.restype = I
     L.quant_bf16.argtypes = [P, I64, P, P]
     L.quant_bf16.restype = I
+    SZ = ctypes.c_size_t
+    L.moe_route_workspace.argtypes = [I64, I64, I64]
+    L.moe_route_workspace.restype = SZ
+    L.moe_route.argtypes = [I, P, I64, I64, I64, I, P, P, P, P, P, P, SZ, P]
+    L.moe_route.restype = I
+    L.moe_route_bwd.argtypes = [I, P, I64, I64, I64, I, P, P, P, P]
+    L.moe_route_bwd.restype = I
+    L.gemm_moe_bf16.argtypes = [P, P, P, P, P, I64, I64, I64, I64, I64, I, P]
+    L.gemm_moe_bf16.restype = I
+    L.gemm_moe_swiglu_bf16.argtypes = [P, P, P, P, P, I64, I64, I64, I64, I64, P]
+    L.gemm_moe_swiglu_bf16.restype = I
+    L.gemm_moe_dw_bf16.argtypes = [I, P, P, P, P, P, I64, I64, I64, I64, I64, I, P]
+    L.gemm_moe_dw_bf16.restype = I
+    L.swiglu_bf16.argtypes = [P, P, I64, I64, P]
+    L.swiglu_bf16.restype = I
+    L.swiglu_bwd_bf16.argtypes = [P, P, P, I64, I64, P]
+    L.swiglu_bwd_bf16.restype = I
+    L.moe_combine_bf16.argtypes = [P, P, P, P, I64, I64, I64, I64, P]
+    L.moe_combine_bf16.restype = I
+    L.moe_combine_bwd_bf16.argtypes = [P, P, P, P, P, I64, P, P, I64, I64, I64, P]
+    L.moe_combine_bwd_bf16.restype = I
     L.dbs_status_str.argtypes = [I]
     L.dbs_status_str.restype = ctypes.c_char_p
     L.dbs_last_error.argtypes = []
@@ -440,3 +466,244 @@ def gemm_nvfp4_fp6(A: torch.Tensor, sA: torch.Tensor, tA: float, B: torch.Tensor
                                 M, N, K, K_MAJOR, K_MAJOR, ctypes.c_void_p(workspace.data_ptr()),
                                 workspace.numel(), _stream(A)))
     return out
+
+
+# ---- mixture-of-experts operators ------------------------------------------------
+#
+# A routed layer, with W13 (E, 2F, H) the experts' gate and up matrices and W2
+# (E, H, F) their way back:
+#
+#     r = moe_route(logits, k)
+#     a = gemm_moe_swiglu_bf16(x, W13, r.offsets, r.rows)       serving
+#     h = gemm_moe_bf16(x, W13, r.offsets, r.rows)              training: h is kept
+#     a = swiglu(h)
+#     y = gemm_moe_bf16(a, W2, r.offsets)
+#     out = moe_combine(y, r.slots, r.weights)
+#
+# Offsets, rows and slots stay on the GPU: no call synchronises.
+
+_REAL = {torch.float32: 0, torch.bfloat16: 1}
+_BF16 = (torch.bfloat16,)
+_I32 = (torch.int32,)
+_F32 = (torch.float32,)
+
+
+class MoeRouting(NamedTuple):
+    """What moe_route returns: experts (T, k) int32 (-1: none), weights (T, k)
+    fp32, offsets (E + 1) int32 (expert e's sorted rows), rows (T k) int32
+    (token of a sorted row, -1 past the last), slots (T, k) int32 (sorted row
+    of a pair, -1: none)."""
+    experts: torch.Tensor
+    weights: torch.Tensor
+    offsets: torch.Tensor
+    rows: torch.Tensor
+    slots: torch.Tensor
+
+
+def _ptr(t: torch.Tensor | None):
+    return ctypes.c_void_p(None if t is None else t.data_ptr())
+
+
+def _dims(t: torch.Tensor, name: str, n: int) -> tuple:
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
+    if t.dim() != n:
+        raise ValueError(f"{name}: {t.dim()} dimensions, expected {n}")
+    return tuple(t.shape)
+
+
+def _same_device(first: torch.Tensor, **others) -> None:
+    for name, t in others.items():
+        if t is not None and t.device != first.device:
+            raise ValueError(f"{name} is on {t.device}, expected {first.device}")
+
+
+def _on(t: torch.Tensor):
+    """The device of t made current for the call: kernels are launched, and
+    the library asks for its compute units, there."""
+    return torch.cuda.device(t.device)
+
+
+def _given(out: torch.Tensor | None, shape, dtype, like: torch.Tensor) -> torch.Tensor:
+    if out is None:
+        return torch.empty(shape, dtype=dtype, device=like.device)
+    _dev(out, "out", (dtype,), shape)
+    _same_device(like, out=out)
+    return out
+
+
+def moe_route(logits: torch.Tensor, k: int, renormalize: bool = True) -> MoeRouting:
+    """Router: the k best of E experts for each of T tokens from logits (T, E)
+    fp32 or bf16, their softmax weights (over the chosen experts, or over all
+    with renormalize=False) and the stable order of the pairs by expert.
+    Logits of -inf or NaN close an expert to the token; ties go to the lower
+    expert."""
+    T, E = _dims(logits, "logits", 2)
+    pl = _dev(logits, "logits", tuple(_REAL), (T, E))
+    dev = logits.device
+    need = int(lib().moe_route_workspace(T, E, k))
+    i32 = dict(dtype=torch.int32, device=dev)
+    pairs = max(T * k, 0)
+    r = MoeRouting(torch.empty((T, max(k, 0)), **i32), torch.empty((T, max(k, 0)), dtype=torch.float32, device=dev),
+                   torch.empty(E + 1, **i32), torch.empty(pairs, **i32), torch.empty((T, max(k, 0)), **i32))
+    ws = torch.empty(need, dtype=torch.uint8, device=dev) if need else None
+    with _on(logits):
+        _check(lib().moe_route(_REAL[logits.dtype], pl, T, E, k, int(bool(renormalize)), _ptr(r.experts),
+                               _ptr(r.weights), _ptr(r.offsets), _ptr(r.rows), _ptr(r.slots), _ptr(ws), need,
+                               _stream(logits)))
+    return r
+
+
+def moe_route_backward(logits: torch.Tensor, experts: torch.Tensor, dweights: torch.Tensor,
+                       renormalize: bool = True) -> torch.Tensor:
+    """Gradient of moe_route's weights with respect to its logits (T, E):
+    experts (T, k) as moe_route gave them, dweights (T, k) fp32."""
+    T, E = _dims(logits, "logits", 2)
+    k = _dims(experts, "experts", 2)[1]
+    pl = _dev(logits, "logits", tuple(_REAL), (T, E))
+    pe = _dev(experts, "experts", _I32, (T, k))
+    pw = _dev(dweights, "dweights", _F32, (T, k))
+    _same_device(logits, experts=experts, dweights=dweights)
+    out = torch.empty_like(logits)
+    with _on(logits):
+        _check(lib().moe_route_bwd(_REAL[logits.dtype], pl, T, E, k, int(bool(renormalize)), pe, pw, _ptr(out),
+                                   _stream(logits)))
+    return out
+
+
+def _sorted(X, offsets, rows, E):
+    """Checked pointers of X, offsets and rows, with T, M and K."""
+    T, K = _dims(X, "X", 2)
+    px = _dev(X, "X", _BF16, (T, K))
+    po = _dev(offsets, "offsets", _I32, (E + 1,))
+    M, pr = T, ctypes.c_void_p(None)
+    if rows is not None:
+        M = _dims(rows, "rows", 1)[0]
+        pr = _dev(rows, "rows", _I32, (M,))
+    _same_device(X, offsets=offsets, rows=rows)
+    return px, po, pr, T, M, K
+
+
+def gemm_moe_bf16(X: torch.Tensor, W: torch.Tensor, offsets: torch.Tensor, rows: torch.Tensor | None = None,
+                  out: torch.Tensor | None = None, lw: int = K_MAJOR) -> torch.Tensor:
+    """Experts' products: D[i] = X[rows[i]] @ W[g].T for the sorted rows i of
+    expert g (offsets (E + 1) int32 on the GPU).  X (T, K) bf16, gathered
+    through rows (M,) int32, or sorted already (rows=None); W (E, N, K), or
+    with lw=MN_MAJOR (E, K, N): D[i] = X[rows[i]] @ W[g], the gradient with
+    respect to the rows.  Rows of D past offsets[E] are zero."""
+    lw = _layout(lw, "lw")
+    E, a, b = _dims(W, "W", 3)
+    px, po, pr, T, M, K = _sorted(X, offsets, rows, E)
+    N = a if lw == K_MAJOR else b
+    pw = _dev(W, "W", _BF16, (E, N, K) if lw == K_MAJOR else (E, K, N))
+    _same_device(X, W=W)
+    out = _given(out, (M, N), torch.bfloat16, X)
+    with _on(X):
+        _check(lib().gemm_moe_bf16(px, pw, _ptr(out), po, pr, T, M, E, N, K, lw, _stream(X)))
+    return out
+
+
+def gemm_moe_swiglu_bf16(X: torch.Tensor, W: torch.Tensor, offsets: torch.Tensor, rows: torch.Tensor | None = None,
+                         out: torch.Tensor | None = None) -> torch.Tensor:
+    """gemm_moe_bf16 with the gate applied on the way out: W (E, 2F, K) holds
+    every expert's gate matrix (first F rows) and up matrix; returns
+    silu(gate) * up, (M, F)."""
+    E, N, _ = _dims(W, "W", 3)
+    if N % 2:
+        raise ValueError(f"W: {N} rows per expert, expected an even number (gate and up matrices)")
+    px, po, pr, T, M, K = _sorted(X, offsets, rows, E)
+    pw = _dev(W, "W", _BF16, (E, N, K))
+    _same_device(X, W=W)
+    out = _given(out, (M, N // 2), torch.bfloat16, X)
+    with _on(X):
+        _check(lib().gemm_moe_swiglu_bf16(px, pw, _ptr(out), po, pr, T, M, E, N // 2, K, _stream(X)))
+    return out
+
+
+def gemm_moe_dw_bf16(dY: torch.Tensor, X: torch.Tensor, offsets: torch.Tensor, rows: torch.Tensor | None = None,
+                     out: torch.Tensor | None = None, out_dtype: torch.dtype = torch.bfloat16,
+                     accumulate: bool = False) -> torch.Tensor:
+    """Gradient with respect to the experts' matrices: dW[g] = dY_g.T @ X_g
+    over the sorted rows of expert g; dY (M, N), X (T, K) gathered through rows
+    or (M, K); dW (E, N, K) bf16 or fp32.  accumulate=True adds to the fp32
+    ``out``; otherwise an expert without rows gets zeros."""
+    if out_dtype not in _REAL:
+        raise TypeError(f"out_dtype: {out_dtype} not in {tuple(_REAL)}")
+    E = _dims(offsets, "offsets", 1)[0] - 1
+    px, po, pr, T, M, K = _sorted(X, offsets, rows, E)
+    N = _dims(dY, "dY", 2)[1]
+    py = _dev(dY, "dY", _BF16, (M, N))
+    _same_device(X, dY=dY)
+    if accumulate and out is None:
+        raise ValueError("accumulate needs out")
+    if out is not None:
+        out_dtype = out.dtype if out.dtype in _REAL else out_dtype
+    out = _given(out, (E, N, K), out_dtype, X)
+    with _on(X):
+        _check(lib().gemm_moe_dw_bf16(_REAL[out_dtype], py, px, _ptr(out), po, pr, T, M, E, N, K,
+                                      int(bool(accumulate)), _stream(X)))
+    return out
+
+
+def swiglu(H: torch.Tensor, out: torch.Tensor | None = None) -> torch.Tensor:
+    """silu(H[:, :F]) * H[:, F:] for H (M, 2F) bf16."""
+    M, N = _dims(H, "H", 2)
+    if N % 2:
+        raise ValueError(f"H: {N} columns, expected an even number")
+    ph = _dev(H, "H", _BF16, (M, N))
+    out = _given(out, (M, N // 2), torch.bfloat16, H)
+    with _on(H):
+        _check(lib().swiglu_bf16(ph, _ptr(out), M, N // 2, _stream(H)))
+    return out
+
+
+def swiglu_backward(dA: torch.Tensor, H: torch.Tensor, out: torch.Tensor | None = None) -> torch.Tensor:
+    """Gradient of swiglu with respect to H (M, 2F) from dA (M, F)."""
+    M, N = _dims(H, "H", 2)
+    if N % 2:
+        raise ValueError(f"H: {N} columns, expected an even number")
+    ph = _dev(H, "H", _BF16, (M, N))
+    pa = _dev(dA, "dA", _BF16, (M, N // 2))
+    _same_device(H, dA=dA)
+    out = _given(out, (M, N), torch.bfloat16, H)
+    with _on(H):
+        _check(lib().swiglu_bwd_bf16(pa, ph, _ptr(out), M, N // 2, _stream(H)))
+    return out
+
+
+def moe_combine(Y: torch.Tensor, slots: torch.Tensor, weights: torch.Tensor | None = None,
+                out: torch.Tensor | None = None) -> torch.Tensor:
+    """Back to token order: out[t] = sum over j of weights[t, j] * Y[slots[t, j]]
+    (weights=None: ones; slots of -1 add nothing); Y (M, H) bf16, slots (T, k)
+    int32, weights (T, k) fp32."""
+    M, H = _dims(Y, "Y", 2)
+    T, k = _dims(slots, "slots", 2)
+    py = _dev(Y, "Y", _BF16, (M, H))
+    ps = _dev(slots, "slots", _I32, (T, k))
+    if weights is not None:
+        _dev(weights, "weights", _F32, (T, k))
+    _same_device(Y, slots=slots, weights=weights)
+    out = _given(out, (T, H), torch.bfloat16, Y)
+    with _on(Y):
+        _check(lib().moe_combine_bf16(py, ps, _ptr(weights), _ptr(out), T, M, k, H, _stream(Y)))
+    return out
+
+
+def moe_combine_backward(dO: torch.Tensor, Y: torch.Tensor, slots: torch.Tensor, weights: torch.Tensor,
+                         offsets: torch.Tensor) -> tuple[torch.Tensor, torch.Tensor]:
+    """Gradients of moe_combine with respect to Y (T k, H) and weights (T, k)
+    from dO (T, H); rows of dY past offsets[E] are zero."""
+    T, H = _dims(dO, "dO", 2)
+    k = _dims(slots, "slots", 2)[1]
+    E = _dims(offsets, "offsets", 1)[0] - 1
+    pd = _dev(dO, "dO", _BF16, (T, H))
+    py = _dev(Y, "Y", _BF16, (T * k, H))
+    ps = _dev(slots, "slots", _I32, (T, k))
+    pw = _dev(weights, "weights", _F32, (T, k))
+    po = _dev(offsets, "offsets", _I32, (E + 1,))
+    _same_device(dO, Y=Y, slots=slots, weights=weights, offsets=offsets)
+    dY = torch.empty_like(Y)
+    dweights = torch.empty_like(weights)
+    with _on(dO):
+        _check(lib().moe_combine_bwd_bf16(pd, py, ps, pw, po, E, _ptr(dY), _ptr(dweights), T, k, H, _stream(dO)))
+    return dY, dweights

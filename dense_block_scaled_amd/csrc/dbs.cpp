@@ -10,6 +10,7 @@
 #include <cstring>
 
 #include "launch.h"
+#include "moe.h"
 
 namespace {
 
@@ -279,6 +280,8 @@ dbs_status fp6_gemm(dbs_mx_elem ea, dbs_mx_elem eb, const void *A, const uint8_t
 namespace dbs {
 
 void set_error(const char *msg) { std::snprintf(g_err, sizeof(g_err), "%s", msg); }
+
+int device_compute_units(int *cus) { return device_cus(cus); }
 
 int nvfp4_fp8_check(const void *A, const uint8_t *sA, const void *B, const uint8_t *sB, const void *D, int64_t M,
                     int64_t N, int64_t K, int la, int lb)

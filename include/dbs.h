@@ -311,6 +311,88 @@ dbs_status quant_nvfp4(const float *x, int64_t rows, int64_t K, void *codes, uin
                        hipStream_t stream);
 dbs_status quant_bf16(const float *x, int64_t n, void *out, hipStream_t stream);
 
+/*
+ * Mixture-of-experts operators: the router, the experts' products in both
+ * directions, the gate between them and the way back to token order.  A layer
+ * of E experts (1 .. 1024) sends each of T tokens to its k (1 .. 16) best.
+ * The T k pairs (t, j), sorted by expert (stably: by pair index within an
+ * expert), are the M = T k rows of the sorted order:
+ *
+ *   experts (T x k)  expert of pair (t, j), -1 if the token has fewer open experts
+ *   offsets (E + 1)  expert e's rows are offsets[e] .. offsets[e + 1] - 1
+ *   rows    (M)      token of a sorted row; -1 at and past offsets[E]
+ *   slots   (T x k)  sorted row of pair (t, j), -1 if it has none
+ *
+ * all int32 in DEVICE memory: nothing is copied to the host between the calls
+ * of a layer, so they can be captured in a HIP graph.  Arrays are dense, rows
+ * contiguous; bf16 arrays of 16-byte alignment unless stated.  Sums, softmax
+ * and gate are fp32 and rounded once.  Every result is the same from run to
+ * run (no floating-point atomics).  T k at most 2^25.
+ *
+ * moe_route: experts and weights of every token from its logits (T x E of
+ *   `type`): the k largest, ties to the lower expert; weights = softmax over
+ *   all E logits, or, with renormalize = 1, over the chosen ones.  A logit of
+ *   -inf or NaN closes its expert to the token (weight 0, never chosen); a
+ *   token may have no open expert.  +inf counts as the largest finite value.
+ *   workspace: device memory of moe_route_workspace(T, E, k) bytes (0 up to
+ *   64 tokens), 4-byte aligned, the caller's; calls that share one must not
+ *   overlap.  One kernel up to 64 tokens, three above.
+ * moe_route_bwd: dlogits (T x E of `type`, fully written) from the weights'
+ *   gradients: p (u - sum p u), p the softmax of moe_route's weights and u the
+ *   gradients at the chosen experts; dweights of pairs without an expert are
+ *   not read into it.
+ * gemm_moe_bf16: D[i] = X[rows[i]] W_g^T for the rows i of expert g.  X: T x K
+ *   (rows null: X is sorted already, M x K, T = M); W: E x N x K (lw =
+ *   DBS_K_MAJOR) or E x K x N (lw = DBS_MN_MAJOR; D[i] = X[rows[i]] W_g, the
+ *   gradient with respect to the rows of a K-major product; N a multiple of
+ *   8, else DBS_EUNSUPPORTED); D: M x N.  K a multiple of 8; D 2-byte aligned.
+ *   Rows of D at and past offsets[E] are set to zero.  Offsets outside
+ *   0 .. M are clamped and descending ones read as empty; row indices outside
+ *   0 .. T - 1 stand for a zero row.
+ * gemm_moe_swiglu_bf16: the same with W: E x 2F x K and D[i, f] = silu(h[f])
+ *   h[F + f], h = X[rows[i]] W_g^T kept in fp32.
+ * gemm_moe_dw_bf16: dW[g] = sum over expert g's rows i of dY[i]^T X[rows[i]]:
+ *   dY M x N, dW E x N x K of `type`; N and K multiples of 8.  An expert
+ *   without rows gets zeros.  accumulate = 1 (fp32 only): dW is added to.
+ * swiglu_bf16: A[m, f] = silu(H[m, f]) H[m, F + f] (H M x 2F, A M x F, any F,
+ *   2-byte aligned); swiglu_bwd_bf16: dH from dA.
+ * moe_combine_bf16: out[t] = sum over j of weights[t, j] Y[slots[t, j]] (Y M x
+ *   H; weights null: ones, which sums the rows' gradients back to tokens;
+ *   slots of -1 add nothing; any H, 2-byte aligned).
+ * moe_combine_bwd_bf16: dY[slots[t, j]] = weights[t, j] dO[t] (rows at and past
+ *   offsets[E] zero) and dweights[t, j] = <dO[t], Y[slots[t, j]]> (0 without a
+ *   slot); Y and dY have M = T k rows.
+ *
+ * Limits: N and K at most 2^21 (F 2^20), an expert's matrix below 2 GiB and a
+ * gathered X below 4 GiB - 16 MiB (DBS_EUNSUPPORTED).  D, dW, dY and the
+ * other outputs must not alias inputs.
+ */
+typedef enum {
+    DBS_F32 = 0,
+    DBS_BF16 = 1
+} dbs_real;
+
+size_t moe_route_workspace(int64_t T, int64_t E, int64_t k);      /* 0 for invalid sizes too */
+dbs_status moe_route(dbs_real type, const void *logits, int64_t T, int64_t E, int64_t k, int renormalize,
+                     int32_t *experts, float *weights, int32_t *offsets, int32_t *rows, int32_t *slots,
+                     void *workspace, size_t workspace_bytes, hipStream_t stream);
+dbs_status moe_route_bwd(dbs_real type, const void *logits, int64_t T, int64_t E, int64_t k, int renormalize,
+                         const int32_t *experts, const float *dweights, void *dlogits, hipStream_t stream);
+dbs_status gemm_moe_bf16(const void *X, const void *W, void *D, const int32_t *offsets, const int32_t *rows,
+                         int64_t T, int64_t M, int64_t E, int64_t N, int64_t K, dbs_layout lw, hipStream_t stream);
+dbs_status gemm_moe_swiglu_bf16(const void *X, const void *W, void *D, const int32_t *offsets, const int32_t *rows,
+                                int64_t T, int64_t M, int64_t E, int64_t F, int64_t K, hipStream_t stream);
+dbs_status gemm_moe_dw_bf16(dbs_real type, const void *dY, const void *X, void *dW, const int32_t *offsets,
+                            const int32_t *rows, int64_t T, int64_t M, int64_t E, int64_t N, int64_t K,
+                            int accumulate, hipStream_t stream);
+dbs_status swiglu_bf16(const void *H, void *A, int64_t M, int64_t F, hipStream_t stream);
+dbs_status swiglu_bwd_bf16(const void *dA, const void *H, void *dH, int64_t M, int64_t F, hipStream_t stream);
+dbs_status moe_combine_bf16(const void *Y, const int32_t *slots, const float *weights, void *out, int64_t T,
+                            int64_t M, int64_t k, int64_t H, hipStream_t stream);
+dbs_status moe_combine_bwd_bf16(const void *dO, const void *Y, const int32_t *slots, const float *weights,
+                                const int32_t *offsets, int64_t E, void *dY, float *dweights, int64_t T, int64_t k,
+                                int64_t H, hipStream_t stream);
+
 /* Static text for a status code. */
 const char *dbs_status_str(dbs_status st);
 
