@@ -64,23 +64,31 @@ __device__ __forceinline__ Lane lane_of()
     return c;
 }
 
-template <class S>
+template <class S, int MBA = S::MB>
 struct Frag2 {
-    bf16x8 a[S::MB], b[S::NB];
+    bf16x8 a[MBA], b[S::NB];
 };
+
+// K-major A: the two wave rows take the tile's blocks of 32 rows in turn
+// (wave row wm: blocks wm, wm + 2, ...), so a tile whose group ends early
+// leaves both with the same number of blocks, MBA, to compute.  Blocks of one
+// wave lie 64 rows apart, where the swizzle repeats.
+template <class S>
+__device__ __forceinline__ bf16x8 read_a2(const uint8_t *lds, uint32_t fa, int kk, int i)
+{
+    if constexpr (S::AMN) return read_frag_mn<kBF16, S::TM>(lds, fa, 0, kk, i);
+    else return lds_read<bf16x8>(lds, (fa ^ (uint32_t)(kk << 5)) + (uint32_t)(64 * kRowBytes * i));
+}
 
 // One k-step: the MFMAs of `cur` while k-step PH of the slot behind fa / fb
 // is read into `nxt` (if RD); after MFMA i, issue(i).
-template <class S, int PH, bool RD, class ISSUE>
-__device__ __forceinline__ void phase2(f32x16 (&acc)[S::MB][S::NB], Frag2<S> &cur, Frag2<S> &nxt, const uint8_t *lds,
-                                       uint32_t fa, uint32_t fb, ISSUE &&issue)
+template <class S, int MBA, int PH, bool RD, class ISSUE>
+__device__ __forceinline__ void phase2(f32x16 (&acc)[MBA][S::NB], Frag2<S, MBA> &cur, Frag2<S, MBA> &nxt,
+                                       const uint8_t *lds, uint32_t fa, uint32_t fb, ISSUE &&issue)
 {
     if constexpr (RD) {
 #pragma unroll
-        for (int i = 0; i < S::MB; ++i) {
-            if constexpr (S::AMN) nxt.a[i] = read_frag_mn<kBF16, S::TM>(lds, fa, 0, PH, i);
-            else nxt.a[i] = read_frag<kBF16>(lds, fa, 0, PH, i);
-        }
+        for (int i = 0; i < MBA; ++i) nxt.a[i] = read_a2<S>(lds, fa, PH, i);
 #pragma unroll
         for (int j = 0; j < S::NB; ++j) {
             if constexpr (S::BMN) nxt.b[j] = read_frag_mn<kBF16, S::TN>(lds, fb, 0, PH, j);
@@ -89,12 +97,12 @@ __device__ __forceinline__ void phase2(f32x16 (&acc)[S::MB][S::NB], Frag2<S> &cu
     }
     DBS_FENCE();
 #pragma unroll
-    for (int i = 0; i < S::MB; ++i) {
+    for (int i = 0; i < MBA; ++i) {
 #pragma unroll
         for (int j = 0; j < S::NB; ++j) {
             mma1<kBF16, 0>(acc[i][j], cur.a[i], 0u, cur.b[j], 0u);
             DBS_FENCE();
-            issue(PH * S::MB * S::NB + i * S::NB + j);
+            issue(PH * MBA * S::NB + i * S::NB + j);
             DBS_FENCE();
         }
     }
@@ -103,18 +111,18 @@ __device__ __forceinline__ void phase2(f32x16 (&acc)[S::MB][S::NB], Frag2<S> &cu
 // One stage of four k-steps out of the slot behind fa / fb.  On entry F1
 // holds the previous stage's last k-step, whose MFMAs come first; piece q of
 // the stage being loaded goes out after MFMA q.
-template <class S, class PIECE>
-__device__ __forceinline__ void stage2(f32x16 (&acc)[S::MB][S::NB], Frag2<S> &F0, Frag2<S> &F1, const uint8_t *lds,
-                                       uint32_t fa, uint32_t fb, PIECE &&piece)
+template <class S, int MBA, class PIECE>
+__device__ __forceinline__ void stage2(f32x16 (&acc)[MBA][S::NB], Frag2<S, MBA> &F0, Frag2<S, MBA> &F1,
+                                       const uint8_t *lds, uint32_t fa, uint32_t fb, PIECE &&piece)
 {
     auto issue = [&](int i) {
         if (i < S::QB) piece(i);
     };
-    static_assert(S::QA <= S::QB, "piece q loads A (q < QA) and B");
-    phase2<S, 0, true>(acc, F1, F0, lds, fa, fb, issue);
-    phase2<S, 1, true>(acc, F0, F1, lds, fa, fb, issue);
-    phase2<S, 2, true>(acc, F1, F0, lds, fa, fb, issue);
-    phase2<S, 3, true>(acc, F0, F1, lds, fa, fb, issue);
+    static_assert(S::QA <= S::QB && S::QB <= 4 * S::NB, "piece q loads A (q < QA) and B");
+    phase2<S, MBA, 0, true>(acc, F1, F0, lds, fa, fb, issue);
+    phase2<S, MBA, 1, true>(acc, F0, F1, lds, fa, fb, issue);
+    phase2<S, MBA, 2, true>(acc, F1, F0, lds, fa, fb, issue);
+    phase2<S, MBA, 3, true>(acc, F0, F1, lds, fa, fb, issue);
     stage_barrier<(S::NS - 2) * (S::QA + S::QB)>();
 }
 
@@ -123,7 +131,7 @@ template <class S>
 __device__ __forceinline__ uint32_t frag_a(const Lane &c)
 {
     if constexpr (S::AMN) return mn_base<kBF16, S::TM>(c.lane, c.wm * (S::TM / S::WM), S::kLdsA);
-    const int r = c.wm * (S::TM / S::WM) + c.lr;
+    const int r = c.wm * 32 + c.lr;
     return (uint32_t)(S::kLdsA + r * kRowBytes + ((c.h ^ swz(r)) << 4));
 }
 
@@ -138,18 +146,17 @@ __device__ __forceinline__ uint32_t frag_b(const Lane &c)
 // ------------------------------------------------------------ group tables
 
 // first[g] = first row of group g (g <= E; offsets clamped to 0 .. M and made
-// ascending), tile[g] = units of work before group g, per(rows) of them in a
-// group; by wave 0, the others wait at the caller's barrier.
-template <class PER>
-__device__ __forceinline__ void group_table(int32_t *first, int32_t *tile, const int32_t *offsets, int E, int M,
-                                            const Lane &c, PER &&per)
+// ascending; with FIRST), and at[g] = units of work before group g, per(rows)
+// of them in a group: by one wave, the others wait at the caller's barrier.
+template <bool FIRST, class T, class PER>
+__device__ __forceinline__ void group_table(int32_t *first, T *at, const int32_t *offsets, int E, int M, const Lane &c,
+                                            PER &&per)
 {
-    if (c.w != 0) return;
     int hi = 0, sum = 0;                       // last row and work before this chunk of 64 groups
     if (c.lane == 0) {
         hi = min(max(offsets[0], 0), M);
-        first[0] = hi;
-        tile[0] = 0;
+        if constexpr (FIRST) first[0] = hi;
+        at[0] = 0;
     }
     hi = __shfl(hi, 0);
     for (int g0 = 0; g0 < E; g0 += 64) {
@@ -170,22 +177,23 @@ __device__ __forceinline__ void group_table(int32_t *first, int32_t *tile, const
             if (c.lane >= d) n += o;
         }
         if (g < E) {
-            first[g + 1] = end;
-            tile[g + 1] = sum + n;
+            if constexpr (FIRST) first[g + 1] = end;
+            at[g + 1] = (T)(sum + n);
         }
         hi = __shfl(end, 63);
         sum += __shfl(n, 63);
     }
 }
 
-// The last group g with tile[g] <= id (groups without work have equal
+// The last group g with at[g] <= id (groups without work have equal
 // neighbours): 64 entries a step, one LDS read each.
-__device__ __forceinline__ int group_of(const int32_t *tile, int E, int id, const Lane &c)
+template <class T>
+__device__ __forceinline__ int group_of(const T *at, int E, int id, const Lane &c)
 {
     int n = 0;
     for (int g0 = 0; g0 < E; g0 += 64) {
         const int g = g0 + c.lane;
-        n += __popcll(__ballot(g < E && tile[g] <= id));
+        n += __popcll(__ballot(g < E && (int)at[g] <= id));
     }
     return __builtin_amdgcn_readfirstlane(n - 1);
 }
@@ -203,14 +211,16 @@ __device__ __forceinline__ int first_tile()
 // (ld elements a row, OUT a bf16 or float): NBO blocks of 32 columns, value
 // q of block j in block-row i from value(i, j, q).  vec: through LDS and in
 // 16-byte pieces (bf16; the caller's slot is free); otherwise by element.
-template <class S, int NBO, class VALUE>
+template <class S, int MBA, int NBO, class VALUE>
 __device__ __forceinline__ void store_bf16(uint8_t *buf, uint8_t *D, int64_t ld, int m0, int mend, int n0, int ncols,
-                                           int vec, const Lane &c, VALUE &&value)
+                                           int vec, Lane c, VALUE &&value)
 {
+    // (addresses are made here, not before the tile's stages, whose registers they would take)
+    asm volatile("" : "+v"(c.lane), "+v"(c.lr), "+v"(c.h));
     constexpr int RB = NBO * 64, CPR = RB / 16, RPI = 64 / CPR;
 #pragma unroll
-    for (int i = 0; i < S::MB; ++i) {
-        const int r0 = m0 + c.wm * (S::TM / S::WM) + i * 32;
+    for (int i = 0; i < MBA; ++i) {
+        const int r0 = m0 + (S::AMN ? c.wm * (S::TM / S::WM) + i * 32 : (2 * i + c.wm) * 32);
         const int left = __builtin_amdgcn_readfirstlane(max(0, min(32, mend - r0)));
         const __amdgpu_buffer_rsrc_t rd = make_rsrc(D + (int64_t)r0 * ld * 2, (uint32_t)left * (uint32_t)ld * 2u);
         if (vec) {
@@ -249,12 +259,27 @@ __device__ __forceinline__ void store_bf16(uint8_t *buf, uint8_t *D, int64_t ld,
 
 // ------------------------------------------------------------------- tiles
 
-// GATE: see the head of the file.  WMN: W MN-major.
+// A group of r rows has r / TM whole tile rows and a rest, computed with the
+// ceil(rest / 64) blocks per wave that hold it.  Tiles are handed out by
+// descending cost -- all groups' whole tile rows (and rests that need every
+// block), then the rests by blocks -- in a snake over the workgroups, so
+// that those with a tile less of one kind come first for the next.
+template <class S>
+struct Table {
+    int32_t first[kMoeMaxExperts + 1], whole[kMoeMaxExperts + 1];   // tile rows before a group
+    uint16_t rest[S::MB > 1 ? S::MB - 1 : 1][kMoeMaxExperts + 1];   // rests of b + 1 blocks before a group
+};
+
+// blocks per wave of a group's rest; S::MB counts as a whole tile row
+template <class S>
+__device__ __forceinline__ int rest_blocks(int rows) { return (rows % S::TM + 63) / 64; }
+
+// GATE: see the head of the file.
 template <class S, bool GATE>
 __global__ __launch_bounds__(512, 1) void moe_tiles(MoeGemm p)
 {
     __shared__ __attribute__((aligned(1024))) uint8_t lds[S::kRing];
-    __shared__ int32_t first[kMoeMaxExperts + 1], tile_at[kMoeMaxExperts + 1];
+    __shared__ Table<S> tab;
     static_assert(!(GATE && S::BMN), "the gate takes K-major matrices");
     constexpr int MB = S::MB, NB = S::NB;
     constexpr int TNO = GATE ? S::TN / 2 : S::TN;      // output columns of a tile
@@ -262,13 +287,17 @@ __global__ __launch_bounds__(512, 1) void moe_tiles(MoeGemm p)
     const Lane c = lane_of();
     const int lda = p.K * 2;
     const int tiles_n = (p.ncols + TNO - 1) / TNO;
-    group_table(first, tile_at, p.offsets, p.E, p.M, c,
-                [&](int rows) { return (rows + S::TM - 1) / S::TM * tiles_n; });
+    if (c.w == 0)
+        group_table<true>(tab.first, tab.whole, p.offsets, p.E, p.M, c,
+                          [&](int rows) { return rows / S::TM + (rest_blocks<S>(rows) == MB); });
+    else if (c.w < MB)
+        group_table<false>(tab.first, tab.rest[c.w - 1], p.offsets, p.E, p.M, c,
+                           [&](int rows) { return (int)(rest_blocks<S>(rows) == c.w); });
     __syncthreads();
 
     // rows behind the last group are zero
     {
-        const int64_t total = first[p.E];
+        const int64_t total = tab.first[p.E];
         const int64_t bytes = (p.M - total) * p.ncols * 2;
         uint8_t *z = p.D + total * p.ncols * 2;
         const int64_t me = (int64_t)blockIdx.x * S::kThreads + threadIdx.x, all = (int64_t)gridDim.x * S::kThreads;
@@ -278,10 +307,50 @@ __global__ __launch_bounds__(512, 1) void moe_tiles(MoeGemm p)
             for (int64_t o = me * 2; o < bytes; o += all * 2) *reinterpret_cast<uint16_t *>(z + o) = 0;
     }
 
-    const int ntiles = tile_at[p.E], nwg = gridDim.x;
-    int tile = first_tile();
-    if (tile >= ntiles) return;
+    int ntiles = __builtin_amdgcn_readfirstlane(tab.whole[p.E]);
+#pragma unroll
+    for (int b = 1; b < MB; ++b) ntiles += __builtin_amdgcn_readfirstlane((int)tab.rest[b - 1][p.E]);
+    ntiles *= tiles_n;
+    const int nwg = gridDim.x, self = first_tile();
+    if (self >= ntiles) return;
     const int nk = max((p.K + S::KS - 1) / S::KS, S::NS - 1);
+
+    struct Ref {
+        int m0, mend, n0, g, blocks;
+    };
+    // output tile id of the order above; past the last: no rows
+    auto ref_of = [&](int id) {
+        Ref r{};
+        if (id >= ntiles) return r;
+        const int whole = __builtin_amdgcn_readfirstlane(tab.whole[p.E]) * tiles_n;
+        if (id < whole) {
+            const int row = id / tiles_n;              // groups of one tile row need no more than this
+            r.g = group_of(tab.whole, p.E, row, c);
+            const int before = __builtin_amdgcn_readfirstlane(tab.whole[r.g]);
+            const int n = __builtin_amdgcn_readfirstlane(tab.whole[r.g + 1]) - before;
+            const int local = id - before * tiles_n;   // tile rows fastest: they share W's rows
+            r.m0 = local % n * S::TM;
+            r.n0 = local / n * TNO;
+            r.blocks = MB;
+        } else {
+            id -= whole;
+#pragma unroll
+            for (int b = MB - 1; b >= 1; --b) {
+                const int n = __builtin_amdgcn_readfirstlane((int)tab.rest[b - 1][p.E]) * tiles_n;
+                if (r.blocks == 0 && id < n) {
+                    r.g = group_of(tab.rest[b - 1], p.E, id / tiles_n, c);
+                    r.n0 = id % tiles_n * TNO;
+                    r.blocks = b;
+                }
+                id -= r.blocks == 0 ? n : 0;
+            }
+        }
+        const int lo = __builtin_amdgcn_readfirstlane(tab.first[r.g]);
+        r.mend = __builtin_amdgcn_readfirstlane(tab.first[r.g + 1]);
+        if (r.blocks < MB) r.m0 = (r.mend - lo) / S::TM * S::TM;
+        r.m0 += lo;
+        return r;
+    };
 
     // where a tile's stages come from
     struct Source {
@@ -289,6 +358,9 @@ __global__ __launch_bounds__(512, 1) void moe_tiles(MoeGemm p)
         uint32_t a[S::QA];       // the lane's byte offset in ra per wave-load, its chunk included
         int f0;                  // the tile's first output column
     } src;
+    // the rows of X behind the next tile's wave-loads, read while this tile is
+    // computed (~0: none, a zero row)
+    uint32_t row[S::QA];
     uint32_t x4 = (uint32_t)(((c.lane & 7) ^ (c.lane >> 3)) << 4);
     const int ldb = S::BMN ? p.N * 2 : lda;            // bytes of a row of W as stored
     uint32_t r8ldb = (uint32_t)((c.lane >> 3) * ldb);
@@ -297,26 +369,18 @@ __global__ __launch_bounds__(512, 1) void moe_tiles(MoeGemm p)
         mb[0] = mn_dma_lane<kBF16, S::TN>(c.lane, 0, ldb);
         mb[1] = mn_dma_lane<kBF16, S::TN>(c.lane, 1, ldb);
     }
-    struct Ref {
-        int m0, mend, n0, g;
+    auto fetch = [&](const Ref &r) {
+#pragma unroll
+        for (int q = 0; q < S::QA; ++q) {
+            const int m = (c.w * S::QA + q) * 8 + (c.lane >> 3);
+            row[q] = !p.rows ? (uint32_t)m : r.m0 + m < r.mend ? (uint32_t)p.rows[r.m0 + m] : ~0u;
+        }
     };
-    auto ref_of = [&](int id) {
-        Ref r;
-        r.g = group_of(tile_at, p.E, id, c);
-        const int lo = __builtin_amdgcn_readfirstlane(first[r.g]), hi = __builtin_amdgcn_readfirstlane(first[r.g + 1]);
-        const int local = id - __builtin_amdgcn_readfirstlane(tile_at[r.g]);
-        const int tmg = (hi - lo + S::TM - 1) / S::TM;
-        r.m0 = lo + local % tmg * S::TM;
-        r.mend = hi;
-        r.n0 = local / tmg * TNO;
-        return r;
-    };
-    auto aim = [&](int id) {
-        if (id >= ntiles) {
+    auto aim = [&](const Ref &r) {
+        if (r.blocks == 0) {
             src.ra = src.rb = make_rsrc(nullptr, 0);
             return;
         }
-        const Ref r = ref_of(id);
         const int64_t wbytes = (int64_t)p.N * p.K * 2;
         const uint8_t *wg = p.W + r.g * wbytes;
         src.f0 = r.n0;
@@ -326,21 +390,12 @@ __global__ __launch_bounds__(512, 1) void moe_tiles(MoeGemm p)
             src.rb = make_rsrc(wg, (uint32_t)wbytes);
         else
             src.rb = make_rsrc(wg + (int64_t)r.n0 * lda, (uint32_t)(min(p.N - r.n0, S::TN) * lda));
-        if (p.rows)
-            src.ra = make_rsrc(p.X, (uint32_t)(p.T * lda));
-        else
-            src.ra = make_rsrc(p.X + (int64_t)r.m0 * lda, (uint32_t)(min(r.mend - r.m0, S::TM) * lda));
+        const uint32_t have = p.rows ? (uint32_t)p.T : (uint32_t)min(r.mend - r.m0, S::TM);
+        src.ra = make_rsrc(p.rows ? p.X : p.X + (int64_t)r.m0 * lda, have * (uint32_t)lda);
 #pragma unroll
         for (int q = 0; q < S::QA; ++q) {
-            const int L = c.w * S::QA + q, m = L * 8 + (c.lane >> 3);
-            uint32_t row = (uint32_t)m;
-            bool in = true;
-            if (p.rows) {
-                in = r.m0 + m < r.mend;
-                row = in ? (uint32_t)p.rows[r.m0 + m] : 0u;
-                in = in && row < (uint32_t)p.T;
-            }
-            src.a[q] = (in ? row * (uint32_t)lda : kRowOOB) + (x4 ^ (uint32_t)((L & 7) << 4));
+            const int L = c.w * S::QA + q;
+            src.a[q] = (row[q] < have ? row[q] * (uint32_t)lda : kRowOOB) + (x4 ^ (uint32_t)((L & 7) << 4));
         }
     };
     auto load = [&](int slot, int ks, int q) {
@@ -371,7 +426,9 @@ __global__ __launch_bounds__(512, 1) void moe_tiles(MoeGemm p)
         }
     };
 
-    aim(tile);
+    Ref cur = ref_of(self), next{};
+    fetch(cur);
+    aim(cur);
 #pragma unroll
     for (int f = 0; f < S::NS - 1; ++f) {
 #pragma unroll
@@ -380,15 +437,18 @@ __global__ __launch_bounds__(512, 1) void moe_tiles(MoeGemm p)
     uint32_t fa = frag_a<S>(c), fb = frag_b<S>(c);
     __syncthreads();
 
-    int rs = 0, xs = 0;       // slots the next stage reads, the last one read
-    for (;;) {
-        f32x16 acc[MB][NB];
+    int rs = 0;               // slot the next stage reads
+    int round = 0;
+    // one output tile of MBA blocks per wave
+    auto run = [&](auto blocks) {
+        constexpr int MBA = decltype(blocks)::value;
+        f32x16 acc[MBA][NB];
 #pragma unroll
-        for (int i = 0; i < MB; ++i)
+        for (int i = 0; i < MBA; ++i)
 #pragma unroll
             for (int j = 0; j < NB; ++j) acc[i][j] = f32x16{};
-        Frag2<S> F0, F1{};
-        const int next = tile + nwg;
+        Frag2<S, MBA> F0, F1{};
+        int xs = 0;           // slot the last stage read
         for (int s = 0; s < nk; ++s) {
             int ks = s + S::NS - 1;
             if (ks >= nk) {
@@ -397,30 +457,43 @@ __global__ __launch_bounds__(512, 1) void moe_tiles(MoeGemm p)
             }
             const int ls = rs == 0 ? S::NS - 1 : rs - 1;
             asm volatile("" : "+v"(x4), "+v"(r8ldb), "+v"(fa), "+v"(fb));
-            stage2<S>(acc, F0, F1, lds, fa + (uint32_t)(rs * S::kSlotA), fb + (uint32_t)(rs * S::kSlotB),
-                      [&](int q) { load(ls, ks, q); });
+            stage2<S, MBA>(acc, F0, F1, lds, fa + (uint32_t)(rs * S::kSlotA), fb + (uint32_t)(rs * S::kSlotB),
+                           [&](int q) { load(ls, ks, q); });
             xs = rs;
             rs = rs + 1 == S::NS ? 0 : rs + 1;
         }
-        phase2<S, 0, false>(acc, F1, F0, lds, fa, fb, [](int) {});
+        phase2<S, MBA, 0, false>(acc, F1, F0, lds, fa, fb, [](int) {});
 
-        const Ref r = ref_of(tile);
         // the slot the last stage read is free until the next tile's first
         // stage refills it: its B part holds 8 waves' 32-row buffers
         constexpr int NBO = GATE ? NB / 2 : NB;
         uint8_t *buf = lds + S::kLdsB + xs * S::kSlotB + c.w * (32 * NBO * 64);
-        store_bf16<S, NBO>(buf, p.D, p.ncols, r.m0, r.mend, r.n0 + c.wn * (NBO * 32), p.ncols, p.vec, c,
-                           [&](int i, int j, int q) {
-                               if constexpr (GATE) {
-                                   const float g = acc[i][0][q];
-                                   return g * __builtin_amdgcn_rcpf(1.0f + __expf(-g)) * acc[i][1][q];
-                               } else {
-                                   return acc[i][j][q];
-                               }
-                           });
+        store_bf16<S, MBA, NBO>(buf, p.D, p.ncols, cur.m0, cur.mend, cur.n0 + c.wn * (NBO * 32), p.ncols, p.vec, c,
+                                [&](int i, int j, int q) {
+                                    if constexpr (GATE) {
+                                        const float g = acc[i][0][q];
+                                        return g * __builtin_amdgcn_rcpf(1.0f + __expf(-g)) * acc[i][1][q];
+                                    } else {
+                                        return acc[i][j][q];
+                                    }
+                                });
         asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory");
-        if (next >= ntiles) break;
-        tile = next;
+    };
+    for (;;) {
+        // the next tile's rows are looked up while this one is computed
+        ++round;
+        next = ref_of(round * nwg + (round & 1 ? nwg - 1 - self : self));
+        fetch(next);
+        if (MB == 1 || cur.blocks == MB) run(std::integral_constant<int, MB>{});
+        if constexpr (MB > 1) {
+            if (cur.blocks == 1) run(std::integral_constant<int, 1>{});
+        }
+        if constexpr (MB > 2) {
+            if (cur.blocks == 2) run(std::integral_constant<int, 2>{});
+            if (cur.blocks == 3) run(std::integral_constant<int, 3>{});
+        }
+        if (next.blocks == 0) break;
+        cur = next;
     }
 }
 
@@ -440,8 +513,9 @@ __global__ __launch_bounds__(512, 1) void moe_dw(MoeGemmDw p)
     const Lane c = lane_of();
     const int lda = p.N * 2, ldb = p.K * 2;            // bytes of a row of dY, of X
     const int tiles_n = (p.N + S::TM - 1) / S::TM, tiles_k = (p.K + S::TN - 1) / S::TN, per = tiles_n * tiles_k;
-    group_table(first, tile_at, p.offsets, p.E, p.M, c,
-                [&](int rows) { return p.accumulate && rows == 0 ? 0 : per; });
+    if (c.w == 0)
+        group_table<true>(first, tile_at, p.offsets, p.E, p.M, c,
+                          [&](int rows) { return p.accumulate && rows == 0 ? 0 : per; });
     __syncthreads();
     const int ntiles = tile_at[p.E], nwg = gridDim.x;
     int tile = first_tile();
@@ -531,7 +605,7 @@ __global__ __launch_bounds__(512, 1) void moe_dw(MoeGemmDw p)
                 if (i < S::QB) load(ls, ks, i);
             };
             const uint32_t a = fa + (uint32_t)(rs * S::kSlotA), b = fb + (uint32_t)(rs * S::kSlotB);
-            phase2<S, 0, true>(acc, F1, F0, lds, a, b, issue);
+            phase2<S, MB, 0, true>(acc, F1, F0, lds, a, b, issue);
             // the row indices of the stage after that
             if (s + 2 < nk) {
                 fetch_rows(s + 2);
@@ -541,13 +615,13 @@ __global__ __launch_bounds__(512, 1) void moe_dw(MoeGemmDw p)
             } else if (stages(nref) > 1) {
                 fetch_rows(1);
             }
-            phase2<S, 1, true>(acc, F0, F1, lds, a, b, [](int) {});
-            phase2<S, 2, true>(acc, F1, F0, lds, a, b, [](int) {});
-            phase2<S, 3, true>(acc, F0, F1, lds, a, b, [](int) {});
+            phase2<S, MB, 1, true>(acc, F0, F1, lds, a, b, [](int) {});
+            phase2<S, MB, 2, true>(acc, F1, F0, lds, a, b, [](int) {});
+            phase2<S, MB, 3, true>(acc, F0, F1, lds, a, b, [](int) {});
             stage_barrier<0>();
             rs ^= 1;
         }
-        phase2<S, 0, false>(acc, F1, F0, lds, fa, fb, [](int) {});
+        phase2<S, MB, 0, false>(acc, F1, F0, lds, fa, fb, [](int) {});
 
         const int n0 = cur.n0, k0 = cur.k0 + c.wn * 64;
         if constexpr (F32) {
@@ -574,7 +648,7 @@ __global__ __launch_bounds__(512, 1) void moe_dw(MoeGemmDw p)
             }
         } else {
             uint8_t *buf = lds + S::kLdsB + (rs ^ 1) * S::kSlotB + c.w * (32 * NB * 64);
-            store_bf16<S, NB>(buf, p.dW + (int64_t)cur.g * p.N * p.K * 2, p.K, n0, p.N, k0, p.K, 1, c,
+            store_bf16<S, MB, NB>(buf, p.dW + (int64_t)cur.g * p.N * p.K * 2, p.K, n0, p.N, k0, p.K, 1, c,
                               [&](int i, int j, int q) { return acc[i][j][q]; });
         }
         asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory");
