@@ -61,7 +61,7 @@ dbs_status run_product(dbs::MoeGemm p, hipStream_t stream)
     // Tile rows by the rows an expert has on average: a tile's height beyond
     // them is computed for nothing.
     const int64_t mean = p.M / p.E;
-    const int tm = mean <= 96 ? 64 : mean <= 192 ? 128 : 256;
+    const int tm = mean <= 96 ? 64 : 256;
     const int64_t tiles_n = (p.ncols + 127) / 128;
     if ((p.M / 64 + p.E) * tiles_n >= kTwoGiB) return fail(DBS_EUNSUPPORTED, "too many output tiles");
     return done(dbs::launch_moe_tiles(p, tm, cus, stream));

@@ -34,6 +34,43 @@ namespace {
 
 constexpr uint32_t kRowOOB = 0xFF000000u;        // + a row's bytes (at most 2^22) still lies past every resource
 
+// Buffer descriptor (see make_rsrc) as the four words an instruction takes;
+// base and bytes are the same in every lane.
+__device__ __forceinline__ i32x4 words_of(const void *base, uint32_t bytes)
+{
+    const uint64_t b = (uint64_t)base;
+    return i32x4{__builtin_amdgcn_readfirstlane((int)(uint32_t)b),
+                 __builtin_amdgcn_readfirstlane((int)((uint32_t)(b >> 32) & 0xFFFFu)),
+                 __builtin_amdgcn_readfirstlane((int)bytes), 0x00020000};
+}
+
+// Direct-to-LDS load of BYTES per lane, as lds_dma in gemm_kernel.h, but
+// written out: the compiler follows the builtin's loads and waits for all of
+// them before any LDS read, which would end the overlap this file's kernels
+// are built on.  They wait by count themselves, at every barrier.  Lane i's
+// bytes land at dst + BYTES i; nothing is returned to registers.  (M0, which
+// holds the destination, is a register the compiler sets before its own uses.)
+template <int BYTES>
+__device__ __forceinline__ void dma(const i32x4 &words, uint8_t *dst, uint32_t voff)
+{
+    static_assert(BYTES == 4 || BYTES == 16, "dword or dwordx4");
+#if DBS_LDS_POISON
+    const uint32_t lane = __builtin_amdgcn_mbcnt_hi(~0u, __builtin_amdgcn_mbcnt_lo(~0u, 0u));
+    if constexpr (BYTES == 4)
+        *reinterpret_cast<uint32_t *>(dst + 4 * lane) = ~0u;
+    else
+        *reinterpret_cast<i32x4 *>(dst + 16 * lane) = i32x4{-1, -1, -1, -1};
+    asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+#endif
+    const int m0 = __builtin_amdgcn_readfirstlane((int)(uint32_t)(uintptr_t)(lds_void *)dst);
+    if constexpr (BYTES == 4)
+        asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dword %1, %2, 0 offen lds" ::"s"(m0), "v"(voff), "s"(words)
+                     : "memory");
+    else
+        asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dwordx4 %1, %2, 0 offen lds" ::"s"(m0), "v"(voff), "s"(words)
+                     : "memory");
+}
+
 // TM x 256 output tiles of 8 waves (2 x 4), each TM / 2 x 64, over NS slots.
 // AMN / BMN: the operand's slots hold K-rows (see Mn in gemm_kernel.h).
 template <int TM_, int NS_, bool AMN_, bool BMN_>
@@ -205,54 +242,184 @@ __device__ __forceinline__ int first_tile()
     return (nwg & 7) == 0 ? (wg & 7) * (nwg >> 3) + (wg >> 3) : wg;
 }
 
-// ---------------------------------------------------------------- epilogue
+// --------------------------------------------------- the 256 x 256 x 64 core
 
-// The wave's accumulators as rows m0 .. mend-1, columns n0 .. ncols-1 of D
-// (ld elements a row, OUT a bf16 or float): NBO blocks of 32 columns, value
-// q of block j in block-row i from value(i, j, q).  vec: through LDS and in
-// 16-byte pieces (bf16; the caller's slot is free); otherwise by element.
-template <class S, int MBA, int NBO, class VALUE>
-__device__ __forceinline__ void store_bf16(uint8_t *buf, uint8_t *D, int64_t ld, int m0, int mend, int n0, int ncols,
-                                           int vec, Lane c, VALUE &&value)
+// 256 x 256 output tiles over stages of 64, 8 waves (2 x 4, two per SIMD),
+// each owning 128 x 64 as 4 x 2 blocks of 32 x 32.  A stage is four parts of
+// 16 KiB -- A's rows (or columns) 0 .. 127 and 128 .. 255, B's likewise -- in
+// one of two LDS slots, and is computed as four quadrants of 2 x 1 blocks:
+// (A lo, B lo), (A lo, B hi), (A hi, B hi), (A hi, B lo).  A wave reads a
+// quadrant's new operand part whole, all four k-steps, into registers: the
+// part of the slot is free again a quarter of a stage later, and its refill
+// for the stage after next starts then.  Loads so get six of the eight
+// half-phases of one and a half stages to land (measured need: rows that
+// nothing else has touched come from HBM), with two slots.
+//
+// The two waves of a SIMD take turns: while one reads its next part and
+// issues two wave-loads, the other runs eight MFMAs, with a workgroup barrier
+// between turns.  Waves 4 .. 7 start one turn late.
+//
+//   turn   reads           loads issued          MFMAs of the turn after
+//   0      A lo, B lo      A hi of stage s + 1   (lo, lo)
+//   1      B hi            A lo of stage s + 2   (lo, hi)
+//   2      A hi            B lo of stage s + 2   (hi, hi)
+//   3                      B hi of stage s + 2   (hi, lo)
+//
+// Every wave waits, at the end of turns 3, 0 and 1, for its loads of the
+// parts read in the turn after: 10 newer wave-loads are in flight by then
+// (kInFlight); its own reads are complete before the barrier that lets
+// others refill what it read.
+constexpr int kPart = 128 * kRowBytes, kSlot = 4 * kPart, kInFlight = 10;
+enum PartId : int { kALo = 0, kAHi = 1, kBLo = 2, kBHi = 3 };
+constexpr int kStage = 2 * kSlot;              // LDS offset of the waves' output buffers, 2 KiB each
+constexpr int kCoreLds = kStage + 8 * 2048;
+
+// K-major part: 128 rows of 128 bytes; wave-load L (0 .. 15) covers rows 8 L
+// .. 8 L + 7.  MN-major part: 64 K-rows of 128 columns, wave-load L covers
+// K-rows 4 L .. 4 L + 3.  Wave w issues wave-loads 2 w and 2 w + 1.
+using MnPart = Mn<kBF16, 128>;
+static_assert(MnPart::RPL == 4 && MnPart::RPL % MnPart::PERIOD == 0, "one lane offset for every wave-load");
+
+template <bool MN>
+__device__ __forceinline__ uint32_t part_base(const Lane &c, int block0)
+{
+    if constexpr (MN) {
+        return mn_base<kBF16, 128>(c.lane, 32 * block0, 0);
+    } else {
+        const int r = 32 * block0 + c.lr;
+        return (uint32_t)(r * kRowBytes + ((c.h ^ swz(r)) << 4));
+    }
+}
+
+// k-step kk of block i of a part (blocks of one wave lie 64 rows or columns apart)
+template <bool MN>
+__device__ __forceinline__ bf16x8 part_frag(const uint8_t *lds, uint32_t base, int kk, int i)
+{
+    if constexpr (MN)
+        return read_frag_mn<kBF16, 128>(lds, base, 0, kk, 2 * i);
+    else
+        return lds_read<bf16x8>(lds, (base ^ (uint32_t)(kk << 5)) + (uint32_t)(64 * kRowBytes * i));
+}
+
+template <int N>
+__device__ __forceinline__ void turn_end()
+{
+    DBS_FENCE();
+    asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)\n\ts_barrier" ::"i"(N) : "memory");
+    DBS_FENCE();
+}
+
+__device__ __forceinline__ void turn_end_reads()
+{
+    DBS_FENCE();
+    asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory");
+    DBS_FENCE();
+}
+
+__device__ __forceinline__ void turn_end_math()
+{
+    DBS_FENCE();
+    __builtin_amdgcn_s_setprio(0);
+    asm volatile("s_barrier" ::: "memory");
+    DBS_FENCE();
+}
+
+// One stage out of slot `slot`.  NLO, NHI: blocks per wave in the two halves
+// of A (fewer than 2 where a group ends).  load(part) issues the two
+// wave-loads of a part (the parts in the order above); advance() moves the
+// loads on to the next stage, ahead() looks up what that one needs.  extra: STORES stores of the last tile's results
+// went out between the loads awaited here and now, and may still be under way.
+template <bool AMN, bool BMN, int NLO, int NHI, class LOAD, class ADVANCE, class AHEAD, int STORES>
+__device__ __forceinline__ void core_stage(f32x16 (&acc)[4][2], const uint8_t *lds, uint32_t fa, uint32_t fb, int slot,
+                                           int extra, LOAD &&load, ADVANCE &&advance, AHEAD &&ahead,
+                                           std::integral_constant<int, STORES>)
+{
+    bf16x8 a[2][4], b0[4], b1[4];
+    const uint32_t so = (uint32_t)(slot * kSlot);
+    auto wait = [&] {
+        if (extra) turn_end<kInFlight + STORES>();
+        else turn_end<kInFlight>();
+    };
+    // turn 0
+#pragma unroll
+    for (int kk = 0; kk < 4; ++kk) {
+        b0[kk] = part_frag<BMN>(lds, fb + so + kBLo * kPart, kk, 0);
+#pragma unroll
+        for (int i = 0; i < NLO; ++i) a[i][kk] = part_frag<AMN>(lds, fa + so + kALo * kPart, kk, i);
+    }
+    load(kAHi);
+    wait();
+    ahead();
+    __builtin_amdgcn_s_setprio(1);
+#pragma unroll
+    for (int kk = 0; kk < 4; ++kk)
+#pragma unroll
+        for (int i = 0; i < NLO; ++i) mma1<kBF16, 0>(acc[i][0], a[i][kk], 0u, b0[kk], 0u);
+    turn_end_math();
+    // turn 1
+#pragma unroll
+    for (int kk = 0; kk < 4; ++kk) b1[kk] = part_frag<BMN>(lds, fb + so + kBHi * kPart, kk, 0);
+    advance();
+    load(kALo);
+    wait();
+    __builtin_amdgcn_s_setprio(1);
+#pragma unroll
+    for (int kk = 0; kk < 4; ++kk)
+#pragma unroll
+        for (int i = 0; i < NLO; ++i) mma1<kBF16, 0>(acc[i][1], a[i][kk], 0u, b1[kk], 0u);
+    turn_end_math();
+    // turn 2
+#pragma unroll
+    for (int kk = 0; kk < 4; ++kk)
+#pragma unroll
+        for (int i = 0; i < NHI; ++i) a[i][kk] = part_frag<AMN>(lds, fa + so + kAHi * kPart, kk, i);
+    load(kBLo);
+    turn_end_reads();
+    __builtin_amdgcn_s_setprio(1);
+#pragma unroll
+    for (int kk = 0; kk < 4; ++kk)
+#pragma unroll
+        for (int i = 0; i < NHI; ++i) mma1<kBF16, 0>(acc[2 + i][1], a[i][kk], 0u, b1[kk], 0u);
+    turn_end_math();
+    // turn 3
+    load(kBHi);
+    wait();
+    __builtin_amdgcn_s_setprio(1);
+#pragma unroll
+    for (int kk = 0; kk < 4; ++kk)
+#pragma unroll
+        for (int i = 0; i < NHI; ++i) mma1<kBF16, 0>(acc[2 + i][0], a[i][kk], 0u, b0[kk], 0u);
+    turn_end_math();
+}
+
+// One 32 x 32 block of results as bf16 rows r0 .. mend-1, columns n .. ncols-1
+// of D, through the wave's 2 KiB buffer (vec) or by element.
+template <class VALUE>
+__device__ __forceinline__ void store_block(uint8_t *buf, uint8_t *D, int64_t ld, int r0, int mend, int n0, int ncols,
+                                            int vec, Lane c, VALUE &&value)
 {
     // (addresses are made here, not before the tile's stages, whose registers they would take)
     asm volatile("" : "+v"(c.lane), "+v"(c.lr), "+v"(c.h));
-    constexpr int RB = NBO * 64, CPR = RB / 16, RPI = 64 / CPR;
+    const int left = __builtin_amdgcn_readfirstlane(max(0, min(32, mend - r0)));
+    const __amdgpu_buffer_rsrc_t rd = make_rsrc(D + (int64_t)r0 * ld * 2, (uint32_t)left * (uint32_t)ld * 2u);
+    if (vec) {
 #pragma unroll
-    for (int i = 0; i < MBA; ++i) {
-        const int r0 = m0 + (S::AMN ? c.wm * (S::TM / S::WM) + i * 32 : (2 * i + c.wm) * 32);
-        const int left = __builtin_amdgcn_readfirstlane(max(0, min(32, mend - r0)));
-        const __amdgpu_buffer_rsrc_t rd = make_rsrc(D + (int64_t)r0 * ld * 2, (uint32_t)left * (uint32_t)ld * 2u);
-        if (vec) {
+        for (int g = 0; g < 4; ++g) {
+            const uint32_t lo = pack_bf16(value(4 * g), value(4 * g + 1)), hi = pack_bf16(value(4 * g + 2), value(4 * g + 3));
+            *reinterpret_cast<u32x2 *>(buf + c.lr * 64 + 16 * (g ^ ((c.lr >> 1) & 3)) + 8 * c.h) = u32x2{lo, hi};
+        }
 #pragma unroll
-            for (int j = 0; j < NBO; ++j) {
+        for (int q = 0; q < 2; ++q) {
+            const int r = q * 16 + (c.lane >> 2), ch = c.lane & 3, n = n0 + ch * 8;
+            const i32x4 v = *reinterpret_cast<const i32x4 *>(buf + r * 64 + 16 * (ch ^ ((r >> 1) & 3)));
+            __builtin_amdgcn_raw_buffer_store_b128(v, rd, n < ncols ? (uint32_t)(r * (int)ld + n) * 2u : kOOB, 0, kStoreNT);
+        }
+    } else {
 #pragma unroll
-                for (int g = 0; g < 4; ++g) {
-                    const uint32_t lo = pack_bf16(value(i, j, 4 * g), value(i, j, 4 * g + 1));
-                    const uint32_t hi = pack_bf16(value(i, j, 4 * g + 2), value(i, j, 4 * g + 3));
-                    const int ch = (4 * j + g) ^ (c.lr & (CPR - 1));
-                    *reinterpret_cast<u32x2 *>(buf + c.lr * RB + 16 * ch + 8 * c.h) = u32x2{lo, hi};
-                }
-            }
-#pragma unroll
-            for (int q = 0; q < 32 / RPI; ++q) {
-                const int r = q * RPI + c.lane / CPR, ch = c.lane % CPR;
-                const i32x4 v = *reinterpret_cast<const i32x4 *>(buf + r * RB + 16 * (ch ^ (r & (CPR - 1))));
-                const int n = n0 + ch * 8;
-                __builtin_amdgcn_raw_buffer_store_b128(v, rd, n < ncols ? (uint32_t)(r * (int)ld + n) * 2u : kOOB, 0,
-                                                       kStoreNT);
-            }
-        } else {
-#pragma unroll
-            for (int j = 0; j < NBO; ++j) {
-#pragma unroll
-                for (int q = 0; q < 16; ++q) {
-                    const int n = n0 + j * 32 + (q / 4) * 8 + c.h * 4 + q % 4;
-                    __builtin_amdgcn_raw_buffer_store_b16((uint16_t)pack_bf16(value(i, j, q), 0.0f), rd,
-                                                          n < ncols ? (uint32_t)(c.lr * (int)ld + n) * 2u : kOOB, 0,
-                                                          kStoreNT);
-                }
-            }
+        for (int q = 0; q < 16; ++q) {
+            const int n = n0 + (q / 4) * 8 + c.h * 4 + q % 4;
+            __builtin_amdgcn_raw_buffer_store_b16((uint16_t)pack_bf16(value(q), 0.0f), rd,
+                                                  n < ncols ? (uint32_t)(c.lr * (int)ld + n) * 2u : kOOB, 0, kStoreNT);
         }
     }
 }
@@ -264,22 +431,260 @@ __device__ __forceinline__ void store_bf16(uint8_t *buf, uint8_t *D, int64_t ld,
 // descending cost -- all groups' whole tile rows (and rests that need every
 // block), then the rests by blocks -- in a snake over the workgroups, so
 // that those with a tile less of one kind come first for the next.
-template <class S>
+template <int TM>
 struct Table {
+    static constexpr int kRests = TM / 64 - 1;
     int32_t first[kMoeMaxExperts + 1], whole[kMoeMaxExperts + 1];   // tile rows before a group
-    uint16_t rest[S::MB > 1 ? S::MB - 1 : 1][kMoeMaxExperts + 1];   // rests of b + 1 blocks before a group
+    uint16_t rest[kRests > 0 ? kRests : 1][kMoeMaxExperts + 1];     // rests of b + 1 blocks before a group
 };
 
-// blocks per wave of a group's rest; S::MB counts as a whole tile row
-template <class S>
-__device__ __forceinline__ int rest_blocks(int rows) { return (rows % S::TM + 63) / 64; }
+struct RowTile {
+    int m0, mend, n0, g, blocks;      // blocks 0: nothing
+};
 
-// GATE: see the head of the file.
+template <int TM>
+__device__ __forceinline__ void fill_table(Table<TM> &tab, const MoeGemm &p, const Lane &c)
+{
+    constexpr int MB = TM / 64;
+    const auto blocks = [](int rows) { return (rows % TM + 63) / 64; };   // of a group's rest
+    if (c.w == 0)
+        group_table<true>(tab.first, tab.whole, p.offsets, p.E, p.M, c,
+                          [&](int rows) { return rows / TM + (blocks(rows) == MB); });
+    else if (c.w < MB)
+        group_table<false>(tab.first, tab.rest[c.w - 1], p.offsets, p.E, p.M, c,
+                           [&](int rows) { return (int)(blocks(rows) == c.w); });
+}
+
+template <int TM>
+__device__ __forceinline__ int count_tiles(const Table<TM> &tab, int E, int tiles_n)
+{
+    int n = __builtin_amdgcn_readfirstlane(tab.whole[E]);
+#pragma unroll
+    for (int b = 0; b < Table<TM>::kRests; ++b) n += __builtin_amdgcn_readfirstlane((int)tab.rest[b][E]);
+    return n * tiles_n;
+}
+
+// Output tile id of the order above, tno columns wide.
+template <int TM>
+__device__ __forceinline__ RowTile find_tile(const Table<TM> &tab, int E, int ntiles, int tiles_n, int tno, int id,
+                                             const Lane &c)
+{
+    constexpr int MB = TM / 64;
+    RowTile r{};
+    if (id >= ntiles) return r;
+    const int whole = __builtin_amdgcn_readfirstlane(tab.whole[E]) * tiles_n;
+    if (id < whole) {
+        r.g = group_of(tab.whole, E, id / tiles_n, c);
+        const int before = __builtin_amdgcn_readfirstlane(tab.whole[r.g]);
+        const int n = __builtin_amdgcn_readfirstlane(tab.whole[r.g + 1]) - before;
+        const int local = id - before * tiles_n;   // tile rows fastest: they share W's rows
+        r.m0 = local % n * TM;
+        r.n0 = local / n * tno;
+        r.blocks = MB;
+    } else {
+        id -= whole;
+#pragma unroll
+        for (int b = MB - 1; b >= 1; --b) {
+            const int n = __builtin_amdgcn_readfirstlane((int)tab.rest[b - 1][E]) * tiles_n;
+            if (r.blocks == 0 && id < n) {
+                r.g = group_of(tab.rest[b - 1], E, id / tiles_n, c);
+                r.n0 = id % tiles_n * tno;
+                r.blocks = b;
+            }
+            id -= r.blocks == 0 ? n : 0;
+        }
+    }
+    const int lo = __builtin_amdgcn_readfirstlane(tab.first[r.g]);
+    r.mend = __builtin_amdgcn_readfirstlane(tab.first[r.g + 1]);
+    if (r.blocks < MB) r.m0 = (r.mend - lo) / TM * TM;
+    r.m0 += lo;
+    return r;
+}
+
+// rows total .. M-1 of D, behind the last group, are zero
+__device__ __forceinline__ void zero_rest(const MoeGemm &p, int64_t total)
+{
+    const int64_t bytes = (p.M - total) * p.ncols * 2;
+    uint8_t *z = p.D + total * p.ncols * 2;
+    const int64_t me = (int64_t)blockIdx.x * blockDim.x + threadIdx.x, all = (int64_t)gridDim.x * blockDim.x;
+    if (p.vec)
+        for (int64_t o = me * 16; o < bytes; o += all * 16) *reinterpret_cast<i32x4 *>(z + o) = i32x4{};
+    else
+        for (int64_t o = me * 2; o < bytes; o += all * 2) *reinterpret_cast<uint16_t *>(z + o) = 0;
+}
+
+__device__ __forceinline__ float gated(float g, float u)
+{
+    return g * __builtin_amdgcn_rcpf(1.0f + __expf(-g)) * u;
+}
+
+// 256-row tiles.  BMN: W MN-major; GATE: see the head of the file.
+template <bool BMN, bool GATE>
+__global__ __launch_bounds__(512, 1) void moe_tiles_256(MoeGemm p)
+{
+    __shared__ __attribute__((aligned(1024))) uint8_t lds[kCoreLds];
+    __shared__ Table<256> tab;
+    __shared__ uint32_t rowbuf[256];
+    static_assert(!(GATE && BMN), "the gate takes K-major matrices");
+    constexpr int TNO = GATE ? 128 : 256;              // output columns of a tile
+    constexpr int kStores = GATE ? 8 : 16;             // store instructions of a whole tile (vec)
+
+    const Lane c = lane_of();
+    const int lda = p.K * 2, ldb = BMN ? p.N * 2 : lda;
+    const int tiles_n = (p.ncols + TNO - 1) / TNO;
+    fill_table(tab, p, c);
+    __syncthreads();
+    zero_rest(p, tab.first[p.E]);
+    const int ntiles = count_tiles(tab, p.E, tiles_n);
+    const int nwg = gridDim.x, self = first_tile();
+    if (self >= ntiles) return;
+    // at least four stages (the surplus reads zeros): the next tile's rows
+    // land within a tile (see rowbuf)
+    const int nk = max((p.K + 63) / 64, 4);
+    auto find = [&](int round) {
+        return find_tile(tab, p.E, ntiles, tiles_n, TNO, round * nwg + (round & 1 ? nwg - 1 - self : self), c);
+    };
+
+    // What the loads read: stage lk of the tile behind ra and rb.
+    i32x4 ra, rb;
+    uint32_t aoff[4];                     // the lane's row offsets in ra: A lo's two wave-loads, A hi's
+    int f0 = 0, lk = 0;
+    const int lrow = c.lane >> 3;
+    uint32_t x4 = (uint32_t)(((c.lane & 7) ^ lrow) << 4);
+    uint32_t lb = BMN ? mn_dma_lane<kBF16, 128>(c.lane, 0, ldb) : (uint32_t)(lrow * ldb);
+    // Row indices of the tile `r` on their way into rowbuf (lanes past the
+    // group's end load zeros, which aim does not use)
+    auto fetch = [&](const RowTile &r) {
+        const int n = max(r.mend - r.m0, 0);
+        const i32x4 rr = words_of(p.rows ? p.rows + r.m0 : nullptr, p.rows ? (uint32_t)min(n, 256) * 4u : 0u);
+        dma<4>(rr, reinterpret_cast<uint8_t *>(rowbuf) + (c.w & 3) * 256, (uint32_t)((c.w & 3) * 256 + c.lane * 4));
+    };
+    auto aim = [&](const RowTile &r) {
+        lk = 0;
+        if (r.blocks == 0) {
+            ra = rb = words_of(nullptr, 0);
+            return;
+        }
+        const int64_t wbytes = (int64_t)p.N * p.K * 2;
+        const uint8_t *wg = p.W + r.g * wbytes;
+        f0 = r.n0;
+        if constexpr (BMN)
+            rb = words_of(wg + r.n0 * 2, (uint32_t)(wbytes - r.n0 * 2));
+        else if constexpr (GATE)
+            rb = words_of(wg, (uint32_t)wbytes);
+        else
+            rb = words_of(wg + (int64_t)r.n0 * lda, (uint32_t)(min(p.N - r.n0, 256) * lda));
+        const int left = min(r.mend - r.m0, 256);
+        const uint32_t have = p.rows ? (uint32_t)p.T : (uint32_t)left;
+        ra = words_of(p.rows ? p.X : p.X + (int64_t)r.m0 * lda, have * (uint32_t)lda);
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+            const int m = (q >> 1) * 128 + c.w * 16 + (q & 1) * 8 + lrow;
+            const uint32_t row = p.rows ? rowbuf[m] : (uint32_t)m;
+            aoff[q] = m < left && row < have ? row * (uint32_t)lda : kRowOOB;
+        }
+    };
+    auto load = [&](int part, int slot) {
+        const int k0 = lk * kRowBytes;
+#pragma unroll
+        for (int q = 0; q < 2; ++q) {
+            const int L = c.w * 2 + q;
+            uint8_t *dst = lds + slot * kSlot + part * kPart + L * 1024;
+            const int kc = (int)(x4 ^ (uint32_t)((L & 7) << 4)) + k0;
+            if (part == kALo || part == kAHi) {
+                dma<16>(ra, dst, kc < lda ? aoff[(part == kAHi ? 2 : 0) + q] + kc : kRowOOB);
+            } else {
+                const int j = part == kBHi;
+                if constexpr (BMN) {
+                    const uint32_t row = (uint32_t)(lk * 64 + L * 4);          // four K-rows a wave-load
+                    dma<16>(rb, dst, row < (uint32_t)p.K ? lb + row * (uint32_t)ldb + j * 256 : kOOB);
+                } else if constexpr (GATE) {
+                    const int f = f0 + L * 8;                                  // of matrix j
+                    dma<16>(rb, dst, kc < lda && f + lrow < p.ncols
+                                             ? lb + (uint32_t)((j * p.ncols + f) * lda) + kc : kOOB);
+                } else {
+                    // wave column L / 4's rows: 32 of its 64
+                    const int n = (L >> 2) * 64 + j * 32 + (L & 3) * 8;
+                    dma<16>(rb, dst, kc < lda ? lb + (uint32_t)(n * lda) + kc : kOOB);
+                }
+            }
+        }
+    };
+
+    RowTile cur = find(0), next = cur;
+    fetch(cur);
+    turn_end<0>();
+    aim(cur);
+    load(kALo, 0);
+    load(kBLo, 0);
+    load(kBHi, 0);
+    load(kAHi, 0);
+    ++lk;
+    load(kALo, 1);
+    load(kBLo, 1);
+    load(kBHi, 1);
+    uint32_t fa = part_base<false>(c, c.wm), fb = part_base<BMN>(c, c.wn);
+    uint8_t *buf = lds + kStage + c.w * 2048;
+    turn_end<kInFlight>();
+
+    int slot = 0, round = 0, stored = 0;
+    auto run = [&](auto nlo, auto nhi) {
+        constexpr int NLO = decltype(nlo)::value, NHI = decltype(nhi)::value;
+        f32x16 acc[4][2];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) acc[i][0] = acc[i][1] = f32x16{};
+        if (c.w >= 4) asm volatile("s_barrier" ::: "memory");      // one turn behind
+        for (int s = 0; s < nk; ++s) {
+            asm volatile("" : "+v"(x4), "+v"(lb), "+v"(fa), "+v"(fb));
+            core_stage<false, BMN, NLO, NHI>(
+                acc, lds, fa, fb, slot, s == 0 ? stored : 0,
+                [&](int part) { load(part, part == kAHi ? slot ^ 1 : slot); },
+                [&] {
+                    if (s == 0) fetch(next);
+                    if (++lk == nk) aim(next);
+                },
+                [] {},
+                std::integral_constant<int, kStores>{});
+            slot ^= 1;
+        }
+        if (c.w < 4) asm volatile("s_barrier" ::: "memory");
+        DBS_FENCE();
+#pragma unroll
+        for (int i = 0; i < NLO + NHI; ++i) {
+            const int r0 = cur.m0 + (2 * i + c.wm) * 32;
+            if constexpr (GATE) {
+                store_block(buf, p.D, p.ncols, r0, cur.mend, cur.n0 + c.wn * 32, p.ncols, p.vec, c,
+                            [&](int q) { return gated(acc[i][0][q], acc[i][1][q]); });
+            } else {
+#pragma unroll
+                for (int j = 0; j < 2; ++j)
+                    store_block(buf, p.D, p.ncols, r0, cur.mend, cur.n0 + (BMN ? j * 128 + c.wn * 32 : c.wn * 64 + j * 32),
+                                p.ncols, p.vec, c, [&](int q) { return acc[i][j][q]; });
+            }
+        }
+        stored = p.vec && NLO + NHI == 4;
+    };
+    using I0 = std::integral_constant<int, 0>;
+    using I1 = std::integral_constant<int, 1>;
+    using I2 = std::integral_constant<int, 2>;
+    for (;;) {
+        next = find(++round);
+        if (cur.blocks == 4) run(I2{}, I2{});
+        else if (cur.blocks == 3) run(I2{}, I1{});
+        else if (cur.blocks == 2) run(I2{}, I0{});
+        else run(I1{}, I0{});
+        if (next.blocks == 0) break;
+        cur = next;
+    }
+    asm volatile("s_waitcnt vmcnt(0)" ::: "memory");   // nothing is left to land in LDS
+}
+
+// 64-row tiles, for groups of fewer rows.  GATE: see the head of the file.
 template <class S, bool GATE>
-__global__ __launch_bounds__(512, 1) void moe_tiles(MoeGemm p)
+__global__ __launch_bounds__(512, 1) void moe_tiles_64(MoeGemm p)
 {
     __shared__ __attribute__((aligned(1024))) uint8_t lds[S::kRing];
-    __shared__ Table<S> tab;
+    __shared__ Table<S::TM> tab;
     static_assert(!(GATE && S::BMN), "the gate takes K-major matrices");
     constexpr int MB = S::MB, NB = S::NB;
     constexpr int TNO = GATE ? S::TN / 2 : S::TN;      // output columns of a tile
@@ -287,74 +692,19 @@ __global__ __launch_bounds__(512, 1) void moe_tiles(MoeGemm p)
     const Lane c = lane_of();
     const int lda = p.K * 2;
     const int tiles_n = (p.ncols + TNO - 1) / TNO;
-    if (c.w == 0)
-        group_table<true>(tab.first, tab.whole, p.offsets, p.E, p.M, c,
-                          [&](int rows) { return rows / S::TM + (rest_blocks<S>(rows) == MB); });
-    else if (c.w < MB)
-        group_table<false>(tab.first, tab.rest[c.w - 1], p.offsets, p.E, p.M, c,
-                           [&](int rows) { return (int)(rest_blocks<S>(rows) == c.w); });
+    fill_table(tab, p, c);
     __syncthreads();
-
-    // rows behind the last group are zero
-    {
-        const int64_t total = tab.first[p.E];
-        const int64_t bytes = (p.M - total) * p.ncols * 2;
-        uint8_t *z = p.D + total * p.ncols * 2;
-        const int64_t me = (int64_t)blockIdx.x * S::kThreads + threadIdx.x, all = (int64_t)gridDim.x * S::kThreads;
-        if (p.vec)
-            for (int64_t o = me * 16; o < bytes; o += all * 16) *reinterpret_cast<i32x4 *>(z + o) = i32x4{};
-        else
-            for (int64_t o = me * 2; o < bytes; o += all * 2) *reinterpret_cast<uint16_t *>(z + o) = 0;
-    }
-
-    int ntiles = __builtin_amdgcn_readfirstlane(tab.whole[p.E]);
-#pragma unroll
-    for (int b = 1; b < MB; ++b) ntiles += __builtin_amdgcn_readfirstlane((int)tab.rest[b - 1][p.E]);
-    ntiles *= tiles_n;
-    const int nwg = gridDim.x, self = first_tile();
-    if (self >= ntiles) return;
+    zero_rest(p, tab.first[p.E]);
+    const int ntiles = count_tiles(tab, p.E, tiles_n);
+    const int nwg = gridDim.x;
+    int tile = first_tile();
+    if (tile >= ntiles) return;
     const int nk = max((p.K + S::KS - 1) / S::KS, S::NS - 1);
-
-    struct Ref {
-        int m0, mend, n0, g, blocks;
-    };
-    // output tile id of the order above; past the last: no rows
-    auto ref_of = [&](int id) {
-        Ref r{};
-        if (id >= ntiles) return r;
-        const int whole = __builtin_amdgcn_readfirstlane(tab.whole[p.E]) * tiles_n;
-        if (id < whole) {
-            const int row = id / tiles_n;              // groups of one tile row need no more than this
-            r.g = group_of(tab.whole, p.E, row, c);
-            const int before = __builtin_amdgcn_readfirstlane(tab.whole[r.g]);
-            const int n = __builtin_amdgcn_readfirstlane(tab.whole[r.g + 1]) - before;
-            const int local = id - before * tiles_n;   // tile rows fastest: they share W's rows
-            r.m0 = local % n * S::TM;
-            r.n0 = local / n * TNO;
-            r.blocks = MB;
-        } else {
-            id -= whole;
-#pragma unroll
-            for (int b = MB - 1; b >= 1; --b) {
-                const int n = __builtin_amdgcn_readfirstlane((int)tab.rest[b - 1][p.E]) * tiles_n;
-                if (r.blocks == 0 && id < n) {
-                    r.g = group_of(tab.rest[b - 1], p.E, id / tiles_n, c);
-                    r.n0 = id % tiles_n * TNO;
-                    r.blocks = b;
-                }
-                id -= r.blocks == 0 ? n : 0;
-            }
-        }
-        const int lo = __builtin_amdgcn_readfirstlane(tab.first[r.g]);
-        r.mend = __builtin_amdgcn_readfirstlane(tab.first[r.g + 1]);
-        if (r.blocks < MB) r.m0 = (r.mend - lo) / S::TM * S::TM;
-        r.m0 += lo;
-        return r;
-    };
+    auto find = [&](int id) { return find_tile(tab, p.E, ntiles, tiles_n, TNO, id, c); };
 
     // where a tile's stages come from
     struct Source {
-        __amdgpu_buffer_rsrc_t ra, rb;
+        i32x4 ra, rb;
         uint32_t a[S::QA];       // the lane's byte offset in ra per wave-load, its chunk included
         int f0;                  // the tile's first output column
     } src;
@@ -369,29 +719,29 @@ __global__ __launch_bounds__(512, 1) void moe_tiles(MoeGemm p)
         mb[0] = mn_dma_lane<kBF16, S::TN>(c.lane, 0, ldb);
         mb[1] = mn_dma_lane<kBF16, S::TN>(c.lane, 1, ldb);
     }
-    auto fetch = [&](const Ref &r) {
+    auto fetch = [&](const RowTile &r) {
 #pragma unroll
         for (int q = 0; q < S::QA; ++q) {
             const int m = (c.w * S::QA + q) * 8 + (c.lane >> 3);
             row[q] = !p.rows ? (uint32_t)m : r.m0 + m < r.mend ? (uint32_t)p.rows[r.m0 + m] : ~0u;
         }
     };
-    auto aim = [&](const Ref &r) {
+    auto aim = [&](const RowTile &r) {
         if (r.blocks == 0) {
-            src.ra = src.rb = make_rsrc(nullptr, 0);
+            src.ra = src.rb = words_of(nullptr, 0);
             return;
         }
         const int64_t wbytes = (int64_t)p.N * p.K * 2;
         const uint8_t *wg = p.W + r.g * wbytes;
         src.f0 = r.n0;
         if constexpr (S::BMN)
-            src.rb = make_rsrc(wg + r.n0 * 2, (uint32_t)(wbytes - r.n0 * 2));
+            src.rb = words_of(wg + r.n0 * 2, (uint32_t)(wbytes - r.n0 * 2));
         else if constexpr (GATE)
-            src.rb = make_rsrc(wg, (uint32_t)wbytes);
+            src.rb = words_of(wg, (uint32_t)wbytes);
         else
-            src.rb = make_rsrc(wg + (int64_t)r.n0 * lda, (uint32_t)(min(p.N - r.n0, S::TN) * lda));
+            src.rb = words_of(wg + (int64_t)r.n0 * lda, (uint32_t)(min(p.N - r.n0, S::TN) * lda));
         const uint32_t have = p.rows ? (uint32_t)p.T : (uint32_t)min(r.mend - r.m0, S::TM);
-        src.ra = make_rsrc(p.rows ? p.X : p.X + (int64_t)r.m0 * lda, have * (uint32_t)lda);
+        src.ra = words_of(p.rows ? p.X : p.X + (int64_t)r.m0 * lda, have * (uint32_t)lda);
 #pragma unroll
         for (int q = 0; q < S::QA; ++q) {
             const int L = c.w * S::QA + q;
@@ -403,13 +753,13 @@ __global__ __launch_bounds__(512, 1) void moe_tiles(MoeGemm p)
         if (q < S::QA) {
             const int L = c.w * S::QA + q;
             const int kc = (int)(x4 ^ (uint32_t)((L & 7) << 4));
-            lds_dma<16>(src.ra, lds + S::kLdsA + slot * S::kSlotA + L * 1024, kc < lda - k0 ? src.a[q] + k0 : kRowOOB);
+            dma<16>(src.ra, lds + S::kLdsA + slot * S::kSlotA + L * 1024, kc < lda - k0 ? src.a[q] + k0 : kRowOOB);
         }
         const int L = c.w * S::QB + q;
         uint8_t *dst = lds + S::kLdsB + slot * S::kSlotB + L * 1024;
         if constexpr (S::BMN) {
             const uint32_t row = (uint32_t)(ks * S::KS + L * 2);           // two K-rows a wave-load
-            lds_dma<16>(src.rb, dst, row < (uint32_t)p.K ? mb[q & 1] + row * (uint32_t)ldb : kOOB);
+            dma<16>(src.rb, dst, row < (uint32_t)p.K ? mb[q & 1] + row * (uint32_t)ldb : kOOB);
         } else {
             const int kc = (int)(x4 ^ (uint32_t)((L & 7) << 4));
             uint32_t off = r8ldb + (uint32_t)(kc + k0);
@@ -422,11 +772,11 @@ __global__ __launch_bounds__(512, 1) void moe_tiles(MoeGemm p)
             } else {
                 off += (uint32_t)(L * 8 * lda);
             }
-            lds_dma<16>(src.rb, dst, in ? off : kOOB);
+            dma<16>(src.rb, dst, in ? off : kOOB);
         }
     };
 
-    Ref cur = ref_of(self), next{};
+    RowTile cur = find(tile), next{};
     fetch(cur);
     aim(cur);
 #pragma unroll
@@ -435,19 +785,20 @@ __global__ __launch_bounds__(512, 1) void moe_tiles(MoeGemm p)
         for (int q = 0; q < S::QB; ++q) load(f, f, q);
     }
     uint32_t fa = frag_a<S>(c), fb = frag_b<S>(c);
-    __syncthreads();
+    stage_barrier<(S::NS - 2) * (S::QA + S::QB)>();
 
     int rs = 0;               // slot the next stage reads
-    int round = 0;
-    // one output tile of MBA blocks per wave
-    auto run = [&](auto blocks) {
-        constexpr int MBA = decltype(blocks)::value;
-        f32x16 acc[MBA][NB];
+    for (;;) {
+        // the next tile's rows are looked up while this one is computed
+        tile += nwg;
+        next = find(tile);
+        fetch(next);
+        f32x16 acc[MB][NB];
 #pragma unroll
-        for (int i = 0; i < MBA; ++i)
+        for (int i = 0; i < MB; ++i)
 #pragma unroll
             for (int j = 0; j < NB; ++j) acc[i][j] = f32x16{};
-        Frag2<S, MBA> F0, F1{};
+        Frag2<S> F0, F1{};
         int xs = 0;           // slot the last stage read
         for (int s = 0; s < nk; ++s) {
             int ks = s + S::NS - 1;
@@ -457,255 +808,234 @@ __global__ __launch_bounds__(512, 1) void moe_tiles(MoeGemm p)
             }
             const int ls = rs == 0 ? S::NS - 1 : rs - 1;
             asm volatile("" : "+v"(x4), "+v"(r8ldb), "+v"(fa), "+v"(fb));
-            stage2<S, MBA>(acc, F0, F1, lds, fa + (uint32_t)(rs * S::kSlotA), fb + (uint32_t)(rs * S::kSlotB),
-                           [&](int q) { load(ls, ks, q); });
+            stage2<S, MB>(acc, F0, F1, lds, fa + (uint32_t)(rs * S::kSlotA), fb + (uint32_t)(rs * S::kSlotB),
+                          [&](int q) { load(ls, ks, q); });
             xs = rs;
             rs = rs + 1 == S::NS ? 0 : rs + 1;
         }
-        phase2<S, MBA, 0, false>(acc, F1, F0, lds, fa, fb, [](int) {});
+        phase2<S, MB, 0, false>(acc, F1, F0, lds, fa, fb, [](int) {});
 
         // the slot the last stage read is free until the next tile's first
-        // stage refills it: its B part holds 8 waves' 32-row buffers
-        constexpr int NBO = GATE ? NB / 2 : NB;
-        uint8_t *buf = lds + S::kLdsB + xs * S::kSlotB + c.w * (32 * NBO * 64);
-        store_bf16<S, MBA, NBO>(buf, p.D, p.ncols, cur.m0, cur.mend, cur.n0 + c.wn * (NBO * 32), p.ncols, p.vec, c,
-                                [&](int i, int j, int q) {
-                                    if constexpr (GATE) {
-                                        const float g = acc[i][0][q];
-                                        return g * __builtin_amdgcn_rcpf(1.0f + __expf(-g)) * acc[i][1][q];
-                                    } else {
-                                        return acc[i][j][q];
-                                    }
-                                });
+        // stage refills it: its B part holds the waves' buffers
+        uint8_t *buf = lds + S::kLdsB + xs * S::kSlotB + c.w * 2048;
+#pragma unroll
+        for (int i = 0; i < MB; ++i) {
+            const int r0 = cur.m0 + (2 * i + c.wm) * 32;
+            if constexpr (GATE) {
+                store_block(buf, p.D, p.ncols, r0, cur.mend, cur.n0 + c.wn * 32, p.ncols, p.vec, c,
+                            [&](int q) { return gated(acc[i][0][q], acc[i][1][q]); });
+            } else {
+#pragma unroll
+                for (int j = 0; j < NB; ++j)
+                    store_block(buf, p.D, p.ncols, r0, cur.mend, cur.n0 + c.wn * 64 + j * 32, p.ncols, p.vec, c,
+                                [&](int q) { return acc[i][j][q]; });
+            }
+        }
         asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory");
-    };
-    for (;;) {
-        // the next tile's rows are looked up while this one is computed
-        ++round;
-        next = ref_of(round * nwg + (round & 1 ? nwg - 1 - self : self));
-        fetch(next);
-        if (MB == 1 || cur.blocks == MB) run(std::integral_constant<int, MB>{});
-        if constexpr (MB > 1) {
-            if (cur.blocks == 1) run(std::integral_constant<int, 1>{});
-        }
-        if constexpr (MB > 2) {
-            if (cur.blocks == 2) run(std::integral_constant<int, 2>{});
-            if (cur.blocks == 3) run(std::integral_constant<int, 3>{});
-        }
         if (next.blocks == 0) break;
         cur = next;
     }
+    asm volatile("s_waitcnt vmcnt(0)" ::: "memory");   // nothing is left to land in LDS
 }
 
 // ---------------------------------------------------------------------- dw
-
-using DwTile = Tile<256, 2, true, true>;
 
 // GATHER: rows of X through p.rows.  F32: dW holds fp32.
 template <bool GATHER, bool F32>
 __global__ __launch_bounds__(512, 1) void moe_dw(MoeGemmDw p)
 {
-    using S = DwTile;
-    __shared__ __attribute__((aligned(1024))) uint8_t lds[S::kRing];
+    __shared__ __attribute__((aligned(1024))) uint8_t lds[kCoreLds];
     __shared__ int32_t first[kMoeMaxExperts + 1], tile_at[kMoeMaxExperts + 1];
-    constexpr int MB = S::MB, NB = S::NB;
+    constexpr int kStores = F32 ? 32 : 16;             // store instructions of a tile
 
     const Lane c = lane_of();
     const int lda = p.N * 2, ldb = p.K * 2;            // bytes of a row of dY, of X
-    const int tiles_n = (p.N + S::TM - 1) / S::TM, tiles_k = (p.K + S::TN - 1) / S::TN, per = tiles_n * tiles_k;
+    const int tiles_n = (p.N + 255) / 256, tiles_k = (p.K + 255) / 256, per = tiles_n * tiles_k;
     if (c.w == 0)
         group_table<true>(first, tile_at, p.offsets, p.E, p.M, c,
                           [&](int rows) { return p.accumulate && rows == 0 ? 0 : per; });
     __syncthreads();
-    const int ntiles = tile_at[p.E], nwg = gridDim.x;
+    const int ntiles = __builtin_amdgcn_readfirstlane(tile_at[p.E]), nwg = gridDim.x;
     int tile = first_tile();
     if (tile >= ntiles) return;
 
-    uint32_t ma[2] = {mn_dma_lane<kBF16, S::TM>(c.lane, 0, lda), mn_dma_lane<kBF16, S::TM>(c.lane, 1, lda)};
-    // the lane's bytes within a K-row of X (gathered: the row's own offset is added)
-    uint32_t mb[2] = {mn_dma_lane<kBF16, S::TN>(c.lane, 0, GATHER ? 0 : ldb),
-                      mn_dma_lane<kBF16, S::TN>(c.lane, 1, GATHER ? 0 : ldb)};
-
     struct Ref {
-        int lo, hi, n0, k0, g;
+        int lo, hi, n0, k0, g, nk;
     };
-    auto ref_of = [&](int id) {
-        Ref r;
+    // past the last tile: no rows
+    auto find = [&](int id) {
+        Ref r{};
+        r.nk = 2;
+        if (id >= ntiles) return r;
         r.g = group_of(tile_at, p.E, id, c);
         r.lo = __builtin_amdgcn_readfirstlane(first[r.g]);
         r.hi = __builtin_amdgcn_readfirstlane(first[r.g + 1]);
         const int local = id - __builtin_amdgcn_readfirstlane(tile_at[r.g]);
-        r.n0 = local % tiles_n * S::TM;
-        r.k0 = local / tiles_n * S::TN;
+        r.n0 = local % tiles_n * 256;
+        r.k0 = local / tiles_n * 256;
+        // the loads run up to two stages ahead: two at least
+        r.nk = max(2, (r.hi - r.lo + 63) / 64);
         return r;
     };
-    auto stages = [](const Ref &r) { return max(1, (r.hi - r.lo + S::KS - 1) / S::KS); };
-    Ref src{};                                         // the tile whose stages are loaded (hi = lo: nothing)
-    const __amdgpu_buffer_rsrc_t rrows = make_rsrc(p.rows, GATHER ? (uint32_t)p.M * 4u : 0u);
-    uint32_t idx[S::QB] = {};                          // X's rows of the lane's wave-loads in the next stage to load
-    auto fetch_rows = [&](int ks) {
+    Ref cur = find(tile), next = cur;
+
+    // What the loads read: stage lk of tile src.
+    Ref src = cur;
+    int lk = 0;
+    uint32_t la = mn_dma_lane<kBF16, 128>(c.lane, 0, lda);
+    uint32_t lb = mn_dma_lane<kBF16, 128>(c.lane, 0, GATHER ? 0 : ldb);
+    // Gathered: X's rows behind the wave's eight K-rows of the stage, through
+    // the scalar cache (its loads do not queue with the tiles' loads), and
+    // the lane's byte offsets of its two wave-loads.
+    typedef const __attribute__((address_space(4))) int32_t *const_i32;
+    const const_i32 rows = (const_i32)(uintptr_t)p.rows;
+    int idx[8];
+    uint32_t boff[2] = {};
+    auto fetch = [&](const Ref &r, int k) {
         if constexpr (GATHER) {
+            const int m = r.lo + k * 64 + c.w * 8;
 #pragma unroll
-            for (int q = 0; q < S::QB; ++q) {
-                const int m = src.lo + ks * S::KS + (c.w * S::QB + q) * 2 + c.h;
-                idx[q] = m < src.hi ? __builtin_amdgcn_raw_buffer_load_b32(rrows, (uint32_t)m * 4u, 0, 0) : ~0u;
+            for (int i = 0; i < 8; ++i) {
+                const int v = rows[min(m + i, p.M - 1)];
+                idx[i] = m + i < r.hi ? v : -1;
             }
         }
     };
-    auto load = [&](int slot, int ks, int q) {
-        const int m0 = src.lo + ks * S::KS, left = min(S::KS, src.hi - m0);       // rows of the stage
-        const int L = c.w * S::QA + q;
-        const uint32_t row = (uint32_t)(L * 2);
-        const __amdgpu_buffer_rsrc_t ra =
-            make_rsrc(p.dY + (int64_t)m0 * lda + src.n0 * 2, left > 0 ? (uint32_t)left * (uint32_t)lda - src.n0 * 2 : 0u);
-        lds_dma<16>(ra, lds + S::kLdsA + slot * S::kSlotA + L * 1024, ma[q & 1] + row * (uint32_t)lda);
-        uint8_t *dst = lds + S::kLdsB + slot * S::kSlotB + L * 1024;
-        if constexpr (GATHER) {
-            const __amdgpu_buffer_rsrc_t rb = make_rsrc(p.X + src.k0 * 2, (uint32_t)(p.T * ldb - src.k0 * 2));
-            lds_dma<16>(rb, dst, idx[q] < (uint32_t)p.T ? idx[q] * (uint32_t)ldb + mb[q & 1] : kRowOOB);
-        } else {
-            const __amdgpu_buffer_rsrc_t rb = make_rsrc(p.X + (int64_t)m0 * ldb + src.k0 * 2,
-                                                        left > 0 ? (uint32_t)left * (uint32_t)ldb - src.k0 * 2 : 0u);
-            lds_dma<16>(rb, dst, mb[q & 1] + row * (uint32_t)ldb);
+    auto load = [&](int part, int slot) {
+        const int m0 = src.lo + lk * 64, left = min(64, src.hi - m0);       // rows of the stage
+        const bool a = part == kALo || part == kAHi;
+        const int col = (part == kAHi || part == kBHi ? 256 : 0);
+        const int ld = a ? lda : ldb, c0 = (a ? src.n0 : src.k0) * 2;
+        const uint8_t *base = (a ? p.dY : p.X) + c0 + (GATHER && !a ? 0 : (int64_t)m0 * ld);
+        const uint32_t bytes = GATHER && !a ? (uint32_t)p.T * (uint32_t)ld - c0
+                                            : left > 0 ? (uint32_t)left * (uint32_t)ld - c0 : 0u;
+        const i32x4 r = words_of(base, bytes);
+#pragma unroll
+        for (int q = 0; q < 2; ++q) {
+            const int L = c.w * 2 + q;
+            uint8_t *dst = lds + slot * kSlot + part * kPart + L * 1024;
+            if (GATHER && !a) {
+                if (part == kBLo) {
+                    const int l4 = c.lane >> 4;
+                    const int lo = l4 & 1 ? idx[4 * q + 1] : idx[4 * q], hi = l4 & 1 ? idx[4 * q + 3] : idx[4 * q + 2];
+                    const uint32_t row = (uint32_t)(l4 & 2 ? hi : lo);
+                    boff[q] = row < (uint32_t)p.T ? row * (uint32_t)ldb + lb : kRowOOB;
+                }
+                dma<16>(r, dst, boff[q] + col);
+            } else {
+                dma<16>(r, dst, (a ? la : lb) + (uint32_t)(L * 4) * (uint32_t)ld + col);
+            }
         }
     };
 
-    Ref cur = ref_of(tile);
-    src = cur;
-    fetch_rows(0);
-#pragma unroll
-    for (int q = 0; q < S::QB; ++q) load(0, 0, q);
-    int nk = stages(cur);
-    uint32_t fa = frag_a<S>(c), fb = frag_b<S>(c);
-    int next = tile + nwg;
-    // rows of the stage after the first: this tile's, or the next tile's
-    Ref nref = next < ntiles ? ref_of(next) : Ref{};
-    if (nk > 1) {
-        fetch_rows(1);
-    } else {
-        src = nref;
-        fetch_rows(0);
-    }
-    __syncthreads();
+    fetch(src, 0);
+    load(kALo, 0);
+    load(kBLo, 0);
+    load(kBHi, 0);
+    load(kAHi, 0);
+    ++lk;
+    fetch(src, 1);
+    load(kALo, 1);
+    load(kBLo, 1);
+    load(kBHi, 1);
+    uint32_t fa = part_base<true>(c, c.wm), fb = part_base<true>(c, c.wn);
+    uint8_t *buf = lds + kStage + c.w * 2048;
+    turn_end<kInFlight>();
 
-    int rs = 0;
+    int slot = 0, stored = 0;
     for (;;) {
-        f32x16 acc[MB][NB];
+        tile += nwg;
+        next = find(tile);
+        f32x16 acc[4][2];
 #pragma unroll
-        for (int i = 0; i < MB; ++i)
-#pragma unroll
-            for (int j = 0; j < NB; ++j) acc[i][j] = f32x16{};
-        Frag2<S> F0, F1{};
-        for (int s = 0; s < nk; ++s) {
-            // stage s + 1 of this tile, or the next tile's first, is loaded now; src and idx are its
-            const int ks = s + 1 < nk ? s + 1 : 0;
-            asm volatile("" : "+v"(ma[0]), "+v"(ma[1]), "+v"(mb[0]), "+v"(mb[1]), "+v"(fa), "+v"(fb));
-            const int ls = rs ^ 1;
-            auto issue = [&](int i) {
-                if (i < S::QB) load(ls, ks, i);
-            };
-            const uint32_t a = fa + (uint32_t)(rs * S::kSlotA), b = fb + (uint32_t)(rs * S::kSlotB);
-            phase2<S, MB, 0, true>(acc, F1, F0, lds, a, b, issue);
-            // the row indices of the stage after that
-            if (s + 2 < nk) {
-                fetch_rows(s + 2);
-            } else if (s + 2 == nk) {
-                src = nref;
-                fetch_rows(0);
-            } else if (stages(nref) > 1) {
-                fetch_rows(1);
-            }
-            phase2<S, MB, 1, true>(acc, F0, F1, lds, a, b, [](int) {});
-            phase2<S, MB, 2, true>(acc, F1, F0, lds, a, b, [](int) {});
-            phase2<S, MB, 3, true>(acc, F0, F1, lds, a, b, [](int) {});
-            stage_barrier<0>();
-            rs ^= 1;
+        for (int i = 0; i < 4; ++i) acc[i][0] = acc[i][1] = f32x16{};
+        if (c.w >= 4) asm volatile("s_barrier" ::: "memory");      // one turn behind
+        for (int s = 0; s < cur.nk; ++s) {
+            asm volatile("" : "+v"(la), "+v"(lb), "+v"(fa), "+v"(fb));
+            core_stage<true, true, 2, 2>(
+                acc, lds, fa, fb, slot, s == 0 ? stored : 0,
+                [&](int part) { load(part, part == kAHi ? slot ^ 1 : slot); },
+                [&] {
+                    if (++lk == src.nk) {
+                        lk = 0;
+                        src = next;
+                    }
+                },
+                [&] {
+                    if (lk + 1 < src.nk) fetch(src, lk + 1);
+                    else fetch(next, 0);
+                },
+                std::integral_constant<int, kStores>{});
+            slot ^= 1;
         }
-        phase2<S, MB, 0, false>(acc, F1, F0, lds, fa, fb, [](int) {});
-
-        const int n0 = cur.n0, k0 = cur.k0 + c.wn * 64;
-        if constexpr (F32) {
-            // four consecutive columns a lane and block of four registers
-            uint8_t *D = p.dW + (int64_t)cur.g * p.N * p.K * 4;
+        if (c.w < 4) asm volatile("s_barrier" ::: "memory");
+        DBS_FENCE();
 #pragma unroll
-            for (int i = 0; i < MB; ++i) {
-                const int r0 = n0 + c.wm * 128 + i * 32;
-                const uint32_t left = __builtin_amdgcn_readfirstlane(max(0, min(32, p.N - r0)));
-                const __amdgpu_buffer_rsrc_t rd = make_rsrc(D + (int64_t)r0 * p.K * 4, left * (uint32_t)p.K * 4u);
+        for (int i = 0; i < 4; ++i) {
+            const int r0 = cur.n0 + (2 * i + c.wm) * 32;
 #pragma unroll
-                for (int j = 0; j < NB; ++j) {
+            for (int j = 0; j < 2; ++j) {
+                const int k0 = cur.k0 + j * 128 + c.wn * 32;
+                if constexpr (F32) {
+                    // four consecutive columns a lane and group of four registers
+                    typedef __attribute__((ext_vector_type(4))) float f32x4;
+                    const int left = __builtin_amdgcn_readfirstlane(max(0, min(32, p.N - r0)));
+                    const __amdgpu_buffer_rsrc_t rd = make_rsrc(p.dW + ((int64_t)cur.g * p.N + r0) * p.K * 4,
+                                                                (uint32_t)left * (uint32_t)p.K * 4u);
 #pragma unroll
                     for (int g = 0; g < 4; ++g) {
-                        typedef __attribute__((ext_vector_type(4))) float f32x4;
-                        const int k = k0 + j * 32 + g * 8 + c.h * 4;
+                        const int k = k0 + g * 8 + c.h * 4;
                         const uint32_t off = k < p.K ? (uint32_t)(c.lr * p.K + k) * 4u : kOOB;   // K % 8 == 0
-                        f32x4 v = {acc[i][j][4 * g], acc[i][j][4 * g + 1], acc[i][j][4 * g + 2], acc[i][j][4 * g + 3]};
+                        const f32x16 &v16 = acc[i][j];
+                        f32x4 v = {v16[4 * g], v16[4 * g + 1], v16[4 * g + 2], v16[4 * g + 3]};
                         if (p.accumulate)
                             v += __builtin_bit_cast(f32x4, __builtin_amdgcn_raw_buffer_load_b128(rd, off, 0, 0));
                         __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(i32x4, v), rd, off, 0, kStoreNT);
                     }
+                } else {
+                    store_block(buf, p.dW + (int64_t)cur.g * p.N * p.K * 2, p.K, r0, p.N, k0, p.K, 1, c,
+                                [&](int q) { return acc[i][j][q]; });
                 }
             }
-        } else {
-            uint8_t *buf = lds + S::kLdsB + (rs ^ 1) * S::kSlotB + c.w * (32 * NB * 64);
-            store_bf16<S, MB, NB>(buf, p.dW + (int64_t)cur.g * p.N * p.K * 2, p.K, n0, p.N, k0, p.K, 1, c,
-                              [&](int i, int j, int q) { return acc[i][j][q]; });
         }
-        asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory");
-        if (next >= ntiles) break;
-        tile = next;
-        cur = nref;
-        nk = stages(cur);
-        next = tile + nwg;
-        nref = next < ntiles ? ref_of(next) : Ref{};
-        // a tile of one stage: the stage after it is the next tile's first
-        if (nk == 1) {
-            src = nref;
-            fetch_rows(0);
-        }
+        stored = !p.accumulate;
+        if (tile >= ntiles) break;
+        cur = next;
     }
+    asm volatile("s_waitcnt vmcnt(0)" ::: "memory");   // nothing is left to land in LDS
 }
 
-template <class S>
-hipError_t launch_tiles(const MoeGemm &p, int cus, hipStream_t stream)
+// At most as many workgroups as there can be tiles of tm rows and tno columns.
+dim3 tile_grid(const MoeGemm &p, int tm, int cus)
 {
-    const int tno = p.gate ? S::TN / 2 : S::TN;
-    const int64_t most = ((int64_t)p.M / S::TM + (p.M < p.E ? p.M : p.E)) * ((p.ncols + tno - 1) / tno);
-    const dim3 grid((uint32_t)(most < cus ? (most > 0 ? most : 1) : cus));
-    if constexpr (!S::BMN) {
-        if (p.gate) {
-            hipLaunchKernelGGL((moe_tiles<S, true>), grid, dim3(S::kThreads), 0, stream, p);
-            return hipGetLastError();
-        }
-    }
-    hipLaunchKernelGGL((moe_tiles<S, false>), grid, dim3(S::kThreads), 0, stream, p);
-    return hipGetLastError();
+    const int tno = p.gate ? 128 : 256;
+    const int64_t most = ((int64_t)p.M / tm + (p.M < p.E ? p.M : p.E)) * ((p.ncols + tno - 1) / tno);
+    return dim3((uint32_t)(most < cus ? most : cus));
 }
 
 }  // namespace
 
 hipError_t launch_moe_tiles(const MoeGemm &p, int tm, int cus, hipStream_t stream)
 {
-    if (p.wmn) {
-        switch (tm) {
-        case 64: return launch_tiles<Tile<64, 3, false, true>>(p, cus, stream);
-        case 128: return launch_tiles<Tile<128, 3, false, true>>(p, cus, stream);
-        case 256: return launch_tiles<Tile<256, 2, false, true>>(p, cus, stream);
-        }
+    const dim3 grid = tile_grid(p, tm, cus), block(512);
+    using Small = Tile<64, 3, false, false>;
+    using SmallMn = Tile<64, 3, false, true>;
+    if (tm == 64) {
+        if (p.wmn) hipLaunchKernelGGL((moe_tiles_64<SmallMn, false>), grid, block, 0, stream, p);
+        else if (p.gate) hipLaunchKernelGGL((moe_tiles_64<Small, true>), grid, block, 0, stream, p);
+        else hipLaunchKernelGGL((moe_tiles_64<Small, false>), grid, block, 0, stream, p);
     } else {
-        switch (tm) {
-        case 64: return launch_tiles<Tile<64, 3, false, false>>(p, cus, stream);
-        case 128: return launch_tiles<Tile<128, 3, false, false>>(p, cus, stream);
-        case 256: return launch_tiles<Tile<256, 2, false, false>>(p, cus, stream);
-        }
+        if (p.wmn) hipLaunchKernelGGL((moe_tiles_256<true, false>), grid, block, 0, stream, p);
+        else if (p.gate) hipLaunchKernelGGL((moe_tiles_256<false, true>), grid, block, 0, stream, p);
+        else hipLaunchKernelGGL((moe_tiles_256<false, false>), grid, block, 0, stream, p);
     }
-    return hipErrorInvalidValue;
+    return hipGetLastError();
 }
 
 hipError_t launch_moe_dw(const MoeGemmDw &p, int cus, hipStream_t stream)
 {
     const int64_t tiles = (int64_t)p.E * ((p.N + 255) / 256) * ((p.K + 255) / 256);
-    const dim3 grid((uint32_t)(tiles < cus ? tiles : cus)), block(DwTile::kThreads);
+    const dim3 grid((uint32_t)(tiles < cus ? tiles : cus)), block(512);
     if (p.rows) {
         if (p.f32) hipLaunchKernelGGL((moe_dw<true, true>), grid, block, 0, stream, p);
         else hipLaunchKernelGGL((moe_dw<true, false>), grid, block, 0, stream, p);
