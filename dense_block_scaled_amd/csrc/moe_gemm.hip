@@ -48,21 +48,21 @@ __device__ __forceinline__ i32x4 words_of(const void *base, uint32_t bytes)
 // written out: the compiler follows the builtin's loads and waits for all of
 // them before any LDS read, which would end the overlap this file's kernels
 // are built on.  They wait by count themselves, at every barrier.  Lane i's
-// bytes land at dst + BYTES i; nothing is returned to registers.  (M0, which
+// bytes land at lds + dst + BYTES i; nothing is returned to registers.  (M0, which
 // holds the destination, is a register the compiler sets before its own uses.)
 template <int BYTES>
-__device__ __forceinline__ void dma(const i32x4 &words, uint8_t *dst, uint32_t voff)
+__device__ __forceinline__ void dma(const i32x4 &words, uint8_t *lds, uint32_t dst, uint32_t voff)
 {
     static_assert(BYTES == 4 || BYTES == 16, "dword or dwordx4");
 #if DBS_LDS_POISON
     const uint32_t lane = __builtin_amdgcn_mbcnt_hi(~0u, __builtin_amdgcn_mbcnt_lo(~0u, 0u));
     if constexpr (BYTES == 4)
-        *reinterpret_cast<uint32_t *>(dst + 4 * lane) = ~0u;
+        *reinterpret_cast<uint32_t *>(lds + dst + 4 * lane) = ~0u;
     else
-        *reinterpret_cast<i32x4 *>(dst + 16 * lane) = i32x4{-1, -1, -1, -1};
+        *reinterpret_cast<i32x4 *>(lds + dst + 16 * lane) = i32x4{-1, -1, -1, -1};
     asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
 #endif
-    const int m0 = __builtin_amdgcn_readfirstlane((int)(uint32_t)(uintptr_t)(lds_void *)dst);
+    const uint32_t m0 = (uint32_t)(uintptr_t)(lds_void *)lds + dst;
     if constexpr (BYTES == 4)
         asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dword %1, %2, 0 offen lds" ::"s"(m0), "v"(voff), "s"(words)
                      : "memory");
@@ -247,29 +247,28 @@ __device__ __forceinline__ int first_tile()
 // 256 x 256 output tiles over stages of 64, 8 waves (2 x 4, two per SIMD),
 // each owning 128 x 64 as 4 x 2 blocks of 32 x 32.  A stage is four parts of
 // 16 KiB -- A's rows (or columns) 0 .. 127 and 128 .. 255, B's likewise -- in
-// one of two LDS slots, and is computed as four quadrants of 2 x 1 blocks:
-// (A lo, B lo), (A lo, B hi), (A hi, B hi), (A hi, B lo).  A wave reads a
-// quadrant's new operand part whole, all four k-steps, into registers: the
-// part of the slot is free again a quarter of a stage later, and its refill
-// for the stage after next starts then.  Loads so get six of the eight
-// half-phases of one and a half stages to land (measured need: rows that
-// nothing else has touched come from HBM), with two slots.
+// one of two LDS slots, and is computed as four quadrants of 2 x 1 blocks.  A
+// wave reads one part whole, all four k-steps, into registers per quadrant,
+// so the part's place in the slot is free again at once, and its refill for
+// the stage after next starts a turn later: loads get six turns of the eight
+// that two stages take to land, with two slots.  (Rows that nothing else has
+// touched come from HBM: with loads of one stage's lead, waited for in full
+// at its end, the same tiles took a quarter longer.)
 //
 // The two waves of a SIMD take turns: while one reads its next part and
 // issues two wave-loads, the other runs eight MFMAs, with a workgroup barrier
 // between turns.  Waves 4 .. 7 start one turn late.
 //
-//   turn   reads           loads issued          MFMAs of the turn after
-//   0      A lo, B lo      A hi of stage s + 1   (lo, lo)
-//   1      B hi            A lo of stage s + 2   (lo, hi)
-//   2      A hi            B lo of stage s + 2   (hi, hi)
-//   3                      B hi of stage s + 2   (hi, lo)
+//   turn   reads              loads issued            MFMAs of the turn after
+//   0      A lo               B lo of stage s + 2     (lo, lo)
+//   1      B hi               A lo of stage s + 2     (lo, hi)
+//   2      A hi               B hi of stage s + 2     (hi, hi)
+//   3      B lo of s + 1      A hi of stage s + 2     (hi, lo)
 //
-// Every wave waits, at the end of turns 3, 0 and 1, for its loads of the
-// parts read in the turn after: 10 newer wave-loads are in flight by then
-// (kInFlight); its own reads are complete before the barrier that lets
-// others refill what it read.
-constexpr int kPart = 128 * kRowBytes, kSlot = 4 * kPart, kInFlight = 10;
+// At the end of every turn a wave waits for its loads of the part read in the
+// turn after: kInFlight newer wave-loads may be under way by then.  Its own
+// reads are complete before the barrier that lets others refill their place.
+constexpr int kPart = 128 * kRowBytes, kSlot = 4 * kPart, kInFlight = 12;
 enum PartId : int { kALo = 0, kAHi = 1, kBLo = 2, kBHi = 3 };
 constexpr int kStage = 2 * kSlot;              // LDS offset of the waves' output buffers, 2 KiB each
 constexpr int kCoreLds = kStage + 8 * 2048;
@@ -309,13 +308,6 @@ __device__ __forceinline__ void turn_end()
     DBS_FENCE();
 }
 
-__device__ __forceinline__ void turn_end_reads()
-{
-    DBS_FENCE();
-    asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory");
-    DBS_FENCE();
-}
-
 __device__ __forceinline__ void turn_end_math()
 {
     DBS_FENCE();
@@ -324,72 +316,60 @@ __device__ __forceinline__ void turn_end_math()
     DBS_FENCE();
 }
 
-// One stage out of slot `slot`.  NLO, NHI: blocks per wave in the two halves
-// of A (fewer than 2 where a group ends).  load(part) issues the two
-// wave-loads of a part (the parts in the order above); advance() moves the
-// loads on to the next stage, ahead() looks up what that one needs.  extra: STORES stores of the last tile's results
-// went out between the loads awaited here and now, and may still be under way.
-template <bool AMN, bool BMN, int NLO, int NHI, class LOAD, class ADVANCE, class AHEAD, int STORES>
-__device__ __forceinline__ void core_stage(f32x16 (&acc)[4][2], const uint8_t *lds, uint32_t fa, uint32_t fb, int slot,
-                                           int extra, LOAD &&load, ADVANCE &&advance, AHEAD &&ahead,
-                                           std::integral_constant<int, STORES>)
+// One stage out of slot `slot`; b0 holds its B lo, b0n takes the next stage's.
+// NLO, NHI: blocks per wave in the two halves of A (fewer than 2 where a group
+// ends).  advance() moves the loads on to the next stage, load(part) issues
+// the two wave-loads of a part of it.  extra: STORES stores of the last tile's
+// results went out between the loads awaited here and now, and may still be
+// under way.
+template <bool AMN, bool BMN, int NLO, int NHI, class LOAD, class ADVANCE, int STORES>
+__device__ __forceinline__ void core_stage(f32x16 (&acc)[4][2], bf16x8 (&b0)[4], bf16x8 (&b0n)[4], const uint8_t *lds,
+                                           uint32_t fa, uint32_t fb, int slot, int extra, LOAD &&load,
+                                           ADVANCE &&advance, std::integral_constant<int, STORES>)
 {
-    bf16x8 a[2][4], b0[4], b1[4];
-    const uint32_t so = (uint32_t)(slot * kSlot);
+    bf16x8 a[2][4], b1[4];
+    const uint32_t so = (uint32_t)(slot * kSlot), sn = so ^ kSlot;
     auto wait = [&] {
         if (extra) turn_end<kInFlight + STORES>();
         else turn_end<kInFlight>();
     };
+    auto math = [&](int i0, int j, int n, const bf16x8 (&b)[4]) {
+        __builtin_amdgcn_s_setprio(1);
+#pragma unroll
+        for (int kk = 0; kk < 4; ++kk)
+#pragma unroll
+            for (int i = 0; i < n; ++i) mma1<kBF16, 0>(acc[i0 + i][j], a[i][kk], 0u, b[kk], 0u);
+        turn_end_math();
+    };
     // turn 0
-#pragma unroll
-    for (int kk = 0; kk < 4; ++kk) {
-        b0[kk] = part_frag<BMN>(lds, fb + so + kBLo * kPart, kk, 0);
-#pragma unroll
-        for (int i = 0; i < NLO; ++i) a[i][kk] = part_frag<AMN>(lds, fa + so + kALo * kPart, kk, i);
-    }
-    load(kAHi);
-    wait();
-    ahead();
-    __builtin_amdgcn_s_setprio(1);
+    advance();
 #pragma unroll
     for (int kk = 0; kk < 4; ++kk)
 #pragma unroll
-        for (int i = 0; i < NLO; ++i) mma1<kBF16, 0>(acc[i][0], a[i][kk], 0u, b0[kk], 0u);
-    turn_end_math();
+        for (int i = 0; i < NLO; ++i) a[i][kk] = part_frag<AMN>(lds, fa + so + kALo * kPart, kk, i);
+    load(kBLo);
+    wait();
+    math(0, 0, NLO, b0);
     // turn 1
 #pragma unroll
     for (int kk = 0; kk < 4; ++kk) b1[kk] = part_frag<BMN>(lds, fb + so + kBHi * kPart, kk, 0);
-    advance();
     load(kALo);
     wait();
-    __builtin_amdgcn_s_setprio(1);
-#pragma unroll
-    for (int kk = 0; kk < 4; ++kk)
-#pragma unroll
-        for (int i = 0; i < NLO; ++i) mma1<kBF16, 0>(acc[i][1], a[i][kk], 0u, b1[kk], 0u);
-    turn_end_math();
+    math(0, 1, NLO, b1);
     // turn 2
 #pragma unroll
     for (int kk = 0; kk < 4; ++kk)
 #pragma unroll
         for (int i = 0; i < NHI; ++i) a[i][kk] = part_frag<AMN>(lds, fa + so + kAHi * kPart, kk, i);
-    load(kBLo);
-    turn_end_reads();
-    __builtin_amdgcn_s_setprio(1);
-#pragma unroll
-    for (int kk = 0; kk < 4; ++kk)
-#pragma unroll
-        for (int i = 0; i < NHI; ++i) mma1<kBF16, 0>(acc[2 + i][1], a[i][kk], 0u, b1[kk], 0u);
-    turn_end_math();
-    // turn 3
     load(kBHi);
     wait();
-    __builtin_amdgcn_s_setprio(1);
+    math(2, 1, NHI, b1);
+    // turn 3
 #pragma unroll
-    for (int kk = 0; kk < 4; ++kk)
-#pragma unroll
-        for (int i = 0; i < NHI; ++i) mma1<kBF16, 0>(acc[2 + i][0], a[i][kk], 0u, b0[kk], 0u);
-    turn_end_math();
+    for (int kk = 0; kk < 4; ++kk) b0n[kk] = part_frag<BMN>(lds, fb + sn + kBLo * kPart, kk, 0);
+    load(kAHi);
+    wait();
+    math(2, 0, NHI, b0);
 }
 
 // One 32 x 32 block of results as bf16 rows r0 .. mend-1, columns n .. ncols-1
@@ -399,7 +379,9 @@ __device__ __forceinline__ void store_block(uint8_t *buf, uint8_t *D, int64_t ld
                                             int vec, Lane c, VALUE &&value)
 {
     // (addresses are made here, not before the tile's stages, whose registers they would take)
-    asm volatile("" : "+v"(c.lane), "+v"(c.lr), "+v"(c.h));
+    asm volatile("" : "+v"(c.lane));
+    c.lr = c.lane & 31;
+    c.h = c.lane >> 5;
     const int left = __builtin_amdgcn_readfirstlane(max(0, min(32, mend - r0)));
     const __amdgpu_buffer_rsrc_t rd = make_rsrc(D + (int64_t)r0 * ld * 2, (uint32_t)left * (uint32_t)ld * 2u);
     if (vec) {
@@ -529,7 +511,7 @@ __global__ __launch_bounds__(512, 1) void moe_tiles_256(MoeGemm p)
     constexpr int TNO = GATE ? 128 : 256;              // output columns of a tile
     constexpr int kStores = GATE ? 8 : 16;             // store instructions of a whole tile (vec)
 
-    const Lane c = lane_of();
+    Lane c = lane_of();
     const int lda = p.K * 2, ldb = BMN ? p.N * 2 : lda;
     const int tiles_n = (p.ncols + TNO - 1) / TNO;
     fill_table(tab, p, c);
@@ -538,9 +520,10 @@ __global__ __launch_bounds__(512, 1) void moe_tiles_256(MoeGemm p)
     const int ntiles = count_tiles(tab, p.E, tiles_n);
     const int nwg = gridDim.x, self = first_tile();
     if (self >= ntiles) return;
-    // at least four stages (the surplus reads zeros): the next tile's rows
+    // an even number of stages, at least four (the surplus reads zeros): the
+    // stages' B lo registers change places, and the next tile's row indices
     // land within a tile (see rowbuf)
-    const int nk = max((p.K + 63) / 64, 4);
+    const int nk = max((p.K + 127) / 128 * 2, 4);
     auto find = [&](int round) {
         return find_tile(tab, p.E, ntiles, tiles_n, TNO, round * nwg + (round & 1 ? nwg - 1 - self : self), c);
     };
@@ -549,15 +532,14 @@ __global__ __launch_bounds__(512, 1) void moe_tiles_256(MoeGemm p)
     i32x4 ra, rb;
     uint32_t aoff[4];                     // the lane's row offsets in ra: A lo's two wave-loads, A hi's
     int f0 = 0, lk = 0;
-    const int lrow = c.lane >> 3;
-    uint32_t x4 = (uint32_t)(((c.lane & 7) ^ lrow) << 4);
-    uint32_t lb = BMN ? mn_dma_lane<kBF16, 128>(c.lane, 0, ldb) : (uint32_t)(lrow * ldb);
+    uint32_t x4 = (uint32_t)(((c.lane & 7) ^ (c.lane >> 3)) << 4);
+    uint32_t lb = BMN ? mn_dma_lane<kBF16, 128>(c.lane, 0, ldb) : (uint32_t)((c.lane >> 3) * ldb);
     // Row indices of the tile `r` on their way into rowbuf (lanes past the
     // group's end load zeros, which aim does not use)
     auto fetch = [&](const RowTile &r) {
         const int n = max(r.mend - r.m0, 0);
         const i32x4 rr = words_of(p.rows ? p.rows + r.m0 : nullptr, p.rows ? (uint32_t)min(n, 256) * 4u : 0u);
-        dma<4>(rr, reinterpret_cast<uint8_t *>(rowbuf) + (c.w & 3) * 256, (uint32_t)((c.w & 3) * 256 + c.lane * 4));
+        dma<4>(rr, reinterpret_cast<uint8_t *>(rowbuf), (c.w & 3) * 256, (uint32_t)((c.w & 3) * 256 + c.lane * 4));
     };
     auto aim = [&](const RowTile &r) {
         lk = 0;
@@ -579,7 +561,7 @@ __global__ __launch_bounds__(512, 1) void moe_tiles_256(MoeGemm p)
         ra = words_of(p.rows ? p.X : p.X + (int64_t)r.m0 * lda, have * (uint32_t)lda);
 #pragma unroll
         for (int q = 0; q < 4; ++q) {
-            const int m = (q >> 1) * 128 + c.w * 16 + (q & 1) * 8 + lrow;
+            const int m = (q >> 1) * 128 + c.w * 16 + (q & 1) * 8 + (c.lane >> 3);
             const uint32_t row = p.rows ? rowbuf[m] : (uint32_t)m;
             aoff[q] = m < left && row < have ? row * (uint32_t)lda : kRowOOB;
         }
@@ -589,23 +571,23 @@ __global__ __launch_bounds__(512, 1) void moe_tiles_256(MoeGemm p)
 #pragma unroll
         for (int q = 0; q < 2; ++q) {
             const int L = c.w * 2 + q;
-            uint8_t *dst = lds + slot * kSlot + part * kPart + L * 1024;
+            const uint32_t dst = slot * kSlot + part * kPart + L * 1024;
             const int kc = (int)(x4 ^ (uint32_t)((L & 7) << 4)) + k0;
             if (part == kALo || part == kAHi) {
-                dma<16>(ra, dst, kc < lda ? aoff[(part == kAHi ? 2 : 0) + q] + kc : kRowOOB);
+                dma<16>(ra, lds, dst, kc < lda ? aoff[(part == kAHi ? 2 : 0) + q] + kc : kRowOOB);
             } else {
                 const int j = part == kBHi;
                 if constexpr (BMN) {
                     const uint32_t row = (uint32_t)(lk * 64 + L * 4);          // four K-rows a wave-load
-                    dma<16>(rb, dst, row < (uint32_t)p.K ? lb + row * (uint32_t)ldb + j * 256 : kOOB);
+                    dma<16>(rb, lds, dst, row < (uint32_t)p.K ? lb + row * (uint32_t)ldb + j * 256 : kOOB);
                 } else if constexpr (GATE) {
                     const int f = f0 + L * 8;                                  // of matrix j
-                    dma<16>(rb, dst, kc < lda && f + lrow < p.ncols
+                    dma<16>(rb, lds, dst, kc < lda && f + (c.lane >> 3) < p.ncols
                                              ? lb + (uint32_t)((j * p.ncols + f) * lda) + kc : kOOB);
                 } else {
                     // wave column L / 4's rows: 32 of its 64
                     const int n = (L >> 2) * 64 + j * 32 + (L & 3) * 8;
-                    dma<16>(rb, dst, kc < lda ? lb + (uint32_t)(n * lda) + kc : kOOB);
+                    dma<16>(rb, lds, dst, kc < lda ? lb + (uint32_t)(n * lda) + kc : kOOB);
                 }
             }
         }
@@ -615,16 +597,20 @@ __global__ __launch_bounds__(512, 1) void moe_tiles_256(MoeGemm p)
     fetch(cur);
     turn_end<0>();
     aim(cur);
-    load(kALo, 0);
-    load(kBLo, 0);
-    load(kBHi, 0);
-    load(kAHi, 0);
-    ++lk;
-    load(kALo, 1);
-    load(kBLo, 1);
-    load(kBHi, 1);
+#pragma unroll
+    for (lk = 0; lk < 2; ++lk) {
+        load(kBLo, lk);
+        load(kALo, lk);
+        load(kBHi, lk);
+        load(kAHi, lk);
+    }
+    lk = 1;
     uint32_t fa = part_base<false>(c, c.wm), fb = part_base<BMN>(c, c.wn);
     uint8_t *buf = lds + kStage + c.w * 2048;
+    turn_end<kInFlight>();
+    bf16x8 b0[4], b0n[4];
+#pragma unroll
+    for (int kk = 0; kk < 4; ++kk) b0[kk] = part_frag<BMN>(lds, fb + kBLo * kPart, kk, 0);
     turn_end<kInFlight>();
 
     int slot = 0, round = 0, stored = 0;
@@ -634,21 +620,25 @@ __global__ __launch_bounds__(512, 1) void moe_tiles_256(MoeGemm p)
 #pragma unroll
         for (int i = 0; i < 4; ++i) acc[i][0] = acc[i][1] = f32x16{};
         if (c.w >= 4) asm volatile("s_barrier" ::: "memory");      // one turn behind
-        for (int s = 0; s < nk; ++s) {
+        auto stage = [&](int s, bf16x8 (&now)[4], bf16x8 (&then)[4]) {
             asm volatile("" : "+v"(x4), "+v"(lb), "+v"(fa), "+v"(fb));
             core_stage<false, BMN, NLO, NHI>(
-                acc, lds, fa, fb, slot, s == 0 ? stored : 0,
-                [&](int part) { load(part, part == kAHi ? slot ^ 1 : slot); },
+                acc, now, then, lds, fa, fb, slot, s == 0 ? stored : 0, [&](int part) { load(part, slot); },
                 [&] {
                     if (s == 0) fetch(next);
                     if (++lk == nk) aim(next);
                 },
-                [] {},
                 std::integral_constant<int, kStores>{});
             slot ^= 1;
+        };
+#pragma clang loop unroll(disable)
+        for (int s = 0; s < nk; s += 2) {
+            stage(s, b0, b0n);
+            stage(s + 1, b0n, b0);
         }
         if (c.w < 4) asm volatile("s_barrier" ::: "memory");
         DBS_FENCE();
+        asm volatile("" : "+v"(c.lane));
 #pragma unroll
         for (int i = 0; i < NLO + NHI; ++i) {
             const int r0 = cur.m0 + (2 * i + c.wm) * 32;
@@ -753,13 +743,13 @@ __global__ __launch_bounds__(512, 1) void moe_tiles_64(MoeGemm p)
         if (q < S::QA) {
             const int L = c.w * S::QA + q;
             const int kc = (int)(x4 ^ (uint32_t)((L & 7) << 4));
-            dma<16>(src.ra, lds + S::kLdsA + slot * S::kSlotA + L * 1024, kc < lda - k0 ? src.a[q] + k0 : kRowOOB);
+            dma<16>(src.ra, lds, S::kLdsA + slot * S::kSlotA + L * 1024, kc < lda - k0 ? src.a[q] + k0 : kRowOOB);
         }
         const int L = c.w * S::QB + q;
-        uint8_t *dst = lds + S::kLdsB + slot * S::kSlotB + L * 1024;
+        const uint32_t dst = S::kLdsB + slot * S::kSlotB + L * 1024;
         if constexpr (S::BMN) {
             const uint32_t row = (uint32_t)(ks * S::KS + L * 2);           // two K-rows a wave-load
-            dma<16>(src.rb, dst, row < (uint32_t)p.K ? mb[q & 1] + row * (uint32_t)ldb : kOOB);
+            dma<16>(src.rb, lds, dst, row < (uint32_t)p.K ? mb[q & 1] + row * (uint32_t)ldb : kOOB);
         } else {
             const int kc = (int)(x4 ^ (uint32_t)((L & 7) << 4));
             uint32_t off = r8ldb + (uint32_t)(kc + k0);
@@ -772,7 +762,7 @@ __global__ __launch_bounds__(512, 1) void moe_tiles_64(MoeGemm p)
             } else {
                 off += (uint32_t)(L * 8 * lda);
             }
-            dma<16>(src.rb, dst, in ? off : kOOB);
+            dma<16>(src.rb, lds, dst, in ? off : kOOB);
         }
     };
 
@@ -841,21 +831,27 @@ __global__ __launch_bounds__(512, 1) void moe_tiles_64(MoeGemm p)
 // ---------------------------------------------------------------------- dw
 
 // GATHER: rows of X through p.rows.  F32: dW holds fp32.
+//
+// Gathered rows: a wave loads eight K-rows of X a stage.  Their indices reach
+// LDS for eight stages at a time by one dword load of the wave's own (it
+// waits for them by its own count, no barrier), into a buffer per parity of
+// the tile for a tile's first eight stages and two in turn for later ones.
 template <bool GATHER, bool F32>
 __global__ __launch_bounds__(512, 1) void moe_dw(MoeGemmDw p)
 {
     __shared__ __attribute__((aligned(1024))) uint8_t lds[kCoreLds];
-    __shared__ int32_t first[kMoeMaxExperts + 1], tile_at[kMoeMaxExperts + 1];
+    __shared__ int32_t first[kMoeMaxExperts + 1];
+    __shared__ uint16_t used[kMoeMaxExperts + 1];      // groups with tiles before a group
+    __shared__ uint32_t rowbuf[GATHER ? 8 * 256 : 1];
     constexpr int kStores = F32 ? 32 : 16;             // store instructions of a tile
 
     const Lane c = lane_of();
     const int lda = p.N * 2, ldb = p.K * 2;            // bytes of a row of dY, of X
     const int tiles_n = (p.N + 255) / 256, tiles_k = (p.K + 255) / 256, per = tiles_n * tiles_k;
     if (c.w == 0)
-        group_table<true>(first, tile_at, p.offsets, p.E, p.M, c,
-                          [&](int rows) { return p.accumulate && rows == 0 ? 0 : per; });
+        group_table<true>(first, used, p.offsets, p.E, p.M, c, [&](int rows) { return !p.accumulate || rows > 0; });
     __syncthreads();
-    const int ntiles = __builtin_amdgcn_readfirstlane(tile_at[p.E]), nwg = gridDim.x;
+    const int ntiles = __builtin_amdgcn_readfirstlane((int)used[p.E]) * per, nwg = gridDim.x;
     int tile = first_tile();
     if (tile >= ntiles) return;
 
@@ -867,10 +863,10 @@ __global__ __launch_bounds__(512, 1) void moe_dw(MoeGemmDw p)
         Ref r{};
         r.nk = 2;
         if (id >= ntiles) return r;
-        r.g = group_of(tile_at, p.E, id, c);
+        r.g = group_of(used, p.E, id / per, c);
         r.lo = __builtin_amdgcn_readfirstlane(first[r.g]);
         r.hi = __builtin_amdgcn_readfirstlane(first[r.g + 1]);
-        const int local = id - __builtin_amdgcn_readfirstlane(tile_at[r.g]);
+        const int local = id % per;
         r.n0 = local % tiles_n * 256;
         r.k0 = local / tiles_n * 256;
         // the loads run up to two stages ahead: two at least
@@ -879,70 +875,71 @@ __global__ __launch_bounds__(512, 1) void moe_dw(MoeGemmDw p)
     };
     Ref cur = find(tile), next = cur;
 
-    // What the loads read: stage lk of tile src.
+    // What the loads read: stage lk of tile src, rows behind wa and wb.
     Ref src = cur;
-    int lk = 0;
+    int lk = 0, left = 0, odd = 0;                     // rows of the stage; parity of src
+    i32x4 wa, wb;
     uint32_t la = mn_dma_lane<kBF16, 128>(c.lane, 0, lda);
     uint32_t lb = mn_dma_lane<kBF16, 128>(c.lane, 0, GATHER ? 0 : ldb);
-    // Gathered: X's rows behind the wave's eight K-rows of the stage, through
-    // the scalar cache (its loads do not queue with the tiles' loads), and
-    // the lane's byte offsets of its two wave-loads.
-    typedef const __attribute__((address_space(4))) int32_t *const_i32;
-    const const_i32 rows = (const_i32)(uintptr_t)p.rows;
-    int idx[8];
-    uint32_t boff[2] = {};
-    auto fetch = [&](const Ref &r, int k) {
+    uint32_t boff[2] = {};                             // gathered: the lane's offsets of its two wave-loads
+    const i32x4 wr = words_of(p.rows, GATHER ? (uint32_t)p.M * 4u : 0u);
+    auto batch = [&](const Ref &r, int b, int buffer) {
         if constexpr (GATHER) {
-            const int m = r.lo + k * 64 + c.w * 8;
+            const int m = r.lo + (8 * b + (c.lane >> 3)) * 64 + c.w * 8 + (c.lane & 7);
+            dma<4>(wr, reinterpret_cast<uint8_t *>(rowbuf), c.w * 1024 + buffer * 256, (uint32_t)m * 4u);
+        }
+    };
+    auto aim = [&] {
+        const int m0 = src.lo + lk * 64;
+        left = min(64, src.hi - m0);
+        wa = words_of(p.dY + (int64_t)m0 * lda + src.n0 * 2, left > 0 ? (uint32_t)left * (uint32_t)lda - src.n0 * 2 : 0u);
+        if constexpr (GATHER) {
+            wb = words_of(p.X + src.k0 * 2, (uint32_t)p.T * (uint32_t)ldb - src.k0 * 2);
+            const int b = lk >> 3;
+            if ((lk & 7) == 0 && 8 * (b + 1) < src.nk) batch(src, b + 1, 2 + ((b + 1) & 1));
+            const uint32_t *ix = rowbuf + c.w * 256 + (b == 0 ? odd : 2 + (b & 1)) * 64 + (lk & 7) * 8;
 #pragma unroll
-            for (int i = 0; i < 8; ++i) {
-                const int v = rows[min(m + i, p.M - 1)];
-                idx[i] = m + i < r.hi ? v : -1;
+            for (int q = 0; q < 2; ++q) {
+                const int i = q * 4 + (c.lane >> 4);
+                const uint32_t row = ix[i];
+                boff[q] = c.w * 8 + i < left && row < (uint32_t)p.T ? row * (uint32_t)ldb + lb : kRowOOB;
             }
+        } else {
+            wb = words_of(p.X + (int64_t)m0 * ldb + src.k0 * 2, left > 0 ? (uint32_t)left * (uint32_t)ldb - src.k0 * 2 : 0u);
         }
     };
     auto load = [&](int part, int slot) {
-        const int m0 = src.lo + lk * 64, left = min(64, src.hi - m0);       // rows of the stage
         const bool a = part == kALo || part == kAHi;
-        const int col = (part == kAHi || part == kBHi ? 256 : 0);
-        const int ld = a ? lda : ldb, c0 = (a ? src.n0 : src.k0) * 2;
-        const uint8_t *base = (a ? p.dY : p.X) + c0 + (GATHER && !a ? 0 : (int64_t)m0 * ld);
-        const uint32_t bytes = GATHER && !a ? (uint32_t)p.T * (uint32_t)ld - c0
-                                            : left > 0 ? (uint32_t)left * (uint32_t)ld - c0 : 0u;
-        const i32x4 r = words_of(base, bytes);
+        const int col = part == kAHi || part == kBHi ? 256 : 0;
 #pragma unroll
         for (int q = 0; q < 2; ++q) {
             const int L = c.w * 2 + q;
-            uint8_t *dst = lds + slot * kSlot + part * kPart + L * 1024;
-            if (GATHER && !a) {
-                if (part == kBLo) {
-                    const int l4 = c.lane >> 4;
-                    const int lo = l4 & 1 ? idx[4 * q + 1] : idx[4 * q], hi = l4 & 1 ? idx[4 * q + 3] : idx[4 * q + 2];
-                    const uint32_t row = (uint32_t)(l4 & 2 ? hi : lo);
-                    boff[q] = row < (uint32_t)p.T ? row * (uint32_t)ldb + lb : kRowOOB;
-                }
-                dma<16>(r, dst, boff[q] + col);
-            } else {
-                dma<16>(r, dst, (a ? la : lb) + (uint32_t)(L * 4) * (uint32_t)ld + col);
-            }
+            const uint32_t dst = slot * kSlot + part * kPart + L * 1024;
+            if (a) dma<16>(wa, lds, dst, la + (uint32_t)(L * 4 * lda + col));
+            else if (GATHER) dma<16>(wb, lds, dst, boff[q] + col);
+            else dma<16>(wb, lds, dst, lb + (uint32_t)(L * 4 * ldb + col));
         }
     };
 
-    fetch(src, 0);
-    load(kALo, 0);
-    load(kBLo, 0);
-    load(kBHi, 0);
-    load(kAHi, 0);
-    ++lk;
-    fetch(src, 1);
-    load(kALo, 1);
-    load(kBLo, 1);
-    load(kBHi, 1);
+    batch(cur, 0, 0);
+    asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+    for (lk = 0; lk < 2; ++lk) {
+        aim();
+        load(kBLo, lk);
+        load(kALo, lk);
+        load(kBHi, lk);
+        load(kAHi, lk);
+    }
+    lk = 1;
     uint32_t fa = part_base<true>(c, c.wm), fb = part_base<true>(c, c.wn);
     uint8_t *buf = lds + kStage + c.w * 2048;
     turn_end<kInFlight>();
+    bf16x8 b0[4], b0n[4];
+#pragma unroll
+    for (int kk = 0; kk < 4; ++kk) b0[kk] = part_frag<true>(lds, fb + kBLo * kPart, kk, 0);
+    turn_end<kInFlight>();
 
-    int slot = 0, stored = 0;
+    int slot = 0, stored = 0, parity = 0;
     for (;;) {
         tile += nwg;
         next = find(tile);
@@ -950,23 +947,33 @@ __global__ __launch_bounds__(512, 1) void moe_dw(MoeGemmDw p)
 #pragma unroll
         for (int i = 0; i < 4; ++i) acc[i][0] = acc[i][1] = f32x16{};
         if (c.w >= 4) asm volatile("s_barrier" ::: "memory");      // one turn behind
-        for (int s = 0; s < cur.nk; ++s) {
+        auto stage = [&](int s, bf16x8 (&now)[4], bf16x8 (&then)[4]) {
             asm volatile("" : "+v"(la), "+v"(lb), "+v"(fa), "+v"(fb));
             core_stage<true, true, 2, 2>(
-                acc, lds, fa, fb, slot, s == 0 ? stored : 0,
-                [&](int part) { load(part, part == kAHi ? slot ^ 1 : slot); },
+                acc, now, then, lds, fa, fb, slot, s == 0 ? stored : 0, [&](int part) { load(part, slot); },
                 [&] {
+                    if (s == 0) batch(next, 0, parity ^ 1);
                     if (++lk == src.nk) {
+                        // (from its fourth stage on a tile knows them landed)
+                        if (GATHER && cur.nk < 4) asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
                         lk = 0;
                         src = next;
+                        odd = parity ^ 1;
                     }
-                },
-                [&] {
-                    if (lk + 1 < src.nk) fetch(src, lk + 1);
-                    else fetch(next, 0);
+                    aim();
                 },
                 std::integral_constant<int, kStores>{});
             slot ^= 1;
+        };
+        int s = 0;
+        for (; s + 1 < cur.nk; s += 2) {
+            stage(s, b0, b0n);
+            stage(s + 1, b0n, b0);
+        }
+        if (s < cur.nk) {
+            stage(s, b0, b0n);
+#pragma unroll
+            for (int kk = 0; kk < 4; ++kk) b0[kk] = b0n[kk];
         }
         if (c.w < 4) asm volatile("s_barrier" ::: "memory");
         DBS_FENCE();
@@ -1001,6 +1008,7 @@ __global__ __launch_bounds__(512, 1) void moe_dw(MoeGemmDw p)
         stored = !p.accumulate;
         if (tile >= ntiles) break;
         cur = next;
+        parity ^= 1;
     }
     asm volatile("s_waitcnt vmcnt(0)" ::: "memory");   // nothing is left to land in LDS
 }
