@@ -245,10 +245,10 @@ __device__ __forceinline__ int first_tile()
 // --------------------------------------------------- the 256 x 256 x 64 core
 
 // 256 x 256 output tiles over stages of 64, 8 waves (2 x 4, two per SIMD),
-// each owning 128 x 64 as 4 x 2 blocks of 32 x 32.  A stage is four parts of
+// each owning 128 x 64.  A stage is four parts of
 // 16 KiB -- A's rows (or columns) 0 .. 127 and 128 .. 255, B's likewise -- in
-// one of two LDS slots, and is computed as four quadrants of 2 x 1 blocks.  A
-// wave reads one part whole, all four k-steps, into registers per quadrant,
+// one of two LDS slots, and is computed as four quadrants of 64 x 32.  A
+// wave reads one part whole into registers per quadrant,
 // so the part's place in the slot is free again at once, and its refill for
 // the stage after next starts a turn later: loads get six turns of the eight
 // that two stages take to land, with two slots.  (Rows that nothing else has
@@ -256,7 +256,7 @@ __device__ __forceinline__ int first_tile()
 // at its end, the same tiles took a quarter longer.)
 //
 // The two waves of a SIMD take turns: while one reads its next part and
-// issues two wave-loads, the other runs eight MFMAs, with a workgroup barrier
+// issues two wave-loads, the other runs its quadrant's MFMAs, a workgroup barrier
 // between turns.  Waves 4 .. 7 start one turn late.
 //
 //   turn   reads              loads issued            MFMAs of the turn after
@@ -273,31 +273,71 @@ enum PartId : int { kALo = 0, kAHi = 1, kBLo = 2, kBHi = 3 };
 constexpr int kStage = 2 * kSlot;              // LDS offset of the waves' output buffers, 2 KiB each
 constexpr int kCoreLds = kStage + 8 * 2048;
 
-// K-major part: 128 rows of 128 bytes; wave-load L (0 .. 15) covers rows 8 L
-// .. 8 L + 7.  MN-major part: 64 K-rows of 128 columns, wave-load L covers
-// K-rows 4 L .. 4 L + 3.  Wave w issues wave-loads 2 w and 2 w + 1.
-using MnPart = Mn<kBF16, 128>;
-static_assert(MnPart::RPL == 4 && MnPart::RPL % MnPart::PERIOD == 0, "one lane offset for every wave-load");
+// K-major part: 128 rows of 128 bytes, chunks swizzled as everywhere (swz);
+// wave-load L (0 .. 15) covers rows 8 L .. 8 L + 7.  MN-major part: 64 K-rows
+// of 128 columns (256 bytes), wave-load L covers K-rows 4 L .. 4 L + 3.  Wave
+// w issues wave-loads 2 w and 2 w + 1.
+//
+// The math is v_mfma_f32_16x16x32_bf16: with random data in the registers it
+// runs at 2.06 PFLOP/s where 32x32x16 runs at 1.82 (both at 2.45 with zeros:
+// it is the power that differs, an accumulator being read and written half
+// as often), and these kernels are bound by the clock that power leaves.  Its
+// lane l holds row (or column) l % 16 and eight K of a 16 x 32 operand block,
+// and of the result, with B's block as the first operand, row l % 16 of A's
+// and columns 4 (l / 16) .. + 3 of B's.  The lane's K are 8 kgroup(l / 16) ..,
+// the same order for A and B: one LDS pass of 16-byte reads takes lanes of
+// groups 0 and 2 (or 1 and 3) together, which then read neighbouring chunks
+// of their rows, apart under the swizzle (chunks two apart were not: half of
+// the LDS cycles were conflicts).
+__device__ __forceinline__ constexpr int kgroup(int g) { return (g >> 1) | (g & 1) << 1; }
 
+constexpr int kMnRow = 256;
+typedef __attribute__((ext_vector_type(4))) float f32x4;
+
+// MN-major swizzle of K-row r, in 16-byte chunks: the transposed reads of 32
+// lanes take 32 bytes of four K-rows of two groups, 8 or 16 K-rows apart: rows
+// 1 apart move by 64 bytes, rows 8 or 16 apart by 32.
+__device__ __forceinline__ constexpr int mn_swz(int r) { return 4 * (r & 3) ^ 2 * (((r >> 3) ^ (r >> 4)) & 1); }
+
+// The lane's byte offset in wave-loads 2 w and 2 w + 1 of an MN-major part
+// whose K-rows lie ld bytes apart in memory (8 w .. 8 w + 7 share the bits above 2).
+__device__ __forceinline__ uint32_t mn_part_lane(const Lane &c, int ld)
+{
+    const int r = c.lane >> 4;
+    return (uint32_t)(r * ld + (((c.lane & 15) ^ mn_swz(8 * c.w + r)) << 4));
+}
+
+// The lane's address of operand block 0, k-step 0 of a part: rows (columns)
+// 32 block0 .. + 15.
 template <bool MN>
 __device__ __forceinline__ uint32_t part_base(const Lane &c, int block0)
 {
+    const int j = c.lane & 15, g = c.lane >> 4;
     if constexpr (MN) {
-        return mn_base<kBF16, 128>(c.lane, 32 * block0, 0);
+        // transposed reads: lane j of a group addresses K-row j / 4 of four at columns 4 (j % 4) ..
+        const int r = 8 * kgroup(g) + (j >> 2);
+        return (uint32_t)(r * kMnRow + ((64 * block0 + 8 * (j & 3)) ^ (mn_swz(r) << 4)));
     } else {
-        const int r = 32 * block0 + c.lr;
-        return (uint32_t)(r * kRowBytes + ((c.h ^ swz(r)) << 4));
+        const int r = 32 * block0 + j;
+        return (uint32_t)(r * kRowBytes + ((kgroup(g) ^ swz(r)) << 4));
     }
 }
 
-// k-step kk of block i of a part (blocks of one wave lie 64 rows or columns apart)
+// k-step kk (32 of the summed axis) of rows (columns) 64 i + 16 u .. + 15 from
+// the lane's base on
 template <bool MN>
-__device__ __forceinline__ bf16x8 part_frag(const uint8_t *lds, uint32_t base, int kk, int i)
+__device__ __forceinline__ bf16x8 part_frag(const uint8_t *lds, uint32_t base, int kk, int i, int u)
 {
-    if constexpr (MN)
-        return read_frag_mn<kBF16, 128>(lds, base, 0, kk, 2 * i);
-    else
-        return lds_read<bf16x8>(lds, (base ^ (uint32_t)(kk << 5)) + (uint32_t)(64 * kRowBytes * i));
+    if constexpr (MN) {
+        typedef __attribute__((address_space(3))) i16x4 lds_i16x4;
+        const uint8_t *x = lds + (base ^ (uint32_t)(128 * i + 32 * u)) + kk * 32 * kMnRow;
+        const i32x2 lo = __builtin_bit_cast(i32x2, __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_i16x4 *)x));
+        const i32x2 hi = __builtin_bit_cast(i32x2, __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_i16x4 *)(x + 4 * kMnRow)));
+        return __builtin_bit_cast(bf16x8, i32x4{lo[0], lo[1], hi[0], hi[1]});
+    } else {
+        // (16 rows further down bit 1 of the swizzle changes)
+        return lds_read<bf16x8>(lds, (base ^ (uint32_t)((kk << 6) ^ (u << 5))) + (uint32_t)((64 * i + 16 * u) * kRowBytes));
+    }
 }
 
 template <int N>
@@ -316,6 +356,19 @@ __device__ __forceinline__ void turn_end_math()
     DBS_FENCE();
 }
 
+// A wave's results: 16 x 16 blocks [rows 64 (i / 4) + 32 (i / 2 % 2) .. of the
+// wave's 128, 16 (i % 2) further down][columns 16 (j % 2) of part j / 2].
+typedef f32x4 Acc[8][4];
+
+template <bool BMN>
+__device__ __forceinline__ void read_b(bf16x8 (&b)[4], const uint8_t *lds, uint32_t base)
+{
+#pragma unroll
+    for (int kk = 0; kk < 2; ++kk)
+#pragma unroll
+        for (int u = 0; u < 2; ++u) b[2 * kk + u] = part_frag<BMN>(lds, base, kk, 0, u);
+}
+
 // One stage out of slot `slot`; b0 holds its B lo, b0n takes the next stage's.
 // NLO, NHI: blocks per wave in the two halves of A (fewer than 2 where a group
 // ends).  advance() moves the loads on to the next stage, load(part) issues
@@ -323,72 +376,90 @@ __device__ __forceinline__ void turn_end_math()
 // results went out between the loads awaited here and now, and may still be
 // under way.
 template <bool AMN, bool BMN, int NLO, int NHI, class LOAD, class ADVANCE, int STORES>
-__device__ __forceinline__ void core_stage(f32x16 (&acc)[4][2], bf16x8 (&b0)[4], bf16x8 (&b0n)[4], const uint8_t *lds,
+__device__ __forceinline__ void core_stage(Acc &acc, bf16x8 (&b0)[4], bf16x8 (&b0n)[4], const uint8_t *lds,
                                            uint32_t fa, uint32_t fb, int slot, int extra, LOAD &&load,
                                            ADVANCE &&advance, std::integral_constant<int, STORES>)
 {
-    bf16x8 a[2][4], b1[4];
+    bf16x8 a[4][2], b1[4];                 // b: [2 kk + u]
     const uint32_t so = (uint32_t)(slot * kSlot), sn = so ^ kSlot;
     auto wait = [&] {
         if (extra) turn_end<kInFlight + STORES>();
         else turn_end<kInFlight>();
     };
-    auto math = [&](int i0, int j, int n, const bf16x8 (&b)[4]) {
+    auto read_a = [&](int part, int n) {
+#pragma unroll
+        for (int kk = 0; kk < 2; ++kk)
+#pragma unroll
+            for (int i = 0; i < 2 * n; ++i) a[i][kk] = part_frag<AMN>(lds, fa + so + part * kPart, kk, i >> 1, i & 1);
+    };
+    auto math = [&](int half, int j, int n, const bf16x8 (&b)[4]) {
         __builtin_amdgcn_s_setprio(1);
 #pragma unroll
-        for (int kk = 0; kk < 4; ++kk)
+        for (int kk = 0; kk < 2; ++kk)
 #pragma unroll
-            for (int i = 0; i < n; ++i) mma1<kBF16, 0>(acc[i0 + i][j], a[i][kk], 0u, b[kk], 0u);
+            for (int i = 0; i < 2 * n; ++i)
+#pragma unroll
+                for (int u = 0; u < 2; ++u)
+                    acc[4 * half + i][2 * j + u] =
+                        __builtin_amdgcn_mfma_f32_16x16x32_bf16(b[2 * kk + u], a[i][kk], acc[4 * half + i][2 * j + u], 0, 0, 0);
         turn_end_math();
     };
     // turn 0
     advance();
-#pragma unroll
-    for (int kk = 0; kk < 4; ++kk)
-#pragma unroll
-        for (int i = 0; i < NLO; ++i) a[i][kk] = part_frag<AMN>(lds, fa + so + kALo * kPart, kk, i);
+    read_a(kALo, NLO);
     load(kBLo);
     wait();
     math(0, 0, NLO, b0);
     // turn 1
-#pragma unroll
-    for (int kk = 0; kk < 4; ++kk) b1[kk] = part_frag<BMN>(lds, fb + so + kBHi * kPart, kk, 0);
+    read_b<BMN>(b1, lds, fb + so + kBHi * kPart);
     load(kALo);
     wait();
     math(0, 1, NLO, b1);
     // turn 2
-#pragma unroll
-    for (int kk = 0; kk < 4; ++kk)
-#pragma unroll
-        for (int i = 0; i < NHI; ++i) a[i][kk] = part_frag<AMN>(lds, fa + so + kAHi * kPart, kk, i);
+    read_a(kAHi, NHI);
     load(kBHi);
     wait();
-    math(2, 1, NHI, b1);
+    math(1, 1, NHI, b1);
     // turn 3
-#pragma unroll
-    for (int kk = 0; kk < 4; ++kk) b0n[kk] = part_frag<BMN>(lds, fb + sn + kBLo * kPart, kk, 0);
+    read_b<BMN>(b0n, lds, fb + sn + kBLo * kPart);
     load(kAHi);
     wait();
-    math(2, 0, NHI, b0);
+    math(1, 0, NHI, b0);
 }
 
-// One 32 x 32 block of results as bf16 rows r0 .. mend-1, columns n .. ncols-1
-// of D, through the wave's 2 KiB buffer (vec) or by element.
-template <class VALUE>
+// One 32 x 32 block of results as bf16 rows r0 .. mend-1, columns n0 ..
+// ncols-1 of D (ld columns), through the wave's 2 KiB buffer and in 16-byte
+// pieces (vec) or by element.  B16: the results of 16 x 16 blocks (value(u, v,
+// q): row block u, column block v, register q), otherwise of one 32 x 32
+// MFMA block (value(0, 0, q)).
+template <bool B16, class VALUE>
 __device__ __forceinline__ void store_block(uint8_t *buf, uint8_t *D, int64_t ld, int r0, int mend, int n0, int ncols,
                                             int vec, Lane c, VALUE &&value)
 {
     // (addresses are made here, not before the tile's stages, whose registers they would take)
     asm volatile("" : "+v"(c.lane));
-    c.lr = c.lane & 31;
-    c.h = c.lane >> 5;
     const int left = __builtin_amdgcn_readfirstlane(max(0, min(32, mend - r0)));
     const __amdgpu_buffer_rsrc_t rd = make_rsrc(D + (int64_t)r0 * ld * 2, (uint32_t)left * (uint32_t)ld * 2u);
+    // four values of consecutive columns: group g of four, at row and column
+    auto quad = [&](int g, int &row, int &col, float (&v)[4]) {
+        if constexpr (B16) {
+            row = 16 * (g >> 1) + (c.lane & 15);
+            col = 16 * (g & 1) + 4 * (c.lane >> 4);
+        } else {
+            row = c.lane & 31;
+            col = 8 * g + 4 * (c.lane >> 5);
+        }
+#pragma unroll
+        for (int q = 0; q < 4; ++q) v[q] = B16 ? value(g >> 1, g & 1, q) : value(0, 0, 4 * g + q);
+    };
     if (vec) {
 #pragma unroll
         for (int g = 0; g < 4; ++g) {
-            const uint32_t lo = pack_bf16(value(4 * g), value(4 * g + 1)), hi = pack_bf16(value(4 * g + 2), value(4 * g + 3));
-            *reinterpret_cast<u32x2 *>(buf + c.lr * 64 + 16 * (g ^ ((c.lr >> 1) & 3)) + 8 * c.h) = u32x2{lo, hi};
+            int row, col;
+            float v[4];
+            quad(g, row, col, v);
+            *reinterpret_cast<u32x2 *>(buf + row * 64 + (((col >> 3) ^ ((row >> 1) & 3)) << 4) + 2 * (col & 4)) =
+                u32x2{pack_bf16(v[0], v[1]), pack_bf16(v[2], v[3])};
         }
 #pragma unroll
         for (int q = 0; q < 2; ++q) {
@@ -398,10 +469,16 @@ __device__ __forceinline__ void store_block(uint8_t *buf, uint8_t *D, int64_t ld
         }
     } else {
 #pragma unroll
-        for (int q = 0; q < 16; ++q) {
-            const int n = n0 + (q / 4) * 8 + c.h * 4 + q % 4;
-            __builtin_amdgcn_raw_buffer_store_b16((uint16_t)pack_bf16(value(q), 0.0f), rd,
-                                                  n < ncols ? (uint32_t)(c.lr * (int)ld + n) * 2u : kOOB, 0, kStoreNT);
+        for (int g = 0; g < 4; ++g) {
+            int row, col;
+            float v[4];
+            quad(g, row, col, v);
+#pragma unroll
+            for (int q = 0; q < 4; ++q) {
+                const int n = n0 + col + q;
+                __builtin_amdgcn_raw_buffer_store_b16((uint16_t)pack_bf16(v[q], 0.0f), rd,
+                                                      n < ncols ? (uint32_t)(row * (int)ld + n) * 2u : kOOB, 0, kStoreNT);
+            }
         }
     }
 }
@@ -533,7 +610,7 @@ __global__ __launch_bounds__(512, 1) void moe_tiles_256(MoeGemm p)
     uint32_t aoff[4];                     // the lane's row offsets in ra: A lo's two wave-loads, A hi's
     int f0 = 0, lk = 0;
     uint32_t x4 = (uint32_t)(((c.lane & 7) ^ (c.lane >> 3)) << 4);
-    uint32_t lb = BMN ? mn_dma_lane<kBF16, 128>(c.lane, 0, ldb) : (uint32_t)((c.lane >> 3) * ldb);
+    uint32_t lb = BMN ? mn_part_lane(c, ldb) : (uint32_t)((c.lane >> 3) * ldb);
     // Row indices of the tile `r` on their way into rowbuf (lanes past the
     // group's end load zeros, which aim does not use)
     auto fetch = [&](const RowTile &r) {
@@ -609,16 +686,17 @@ __global__ __launch_bounds__(512, 1) void moe_tiles_256(MoeGemm p)
     uint8_t *buf = lds + kStage + c.w * 2048;
     turn_end<kInFlight>();
     bf16x8 b0[4], b0n[4];
-#pragma unroll
-    for (int kk = 0; kk < 4; ++kk) b0[kk] = part_frag<BMN>(lds, fb + kBLo * kPart, kk, 0);
+    read_b<BMN>(b0, lds, fb + kBLo * kPart);
     turn_end<kInFlight>();
 
     int slot = 0, round = 0, stored = 0;
     auto run = [&](auto nlo, auto nhi) {
         constexpr int NLO = decltype(nlo)::value, NHI = decltype(nhi)::value;
-        f32x16 acc[4][2];
+        Acc acc;
 #pragma unroll
-        for (int i = 0; i < 4; ++i) acc[i][0] = acc[i][1] = f32x16{};
+        for (int i = 0; i < 8; ++i)
+#pragma unroll
+            for (int j = 0; j < 4; ++j) acc[i][j] = f32x4{};
         if (c.w >= 4) asm volatile("s_barrier" ::: "memory");      // one turn behind
         auto stage = [&](int s, bf16x8 (&now)[4], bf16x8 (&then)[4]) {
             asm volatile("" : "+v"(x4), "+v"(lb), "+v"(fa), "+v"(fb));
@@ -638,18 +716,18 @@ __global__ __launch_bounds__(512, 1) void moe_tiles_256(MoeGemm p)
         }
         if (c.w < 4) asm volatile("s_barrier" ::: "memory");
         DBS_FENCE();
-        asm volatile("" : "+v"(c.lane));
 #pragma unroll
         for (int i = 0; i < NLO + NHI; ++i) {
             const int r0 = cur.m0 + (2 * i + c.wm) * 32;
             if constexpr (GATE) {
-                store_block(buf, p.D, p.ncols, r0, cur.mend, cur.n0 + c.wn * 32, p.ncols, p.vec, c,
-                            [&](int q) { return gated(acc[i][0][q], acc[i][1][q]); });
+                store_block<true>(buf, p.D, p.ncols, r0, cur.mend, cur.n0 + c.wn * 32, p.ncols, p.vec, c,
+                            [&](int u, int v, int q) { return gated(acc[2 * i + u][v][q], acc[2 * i + u][2 + v][q]); });
             } else {
 #pragma unroll
                 for (int j = 0; j < 2; ++j)
-                    store_block(buf, p.D, p.ncols, r0, cur.mend, cur.n0 + (BMN ? j * 128 + c.wn * 32 : c.wn * 64 + j * 32),
-                                p.ncols, p.vec, c, [&](int q) { return acc[i][j][q]; });
+                    store_block<true>(buf, p.D, p.ncols, r0, cur.mend, cur.n0 + (BMN ? j * 128 + c.wn * 32 : c.wn * 64 + j * 32),
+                                p.ncols, p.vec, c,
+                                      [&](int u, int v, int q) { return acc[2 * i + u][2 * j + v][q]; });
             }
         }
         stored = p.vec && NLO + NHI == 4;
@@ -812,13 +890,13 @@ __global__ __launch_bounds__(512, 1) void moe_tiles_64(MoeGemm p)
         for (int i = 0; i < MB; ++i) {
             const int r0 = cur.m0 + (2 * i + c.wm) * 32;
             if constexpr (GATE) {
-                store_block(buf, p.D, p.ncols, r0, cur.mend, cur.n0 + c.wn * 32, p.ncols, p.vec, c,
-                            [&](int q) { return gated(acc[i][0][q], acc[i][1][q]); });
+                store_block<false>(buf, p.D, p.ncols, r0, cur.mend, cur.n0 + c.wn * 32, p.ncols, p.vec, c,
+                            [&](int, int, int q) { return gated(acc[i][0][q], acc[i][1][q]); });
             } else {
 #pragma unroll
                 for (int j = 0; j < NB; ++j)
-                    store_block(buf, p.D, p.ncols, r0, cur.mend, cur.n0 + c.wn * 64 + j * 32, p.ncols, p.vec, c,
-                                [&](int q) { return acc[i][j][q]; });
+                    store_block<false>(buf, p.D, p.ncols, r0, cur.mend, cur.n0 + c.wn * 64 + j * 32, p.ncols, p.vec, c,
+                                [&](int, int, int q) { return acc[i][j][q]; });
             }
         }
         asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory");
@@ -879,8 +957,8 @@ __global__ __launch_bounds__(512, 1) void moe_dw(MoeGemmDw p)
     Ref src = cur;
     int lk = 0, left = 0, odd = 0;                     // rows of the stage; parity of src
     i32x4 wa, wb;
-    uint32_t la = mn_dma_lane<kBF16, 128>(c.lane, 0, lda);
-    uint32_t lb = mn_dma_lane<kBF16, 128>(c.lane, 0, GATHER ? 0 : ldb);
+    uint32_t la = mn_part_lane(c, lda);
+    uint32_t lb = mn_part_lane(c, GATHER ? 0 : ldb);
     uint32_t boff[2] = {};                             // gathered: the lane's offsets of its two wave-loads
     const i32x4 wr = words_of(p.rows, GATHER ? (uint32_t)p.M * 4u : 0u);
     auto batch = [&](const Ref &r, int b, int buffer) {
@@ -935,17 +1013,18 @@ __global__ __launch_bounds__(512, 1) void moe_dw(MoeGemmDw p)
     uint8_t *buf = lds + kStage + c.w * 2048;
     turn_end<kInFlight>();
     bf16x8 b0[4], b0n[4];
-#pragma unroll
-    for (int kk = 0; kk < 4; ++kk) b0[kk] = part_frag<true>(lds, fb + kBLo * kPart, kk, 0);
+    read_b<true>(b0, lds, fb + kBLo * kPart);
     turn_end<kInFlight>();
 
     int slot = 0, stored = 0, parity = 0;
     for (;;) {
         tile += nwg;
         next = find(tile);
-        f32x16 acc[4][2];
+        Acc acc;
 #pragma unroll
-        for (int i = 0; i < 4; ++i) acc[i][0] = acc[i][1] = f32x16{};
+        for (int i = 0; i < 8; ++i)
+#pragma unroll
+            for (int j = 0; j < 4; ++j) acc[i][j] = f32x4{};
         if (c.w >= 4) asm volatile("s_barrier" ::: "memory");      // one turn behind
         auto stage = [&](int s, bf16x8 (&now)[4], bf16x8 (&then)[4]) {
             asm volatile("" : "+v"(la), "+v"(lb), "+v"(fa), "+v"(fb));
@@ -984,24 +1063,23 @@ __global__ __launch_bounds__(512, 1) void moe_dw(MoeGemmDw p)
             for (int j = 0; j < 2; ++j) {
                 const int k0 = cur.k0 + j * 128 + c.wn * 32;
                 if constexpr (F32) {
-                    // four consecutive columns a lane and group of four registers
-                    typedef __attribute__((ext_vector_type(4))) float f32x4;
+                    // four consecutive columns a lane and 16 x 16 block
                     const int left = __builtin_amdgcn_readfirstlane(max(0, min(32, p.N - r0)));
                     const __amdgpu_buffer_rsrc_t rd = make_rsrc(p.dW + ((int64_t)cur.g * p.N + r0) * p.K * 4,
                                                                 (uint32_t)left * (uint32_t)p.K * 4u);
 #pragma unroll
                     for (int g = 0; g < 4; ++g) {
-                        const int k = k0 + g * 8 + c.h * 4;
-                        const uint32_t off = k < p.K ? (uint32_t)(c.lr * p.K + k) * 4u : kOOB;   // K % 8 == 0
-                        const f32x16 &v16 = acc[i][j];
-                        f32x4 v = {v16[4 * g], v16[4 * g + 1], v16[4 * g + 2], v16[4 * g + 3]};
+                        const int u = g >> 1, w = g & 1, k = k0 + 16 * w + 4 * (c.lane >> 4);
+                        const uint32_t off =
+                            k < p.K ? (uint32_t)((16 * u + (c.lane & 15)) * p.K + k) * 4u : kOOB;   // K % 8 == 0
+                        f32x4 v = acc[2 * i + u][2 * j + w];
                         if (p.accumulate)
                             v += __builtin_bit_cast(f32x4, __builtin_amdgcn_raw_buffer_load_b128(rd, off, 0, 0));
                         __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(i32x4, v), rd, off, 0, kStoreNT);
                     }
                 } else {
-                    store_block(buf, p.dW + (int64_t)cur.g * p.N * p.K * 2, p.K, r0, p.N, k0, p.K, 1, c,
-                                [&](int q) { return acc[i][j][q]; });
+                    store_block<true>(buf, p.dW + (int64_t)cur.g * p.N * p.K * 2, p.K, r0, p.N, k0, p.K, 1, c,
+                                [&](int u, int v, int q) { return acc[2 * i + u][2 * j + v][q]; });
                 }
             }
         }
