@@ -268,7 +268,7 @@ __device__ __forceinline__ int first_tile()
 // At the end of every turn a wave waits for its loads of the part read in the
 // turn after: kInFlight newer wave-loads may be under way by then.  Its own
 // reads are complete before the barrier that lets others refill their place.
-constexpr int kPart = 128 * kRowBytes, kSlot = 4 * kPart, kInFlight = 12;
+constexpr int kPart = 128 * kRowBytes, kSlot = 4 * kPart, kInFlight = 8;
 enum PartId : int { kALo = 0, kAHi = 1, kBLo = 2, kBHi = 3 };
 constexpr int kStage = 2 * kSlot;              // LDS offset of the waves' output buffers, 2 KiB each
 constexpr int kCoreLds = kStage + 8 * 2048;
@@ -369,19 +369,17 @@ __device__ __forceinline__ void read_b(bf16x8 (&b)[4], const uint8_t *lds, uint3
         for (int u = 0; u < 2; ++u) b[2 * kk + u] = part_frag<BMN>(lds, base, kk, 0, u);
 }
 
-// One stage out of slot `slot`; b0 holds its B lo, b0n takes the next stage's.
-// NLO, NHI: blocks per wave in the two halves of A (fewer than 2 where a group
-// ends).  advance() moves the loads on to the next stage, load(part) issues
-// the two wave-loads of a part of it.  extra: STORES stores of the last tile's
-// results went out between the loads awaited here and now, and may still be
-// under way.
+// One stage out of slot `slot`.  NLO, NHI: blocks per wave in the two halves
+// of A (fewer than 2 where a group ends).  advance() moves the loads on to the
+// next stage, load(part, slot) issues the two wave-loads of a part of it.
+// extra: STORES stores of the last tile's results went out between the loads
+// awaited here and now, and may still be under way.
 template <bool AMN, bool BMN, int NLO, int NHI, class LOAD, class ADVANCE, int STORES>
-__device__ __forceinline__ void core_stage(Acc &acc, bf16x8 (&b0)[4], bf16x8 (&b0n)[4], const uint8_t *lds,
-                                           uint32_t fa, uint32_t fb, int slot, int extra, LOAD &&load,
-                                           ADVANCE &&advance, std::integral_constant<int, STORES>)
+__device__ __forceinline__ void core_stage(Acc &acc, const uint8_t *lds, uint32_t fa, uint32_t fb, int slot, int extra,
+                                           LOAD &&load, ADVANCE &&advance, std::integral_constant<int, STORES>)
 {
-    bf16x8 a[4][2], b1[4];                 // b: [2 kk + u]
-    const uint32_t so = (uint32_t)(slot * kSlot), sn = so ^ kSlot;
+    bf16x8 a[4][2], b0[4], b1[4];          // b: [2 kk + u]
+    const uint32_t so = (uint32_t)(slot * kSlot);
     auto wait = [&] {
         if (extra) turn_end<kInFlight + STORES>();
         else turn_end<kInFlight>();
@@ -393,7 +391,6 @@ __device__ __forceinline__ void core_stage(Acc &acc, bf16x8 (&b0)[4], bf16x8 (&b
             for (int i = 0; i < 2 * n; ++i) a[i][kk] = part_frag<AMN>(lds, fa + so + part * kPart, kk, i >> 1, i & 1);
     };
     auto math = [&](int half, int j, int n, const bf16x8 (&b)[4]) {
-        __builtin_amdgcn_s_setprio(1);
 #pragma unroll
         for (int kk = 0; kk < 2; ++kk)
 #pragma unroll
@@ -402,29 +399,28 @@ __device__ __forceinline__ void core_stage(Acc &acc, bf16x8 (&b0)[4], bf16x8 (&b
                 for (int u = 0; u < 2; ++u)
                     acc[4 * half + i][2 * j + u] =
                         __builtin_amdgcn_mfma_f32_16x16x32_bf16(b[2 * kk + u], a[i][kk], acc[4 * half + i][2 * j + u], 0, 0, 0);
-        turn_end_math();
     };
     // turn 0
-    advance();
     read_a(kALo, NLO);
-    load(kBLo);
-    wait();
-    math(0, 0, NLO, b0);
-    // turn 1
+    read_b<BMN>(b0, lds, fb + so + kBLo * kPart);
     read_b<BMN>(b1, lds, fb + so + kBHi * kPart);
-    load(kALo);
+    load(kAHi, slot ^ 1);
     wait();
+    __builtin_amdgcn_s_setprio(1);
+    math(0, 0, NLO, b0);
     math(0, 1, NLO, b1);
-    // turn 2
+    turn_end_math();
+    // turn 1
     read_a(kAHi, NHI);
-    load(kBHi);
+    advance();
+    load(kALo, slot);
+    load(kBLo, slot);
+    load(kBHi, slot);
     wait();
+    __builtin_amdgcn_s_setprio(1);
     math(1, 1, NHI, b1);
-    // turn 3
-    read_b<BMN>(b0n, lds, fb + sn + kBLo * kPart);
-    load(kAHi);
-    wait();
     math(1, 0, NHI, b0);
+    turn_end_math();
 }
 
 // One 32 x 32 block of results as bf16 rows r0 .. mend-1, columns n0 ..
@@ -497,6 +493,8 @@ struct Table {
     uint16_t rest[kRests > 0 ? kRests : 1][kMoeMaxExperts + 1];     // rests of b + 1 blocks before a group
 };
 
+constexpr int kBand = 4;              // tile rows of a group handed out together
+
 struct RowTile {
     int m0, mend, n0, g, blocks;      // blocks 0: nothing
 };
@@ -536,9 +534,12 @@ __device__ __forceinline__ RowTile find_tile(const Table<TM> &tab, int E, int nt
         r.g = group_of(tab.whole, E, id / tiles_n, c);
         const int before = __builtin_amdgcn_readfirstlane(tab.whole[r.g]);
         const int n = __builtin_amdgcn_readfirstlane(tab.whole[r.g + 1]) - before;
-        const int local = id - before * tiles_n;   // tile rows fastest: they share W's rows
-        r.m0 = local % n * TM;
-        r.n0 = local / n * tno;
+        // bands of kBand tile rows, columns outside them: the tiles that one
+        // XCD's workgroups hold together share rows of X and of W in its L2
+        const int local = id - before * tiles_n, band = local / (kBand * tiles_n);
+        const int rows = min(n - band * kBand, kBand), in = local - band * kBand * tiles_n;
+        r.m0 = (band * kBand + in % rows) * TM;
+        r.n0 = in / rows * tno;
         r.blocks = MB;
     } else {
         id -= whole;
@@ -597,10 +598,9 @@ __global__ __launch_bounds__(512, 1) void moe_tiles_256(MoeGemm p)
     const int ntiles = count_tiles(tab, p.E, tiles_n);
     const int nwg = gridDim.x, self = first_tile();
     if (self >= ntiles) return;
-    // an even number of stages, at least four (the surplus reads zeros): the
-    // stages' B lo registers change places, and the next tile's row indices
-    // land within a tile (see rowbuf)
-    const int nk = max((p.K + 127) / 128 * 2, 4);
+    // at least three stages (the surplus reads zeros): the next tile's row
+    // indices land within a tile (see rowbuf)
+    const int nk = max((p.K + 63) / 64, 3);
     auto find = [&](int round) {
         return find_tile(tab, p.E, ntiles, tiles_n, TNO, round * nwg + (round & 1 ? nwg - 1 - self : self), c);
     };
@@ -674,19 +674,16 @@ __global__ __launch_bounds__(512, 1) void moe_tiles_256(MoeGemm p)
     fetch(cur);
     turn_end<0>();
     aim(cur);
-#pragma unroll
-    for (lk = 0; lk < 2; ++lk) {
-        load(kBLo, lk);
-        load(kALo, lk);
-        load(kBHi, lk);
-        load(kAHi, lk);
-    }
+    load(kALo, 0);
+    load(kBLo, 0);
+    load(kBHi, 0);
+    load(kAHi, 0);
     lk = 1;
+    load(kALo, 1);
+    load(kBLo, 1);
+    load(kBHi, 1);
     uint32_t fa = part_base<false>(c, c.wm), fb = part_base<BMN>(c, c.wn);
     uint8_t *buf = lds + kStage + c.w * 2048;
-    turn_end<kInFlight>();
-    bf16x8 b0[4], b0n[4];
-    read_b<BMN>(b0, lds, fb + kBLo * kPart);
     turn_end<kInFlight>();
 
     int slot = 0, round = 0, stored = 0;
@@ -698,21 +695,14 @@ __global__ __launch_bounds__(512, 1) void moe_tiles_256(MoeGemm p)
 #pragma unroll
             for (int j = 0; j < 4; ++j) acc[i][j] = f32x4{};
         if (c.w >= 4) asm volatile("s_barrier" ::: "memory");      // one turn behind
-        auto stage = [&](int s, bf16x8 (&now)[4], bf16x8 (&then)[4]) {
+#pragma clang loop unroll(disable)
+        for (int s = 0; s < nk; ++s) {
             asm volatile("" : "+v"(x4), "+v"(lb), "+v"(fa), "+v"(fb));
+            if (s == 0) fetch(next);
             core_stage<false, BMN, NLO, NHI>(
-                acc, now, then, lds, fa, fb, slot, s == 0 ? stored : 0, [&](int part) { load(part, slot); },
-                [&] {
-                    if (s == 0) fetch(next);
-                    if (++lk == nk) aim(next);
-                },
+                acc, lds, fa, fb, slot, s == 0 ? stored : 0, load, [&] { if (++lk == nk) aim(next); },
                 std::integral_constant<int, kStores>{});
             slot ^= 1;
-        };
-#pragma clang loop unroll(disable)
-        for (int s = 0; s < nk; s += 2) {
-            stage(s, b0, b0n);
-            stage(s + 1, b0n, b0);
         }
         if (c.w < 4) asm volatile("s_barrier" ::: "memory");
         DBS_FENCE();
@@ -1001,19 +991,18 @@ __global__ __launch_bounds__(512, 1) void moe_dw(MoeGemmDw p)
 
     batch(cur, 0, 0);
     asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
-    for (lk = 0; lk < 2; ++lk) {
-        aim();
-        load(kBLo, lk);
-        load(kALo, lk);
-        load(kBHi, lk);
-        load(kAHi, lk);
-    }
+    aim();
+    load(kALo, 0);
+    load(kBLo, 0);
+    load(kBHi, 0);
+    load(kAHi, 0);
     lk = 1;
+    aim();
+    load(kALo, 1);
+    load(kBLo, 1);
+    load(kBHi, 1);
     uint32_t fa = part_base<true>(c, c.wm), fb = part_base<true>(c, c.wn);
     uint8_t *buf = lds + kStage + c.w * 2048;
-    turn_end<kInFlight>();
-    bf16x8 b0[4], b0n[4];
-    read_b<true>(b0, lds, fb + kBLo * kPart);
     turn_end<kInFlight>();
 
     int slot = 0, stored = 0, parity = 0;
@@ -1026,15 +1015,16 @@ __global__ __launch_bounds__(512, 1) void moe_dw(MoeGemmDw p)
 #pragma unroll
             for (int j = 0; j < 4; ++j) acc[i][j] = f32x4{};
         if (c.w >= 4) asm volatile("s_barrier" ::: "memory");      // one turn behind
-        auto stage = [&](int s, bf16x8 (&now)[4], bf16x8 (&then)[4]) {
+#pragma clang loop unroll(disable)
+        for (int s = 0; s < cur.nk; ++s) {
             asm volatile("" : "+v"(la), "+v"(lb), "+v"(fa), "+v"(fb));
+            if (s == 0) batch(next, 0, parity ^ 1);
             core_stage<true, true, 2, 2>(
-                acc, now, then, lds, fa, fb, slot, s == 0 ? stored : 0, [&](int part) { load(part, slot); },
+                acc, lds, fa, fb, slot, s == 0 ? stored : 0, load,
                 [&] {
-                    if (s == 0) batch(next, 0, parity ^ 1);
                     if (++lk == src.nk) {
-                        // (from its fourth stage on a tile knows them landed)
-                        if (GATHER && cur.nk < 4) asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+                        // (from its third stage on a tile knows them landed)
+                        if (GATHER && cur.nk < 3) asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
                         lk = 0;
                         src = next;
                         odd = parity ^ 1;
@@ -1043,16 +1033,6 @@ __global__ __launch_bounds__(512, 1) void moe_dw(MoeGemmDw p)
                 },
                 std::integral_constant<int, kStores>{});
             slot ^= 1;
-        };
-        int s = 0;
-        for (; s + 1 < cur.nk; s += 2) {
-            stage(s, b0, b0n);
-            stage(s + 1, b0n, b0);
-        }
-        if (s < cur.nk) {
-            stage(s, b0, b0n);
-#pragma unroll
-            for (int kk = 0; kk < 4; ++kk) b0[kk] = b0n[kk];
         }
         if (c.w < 4) asm volatile("s_barrier" ::: "memory");
         DBS_FENCE();
