@@ -500,35 +500,49 @@ class MoeRouting(NamedTuple):
     slots: torch.Tensor
 
 
-def _ptr(t: torch.Tensor | None):
-    return ctypes.c_void_p(None if t is None else t.data_ptr())
-
-
-def _dims(t: torch.Tensor, name: str, n: int) -> tuple:
+def _dims(t: torch.Tensor, name: str, n: int) -> torch.Size:
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a torch.Tensor")
     if t.dim() != n:
         raise ValueError(f"{name}: {t.dim()} dimensions, expected {n}")
-    return tuple(t.shape)
+    return t.shape
 
 
-def _same_device(first: torch.Tensor, **others) -> None:
-    for name, t in others.items():
-        if t is not None and t.device != first.device:
-            raise ValueError(f"{name} is on {t.device}, expected {first.device}")
+def _arg(t: torch.Tensor, name: str, dtypes, shape, device: torch.device) -> int:
+    """The address of a checked argument (a decoding step makes these calls
+    by the dozen: one pass over what is right, _dev for what is not)."""
+    if isinstance(t, torch.Tensor) and t.dtype in dtypes and t.shape == shape and t.device == device \
+            and device.type == "cuda" and t.is_contiguous():
+        return t.data_ptr()
+    _dev(t, name, dtypes, shape)
+    raise ValueError(f"{name} is on {t.device}, expected {device}")
 
 
-def _on(t: torch.Tensor):
-    """The device of t made current for the call: kernels are launched, and
-    the library asks for its compute units, there."""
-    return torch.cuda.device(t.device)
+def _raw_stream(index: int) -> int:
+    return torch.cuda.current_stream(index).cuda_stream
 
 
-def _given(out: torch.Tensor | None, shape, dtype, like: torch.Tensor) -> torch.Tensor:
+# (the same handle without the Stream object around it: 2 us less a call)
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", _raw_stream)
+
+
+def _call(name: str, device: torch.device, *args) -> None:
+    """Library call on the current stream of the device, with that device
+    current: kernels are launched, and compute units counted, there."""
+    f = getattr(lib(), name)
+    if device.index == torch.cuda.current_device():
+        st = f(*args, _raw_stream(device.index))
+    else:
+        with torch.cuda.device(device):
+            st = f(*args, _raw_stream(device.index))
+    if st:
+        _check(st)
+
+
+def _given(out: torch.Tensor | None, shape, dtype, device: torch.device) -> torch.Tensor:
     if out is None:
-        return torch.empty(shape, dtype=dtype, device=like.device)
-    _dev(out, "out", (dtype,), shape)
-    _same_device(like, out=out)
+        return torch.empty(shape, dtype=dtype, device=device)
+    _arg(out, "out", (dtype,), shape, device)
     return out
 
 
@@ -539,19 +553,20 @@ def moe_route(logits: torch.Tensor, k: int, renormalize: bool = True) -> MoeRout
     Logits of -inf or NaN close an expert to the token; ties go to the lower
     expert."""
     T, E = _dims(logits, "logits", 2)
-    pl = _dev(logits, "logits", tuple(_REAL), (T, E))
     dev = logits.device
-    need = int(lib().moe_route_workspace(T, E, k))
-    i32 = dict(dtype=torch.int32, device=dev)
-    pairs = max(T * k, 0)
-    r = MoeRouting(torch.empty((T, max(k, 0)), **i32), torch.empty((T, max(k, 0)), dtype=torch.float32, device=dev),
-                   torch.empty(E + 1, **i32), torch.empty(pairs, **i32), torch.empty((T, max(k, 0)), **i32))
+    pl = _arg(logits, "logits", _REAL, (T, E), dev)
+    kk = max(int(k), 0)
+    need = int(lib().moe_route_workspace(T, E, kk))
+    experts = torch.empty((T, kk), dtype=torch.int32, device=dev)
+    weights = torch.empty_like(experts, dtype=torch.float32)
+    offsets = torch.empty(E + 1, dtype=torch.int32, device=dev)
+    rows = torch.empty(T * kk, dtype=torch.int32, device=dev)
+    slots = torch.empty_like(experts)
     ws = torch.empty(need, dtype=torch.uint8, device=dev) if need else None
-    with _on(logits):
-        _check(lib().moe_route(_REAL[logits.dtype], pl, T, E, k, int(bool(renormalize)), _ptr(r.experts),
-                               _ptr(r.weights), _ptr(r.offsets), _ptr(r.rows), _ptr(r.slots), _ptr(ws), need,
-                               _stream(logits)))
-    return r
+    _call("moe_route", dev, _REAL[logits.dtype], pl, T, E, int(k), int(bool(renormalize)), experts.data_ptr(),
+          weights.data_ptr(), offsets.data_ptr(), rows.data_ptr(), slots.data_ptr(),
+          None if ws is None else ws.data_ptr(), need)
+    return MoeRouting(experts, weights, offsets, rows, slots)
 
 
 def moe_route_backward(logits: torch.Tensor, experts: torch.Tensor, dweights: torch.Tensor,
@@ -560,28 +575,25 @@ def moe_route_backward(logits: torch.Tensor, experts: torch.Tensor, dweights: to
     experts (T, k) as moe_route gave them, dweights (T, k) fp32."""
     T, E = _dims(logits, "logits", 2)
     k = _dims(experts, "experts", 2)[1]
-    pl = _dev(logits, "logits", tuple(_REAL), (T, E))
-    pe = _dev(experts, "experts", _I32, (T, k))
-    pw = _dev(dweights, "dweights", _F32, (T, k))
-    _same_device(logits, experts=experts, dweights=dweights)
+    dev = logits.device
+    pl = _arg(logits, "logits", _REAL, (T, E), dev)
+    pe = _arg(experts, "experts", _I32, (T, k), dev)
+    pw = _arg(dweights, "dweights", _F32, (T, k), dev)
     out = torch.empty_like(logits)
-    with _on(logits):
-        _check(lib().moe_route_bwd(_REAL[logits.dtype], pl, T, E, k, int(bool(renormalize)), pe, pw, _ptr(out),
-                                   _stream(logits)))
+    _call("moe_route_bwd", dev, _REAL[logits.dtype], pl, T, E, k, int(bool(renormalize)), pe, pw, out.data_ptr())
     return out
 
 
 def _sorted(X, offsets, rows, E):
-    """Checked pointers of X, offsets and rows, with T, M and K."""
+    """Checked addresses of X, offsets and rows, with T, M and K."""
     T, K = _dims(X, "X", 2)
-    px = _dev(X, "X", _BF16, (T, K))
-    po = _dev(offsets, "offsets", _I32, (E + 1,))
-    M, pr = T, ctypes.c_void_p(None)
-    if rows is not None:
-        M = _dims(rows, "rows", 1)[0]
-        pr = _dev(rows, "rows", _I32, (M,))
-    _same_device(X, offsets=offsets, rows=rows)
-    return px, po, pr, T, M, K
+    dev = X.device
+    px = _arg(X, "X", _BF16, (T, K), dev)
+    po = _arg(offsets, "offsets", _I32, (E + 1,), dev)
+    if rows is None:
+        return px, po, None, T, T, K
+    M = _dims(rows, "rows", 1)[0]
+    return px, po, _arg(rows, "rows", _I32, (M,), dev), T, M, K
 
 
 def gemm_moe_bf16(X: torch.Tensor, W: torch.Tensor, offsets: torch.Tensor, rows: torch.Tensor | None = None,
@@ -595,11 +607,9 @@ def gemm_moe_bf16(X: torch.Tensor, W: torch.Tensor, offsets: torch.Tensor, rows:
     E, a, b = _dims(W, "W", 3)
     px, po, pr, T, M, K = _sorted(X, offsets, rows, E)
     N = a if lw == K_MAJOR else b
-    pw = _dev(W, "W", _BF16, (E, N, K) if lw == K_MAJOR else (E, K, N))
-    _same_device(X, W=W)
-    out = _given(out, (M, N), torch.bfloat16, X)
-    with _on(X):
-        _check(lib().gemm_moe_bf16(px, pw, _ptr(out), po, pr, T, M, E, N, K, lw, _stream(X)))
+    pw = _arg(W, "W", _BF16, (E, N, K) if lw == K_MAJOR else (E, K, N), X.device)
+    out = _given(out, (M, N), torch.bfloat16, X.device)
+    _call("gemm_moe_bf16", X.device, px, pw, out.data_ptr(), po, pr, T, M, E, N, K, lw)
     return out
 
 
@@ -612,11 +622,9 @@ def gemm_moe_swiglu_bf16(X: torch.Tensor, W: torch.Tensor, offsets: torch.Tensor
     if N % 2:
         raise ValueError(f"W: {N} rows per expert, expected an even number (gate and up matrices)")
     px, po, pr, T, M, K = _sorted(X, offsets, rows, E)
-    pw = _dev(W, "W", _BF16, (E, N, K))
-    _same_device(X, W=W)
-    out = _given(out, (M, N // 2), torch.bfloat16, X)
-    with _on(X):
-        _check(lib().gemm_moe_swiglu_bf16(px, pw, _ptr(out), po, pr, T, M, E, N // 2, K, _stream(X)))
+    pw = _arg(W, "W", _BF16, (E, N, K), X.device)
+    out = _given(out, (M, N // 2), torch.bfloat16, X.device)
+    _call("gemm_moe_swiglu_bf16", X.device, px, pw, out.data_ptr(), po, pr, T, M, E, N // 2, K)
     return out
 
 
@@ -632,16 +640,14 @@ def gemm_moe_dw_bf16(dY: torch.Tensor, X: torch.Tensor, offsets: torch.Tensor, r
     E = _dims(offsets, "offsets", 1)[0] - 1
     px, po, pr, T, M, K = _sorted(X, offsets, rows, E)
     N = _dims(dY, "dY", 2)[1]
-    py = _dev(dY, "dY", _BF16, (M, N))
-    _same_device(X, dY=dY)
-    if accumulate and out is None:
-        raise ValueError("accumulate needs out")
+    py = _arg(dY, "dY", _BF16, (M, N), X.device)
     if out is not None:
         out_dtype = out.dtype if out.dtype in _REAL else out_dtype
-    out = _given(out, (E, N, K), out_dtype, X)
-    with _on(X):
-        _check(lib().gemm_moe_dw_bf16(_REAL[out_dtype], py, px, _ptr(out), po, pr, T, M, E, N, K,
-                                      int(bool(accumulate)), _stream(X)))
+    elif accumulate:
+        raise ValueError("accumulate needs out")
+    out = _given(out, (E, N, K), out_dtype, X.device)
+    _call("gemm_moe_dw_bf16", X.device, _REAL[out_dtype], py, px, out.data_ptr(), po, pr, T, M, E, N, K,
+          int(bool(accumulate)))
     return out
 
 
@@ -650,10 +656,9 @@ def swiglu(H: torch.Tensor, out: torch.Tensor | None = None) -> torch.Tensor:
     M, N = _dims(H, "H", 2)
     if N % 2:
         raise ValueError(f"H: {N} columns, expected an even number")
-    ph = _dev(H, "H", _BF16, (M, N))
-    out = _given(out, (M, N // 2), torch.bfloat16, H)
-    with _on(H):
-        _check(lib().swiglu_bf16(ph, _ptr(out), M, N // 2, _stream(H)))
+    ph = _arg(H, "H", _BF16, (M, N), H.device)
+    out = _given(out, (M, N // 2), torch.bfloat16, H.device)
+    _call("swiglu_bf16", H.device, ph, out.data_ptr(), M, N // 2)
     return out
 
 
@@ -662,12 +667,10 @@ def swiglu_backward(dA: torch.Tensor, H: torch.Tensor, out: torch.Tensor | None 
     M, N = _dims(H, "H", 2)
     if N % 2:
         raise ValueError(f"H: {N} columns, expected an even number")
-    ph = _dev(H, "H", _BF16, (M, N))
-    pa = _dev(dA, "dA", _BF16, (M, N // 2))
-    _same_device(H, dA=dA)
-    out = _given(out, (M, N), torch.bfloat16, H)
-    with _on(H):
-        _check(lib().swiglu_bwd_bf16(pa, ph, _ptr(out), M, N // 2, _stream(H)))
+    ph = _arg(H, "H", _BF16, (M, N), H.device)
+    pa = _arg(dA, "dA", _BF16, (M, N // 2), H.device)
+    out = _given(out, (M, N), torch.bfloat16, H.device)
+    _call("swiglu_bwd_bf16", H.device, pa, ph, out.data_ptr(), M, N // 2)
     return out
 
 
@@ -678,14 +681,11 @@ def moe_combine(Y: torch.Tensor, slots: torch.Tensor, weights: torch.Tensor | No
     int32, weights (T, k) fp32."""
     M, H = _dims(Y, "Y", 2)
     T, k = _dims(slots, "slots", 2)
-    py = _dev(Y, "Y", _BF16, (M, H))
-    ps = _dev(slots, "slots", _I32, (T, k))
-    if weights is not None:
-        _dev(weights, "weights", _F32, (T, k))
-    _same_device(Y, slots=slots, weights=weights)
-    out = _given(out, (T, H), torch.bfloat16, Y)
-    with _on(Y):
-        _check(lib().moe_combine_bf16(py, ps, _ptr(weights), _ptr(out), T, M, k, H, _stream(Y)))
+    py = _arg(Y, "Y", _BF16, (M, H), Y.device)
+    ps = _arg(slots, "slots", _I32, (T, k), Y.device)
+    pw = None if weights is None else _arg(weights, "weights", _F32, (T, k), Y.device)
+    out = _given(out, (T, H), torch.bfloat16, Y.device)
+    _call("moe_combine_bf16", Y.device, py, ps, pw, out.data_ptr(), T, M, k, H)
     return out
 
 
@@ -696,14 +696,13 @@ def moe_combine_backward(dO: torch.Tensor, Y: torch.Tensor, slots: torch.Tensor,
     T, H = _dims(dO, "dO", 2)
     k = _dims(slots, "slots", 2)[1]
     E = _dims(offsets, "offsets", 1)[0] - 1
-    pd = _dev(dO, "dO", _BF16, (T, H))
-    py = _dev(Y, "Y", _BF16, (T * k, H))
-    ps = _dev(slots, "slots", _I32, (T, k))
-    pw = _dev(weights, "weights", _F32, (T, k))
-    po = _dev(offsets, "offsets", _I32, (E + 1,))
-    _same_device(dO, Y=Y, slots=slots, weights=weights, offsets=offsets)
+    dev = dO.device
+    pd = _arg(dO, "dO", _BF16, (T, H), dev)
+    py = _arg(Y, "Y", _BF16, (T * k, H), dev)
+    ps = _arg(slots, "slots", _I32, (T, k), dev)
+    pw = _arg(weights, "weights", _F32, (T, k), dev)
+    po = _arg(offsets, "offsets", _I32, (E + 1,), dev)
     dY = torch.empty_like(Y)
     dweights = torch.empty_like(weights)
-    with _on(dO):
-        _check(lib().moe_combine_bwd_bf16(pd, py, ps, pw, po, E, _ptr(dY), _ptr(dweights), T, k, H, _stream(dO)))
+    _call("moe_combine_bwd_bf16", dev, pd, py, ps, pw, po, E, dY.data_ptr(), dweights.data_ptr(), T, k, H)
     return dY, dweights

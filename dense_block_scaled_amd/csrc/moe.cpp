@@ -58,12 +58,20 @@ dbs_status run_product(dbs::MoeGemm p, hipStream_t stream)
     const int st = dbs::device_compute_units(&cus);
     if (st != DBS_OK) return (dbs_status)st;
     p.vec = p.ncols % 8 == 0 && aligned(p.D, 16);
+    const int64_t mean = p.M / p.E, tiles_n = (p.ncols + 127) / 128;
+    if ((p.M / 64 + p.E) * tiles_n >= kTwoGiB) return fail(DBS_EUNSUPPORTED, "too many output tiles");
+    // A few rows per expert and fewer 64-row tiles than would fill the CUs:
+    // the kernel that cuts along K too (K-major only).  One token of 8 experts,
+    // K 2048: 2 x 1408 gated columns (88 tiles) 26 us against 31, K 4096 and
+    // 2 x 768 columns (48 tiles) 30 against 47; plain, K 1408 and 2048 columns
+    // (64 tiles) 14 against 20, 128 tiles 24 against 24, 256 tiles 39 against
+    // 31.  The gated tiles are half as wide: 352 of them 66 against 81, 704
+    // 96 against 107, 1408 200 against 196.
+    const int64_t tiles = (p.M < p.E ? p.M : p.E) * ((p.ncols + (p.gate ? 127 : 255)) / (p.gate ? 128 : 256));
+    if (!p.wmn && mean <= 8 && 2 * tiles <= (p.gate ? 3 : 1) * (int64_t)cus) return done(dbs::launch_moe_rows(p, stream));
     // Tile rows by the rows an expert has on average: a tile's height beyond
     // them is computed for nothing.
-    const int64_t mean = p.M / p.E;
     const int tm = mean <= 96 ? 64 : 256;
-    const int64_t tiles_n = (p.ncols + 127) / 128;
-    if ((p.M / 64 + p.E) * tiles_n >= kTwoGiB) return fail(DBS_EUNSUPPORTED, "too many output tiles");
     return done(dbs::launch_moe_tiles(p, tm, cus, stream));
 }
 

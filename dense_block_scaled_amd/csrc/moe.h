@@ -41,6 +41,7 @@ struct MoeGemmDw {
 };
 
 hipError_t launch_moe_tiles(const MoeGemm &p, int tm, int cus, hipStream_t stream);
+hipError_t launch_moe_rows(const MoeGemm &p, hipStream_t stream);
 hipError_t launch_moe_dw(const MoeGemmDw &p, int cus, hipStream_t stream);
 
 struct MoeRoute {

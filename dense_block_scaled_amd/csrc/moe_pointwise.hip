@@ -140,14 +140,25 @@ __global__ __launch_bounds__(kThreads) void combine_kernel(const uint16_t *Y, co
     for (int64_t i = (int64_t)blockIdx.x * kThreads + threadIdx.x; i < pieces; i += (int64_t)gridDim.x * kThreads) {
         const int64_t per = H / V, t = i / per, c = (i - t * per) * V;
         float acc[V] = {};
-        for (int j = 0; j < k; ++j) {
-            const int s = slot_of(slots, t * k + j, M);
-            if (s < 0) continue;
-            const float w = weights ? weights[t * k + j] : 1.0f;
-            float y[V];
-            unpack<V>(load<V>(Y, (int64_t)s * H + c), y);
+        // four rows under way at a time; a pair without a row reads row 0 and adds zeros
+        for (int j0 = 0; j0 < k; j0 += 4) {
+            int s[4];
+            float w[4];
+            Piece<V> y[4];
 #pragma unroll
-            for (int q = 0; q < V; ++q) acc[q] += w * y[q];
+            for (int j = 0; j < 4; ++j) {
+                s[j] = j0 + j < k ? slot_of(slots, t * k + j0 + j, M) : -1;
+                w[j] = j0 + j < k && weights ? weights[t * k + j0 + j] : 1.0f;
+            }
+#pragma unroll
+            for (int j = 0; j < 4; ++j) y[j] = load<V>(Y, (int64_t)max(s[j], 0) * H + c);
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                float f[V];
+                unpack<V>(y[j], f);
+#pragma unroll
+                for (int q = 0; q < V; ++q) acc[q] = s[j] >= 0 ? acc[q] + w[j] * f[q] : acc[q];
+            }
         }
         store<V>(out, t * H + c, pack<V>(acc));
     }

@@ -9,10 +9,10 @@
 // has experts -1 (weight 0) behind them, and such pairs have no place in the
 // order.  +inf counts as the largest finite value.
 //
-// Selection.  16 lanes hold one token's logits in registers (lane l: experts
-// l, 16 + l, ...), so the cross-lane steps of a maximum are four DPP moves
-// inside a row of 16 and one wave works on four tokens: at 128 experts eight
-// logits a lane, about a hundred vector instructions a token.
+// Selection.  16 lanes hold one token's logits in registers, so the
+// cross-lane steps of a maximum are four DPP moves inside a row of 16 and one
+// wave works on four tokens: for every choice the largest value, the lowest
+// expert that has it, and that one struck out.
 //
 // Order.  A token's experts are distinct, so inside a workgroup's 64 tokens
 // the pairs of one expert, in pair order, are its tokens in token order: an
@@ -62,33 +62,60 @@ __device__ __forceinline__ float row_max(float v)
     return fmaxf(v, row_move<3>(v));
 }
 
-template <int STEP>
-__device__ __forceinline__ void best_step(float &v, int &e)
+__device__ __forceinline__ int row_min(int v)
 {
-    const float ov = row_move<STEP>(v);
-    const int oe = row_move<STEP>(e);
-    const bool take = ov > v || (ov == v && oe < e);
-    v = take ? ov : v;
-    e = take ? oe : e;
+    v = min(v, row_move<0>(v));
+    v = min(v, row_move<1>(v));
+    v = min(v, row_move<2>(v));
+    return min(v, row_move<3>(v));
 }
 
 // -inf for a closed expert, at most the largest finite value otherwise
 __device__ __forceinline__ float open_logit(float x) { return x == x ? fminf(x, FLT_MAX) : -INFINITY; }
 
-template <bool BF16>
-__device__ __forceinline__ float load_logit(const void *logits, int64_t i)
+// How a token's experts lie in its 16 lanes: C consecutive ones a lane and
+// step, so value i of lane l is expert 16 C (i / C) + C l + i % C.  C = 4
+// (whole loads of 8 or 16 bytes) where the rows of logits allow it, else 1.
+template <int C>
+__device__ __forceinline__ int expert_of(int i, int l) { return (i / C) * 16 * C + C * l + i % C; }
+
+template <int VPL, int C, bool BF16>
+__device__ __forceinline__ void load_logits(float (&v)[VPL], const void *logits, int64_t tok, int E, int l)
 {
-    if constexpr (BF16)
-        return __builtin_bit_cast(float, (uint32_t) reinterpret_cast<const uint16_t *>(logits)[i] << 16);
-    else
-        return reinterpret_cast<const float *>(logits)[i];
+    typedef __attribute__((ext_vector_type(4))) float f32x4;
+    typedef __attribute__((ext_vector_type(2))) uint32_t u32x2;
+#pragma unroll
+    for (int i = 0; i < VPL; i += C) {
+        const int e = expert_of<C>(i, l);
+        float x[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+        if (e < E) {                             // (E is a multiple of C)
+            const int64_t at = tok * E + e;
+            if constexpr (BF16 && C == 4) {
+                const u32x2 w = *reinterpret_cast<const u32x2 *>(reinterpret_cast<const uint16_t *>(logits) + at);
+                x[0] = __builtin_bit_cast(float, w[0] << 16);
+                x[1] = __builtin_bit_cast(float, w[0] & 0xFFFF0000u);
+                x[2] = __builtin_bit_cast(float, w[1] << 16);
+                x[3] = __builtin_bit_cast(float, w[1] & 0xFFFF0000u);
+            } else if constexpr (BF16) {
+                x[0] = __builtin_bit_cast(float, (uint32_t) reinterpret_cast<const uint16_t *>(logits)[at] << 16);
+            } else if constexpr (C == 4) {
+                const f32x4 w = *reinterpret_cast<const f32x4 *>(reinterpret_cast<const float *>(logits) + at);
+#pragma unroll
+                for (int c = 0; c < 4; ++c) x[c] = w[c];
+            } else {
+                x[0] = reinterpret_cast<const float *>(logits)[at];
+            }
+        }
+#pragma unroll
+        for (int c = 0; c < C; ++c) v[i + c] = open_logit(x[c]);
+    }
 }
 
 // The exclusive sum of total[0 .. E-1] into base[0 .. E] (LDS), by the whole
 // workgroup: thread i sums experts 4 i .. 4 i + 3.
 __device__ __forceinline__ void scan_experts(const int32_t *total, int E, int32_t *base, int32_t *part)
 {
-    static_assert(kMoeMaxExperts <= 4 * kThreads, "four experts a thread");
+    static_assert(kMoeMaxExperts <= 4 * 256, "four experts a thread");
     const int t = threadIdx.x, lane = t & 63, w = t >> 6;
     int v[4], s = 0;
 #pragma unroll
@@ -124,7 +151,7 @@ __device__ __forceinline__ void place(const MoeRoute &p, int64_t t0, int64_t p0,
                                       const int32_t *base, const int32_t *before, const int32_t *experts)
 {
     const int total = base[p.E];
-    for (int64_t q = p0 + threadIdx.x; q < p1; q += kThreads) {
+    for (int64_t q = p0 + threadIdx.x; q < p1; q += blockDim.x) {
         const int64_t t = q / p.k;
         const int e = experts[q - p0];
         int slot = -1;
@@ -138,14 +165,20 @@ __device__ __forceinline__ void place(const MoeRoute &p, int64_t t0, int64_t p0,
     }
 }
 
-// VPL logits per lane (E <= 16 VPL).  ONE: the whole call in this kernel (T <= kRouteTokens).
-template <int VPL, bool BF16, bool ONE>
-__global__ __launch_bounds__(kThreads) void route_select(MoeRoute p)
+// VPL logits per lane (E <= 16 VPL).  ONE: the whole call in this kernel (T <=
+// kRouteTokens); otherwise every token of the workgroup has lanes of its own
+// (up to 512 experts), which puts eight waves on a SIMD from 32768 tokens on.
+template <int VPL, bool ONE>
+constexpr int select_threads() { return ONE ? 256 : VPL > 32 ? 512 : 1024; }
+
+template <int VPL, int C, bool BF16, bool ONE>
+__global__ __launch_bounds__((select_threads<VPL, ONE>())) void route_select(MoeRoute p)
 {
     __shared__ uint64_t mask[16 * VPL];
     __shared__ int32_t chosen[ONE ? kRouteTokens * kMoeMaxK : 1];
     __shared__ int32_t base[ONE ? 16 * VPL + 1 : 1];
-    __shared__ int32_t part[kThreads / 64];
+    __shared__ int32_t part[4];
+    constexpr int kThreads = select_threads<VPL, ONE>();
     const int t = threadIdx.x, l = t & (kLanes - 1);
     for (int e = t; e < p.E; e += kThreads) mask[e] = 0;
     __syncthreads();
@@ -155,27 +188,20 @@ __global__ __launch_bounds__(kThreads) void route_select(MoeRoute p)
         const int64_t tok = t0 + tl;
         if (tok >= p.T) break;                   // (uniform in the token's 16 lanes)
         float v[VPL];
-#pragma unroll
-        for (int i = 0; i < VPL; ++i) {
-            const int e = 16 * i + l;
-            v[i] = e < p.E ? open_logit(load_logit<BF16>(p.logits, tok * p.E + e)) : -INFINITY;
-        }
+        load_logits<VPL, C, BF16>(v, p.logits, tok, p.E, l);
         float mine = -INFINITY, top = 0.0f, whole = 0.0f;   // lane j: the j-th choice
         int mine_e = -1;
         for (int j = 0; j < p.k; ++j) {
-            float b = -INFINITY;
+            // the largest value, then the lowest expert that has it
+            float b = v[0];
+#pragma unroll
+            for (int i = 1; i < VPL; ++i) b = fmaxf(b, v[i]);
+            b = row_max(b);
+            if (b == -INFINITY) break;           // no open expert is left
             int be = 1 << 30;
 #pragma unroll
-            for (int i = 0; i < VPL; ++i) {
-                const bool take = v[i] > b;      // experts of a lane ascend: a tie keeps the lower
-                b = take ? v[i] : b;
-                be = take ? 16 * i + l : be;
-            }
-            best_step<0>(b, be);
-            best_step<1>(b, be);
-            best_step<2>(b, be);
-            best_step<3>(b, be);
-            if (b == -INFINITY) break;           // no open expert is left
+            for (int i = VPL - 1; i >= 0; --i) be = v[i] == b ? expert_of<C>(i, l) : be;
+            be = row_min(be);
             if (j == 0) {
                 top = b;
                 if (!p.renorm) {
@@ -189,7 +215,7 @@ __global__ __launch_bounds__(kThreads) void route_select(MoeRoute p)
                 mine_e = be;
             }
 #pragma unroll
-            for (int i = 0; i < VPL; ++i) v[i] = be == 16 * i + l ? -INFINITY : v[i];
+            for (int i = 0; i < VPL; ++i) v[i] = be == expert_of<C>(i, l) ? -INFINITY : v[i];
         }
         const float x = mine_e >= 0 ? expf(mine - top) : 0.0f;
         if (p.renorm) whole = row_sum(x);
@@ -202,7 +228,7 @@ __global__ __launch_bounds__(kThreads) void route_select(MoeRoute p)
     }
     __syncthreads();
     if constexpr (ONE) {
-        // the counts (p.counts is not used) in LDS, summed in place of the totals
+        // the counts in LDS, summed in place
         for (int e = t; e < p.E; e += kThreads) base[e] = __popcll(mask[e]);
         __syncthreads();
         int32_t *b = base;
@@ -223,8 +249,10 @@ __global__ __launch_bounds__(1024) void route_columns(int32_t *counts, int64_t n
     const int e = blockIdx.x * 16 + col;
     const int64_t per = (nb + 63) / 64, r0 = s * per, r1 = r0 + per < nb ? r0 + per : nb;
     int sum = 0;
-    if (e < E)
+    if (e < E) {
+#pragma unroll 8
         for (int64_t r = r0; r < r1; ++r) sum += counts[r * E + e];
+    }
     seg[s][col] = sum;
     __syncthreads();
     if (threadIdx.x < 16) {
@@ -239,6 +267,7 @@ __global__ __launch_bounds__(1024) void route_columns(int32_t *counts, int64_t n
     __syncthreads();
     if (e < E) {
         int run = seg[s][col];
+#pragma unroll 8
         for (int64_t r = r0; r < r1; ++r) {
             const int v = counts[r * E + e];
             counts[r * E + e] = run;
@@ -271,75 +300,97 @@ __global__ __launch_bounds__(kThreads) void route_place(MoeRoute p, int64_t nb)
 
 // dlogits = p (u - sum p u): p the softmax over all experts, or over the
 // chosen ones (renorm), u the weights' gradients at the chosen experts and 0
-// elsewhere.  16 lanes a token, as in route_select.
-template <int VPL, bool BF16>
+// elsewhere.  16 lanes a token, as in route_select; lane j has the j-th
+// choice, and the chosen experts' gradients reach the lanes that hold those
+// experts through a row of E floats in LDS (zeroed, written and read by the
+// token's own lanes of one wave, whose LDS operations keep their order).
+template <int VPL, int C, bool BF16>
 __global__ __launch_bounds__(kThreads) void route_bwd(const void *logits, int64_t T, int E, int k, int renorm,
                                                       const int32_t *experts, const float *dweights, void *dlogits)
 {
+    // lane l's values lie together, C at a time: [token][i / C][l][i % C]
+    __shared__ __attribute__((aligned(16))) float at_chosen[kThreads / kLanes][16 * VPL];
     const int l = threadIdx.x & (kLanes - 1);
     const int64_t tok = (int64_t)blockIdx.x * (kThreads / kLanes) + threadIdx.x / kLanes;
     if (tok >= T) return;                        // (uniform in the token's 16 lanes)
-    float v[VPL], u[VPL];
-    bool sel[VPL];
-#pragma unroll
-    for (int i = 0; i < VPL; ++i) {
-        const int e = 16 * i + l;
-        v[i] = e < E ? open_logit(load_logit<BF16>(logits, tok * E + e)) : -INFINITY;
-        u[i] = 0.0f;
-        sel[i] = false;
-    }
-    for (int j = 0; j < k; ++j) {
-        const int e = experts[tok * k + j];
-        const float d = dweights[tok * k + j];
-#pragma unroll
-        for (int i = 0; i < VPL; ++i) {
-            const bool hit = e == 16 * i + l;
-            u[i] = hit ? d : u[i];
-            sel[i] = sel[i] || hit;
+    float *row = at_chosen[threadIdx.x / kLanes];
+    float v[VPL];
+    load_logits<VPL, C, BF16>(v, logits, tok, E, l);
+    int e = -1;
+    float u = 0.0f, x = -INFINITY;
+    if (l < k) {
+        e = experts[tok * k + l];
+        e = e < E ? e : -1;
+        if (e >= 0) {
+            u = dweights[tok * k + l];
+            const int64_t at = tok * E + e;
+            if constexpr (BF16)
+                x = open_logit(__builtin_bit_cast(float, (uint32_t) reinterpret_cast<const uint16_t *>(logits)[at] << 16));
+            else
+                x = open_logit(reinterpret_cast<const float *>(logits)[at]);
         }
     }
-    float top = -INFINITY;
+    // the softmax's maximum and sum, over all experts or the chosen ones
+    float top = x;
+    if (!renorm) {
 #pragma unroll
-    for (int i = 0; i < VPL; ++i) {
-        if (renorm && !sel[i]) v[i] = -INFINITY;
-        top = fmaxf(top, v[i]);
+        for (int i = 0; i < VPL; ++i) top = fmaxf(top, v[i]);
     }
     top = row_max(top);
     const bool open = top > -INFINITY;           // a closed token has gradient 0
-    float sum = 0.0f, dot = 0.0f;
+    float sum = 0.0f;
+    const float mine = open ? expf(x - top) : 0.0f;
+    if (renorm) {
+        sum = mine;
+    } else {
 #pragma unroll
-    for (int i = 0; i < VPL; ++i) {
-        v[i] = open ? expf(v[i] - top) : 0.0f;
-        sum += v[i];
-        dot += v[i] * u[i];
+        for (int i = 0; i < VPL; ++i) {
+            v[i] = open ? expf(v[i] - top) : 0.0f;
+            sum += v[i];
+        }
     }
-    sum = row_sum(sum);
-    dot = row_sum(dot);
-    const float inv = open ? 1.0f / sum : 0.0f;
-    dot *= inv;
+    const float inv = open ? 1.0f / row_sum(sum) : 0.0f;
+    const float p = mine * inv, dot = row_sum(p * u);
+    const float scale = renorm ? 0.0f : dot * inv;
 #pragma unroll
-    for (int i = 0; i < VPL; ++i) {
-        const int e = 16 * i + l;
-        if (e >= E) continue;
-        const float d = v[i] > 0.0f ? v[i] * inv * (u[i] - dot) : 0.0f;
-        if constexpr (BF16)
-            reinterpret_cast<__bf16 *>(dlogits)[tok * E + e] = (__bf16)d;
-        else
-            reinterpret_cast<float *>(dlogits)[tok * E + e] = d;
+    for (int i = 0; i < VPL; ++i) row[expert_of<C>(i, l)] = 0.0f;
+    __builtin_amdgcn_wave_barrier();
+    if (e >= 0) row[e] = renorm ? p * (u - dot) : p * u;
+    __builtin_amdgcn_wave_barrier();
+#pragma unroll
+    for (int i = 0; i < VPL; i += C) {
+        const int first = expert_of<C>(i, l);
+        if (first >= E) continue;
+        float d[C];
+#pragma unroll
+        for (int c = 0; c < C; ++c) d[c] = renorm ? row[first + c] : row[first + c] - v[i + c] * scale;
+        const int64_t at = tok * E + first;
+        if constexpr (BF16) {
+            __bf16 w[C];
+#pragma unroll
+            for (int c = 0; c < C; ++c) w[c] = (__bf16)d[c];
+            __builtin_memcpy(reinterpret_cast<__bf16 *>(dlogits) + at, w, sizeof(w));
+        } else {
+            __builtin_memcpy(reinterpret_cast<float *>(dlogits) + at, d, sizeof(d));
+        }
     }
 }
 
-// F(VPL) for the smallest number of logits per lane that holds E experts
+// F(VPL, C) for the smallest number of logits per lane that holds E experts;
+// C = 4 if every row starts on a whole load and ends with one.
 template <class F>
-hipError_t by_experts(int E, F &&f)
+hipError_t by_experts(int E, const void *logits, const void *other, F &&f)
 {
-    if (E <= 16) return f(std::integral_constant<int, 1>{});
-    if (E <= 32) return f(std::integral_constant<int, 2>{});
-    if (E <= 64) return f(std::integral_constant<int, 4>{});
-    if (E <= 128) return f(std::integral_constant<int, 8>{});
-    if (E <= 256) return f(std::integral_constant<int, 16>{});
-    if (E <= 512) return f(std::integral_constant<int, 32>{});
-    return f(std::integral_constant<int, 64>{});
+    const bool whole = E % 4 == 0 && ((reinterpret_cast<uintptr_t>(logits) | reinterpret_cast<uintptr_t>(other)) & 15) == 0;
+    auto with = [&](auto v) {
+        return whole ? f(v, std::integral_constant<int, 4>{}) : f(v, std::integral_constant<int, 1>{});
+    };
+    if (E <= 64) return with(std::integral_constant<int, 4>{});
+    if (E <= 128) return with(std::integral_constant<int, 8>{});
+    if (E <= 192) return with(std::integral_constant<int, 12>{});
+    if (E <= 256) return with(std::integral_constant<int, 16>{});
+    if (E <= 512) return with(std::integral_constant<int, 32>{});
+    return with(std::integral_constant<int, 64>{});
 }
 
 int64_t blocks_of(int64_t T) { return (T + kRouteTokens - 1) / kRouteTokens; }
@@ -355,14 +406,14 @@ hipError_t launch_moe_route(const MoeRoute &p, hipStream_t stream)
 {
     const int64_t nb = blocks_of(p.T);
     const bool one = p.T <= kRouteTokens;
-    hipError_t e = by_experts(p.E, [&](auto v) {
-        constexpr int V = decltype(v)::value;
+    hipError_t e = by_experts(p.E, p.logits, nullptr, [&](auto vpl, auto c) {
+        constexpr int V = decltype(vpl)::value, C = decltype(c)::value;
         if (one) {
-            if (p.bf16) hipLaunchKernelGGL((route_select<V, true, true>), dim3(1), dim3(kThreads), 0, stream, p);
-            else hipLaunchKernelGGL((route_select<V, false, true>), dim3(1), dim3(kThreads), 0, stream, p);
+            if (p.bf16) hipLaunchKernelGGL((route_select<V, C, true, true>), dim3(1), dim3(256), 0, stream, p);
+            else hipLaunchKernelGGL((route_select<V, C, false, true>), dim3(1), dim3(256), 0, stream, p);
         } else {
-            if (p.bf16) hipLaunchKernelGGL((route_select<V, true, false>), dim3(nb), dim3(kThreads), 0, stream, p);
-            else hipLaunchKernelGGL((route_select<V, false, false>), dim3(nb), dim3(kThreads), 0, stream, p);
+            if (p.bf16) hipLaunchKernelGGL((route_select<V, C, true, false>), dim3(nb), dim3(select_threads<V, false>()), 0, stream, p);
+            else hipLaunchKernelGGL((route_select<V, C, false, false>), dim3(nb), dim3(select_threads<V, false>()), 0, stream, p);
         }
         return hipGetLastError();
     });
@@ -377,14 +428,14 @@ hipError_t launch_moe_route_bwd(const void *logits, int bf16, int64_t T, int E, 
                                 const int32_t *experts, const float *dweights, void *dlogits, hipStream_t stream)
 {
     const dim3 grid((T + kThreads / kLanes - 1) / (kThreads / kLanes));
-    return by_experts(E, [&](auto v) {
-        constexpr int V = decltype(v)::value;
+    return by_experts(E, logits, dlogits, [&](auto vpl, auto c) {
+        constexpr int V = decltype(vpl)::value, C = decltype(c)::value;
         if (bf16)
-            hipLaunchKernelGGL((route_bwd<V, true>), grid, dim3(kThreads), 0, stream, logits, T, E, k, renorm, experts,
-                               dweights, dlogits);
+            hipLaunchKernelGGL((route_bwd<V, C, true>), grid, dim3(kThreads), 0, stream, logits, T, E, k, renorm,
+                               experts, dweights, dlogits);
         else
-            hipLaunchKernelGGL((route_bwd<V, false>), grid, dim3(kThreads), 0, stream, logits, T, E, k, renorm, experts,
-                               dweights, dlogits);
+            hipLaunchKernelGGL((route_bwd<V, C, false>), grid, dim3(kThreads), 0, stream, logits, T, E, k, renorm,
+                               experts, dweights, dlogits);
         return hipGetLastError();
     });
 }
