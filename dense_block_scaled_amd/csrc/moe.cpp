@@ -69,9 +69,13 @@ dbs_status run_product(dbs::MoeGemm p, hipStream_t stream)
     // 96 against 107, 1408 200 against 196.
     const int64_t tiles = (p.M < p.E ? p.M : p.E) * ((p.ncols + (p.gate ? 127 : 255)) / (p.gate ? 128 : 256));
     if (!p.wmn && mean <= 8 && 2 * tiles <= (p.gate ? 3 : 1) * (int64_t)cus) return done(dbs::launch_moe_rows(p, stream));
-    // Tile rows by the rows an expert has on average: a tile's height beyond
-    // them is computed for nothing.
-    const int tm = mean <= 96 ? 64 : 256;
+    // Tile rows by the rows an expert has on average.  256-row tiles skip what
+    // a group lacks in blocks of 64 and are the faster ones from about 32 rows
+    // on (16 experts of 2048 x 4096: 8 and 16 rows 47 us against 44 on 64-row
+    // tiles with their deeper ring, 32 rows 47 against 63, 128 rows 60 against
+    // 75; 128 experts of 4096 x 1536: 8 rows 304 against 295, 32 rows 319
+    // against 335, 256 rows 520 against 667).
+    const int tm = mean < 24 ? 64 : 256;
     return done(dbs::launch_moe_tiles(p, tm, cus, stream));
 }
 

@@ -565,11 +565,11 @@ __device__ __forceinline__ RowTile find_tile(const Table<TM> &tab, int E, int nt
     return r;
 }
 
-// rows total .. M-1 of D, behind the last group, are zero
-__device__ __forceinline__ void zero_rest(const MoeGemm &p, int64_t total)
+// Rows from .. to-1 of D are zero (those before the first group and behind the last).
+__device__ __forceinline__ void zero_rows(const MoeGemm &p, int64_t from, int64_t to)
 {
-    const int64_t bytes = (p.M - total) * p.ncols * 2;
-    uint8_t *z = p.D + total * p.ncols * 2;
+    const int64_t bytes = (to - from) * p.ncols * 2;
+    uint8_t *z = p.D + from * p.ncols * 2;
     const int64_t me = (int64_t)blockIdx.x * blockDim.x + threadIdx.x, all = (int64_t)gridDim.x * blockDim.x;
     if (p.vec)
         for (int64_t o = me * 16; o < bytes; o += all * 16) *reinterpret_cast<i32x4 *>(z + o) = i32x4{};
@@ -598,7 +598,8 @@ __global__ __launch_bounds__(512, 1) void moe_tiles_256(MoeGemm p)
     const int tiles_n = (p.ncols + TNO - 1) / TNO;
     fill_table(tab, p, c);
     __syncthreads();
-    zero_rest(p, tab.first[p.E]);
+    zero_rows(p, 0, tab.first[0]);
+    zero_rows(p, tab.first[p.E], p.M);
     const int ntiles = count_tiles(tab, p.E, tiles_n);
     const int nwg = gridDim.x, self = first_tile();
     if (self >= ntiles) return;
@@ -756,7 +757,8 @@ __global__ __launch_bounds__(512, 1) void moe_tiles_64(MoeGemm p)
     const int tiles_n = (p.ncols + TNO - 1) / TNO;
     fill_table(tab, p, c);
     __syncthreads();
-    zero_rest(p, tab.first[p.E]);
+    zero_rows(p, 0, tab.first[0]);
+    zero_rows(p, tab.first[p.E], p.M);
     const int ntiles = count_tiles(tab, p.E, tiles_n);
     const int nwg = gridDim.x;
     int tile = first_tile();

@@ -38,11 +38,11 @@ __global__ __launch_bounds__(64 * kWaves) void moe_rows(MoeGemm p)
 
     // this workgroup's group: number blockIdx.y among those with rows; the
     // last row of all groups on the way
-    int g = -1, lo = 0, hi = 0, seen = 0, end = 0;
+    const int begin = min(max(p.offsets[0], 0), p.M);
+    int g = -1, lo = 0, hi = 0, seen = 0, end = begin;
     for (int g0 = 0; g0 < p.E; g0 += 64) {
         const int e = g0 + lane;
         // (clamped and made ascending, as the tile kernels read them)
-        if (g0 == 0) end = min(max(p.offsets[0], 0), p.M);
         int b = e < p.E ? max(min(max(p.offsets[e + 1], 0), p.M), end) : end;
 #pragma unroll
         for (int d = 1; d < 64; d *= 2) {
@@ -67,14 +67,14 @@ __global__ __launch_bounds__(64 * kWaves) void moe_rows(MoeGemm p)
     lo = __builtin_amdgcn_readfirstlane(lo);
     hi = __builtin_amdgcn_readfirstlane(hi);
 
-    // rows behind the last group are zero
-    {
-        const int64_t first = (int64_t)end * p.ncols, count = (int64_t)(p.M - end) * p.ncols;
+    // rows before the first group and behind the last are zero
+    auto zero = [&](int64_t from, int64_t to) {
         const int64_t all = (int64_t)gridDim.x * gridDim.y * blockDim.x;
-        uint16_t *z = reinterpret_cast<uint16_t *>(p.D) + first;
-        for (int64_t i = ((int64_t)blockIdx.y * gridDim.x + blockIdx.x) * blockDim.x + threadIdx.x; i < count; i += all)
-            z[i] = 0;
-    }
+        for (int64_t i = from + ((int64_t)blockIdx.y * gridDim.x + blockIdx.x) * blockDim.x + threadIdx.x; i < to; i += all)
+            reinterpret_cast<uint16_t *>(p.D)[i] = 0;
+    };
+    zero(0, (int64_t)begin * p.ncols);
+    zero((int64_t)end * p.ncols, (int64_t)p.M * p.ncols);
     if (g < 0) return;
 
     // The wave's share of K in whole lines of 64 elements.  Lane l holds row

@@ -1,5 +1,6 @@
 /*
  * dbs.h -- C ABI of the MI355X (gfx950) block-scaled GEMM library libdbs.so
+ * (the mixture-of-experts operators further down describe themselves)
  *
  *     D = bf16( alpha * (sA (.) A) . (sB (.) B)^T )      fp32 accumulation
  *
@@ -29,7 +30,7 @@
  *
  * Ownership and threading: the caller owns every buffer.  A call validates its
  * arguments on the host, then enqueues its kernels on `stream` (one for a
- * GEMM; gemm_nvfp4_fp8, gemm_nvfp4_fp6 and the quantisers name theirs below) and
+ * GEMM; gemm_nvfp4_fp8, gemm_nvfp4_fp6, the quantisers and moe_route name theirs below) and
  * returns without synchronising; faults inside the kernel surface at the
  * caller's next synchronisation of that stream.  The library allocates no
  * device memory and keeps only a per-device cache of the CU count (and, for
@@ -346,9 +347,10 @@ dbs_status quant_bf16(const float *x, int64_t n, void *out, hipStream_t stream);
  *   DBS_K_MAJOR) or E x K x N (lw = DBS_MN_MAJOR; D[i] = X[rows[i]] W_g, the
  *   gradient with respect to the rows of a K-major product; N a multiple of
  *   8, else DBS_EUNSUPPORTED); D: M x N.  K a multiple of 8; D 2-byte aligned.
- *   Rows of D at and past offsets[E] are set to zero.  Offsets outside
- *   0 .. M are clamped and descending ones read as empty; row indices outside
- *   0 .. T - 1 stand for a zero row.
+ *   Rows of D that no expert owns (at and past offsets[E], and before
+ *   offsets[0] if that is not 0) are set to zero.  Offsets outside 0 .. M are
+ *   clamped and descending ones read as empty; row indices outside 0 .. T - 1
+ *   stand for a zero row.
  * gemm_moe_swiglu_bf16: the same with W: E x 2F x K and D[i, f] = silu(h[f])
  *   h[F + f], h = X[rows[i]] W_g^T kept in fp32.
  * gemm_moe_dw_bf16: dW[g] = sum over expert g's rows i of dY[i]^T X[rows[i]]:
