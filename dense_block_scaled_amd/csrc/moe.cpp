@@ -58,25 +58,23 @@ dbs_status run_product(dbs::MoeGemm p, hipStream_t stream)
     const int st = dbs::device_compute_units(&cus);
     if (st != DBS_OK) return (dbs_status)st;
     p.vec = p.ncols % 8 == 0 && aligned(p.D, 16);
-    const int64_t mean = p.M / p.E, tiles_n = (p.ncols + 127) / 128;
-    if ((p.M / 64 + p.E) * tiles_n >= kTwoGiB) return fail(DBS_EUNSUPPORTED, "too many output tiles");
-    // A few rows per expert and fewer 64-row tiles than would fill the CUs:
-    // the kernel that cuts along K too (K-major only).  One token of 8 experts,
-    // K 2048: 2 x 1408 gated columns (88 tiles) 26 us against 31, K 4096 and
-    // 2 x 768 columns (48 tiles) 30 against 47; plain, K 1408 and 2048 columns
-    // (64 tiles) 14 against 20, 128 tiles 24 against 24, 256 tiles 39 against
-    // 31.  The gated tiles are half as wide: 352 of them 66 against 81, 704
-    // 96 against 107, 1408 200 against 196.
-    const int64_t tiles = (p.M < p.E ? p.M : p.E) * ((p.ncols + (p.gate ? 127 : 255)) / (p.gate ? 128 : 256));
-    if (!p.wmn && mean <= 8 && 2 * tiles <= (p.gate ? 3 : 1) * (int64_t)cus) return done(dbs::launch_moe_rows(p, stream));
-    // Tile rows by the rows an expert has on average.  256-row tiles skip what
-    // a group lacks in blocks of 64 and are the faster ones from about 32 rows
-    // on (16 experts of 2048 x 4096: 8 and 16 rows 47 us against 44 on 64-row
-    // tiles with their deeper ring, 32 rows 47 against 63, 128 rows 60 against
-    // 75; 128 experts of 4096 x 1536: 8 rows 304 against 295, 32 rows 319
-    // against 335, 256 rows 520 against 667).
-    const int tm = mean < 24 ? 64 : 256;
-    return done(dbs::launch_moe_tiles(p, tm, cus, stream));
+    if ((p.M / 64 + p.E) * ((p.ncols + 31) / 32) >= kTwoGiB) return fail(DBS_EUNSUPPORTED, "too many output tiles");
+    // 64-row or 256-row tiles: the rounds that either takes over the CUs, for
+    // groups of M / E rows on average (half a tile of each is waste), at the
+    // time a stage of it was measured to take: 0.37 us against 1.5 (K-major),
+    // 0.9 against 1.5 (MN-major, twice as wide).  8 experts of 4096 x 4096, 64
+    // rows each: 61 us against 70, 128 rows 94 against 86; 128 experts of
+    // 1536 x 4096, 32 rows 301 against 346; 64 experts of 2816 x 2048, 32 rows
+    // 147 against 172, 64 rows 183 against 165; MN-major 2048 x 2816, 4 tokens
+    // of 8 experts 52 against 68, 32 rows per expert 141 against 133.
+    const int64_t met = p.M < p.E ? p.M : p.E;
+    auto rounds = [&](int64_t tm, int64_t tn) {
+        int64_t rows = p.M / tm + met / 2;
+        rows = rows > met ? rows : met;
+        return (rows * ((p.ncols + tn - 1) / tn) + cus - 1) / cus;
+    };
+    const int64_t few = rounds(64, p.wmn ? 128 : p.gate ? 32 : 64), many = rounds(256, p.gate ? 128 : 256);
+    return done(dbs::launch_moe_tiles(p, (p.wmn ? 5 : 2) * few <= 8 * many ? 64 : 256, cus, stream));
 }
 
 dbs::MoeGemm product(const void *X, const void *W, void *D, const int32_t *offsets, const int32_t *rows, int64_t T,

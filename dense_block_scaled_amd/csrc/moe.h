@@ -1,6 +1,6 @@
 // moe.h -- internal interface between the C ABI of the mixture-of-experts
 // operators (moe.cpp) and their gfx950 kernels (moe_route.hip, moe_gemm.hip,
-// moe_rows.hip, moe_pointwise.hip).  Not installed; callers use include/dbs.h.
+// moe_pointwise.hip).  Not installed; callers use include/dbs.h.
 #pragma once
 
 #include <hip/hip_runtime_api.h>
@@ -40,8 +40,8 @@ struct MoeGemmDw {
     int accumulate;           // 1: add to dW (fp32 only)
 };
 
-hipError_t launch_moe_tiles(const MoeGemm &p, int tm, int cus, hipStream_t stream);
-hipError_t launch_moe_rows(const MoeGemm &p, hipStream_t stream);
+// rows: 64 or 256 per output tile
+hipError_t launch_moe_tiles(const MoeGemm &p, int rows, int cus, hipStream_t stream);
 hipError_t launch_moe_dw(const MoeGemmDw &p, int cus, hipStream_t stream);
 
 struct MoeRoute {

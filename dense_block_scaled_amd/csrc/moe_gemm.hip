@@ -75,20 +75,6 @@ __device__ __forceinline__ void dma(const i32x4 &words, uint8_t *lds, uint32_t d
                      : "memory");
 }
 
-// TM x 256 output tiles of 8 waves (2 x 4), each TM / 2 x 64, over NS slots.
-// AMN / BMN: the operand's slots hold K-rows (see Mn in gemm_kernel.h).
-template <int TM_, int NS_, bool AMN_, bool BMN_>
-struct Tile {
-    static constexpr int TM = TM_, TN = 256, NS = NS_, WM = 2, WN = 4, NW = 8, kThreads = 512;
-    static constexpr bool AMN = AMN_, BMN = BMN_;
-    static constexpr int MB = TM / WM / 32, NB = TN / WN / 32;
-    static constexpr int QA = TM / 8 / NW, QB = TN / 8 / NW;       // wave-loads per wave and stage
-    static constexpr int kSlotA = TM * kRowBytes, kSlotB = TN * kRowBytes;
-    static constexpr int kLdsA = 0, kLdsB = NS * kSlotA, kRing = NS * (kSlotA + kSlotB);
-    static constexpr int KS = 64;                                  // K per stage
-    static_assert(QA > 0 && MB > 0, "every wave loads and computes");
-};
-
 struct Lane {
     int lane, h, lr, w, wm, wn;
 };
@@ -103,85 +89,6 @@ __device__ __forceinline__ Lane lane_of()
     c.wm = c.w / 4;
     c.wn = c.w % 4;
     return c;
-}
-
-template <class S, int MBA = S::MB>
-struct Frag2 {
-    bf16x8 a[MBA], b[S::NB];
-};
-
-// K-major A: the two wave rows take the tile's blocks of 32 rows in turn
-// (wave row wm: blocks wm, wm + 2, ...), so a tile whose group ends early
-// leaves both with the same number of blocks, MBA, to compute.  Blocks of one
-// wave lie 64 rows apart, where the swizzle repeats.
-template <class S>
-__device__ __forceinline__ bf16x8 read_a2(const uint8_t *lds, uint32_t fa, int kk, int i)
-{
-    if constexpr (S::AMN) return read_frag_mn<kBF16, S::TM>(lds, fa, 0, kk, i);
-    else return lds_read<bf16x8>(lds, (fa ^ (uint32_t)(kk << 5)) + (uint32_t)(64 * kRowBytes * i));
-}
-
-// One k-step: the MFMAs of `cur` while k-step PH of the slot behind fa / fb
-// is read into `nxt` (if RD); after MFMA i, issue(i).
-template <class S, int MBA, int PH, bool RD, class ISSUE>
-__device__ __forceinline__ void phase2(f32x16 (&acc)[MBA][S::NB], Frag2<S, MBA> &cur, Frag2<S, MBA> &nxt,
-                                       const uint8_t *lds, uint32_t fa, uint32_t fb, ISSUE &&issue)
-{
-    if constexpr (RD) {
-#pragma unroll
-        for (int i = 0; i < MBA; ++i) nxt.a[i] = read_a2<S>(lds, fa, PH, i);
-#pragma unroll
-        for (int j = 0; j < S::NB; ++j) {
-            if constexpr (S::BMN) nxt.b[j] = read_frag_mn<kBF16, S::TN>(lds, fb, 0, PH, j);
-            else nxt.b[j] = read_frag<kBF16>(lds, fb, 0, PH, j);
-        }
-    }
-    DBS_FENCE();
-#pragma unroll
-    for (int i = 0; i < MBA; ++i) {
-#pragma unroll
-        for (int j = 0; j < S::NB; ++j) {
-            mma1<kBF16, 0>(acc[i][j], cur.a[i], 0u, cur.b[j], 0u);
-            DBS_FENCE();
-            issue(PH * MBA * S::NB + i * S::NB + j);
-            DBS_FENCE();
-        }
-    }
-}
-
-// One stage of four k-steps out of the slot behind fa / fb.  On entry F1
-// holds the previous stage's last k-step, whose MFMAs come first; piece q of
-// the stage being loaded goes out after MFMA q.
-template <class S, int MBA, class PIECE>
-__device__ __forceinline__ void stage2(f32x16 (&acc)[MBA][S::NB], Frag2<S, MBA> &F0, Frag2<S, MBA> &F1,
-                                       const uint8_t *lds, uint32_t fa, uint32_t fb, PIECE &&piece)
-{
-    auto issue = [&](int i) {
-        if (i < S::QB) piece(i);
-    };
-    static_assert(S::QA <= S::QB && S::QB <= 4 * S::NB, "piece q loads A (q < QA) and B");
-    phase2<S, MBA, 0, true>(acc, F1, F0, lds, fa, fb, issue);
-    phase2<S, MBA, 1, true>(acc, F0, F1, lds, fa, fb, issue);
-    phase2<S, MBA, 2, true>(acc, F1, F0, lds, fa, fb, issue);
-    phase2<S, MBA, 3, true>(acc, F0, F1, lds, fa, fb, issue);
-    stage_barrier<(S::NS - 2) * (S::QA + S::QB)>();
-}
-
-// LDS addresses of the lane's fragment reads: slot 0, block 0, k-step 0.
-template <class S>
-__device__ __forceinline__ uint32_t frag_a(const Lane &c)
-{
-    if constexpr (S::AMN) return mn_base<kBF16, S::TM>(c.lane, c.wm * (S::TM / S::WM), S::kLdsA);
-    const int r = c.wm * 32 + c.lr;
-    return (uint32_t)(S::kLdsA + r * kRowBytes + ((c.h ^ swz(r)) << 4));
-}
-
-template <class S>
-__device__ __forceinline__ uint32_t frag_b(const Lane &c)
-{
-    if constexpr (S::BMN) return mn_base<kBF16, S::TN>(c.lane, c.wn * (S::TN / S::WN), S::kLdsB);
-    const int r = c.wn * (S::TN / S::WN) + c.lr;
-    return (uint32_t)(S::kLdsB + r * kRowBytes + ((c.h ^ swz(r)) << 4));
 }
 
 // ------------------------------------------------------------ group tables
@@ -429,10 +336,8 @@ __device__ __forceinline__ void core_stage(Acc &acc, const uint8_t *lds, uint32_
 
 // One 32 x 32 block of results as bf16 rows r0 .. mend-1, columns n0 ..
 // ncols-1 of D (ld columns), through the wave's 2 KiB buffer and in 16-byte
-// pieces (vec) or by element.  B16: the results of 16 x 16 blocks (value(u, v,
-// q): row block u, column block v, register q), otherwise of one 32 x 32
-// MFMA block (value(0, 0, q)).
-template <bool B16, class VALUE>
+// pieces (vec) or by element; value(u, v, q): register q of 16 x 16 block (u, v).
+template <class VALUE>
 __device__ __forceinline__ void store_block(uint8_t *buf, uint8_t *D, int64_t ld, int r0, int mend, int n0, int ncols,
                                             int vec, Lane c, VALUE &&value)
 {
@@ -440,44 +345,32 @@ __device__ __forceinline__ void store_block(uint8_t *buf, uint8_t *D, int64_t ld
     asm volatile("" : "+v"(c.lane));
     const int left = __builtin_amdgcn_readfirstlane(max(0, min(32, mend - r0)));
     const __amdgpu_buffer_rsrc_t rd = make_rsrc(D + (int64_t)r0 * ld * 2, (uint32_t)left * (uint32_t)ld * 2u);
-    // four values of consecutive columns: group g of four, at row and column
-    auto quad = [&](int g, int &row, int &col, float (&v)[4]) {
-        if constexpr (B16) {
-            row = 16 * (g >> 1) + (c.lane & 15);
-            col = 16 * (g & 1) + 4 * (c.lane >> 4);
-        } else {
-            row = c.lane & 31;
-            col = 8 * g + 4 * (c.lane >> 5);
-        }
-#pragma unroll
-        for (int q = 0; q < 4; ++q) v[q] = B16 ? value(g >> 1, g & 1, q) : value(0, 0, 4 * g + q);
-    };
+    // block g's four values of consecutive columns lie at row and column
+    const int row0 = c.lane & 15, col0 = 4 * (c.lane >> 4);
     if (vec) {
 #pragma unroll
         for (int g = 0; g < 4; ++g) {
-            int row, col;
-            float v[4];
-            quad(g, row, col, v);
+            const int u = g >> 1, v = g & 1, row = 16 * u + row0, col = 16 * v + col0;
             *reinterpret_cast<u32x2 *>(buf + row * 64 + (((col >> 3) ^ ((row >> 1) & 3)) << 4) + 2 * (col & 4)) =
-                u32x2{pack_bf16(v[0], v[1]), pack_bf16(v[2], v[3])};
+                u32x2{pack_bf16(value(u, v, 0), value(u, v, 1)), pack_bf16(value(u, v, 2), value(u, v, 3))};
         }
 #pragma unroll
         for (int q = 0; q < 2; ++q) {
             const int r = q * 16 + (c.lane >> 2), ch = c.lane & 3, n = n0 + ch * 8;
             const i32x4 v = *reinterpret_cast<const i32x4 *>(buf + r * 64 + 16 * (ch ^ ((r >> 1) & 3)));
-            __builtin_amdgcn_raw_buffer_store_b128(v, rd, n < ncols ? (uint32_t)(r * (int)ld + n) * 2u : kOOB, 0, kStoreCached);
+            __builtin_amdgcn_raw_buffer_store_b128(v, rd, n < ncols ? (uint32_t)(r * (int)ld + n) * 2u : kOOB, 0,
+                                                   kStoreCached);
         }
     } else {
 #pragma unroll
         for (int g = 0; g < 4; ++g) {
-            int row, col;
-            float v[4];
-            quad(g, row, col, v);
+            const int u = g >> 1, v = g & 1;
 #pragma unroll
             for (int q = 0; q < 4; ++q) {
-                const int n = n0 + col + q;
-                __builtin_amdgcn_raw_buffer_store_b16((uint16_t)pack_bf16(v[q], 0.0f), rd,
-                                                      n < ncols ? (uint32_t)(row * (int)ld + n) * 2u : kOOB, 0, kStoreCached);
+                const int n = n0 + 16 * v + col0 + q;
+                __builtin_amdgcn_raw_buffer_store_b16((uint16_t)pack_bf16(value(u, v, q), 0.0f), rd,
+                                                      n < ncols ? (uint32_t)((16 * u + row0) * (int)ld + n) * 2u : kOOB, 0,
+                                                      kStoreCached);
             }
         }
     }
@@ -715,12 +608,12 @@ __global__ __launch_bounds__(512, 1) void moe_tiles_256(MoeGemm p)
         for (int i = 0; i < NLO + NHI; ++i) {
             const int r0 = cur.m0 + (2 * i + c.wm) * 32;
             if constexpr (GATE) {
-                store_block<true>(buf, p.D, p.ncols, r0, cur.mend, cur.n0 + c.wn * 32, p.ncols, p.vec, c,
+                store_block(buf, p.D, p.ncols, r0, cur.mend, cur.n0 + c.wn * 32, p.ncols, p.vec, c,
                             [&](int u, int v, int q) { return gated(acc[2 * i + u][v][q], acc[2 * i + u][2 + v][q]); });
             } else {
 #pragma unroll
                 for (int j = 0; j < 2; ++j)
-                    store_block<true>(buf, p.D, p.ncols, r0, cur.mend, cur.n0 + (BMN ? j * 128 + c.wn * 32 : c.wn * 64 + j * 32),
+                    store_block(buf, p.D, p.ncols, r0, cur.mend, cur.n0 + (BMN ? j * 128 + c.wn * 32 : c.wn * 64 + j * 32),
                                 p.ncols, p.vec, c,
                                       [&](int u, int v, int q) { return acc[2 * i + u][2 * j + v][q]; });
             }
@@ -742,18 +635,36 @@ __global__ __launch_bounds__(512, 1) void moe_tiles_256(MoeGemm p)
     asm volatile("s_waitcnt vmcnt(0)" ::: "memory");   // nothing is left to land in LDS
 }
 
-// 64-row tiles, for groups of fewer rows.  GATE: see the head of the file.
-template <class S, bool GATE>
+// 64-row tiles over a deep ring, for a few rows per expert: the time is the
+// reading of W, or a few workgroups' walk along K, where a stage costs the
+// loads' latency over the stages they are ahead.  64 columns and eight slots
+// of 16 KiB; an MN-major W 128 columns and six slots of 24 KiB (its pieces of
+// memory are a tile's K-rows, 256 bytes).  8 waves (4 x 2) of 16 rows and
+// half of the columns.  With the gate a wave's 32 rows of W are 16 gate rows
+// and the 16 up rows that meet them.
+//
+// Against 64 x 256 tiles over three slots (0.7 us a stage): 8 experts of
+// 4096 x 4096, 4 rows 42 us against 45, 32 rows 44 against 63; 64 experts of
+// 2816 x 2048, 16 rows 143 against 169.
+template <bool BMN>
+struct Deep {
+    static constexpr int TN = BMN ? 128 : 64, NS = BMN ? 6 : 8, NB = TN / 32, QB = TN / 64;
+    static constexpr int kA = 64 * kRowBytes, kSlot = kA + TN * kRowBytes, kWait = (NS - 2) * (1 + QB);
+};
+
+template <bool BMN, bool GATE>
 __global__ __launch_bounds__(512, 1) void moe_tiles_64(MoeGemm p)
 {
-    __shared__ __attribute__((aligned(1024))) uint8_t lds[S::kRing];
-    __shared__ Table<S::TM> tab;
-    static_assert(!(GATE && S::BMN), "the gate takes K-major matrices");
-    constexpr int MB = S::MB, NB = S::NB;
-    constexpr int TNO = GATE ? S::TN / 2 : S::TN;      // output columns of a tile
+    using S = Deep<BMN>;
+    constexpr int NB = S::NB;
+    __shared__ __attribute__((aligned(1024))) uint8_t lds[S::NS * S::kSlot];
+    __shared__ Table<64> tab;
+    static_assert(!(GATE && BMN), "the gate takes K-major matrices");
+    constexpr int TNO = GATE ? S::TN / 2 : S::TN;
 
     const Lane c = lane_of();
-    const int lda = p.K * 2;
+    const int wm = c.w >> 1, wn = c.w & 1, j = c.lane & 15, g = c.lane >> 4;
+    const int lda = p.K * 2, ldb = BMN ? p.N * 2 : lda;
     const int tiles_n = (p.ncols + TNO - 1) / TNO;
     fill_table(tab, p, c);
     __syncthreads();
@@ -763,80 +674,53 @@ __global__ __launch_bounds__(512, 1) void moe_tiles_64(MoeGemm p)
     const int nwg = gridDim.x;
     int tile = first_tile();
     if (tile >= ntiles) return;
-    const int nk = max((p.K + S::KS - 1) / S::KS, S::NS - 1);
+    const int nk = max((p.K + 63) / 64, S::NS - 1);
     auto find = [&](int id) { return find_tile(tab, p.E, ntiles, tiles_n, TNO, id, c); };
 
-    // where a tile's stages come from
-    struct Source {
-        i32x4 ra, rb;
-        uint32_t a[S::QA];       // the lane's byte offset in ra per wave-load, its chunk included
-        int f0;                  // the tile's first output column
-    } src;
-    // the rows of X behind the next tile's wave-loads, read while this tile is
-    // computed (~0: none, a zero row)
-    uint32_t row[S::QA];
-    uint32_t x4 = (uint32_t)(((c.lane & 7) ^ (c.lane >> 3)) << 4);
-    const int ldb = S::BMN ? p.N * 2 : lda;            // bytes of a row of W as stored
-    uint32_t r8ldb = (uint32_t)((c.lane >> 3) * ldb);
-    uint32_t mb[2] = {};
-    if constexpr (S::BMN) {
-        mb[0] = mn_dma_lane<kBF16, S::TN>(c.lane, 0, ldb);
-        mb[1] = mn_dma_lane<kBF16, S::TN>(c.lane, 1, ldb);
-    }
+    // wave w loads rows 8 w .. of A and of W (K-rows of an MN-major W)
+    i32x4 ra, rb;
+    const int lrow = 8 * c.w + (c.lane >> 3);
+    uint32_t aoff = 0, boff = BMN ? mn_part_lane(c, ldb) + (uint32_t)(8 * c.w * ldb) : 0u, row = 0;
+    uint32_t kx = (uint32_t)(((c.lane & 7) ^ swz(lrow)) << 4);     // the lane's chunk of its row
     auto fetch = [&](const RowTile &r) {
-#pragma unroll
-        for (int q = 0; q < S::QA; ++q) {
-            const int m = (c.w * S::QA + q) * 8 + (c.lane >> 3);
-            row[q] = !p.rows ? (uint32_t)m : r.m0 + m < r.mend ? (uint32_t)p.rows[r.m0 + m] : ~0u;
-        }
+        row = !p.rows ? (uint32_t)lrow : r.m0 + lrow < r.mend ? (uint32_t)p.rows[r.m0 + lrow] : ~0u;
     };
     auto aim = [&](const RowTile &r) {
         if (r.blocks == 0) {
-            src.ra = src.rb = words_of(nullptr, 0);
+            ra = rb = words_of(nullptr, 0);
             return;
         }
         const int64_t wbytes = (int64_t)p.N * p.K * 2;
         const uint8_t *wg = p.W + r.g * wbytes;
-        src.f0 = r.n0;
-        if constexpr (S::BMN)
-            src.rb = words_of(wg + r.n0 * 2, (uint32_t)(wbytes - r.n0 * 2));
-        else if constexpr (GATE)
-            src.rb = words_of(wg, (uint32_t)wbytes);
-        else
-            src.rb = words_of(wg + (int64_t)r.n0 * lda, (uint32_t)(min(p.N - r.n0, S::TN) * lda));
-        const uint32_t have = p.rows ? (uint32_t)p.T : (uint32_t)min(r.mend - r.m0, S::TM);
-        src.ra = words_of(p.rows ? p.X : p.X + (int64_t)r.m0 * lda, have * (uint32_t)lda);
-#pragma unroll
-        for (int q = 0; q < S::QA; ++q) {
-            const int L = c.w * S::QA + q;
-            src.a[q] = (row[q] < have ? row[q] * (uint32_t)lda : kRowOOB) + (x4 ^ (uint32_t)((L & 7) << 4));
+        const uint32_t have = p.rows ? (uint32_t)p.T : (uint32_t)min(r.mend - r.m0, 64);
+        ra = words_of(p.rows ? p.X : p.X + (int64_t)r.m0 * lda, have * (uint32_t)lda);
+        aoff = row < have ? row * (uint32_t)lda : kRowOOB;
+        if constexpr (BMN) {
+            rb = words_of(wg + r.n0 * 2, (uint32_t)(wbytes - r.n0 * 2));
+        } else if constexpr (GATE) {
+            // rows 32 wn + 16 u + q of the slot: row n0 + 16 wn + q of matrix u
+            const int f = r.n0 + (lrow >> 5) * 16 + (lrow & 15);
+            rb = words_of(wg, (uint32_t)wbytes);
+            boff = f < p.ncols ? (uint32_t)((((lrow >> 4) & 1) * p.ncols + f) * lda) : kRowOOB;
+        } else {
+            rb = words_of(wg + (int64_t)r.n0 * lda, (uint32_t)(min(p.N - r.n0, 64) * lda));
+            boff = (uint32_t)(lrow * lda);
         }
     };
-    auto load = [&](int slot, int ks, int q) {
-        const int k0 = ks * kRowBytes;
-        if (q < S::QA) {
-            const int L = c.w * S::QA + q;
-            const int kc = (int)(x4 ^ (uint32_t)((L & 7) << 4));
-            dma<16>(src.ra, lds, S::kLdsA + slot * S::kSlotA + L * 1024, kc < lda - k0 ? src.a[q] + k0 : kRowOOB);
-        }
-        const int L = c.w * S::QB + q;
-        const uint32_t dst = S::kLdsB + slot * S::kSlotB + L * 1024;
-        if constexpr (S::BMN) {
-            const uint32_t row = (uint32_t)(ks * S::KS + L * 2);           // two K-rows a wave-load
-            dma<16>(src.rb, lds, dst, row < (uint32_t)p.K ? mb[q & 1] + row * (uint32_t)ldb : kOOB);
-        } else {
-            const int kc = (int)(x4 ^ (uint32_t)((L & 7) << 4));
-            uint32_t off = r8ldb + (uint32_t)(kc + k0);
-            bool in = kc < lda - k0;
-            if constexpr (GATE) {
-                // rows 64 wn + 32 j + c of the slot: row f0 + 32 wn + c of matrix j
-                const int r0 = L * 8, f = src.f0 + (r0 >> 6) * 32 + (r0 & 31);
-                off += (uint32_t)((((r0 >> 5) & 1) * p.ncols + f) * lda);
-                in = in && f + (c.lane >> 3) < p.ncols;
-            } else {
-                off += (uint32_t)(L * 8 * lda);
+    auto load = [&](int slot, int ks) {
+        const uint32_t dst = slot * S::kSlot;
+        const int kc = (int)kx + ks * kRowBytes;
+        const bool in = kc < lda;
+        dma<16>(ra, lds, dst + c.w * 1024, in ? aoff + kc : kRowOOB);
+        if constexpr (BMN) {
+#pragma unroll
+            for (int q = 0; q < S::QB; ++q) {
+                const uint32_t k = (uint32_t)(ks * 64 + 4 * q);            // four K-rows a wave-load
+                dma<16>(rb, lds, dst + S::kA + (c.w * S::QB + q) * 1024,
+                        k + 8 * c.w < (uint32_t)p.K ? boff + k * (uint32_t)ldb : kOOB);
             }
-            dma<16>(src.rb, lds, dst, in ? off : kOOB);
+        } else {
+            dma<16>(rb, lds, dst + S::kA + c.w * 1024, in ? boff + kc : kRowOOB);
         }
     };
 
@@ -844,58 +728,62 @@ __global__ __launch_bounds__(512, 1) void moe_tiles_64(MoeGemm p)
     fetch(cur);
     aim(cur);
 #pragma unroll
-    for (int f = 0; f < S::NS - 1; ++f) {
-#pragma unroll
-        for (int q = 0; q < S::QB; ++q) load(f, f, q);
-    }
-    uint32_t fa = frag_a<S>(c), fb = frag_b<S>(c);
-    stage_barrier<(S::NS - 2) * (S::QA + S::QB)>();
+    for (int f = 0; f < S::NS - 1; ++f) load(f, f);
+    const int ar = 16 * wm + j;
+    uint32_t fa = (uint32_t)(ar * kRowBytes + ((kgroup(g) ^ swz(ar)) << 4)), fb = S::kA + part_base<BMN>(c, wn);
+    stage_barrier<S::kWait>();
 
     int rs = 0;               // slot the next stage reads
     for (;;) {
-        // the next tile's rows are looked up while this one is computed
         tile += nwg;
         next = find(tile);
         fetch(next);
-        f32x16 acc[MB][NB];
-#pragma unroll
-        for (int i = 0; i < MB; ++i)
-#pragma unroll
-            for (int j = 0; j < NB; ++j) acc[i][j] = f32x16{};
-        Frag2<S> F0, F1{};
-        int xs = 0;           // slot the last stage read
+        f32x4 acc[NB] = {};
         for (int s = 0; s < nk; ++s) {
             int ks = s + S::NS - 1;
             if (ks >= nk) {
                 ks -= nk;
                 if (ks == 0) aim(next);
             }
-            const int ls = rs == 0 ? S::NS - 1 : rs - 1;
-            asm volatile("" : "+v"(x4), "+v"(r8ldb), "+v"(fa), "+v"(fb));
-            stage2<S, MB>(acc, F0, F1, lds, fa + (uint32_t)(rs * S::kSlotA), fb + (uint32_t)(rs * S::kSlotB),
-                          [&](int q) { load(ls, ks, q); });
-            xs = rs;
+            asm volatile("" : "+v"(kx), "+v"(fa), "+v"(fb));
+            const uint32_t so = (uint32_t)(rs * S::kSlot);
+            bf16x8 a[2], b[2][NB];
+#pragma unroll
+            for (int kk = 0; kk < 2; ++kk) {
+                a[kk] = lds_read<bf16x8>(lds, (fa ^ (uint32_t)(kk << 6)) + so);
+#pragma unroll
+                for (int u = 0; u < NB; ++u) b[kk][u] = part_frag<BMN>(lds, fb + so, kk, u >> 1, u & 1);
+            }
+            load(rs == 0 ? S::NS - 1 : rs - 1, ks);
+#pragma unroll
+            for (int kk = 0; kk < 2; ++kk)
+#pragma unroll
+                for (int u = 0; u < NB; ++u)
+                    acc[u] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(b[kk][u], a[kk], acc[u], 0, 0, 0);
+            stage_barrier<S::kWait>();
             rs = rs + 1 == S::NS ? 0 : rs + 1;
         }
-        phase2<S, MB, 0, false>(acc, F1, F0, lds, fa, fb, [](int) {});
-
-        // the slot the last stage read is free until the next tile's first
-        // stage refills it: its B part holds the waves' buffers
-        uint8_t *buf = lds + S::kLdsB + xs * S::kSlotB + c.w * 2048;
+        // lane: row 16 wm + l % 16, four columns of each block (block u: columns
+        // 32 wn + 64 (u / 2) + 16 (u % 2) ..)
+        const int r0 = cur.m0 + 16 * wm, left = __builtin_amdgcn_readfirstlane(max(0, min(16, cur.mend - r0)));
+        const __amdgpu_buffer_rsrc_t rd = make_rsrc(p.D + (int64_t)r0 * p.ncols * 2, (uint32_t)left * (uint32_t)p.ncols * 2u);
 #pragma unroll
-        for (int i = 0; i < MB; ++i) {
-            const int r0 = cur.m0 + (2 * i + c.wm) * 32;
-            if constexpr (GATE) {
-                store_block<false>(buf, p.D, p.ncols, r0, cur.mend, cur.n0 + c.wn * 32, p.ncols, p.vec, c,
-                            [&](int, int, int q) { return gated(acc[i][0][q], acc[i][1][q]); });
+        for (int u = 0; u < (GATE ? NB / 2 : NB); ++u) {
+            float v[4];
+#pragma unroll
+            for (int q = 0; q < 4; ++q) v[q] = GATE ? gated(acc[0][q], acc[1][q]) : acc[u][q];
+            const int n = cur.n0 + (GATE ? 16 : 32) * wn + 64 * (u >> 1) + 16 * (u & 1) + 4 * g;
+            const uint32_t at = (uint32_t)(j * p.ncols + n) * 2u;
+            const uint32_t lo = pack_bf16(v[0], v[1]), hi = pack_bf16(v[2], v[3]);
+            if (p.vec) {
+                __builtin_amdgcn_raw_buffer_store_b64(u32x2{lo, hi}, rd, n < p.ncols ? at : kOOB, 0, kStoreCached);
             } else {
+                const uint16_t w[4] = {(uint16_t)lo, (uint16_t)(lo >> 16), (uint16_t)hi, (uint16_t)(hi >> 16)};
 #pragma unroll
-                for (int j = 0; j < NB; ++j)
-                    store_block<false>(buf, p.D, p.ncols, r0, cur.mend, cur.n0 + c.wn * 64 + j * 32, p.ncols, p.vec, c,
-                                [&](int, int, int q) { return acc[i][j][q]; });
+                for (int q = 0; q < 4; ++q)
+                    __builtin_amdgcn_raw_buffer_store_b16(w[q], rd, n + q < p.ncols ? at + 2 * q : kOOB, 0, kStoreCached);
             }
         }
-        asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory");
         if (next.blocks == 0) break;
         cur = next;
     }
@@ -1064,7 +952,7 @@ __global__ __launch_bounds__(512, 1) void moe_dw(MoeGemmDw p)
                         __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(i32x4, v), rd, off, 0, kStoreCached);
                     }
                 } else {
-                    store_block<true>(buf, p.dW + (int64_t)cur.g * p.N * p.K * 2, p.K, r0, p.N, k0, p.K, 1, c,
+                    store_block(buf, p.dW + (int64_t)cur.g * p.N * p.K * 2, p.K, r0, p.N, k0, p.K, 1, c,
                                 [&](int u, int v, int q) { return acc[2 * i + u][2 * j + v][q]; });
                 }
             }
@@ -1078,25 +966,24 @@ __global__ __launch_bounds__(512, 1) void moe_dw(MoeGemmDw p)
 }
 
 // At most as many workgroups as there can be tiles of tm rows and tno columns.
-dim3 tile_grid(const MoeGemm &p, int tm, int cus)
+dim3 tile_grid(const MoeGemm &p, int tm, int tno, int cus)
 {
-    const int tno = p.gate ? 128 : 256;
     const int64_t most = ((int64_t)p.M / tm + (p.M < p.E ? p.M : p.E)) * ((p.ncols + tno - 1) / tno);
     return dim3((uint32_t)(most < cus ? most : cus));
 }
 
 }  // namespace
 
-hipError_t launch_moe_tiles(const MoeGemm &p, int tm, int cus, hipStream_t stream)
+hipError_t launch_moe_tiles(const MoeGemm &p, int rows, int cus, hipStream_t stream)
 {
-    const dim3 grid = tile_grid(p, tm, cus), block(512);
-    using Small = Tile<64, 3, false, false>;
-    using SmallMn = Tile<64, 3, false, true>;
-    if (tm == 64) {
-        if (p.wmn) hipLaunchKernelGGL((moe_tiles_64<SmallMn, false>), grid, block, 0, stream, p);
-        else if (p.gate) hipLaunchKernelGGL((moe_tiles_64<Small, true>), grid, block, 0, stream, p);
-        else hipLaunchKernelGGL((moe_tiles_64<Small, false>), grid, block, 0, stream, p);
+    const dim3 block(512);
+    if (rows == 64) {
+        const dim3 grid = tile_grid(p, 64, p.wmn ? Deep<true>::TN : p.gate ? Deep<false>::TN / 2 : Deep<false>::TN, cus);
+        if (p.wmn) hipLaunchKernelGGL((moe_tiles_64<true, false>), grid, block, 0, stream, p);
+        else if (p.gate) hipLaunchKernelGGL((moe_tiles_64<false, true>), grid, block, 0, stream, p);
+        else hipLaunchKernelGGL((moe_tiles_64<false, false>), grid, block, 0, stream, p);
     } else {
+        const dim3 grid = tile_grid(p, 256, p.gate ? 128 : 256, cus);
         if (p.wmn) hipLaunchKernelGGL((moe_tiles_256<true, false>), grid, block, 0, stream, p);
         else if (p.gate) hipLaunchKernelGGL((moe_tiles_256<false, true>), grid, block, 0, stream, p);
         else hipLaunchKernelGGL((moe_tiles_256<false, false>), grid, block, 0, stream, p);

@@ -171,8 +171,7 @@ def test_calls_repeat_bit_for_bit(T, M, E, N, K):
 
 
 def test_one_row_has_the_same_bits_in_any_company():
-    """A row's product does not depend on its group's other rows: on the few-row
-    kernel against itself, and on the tile kernels against each other."""
+    """A row's product does not depend on its group's other rows."""
     g = _gen(7)
     E, N, K = 4, 160, 256
     X, W = _bf16(g, 4000, K).cuda(), _bf16(g, E, N, K).cuda()

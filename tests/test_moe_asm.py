@@ -14,7 +14,7 @@ import pytest
 from tests import test_asm_hazards as hazards
 from tests import test_lds_poison_build as poison
 
-UNITS = ["moe_gemm.hip", "moe_rows.hip"]
+UNITS = ["moe_gemm.hip"]
 
 
 @pytest.fixture(scope="module")
