@@ -792,6 +792,39 @@ __global__ __launch_bounds__(512, 1) void moe_tiles_64(MoeGemm p)
 
 // ---------------------------------------------------------------------- dw
 
+// The groups of E with work (all, or those with rows) into order, by their
+// number of rows in steps of half an octave, the longest first: tiles are
+// handed out in a snake, as the products' are, and end together the better
+// the smaller the last ones are.  By one wave; returns how many.
+__device__ __forceinline__ int sort_groups(uint16_t *order, const int32_t *first, int E, bool all, const Lane &c)
+{
+    auto step = [](int rows) { return rows > 0 ? (int)(__builtin_bit_cast(uint32_t, (float)rows) >> 22) : 0; };
+    int hi = 0, lo = 1 << 30;
+    for (int g = c.lane; g < E; g += 64) {
+        const int k = step(first[g + 1] - first[g]);
+        hi = max(hi, k);
+        lo = min(lo, k > 0 || all ? k : lo);
+    }
+#pragma unroll
+    for (int d = 32; d; d /= 2) {
+        hi = max(hi, __shfl_xor(hi, d));
+        lo = min(lo, __shfl_xor(lo, d));
+    }
+    int n = 0;
+    // (from 0, no rows, to the first step, one row, lie steps that no group has)
+    for (int k = hi; k >= lo; k = k == 254 && lo == 0 ? 0 : k - 1) {
+        for (int g0 = 0; g0 < E; g0 += 64) {
+            const int g = g0 + c.lane;
+            const bool here = g < E && step(first[g + 1] - first[g]) == k;
+            const uint64_t who = __ballot(here);
+            if (here) order[n + __popcll(who & (((uint64_t)1 << c.lane) - 1))] = (uint16_t)g;
+            n += __popcll(who);
+        }
+        if (k == 0) break;
+    }
+    return n;
+}
+
 // GATHER: rows of X through p.rows.  F32: dW holds fp32.
 //
 // Gathered rows: a wave loads eight K-rows of X a stage.  Their indices reach
@@ -803,19 +836,24 @@ __global__ __launch_bounds__(512, 1) void moe_dw(MoeGemmDw p)
 {
     __shared__ __attribute__((aligned(1024))) uint8_t lds[kCoreLds];
     __shared__ int32_t first[kMoeMaxExperts + 1];
-    __shared__ uint16_t used[kMoeMaxExperts + 1];      // groups with tiles before a group
+    __shared__ uint16_t order[kMoeMaxExperts + 1];     // groups with tiles, the longest sums first
+    __shared__ int32_t count;
     __shared__ uint32_t rowbuf[GATHER ? 8 * 256 : 1];
     constexpr int kStores = F32 ? 32 : 16;             // store instructions of a tile
 
     const Lane c = lane_of();
     const int lda = p.N * 2, ldb = p.K * 2;            // bytes of a row of dY, of X
     const int tiles_n = (p.N + 255) / 256, tiles_k = (p.K + 255) / 256, per = tiles_n * tiles_k;
-    if (c.w == 0)
-        group_table<true>(first, used, p.offsets, p.E, p.M, c, [&](int rows) { return !p.accumulate || rows > 0; });
+    if (c.w == 0) {
+        // (the table's second part, rows before a group, is not used)
+        group_table<true>(first, order, p.offsets, p.E, p.M, c, [](int) { return 0; });
+        __builtin_amdgcn_wave_barrier();
+        const int n = sort_groups(order, first, p.E, !p.accumulate, c);
+        if (c.lane == 0) count = n;
+    }
     __syncthreads();
-    const int ntiles = __builtin_amdgcn_readfirstlane((int)used[p.E]) * per, nwg = gridDim.x;
-    int tile = first_tile();
-    if (tile >= ntiles) return;
+    const int ntiles = __builtin_amdgcn_readfirstlane(count) * per, nwg = gridDim.x, self = first_tile();
+    if (self >= ntiles) return;
 
     struct Ref {
         int lo, hi, n0, k0, g, nk;
@@ -825,7 +863,7 @@ __global__ __launch_bounds__(512, 1) void moe_dw(MoeGemmDw p)
         Ref r{};
         r.nk = 2;
         if (id >= ntiles) return r;
-        r.g = group_of(used, p.E, id / per, c);
+        r.g = __builtin_amdgcn_readfirstlane((int)order[id / per]);
         r.lo = __builtin_amdgcn_readfirstlane(first[r.g]);
         r.hi = __builtin_amdgcn_readfirstlane(first[r.g + 1]);
         const int local = id % per;
@@ -835,7 +873,8 @@ __global__ __launch_bounds__(512, 1) void moe_dw(MoeGemmDw p)
         r.nk = max(2, (r.hi - r.lo + 63) / 64);
         return r;
     };
-    Ref cur = find(tile), next = cur;
+    auto tile_of = [&](int round) { return round * nwg + (round & 1 ? nwg - 1 - self : self); };
+    Ref cur = find(self), next = cur;
 
     // What the loads read: stage lk of tile src, rows behind wa and wb.
     Ref src = cur;
@@ -899,9 +938,9 @@ __global__ __launch_bounds__(512, 1) void moe_dw(MoeGemmDw p)
     uint8_t *buf = lds + kStage + c.w * 2048;
     turn_end<kInFlight>();
 
-    int slot = 0, stored = 0, parity = 0;
+    int slot = 0, stored = 0, parity = 0, round = 0;
     for (;;) {
-        tile += nwg;
+        const int tile = tile_of(++round);
         next = find(tile);
         Acc acc;
 #pragma unroll

@@ -22,8 +22,9 @@
 // on the order of atomics, so results repeat bit for bit.  More than 64
 // tokens take three kernels: selection with the counts of each 64 tokens; an
 // exclusive sum down every expert's column of counts; and the placing, where
-// every workgroup sums the expert totals for itself.  Up to 64 tokens take
-// one kernel, which is what a decoding step's latency asks for.
+// every workgroup sums the expert totals for itself -- and, up to 2048 tokens,
+// the columns too, so that two kernels do.  Up to 64 tokens take one kernel,
+// which is what a decoding step's latency asks for.
 #include <hip/hip_runtime.h>
 #include <float.h>
 #include <stdint.h>
@@ -276,15 +277,34 @@ __global__ __launch_bounds__(1024) void route_columns(int32_t *counts, int64_t n
     }
 }
 
+// DIRECT: every workgroup sums the columns for itself (up to kDirect rows of
+// counts), which leaves out the kernel before.
+template <bool DIRECT>
 __global__ __launch_bounds__(kThreads) void route_place(MoeRoute p, int64_t nb)
 {
     __shared__ uint64_t mask[kMoeMaxExperts];
     __shared__ int32_t base[kMoeMaxExperts + 1];
+    __shared__ int32_t before[DIRECT ? kMoeMaxExperts : 1], total[DIRECT ? kMoeMaxExperts : 1];
     __shared__ int32_t chosen[kRouteTokens * kMoeMaxK];
     __shared__ int32_t part[kThreads / 64];
     const int t = threadIdx.x;
-    for (int e = t; e < p.E; e += kThreads) mask[e] = 0;
-    scan_experts(p.counts + nb * p.E, p.E, base, part);     // (ends with a barrier)
+    for (int e = t; e < p.E; e += kThreads) {
+        mask[e] = 0;
+        if constexpr (DIRECT) {
+            int mine = 0, all = 0;
+#pragma unroll 8
+            for (int r = 0; r < (int)nb; ++r) {
+                const int v = p.counts[(int64_t)r * p.E + e];
+                mine += r < (int)blockIdx.x ? v : 0;
+                all += v;
+            }
+            before[e] = mine;
+            total[e] = all;
+        }
+    }
+    if constexpr (DIRECT) __syncthreads();
+    const int32_t *totals = DIRECT ? total : p.counts + nb * p.E;
+    scan_experts(totals, p.E, base, part);                  // (ends with a barrier)
     if (blockIdx.x == 0)
         for (int e = t; e <= p.E; e += kThreads) p.offsets[e] = base[e];
     const int64_t t0 = (int64_t)blockIdx.x * kRouteTokens;
@@ -295,7 +315,7 @@ __global__ __launch_bounds__(kThreads) void route_place(MoeRoute p, int64_t nb)
         if (e >= 0) atomicOr(reinterpret_cast<unsigned long long *>(&mask[e]), 1ull << (q / p.k - t0));
     }
     __syncthreads();
-    place(p, t0, p0, p1, mask, base, p.counts + (int64_t)blockIdx.x * p.E, chosen);
+    place(p, t0, p0, p1, mask, base, DIRECT ? before : p.counts + (int64_t)blockIdx.x * p.E, chosen);
 }
 
 // dlogits = p (u - sum p u): p the softmax over all experts, or over the
@@ -393,6 +413,9 @@ hipError_t by_experts(int E, const void *logits, const void *other, F &&f)
     return with(std::integral_constant<int, 64>{});
 }
 
+// Rows of counts up to which the placing workgroups sum them for themselves.
+constexpr int kDirect = 32;
+
 int64_t blocks_of(int64_t T) { return (T + kRouteTokens - 1) / kRouteTokens; }
 
 }  // namespace
@@ -418,9 +441,13 @@ hipError_t launch_moe_route(const MoeRoute &p, hipStream_t stream)
         return hipGetLastError();
     });
     if (e != hipSuccess || one) return e;
+    if (nb <= kDirect) {
+        hipLaunchKernelGGL((route_place<true>), dim3(nb), dim3(kThreads), 0, stream, p, nb);
+        return hipGetLastError();
+    }
     hipLaunchKernelGGL(route_columns, dim3((p.E + 15) / 16), dim3(1024), 0, stream, p.counts, nb, p.E);
     if ((e = hipGetLastError()) != hipSuccess) return e;
-    hipLaunchKernelGGL(route_place, dim3(nb), dim3(kThreads), 0, stream, p, nb);
+    hipLaunchKernelGGL((route_place<false>), dim3(nb), dim3(kThreads), 0, stream, p, nb);
     return hipGetLastError();
 }
 

@@ -337,7 +337,7 @@ dbs_status quant_bf16(const float *x, int64_t n, void *out, hipStream_t stream);
  *   token may have no open expert.  +inf counts as the largest finite value.
  *   workspace: device memory of moe_route_workspace(T, E, k) bytes (0 up to
  *   64 tokens), 4-byte aligned, the caller's; calls that share one must not
- *   overlap.  One kernel up to 64 tokens, three above.
+ *   overlap.  One kernel up to 64 tokens, two or three above.
  * moe_route_bwd: dlogits (T x E of `type`, fully written) from the weights'
  *   gradients: p (u - sum p u), p the softmax of moe_route's weights and u the
  *   gradients at the chosen experts; dweights of pairs without an expert are
