@@ -1004,6 +1004,180 @@ __global__ __launch_bounds__(512, 1) void moe_dw(MoeGemmDw p)
     asm volatile("s_waitcnt vmcnt(0)" ::: "memory");   // nothing is left to land in LDS
 }
 
+// 64 (N) x 128 (K) tiles over a ring of five slots of 24 KiB, for calls of so
+// few 256 x 256 tiles that the longest sums decide: a stage costs 0.2 us there
+// where the large tiles' costs 1.3.  8 waves (4 x 2) of 16 x 64.
+//
+// dY's part of a slot: 64 K-rows of 64 columns (128 bytes), wave-load w covers
+// K-rows 8 w .. 8 w + 7; the transposed reads of two groups take 32 bytes of
+// four K-rows each, groups 8 or 16 K-rows apart, and two K-rows share a bank
+// line.  X's part as in the core.  Row indices as in moe_dw, but a tile's
+// first eight stages two tiles ahead: the loads run four stages ahead.
+__device__ __forceinline__ constexpr int narrow_swz(int r) { return 2 * ((r >> 1) & 1) ^ 4 * (((r >> 3) ^ (r >> 4)) & 1); }
+
+template <bool GATHER, bool F32>
+__global__ __launch_bounds__(512, 1) void moe_dw_64(MoeGemmDw p)
+{
+    constexpr int NS = 5, kA = 64 * kRowBytes, kSlotD = kA + 128 * kRowBytes, kWait = (NS - 2) * 3;
+    __shared__ __attribute__((aligned(1024))) uint8_t lds[NS * kSlotD];
+    __shared__ int32_t first[kMoeMaxExperts + 1];
+    __shared__ uint16_t order[kMoeMaxExperts + 1];     // groups with tiles, the longest sums first
+    __shared__ int32_t count;
+    __shared__ uint32_t rowbuf[GATHER ? 8 * 5 * 64 : 1];
+
+    const Lane c = lane_of();
+    const int wm = c.w >> 1, wn = c.w & 1, j = c.lane & 15, g4 = c.lane >> 4;
+    const int lda = p.N * 2, ldb = p.K * 2;            // bytes of a row of dY, of X
+    const int tiles_n = (p.N + 63) / 64, tiles_k = (p.K + 127) / 128, per = tiles_n * tiles_k;
+    if (c.w == 0) {
+        group_table<true>(first, order, p.offsets, p.E, p.M, c, [](int) { return 0; });
+        __builtin_amdgcn_wave_barrier();
+        const int n = sort_groups(order, first, p.E, !p.accumulate, c);
+        if (c.lane == 0) count = n;
+    }
+    __syncthreads();
+    const int ntiles = __builtin_amdgcn_readfirstlane(count) * per, nwg = gridDim.x, self = first_tile();
+    if (self >= ntiles) return;
+
+    struct Ref {
+        int lo, hi, n0, k0, g, nk;
+    };
+    // past the last tile: no rows
+    auto find = [&](int round) {
+        Ref r{};
+        r.nk = NS - 1;
+        const int id = round * nwg + (round & 1 ? nwg - 1 - self : self);
+        if (id >= ntiles) return r;
+        r.g = __builtin_amdgcn_readfirstlane((int)order[id / per]);
+        r.lo = __builtin_amdgcn_readfirstlane(first[r.g]);
+        r.hi = __builtin_amdgcn_readfirstlane(first[r.g + 1]);
+        const int local = id % per;
+        r.n0 = local % tiles_n * 64;
+        r.k0 = local / tiles_n * 128;
+        r.nk = max(NS - 1, (r.hi - r.lo + 63) / 64);
+        return r;
+    };
+
+    // What the loads read: stage lk of tile src (its first indices in buffer fb0), rows behind wa and wb.
+    Ref cur = find(0), next = find(1), src = cur;
+    int lk = 0, fb0 = 0;
+    i32x4 wa, wb;
+    const int arow = 8 * c.w + (c.lane >> 3);
+    const uint32_t la = (uint32_t)(arow * lda + (((c.lane & 7) ^ narrow_swz(arow)) << 4));
+    const uint32_t lb = mn_part_lane(c, GATHER ? 0 : ldb) + (GATHER ? 0u : (uint32_t)(8 * c.w * ldb));
+    const i32x4 wr = words_of(p.rows, GATHER ? (uint32_t)p.M * 4u : 0u);
+    auto batch = [&](const Ref &r, int b, int buffer) {
+        if constexpr (GATHER) {
+            const int m = r.lo + (8 * b + (c.lane >> 3)) * 64 + c.w * 8 + (c.lane & 7);
+            dma<4>(wr, reinterpret_cast<uint8_t *>(rowbuf), (c.w * 5 + buffer) * 256, (uint32_t)m * 4u);
+        }
+    };
+    auto load = [&](int slot) {
+        const int m0 = src.lo + lk * 64, left = min(64, src.hi - m0);
+        const uint32_t dst = slot * kSlotD;
+        uint32_t off[2];
+        if constexpr (GATHER) {
+            const int b = lk >> 3;
+            if ((lk & 7) == 0 && 8 * (b + 1) < src.nk) batch(src, b + 1, 3 + ((b + 1) & 1));
+            const uint32_t *ix = rowbuf + (c.w * 5 + (b == 0 ? fb0 : 3 + (b & 1))) * 64 + (lk & 7) * 8;
+#pragma unroll
+            for (int q = 0; q < 2; ++q) {
+                const int i = q * 4 + g4;
+                const uint32_t row = ix[i];
+                off[q] = c.w * 8 + i < left && row < (uint32_t)p.T ? row * (uint32_t)ldb + lb : kRowOOB;
+            }
+            wb = words_of(p.X + src.k0 * 2, (uint32_t)p.T * (uint32_t)ldb - src.k0 * 2);
+        } else {
+            off[0] = lb;
+            off[1] = lb + (uint32_t)(4 * ldb);
+            wb = words_of(p.X + (int64_t)m0 * ldb + src.k0 * 2, left > 0 ? (uint32_t)left * (uint32_t)ldb - src.k0 * 2 : 0u);
+        }
+        wa = words_of(p.dY + (int64_t)m0 * lda + src.n0 * 2, left > 0 ? (uint32_t)left * (uint32_t)lda - src.n0 * 2 : 0u);
+        dma<16>(wa, lds, dst + c.w * 1024, la);
+#pragma unroll
+        for (int q = 0; q < 2; ++q) dma<16>(wb, lds, dst + kA + (2 * c.w + q) * 1024, off[q]);
+    };
+    auto advance = [&](const Ref &then) {
+        if (++lk == src.nk) {
+            lk = 0;
+            src = then;
+            fb0 = fb0 == 2 ? 0 : fb0 + 1;
+        }
+    };
+
+    batch(cur, 0, 0);
+    batch(next, 0, 1);
+    asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+    for (int f = 0; f < NS - 1; ++f) {
+        load(f);
+        advance(next);
+    }
+    uint32_t fa, fb = kA + part_base<true>(c, wn);
+    {
+        const int r = 8 * kgroup(g4) + (j >> 2);
+        fa = (uint32_t)(r * kRowBytes + ((32 * wm + 8 * (j & 3)) ^ (narrow_swz(r) << 4)));
+    }
+    stage_barrier<kWait>();
+
+    int rs = 0, round = 0;
+    for (;;) {
+        // the tile after the next one: its first indices go out a tile's stages ahead of their use
+        const Ref after = find(round + 2);
+        batch(after, 0, (round + 2) % 3);
+        f32x4 acc[4] = {};
+        for (int s = 0; s < cur.nk; ++s) {
+            asm volatile("" : "+v"(fa), "+v"(fb));
+            const uint32_t so = (uint32_t)(rs * kSlotD);
+            bf16x8 a[2], b[2][4];
+#pragma unroll
+            for (int kk = 0; kk < 2; ++kk) {
+                typedef __attribute__((address_space(3))) i16x4 lds_i16x4;
+                const uint8_t *x = lds + fa + so + kk * 32 * kRowBytes;
+                const i32x2 lo = __builtin_bit_cast(i32x2, __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_i16x4 *)x));
+                const i32x2 hi =
+                    __builtin_bit_cast(i32x2, __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_i16x4 *)(x + 4 * kRowBytes)));
+                a[kk] = __builtin_bit_cast(bf16x8, i32x4{lo[0], lo[1], hi[0], hi[1]});
+#pragma unroll
+                for (int u = 0; u < 4; ++u) b[kk][u] = part_frag<true>(lds, fb + so, kk, u >> 1, u & 1);
+            }
+            load(rs == 0 ? NS - 1 : rs - 1);
+            // (past this tile's last stage the loads are the next one's, past that one's the one after's)
+            advance(s + NS - 1 < cur.nk ? next : after);
+#pragma unroll
+            for (int kk = 0; kk < 2; ++kk)
+#pragma unroll
+                for (int u = 0; u < 4; ++u)
+                    acc[u] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(b[kk][u], a[kk], acc[u], 0, 0, 0);
+            stage_barrier<kWait>();
+            rs = rs + 1 == NS ? 0 : rs + 1;
+        }
+        // lane: dW row 16 wm + l % 16, four columns of each block (block u: columns
+        // 32 wn + 64 (u / 2) + 16 (u % 2) ..)
+        constexpr int SZ = F32 ? 4 : 2;
+        const int r0 = cur.n0 + 16 * wm, left = __builtin_amdgcn_readfirstlane(max(0, min(16, p.N - r0)));
+        const __amdgpu_buffer_rsrc_t rd =
+            make_rsrc(p.dW + ((int64_t)cur.g * p.N + r0) * p.K * SZ, (uint32_t)left * (uint32_t)p.K * (uint32_t)SZ);
+#pragma unroll
+        for (int u = 0; u < 4; ++u) {
+            const int k = cur.k0 + 32 * wn + 64 * (u >> 1) + 16 * (u & 1) + 4 * g4;
+            const uint32_t at = k < p.K ? (uint32_t)(j * p.K + k) * (uint32_t)SZ : kOOB;      // K % 8 == 0
+            if constexpr (F32) {
+                f32x4 v = acc[u];
+                if (p.accumulate) v += __builtin_bit_cast(f32x4, __builtin_amdgcn_raw_buffer_load_b128(rd, at, 0, 0));
+                __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(i32x4, v), rd, at, 0, kStoreCached);
+            } else {
+                __builtin_amdgcn_raw_buffer_store_b64(u32x2{pack_bf16(acc[u][0], acc[u][1]), pack_bf16(acc[u][2], acc[u][3])},
+                                                      rd, at, 0, kStoreCached);
+            }
+        }
+        if ((round + 1) * nwg + ((round + 1) & 1 ? nwg - 1 - self : self) >= ntiles) break;
+        cur = next;
+        next = after;
+        ++round;
+    }
+    asm volatile("s_waitcnt vmcnt(0)" ::: "memory");   // nothing is left to land in LDS
+}
+
 // At most as many workgroups as there can be tiles of tm rows and tno columns.
 dim3 tile_grid(const MoeGemm &p, int tm, int tno, int cus)
 {
@@ -1030,18 +1204,19 @@ hipError_t launch_moe_tiles(const MoeGemm &p, int rows, int cus, hipStream_t str
     return hipGetLastError();
 }
 
-hipError_t launch_moe_dw(const MoeGemmDw &p, int cus, hipStream_t stream)
+hipError_t launch_moe_dw(const MoeGemmDw &p, bool narrow, int cus, hipStream_t stream)
 {
-    const int64_t tiles = (int64_t)p.E * ((p.N + 255) / 256) * ((p.K + 255) / 256);
+    const int tm = narrow ? 64 : 256, tn = narrow ? 128 : 256;
+    const int64_t tiles = (int64_t)p.E * ((p.N + tm - 1) / tm) * ((p.K + tn - 1) / tn);
     const dim3 grid((uint32_t)(tiles < cus ? tiles : cus)), block(512);
-    if (p.rows) {
-        if (p.f32) hipLaunchKernelGGL((moe_dw<true, true>), grid, block, 0, stream, p);
-        else hipLaunchKernelGGL((moe_dw<true, false>), grid, block, 0, stream, p);
-    } else {
-        if (p.f32) hipLaunchKernelGGL((moe_dw<false, true>), grid, block, 0, stream, p);
-        else hipLaunchKernelGGL((moe_dw<false, false>), grid, block, 0, stream, p);
-    }
-    return hipGetLastError();
+    auto go = [&](auto gather, auto f32) {
+        constexpr bool G = decltype(gather)::value, F = decltype(f32)::value;
+        if (narrow) hipLaunchKernelGGL((moe_dw_64<G, F>), grid, block, 0, stream, p);
+        else hipLaunchKernelGGL((moe_dw<G, F>), grid, block, 0, stream, p);
+        return hipGetLastError();
+    };
+    if (p.rows) return p.f32 ? go(std::true_type{}, std::true_type{}) : go(std::true_type{}, std::false_type{});
+    return p.f32 ? go(std::false_type{}, std::true_type{}) : go(std::false_type{}, std::false_type{});
 }
 
 }  // namespace dbs

@@ -215,7 +215,17 @@ def test_product_gated(T, M, E, F, K, groups):
     assert np.all(np.abs(got - _moe.silu(a) * u) <= _moe.gate_bound(a, u, acc[:, :F], acc[:, F:]))
 
 
-@pytest.mark.parametrize("T,M,E,N,K,groups", [s for s in SHAPES if s[3] % 8 == 0])
+# few or thin matrices under many rows: one to several of the smaller dw tiles
+# per workgroup, groups that end in a stage or have none
+NARROW = [
+    (300, 192, 1, 8, 8, "even"), (300, 193, 1, 72, 136, "even"), (100, 4000, 4, 64, 128, "ragged"),
+    (2000, 2000, 5, 200, 264, "short"), (500, 3000, 3, 48, 1032, "one"), (700, 2400, 12, 264, 648, "none"),
+    (4000, None, 12, 136, 520, "ragged"), (1030, None, 5, 56, 1160, "ragged"), (900, 12000, 60, 56, 1544, "ragged"),
+    (700, 10000, 50, 320, 640, "ragged"), (64, 13000, 60, 320, 392, "one"),
+]
+
+
+@pytest.mark.parametrize("T,M,E,N,K,groups", [s for s in SHAPES if s[3] % 8 == 0] + NARROW)
 @pytest.mark.parametrize("out", ["bf16", "f32", "add"])
 def test_dw(T, M, E, N, K, groups, out):
     g, X, off, rows = _case(T, M, E, K, groups, N + K + 3)
