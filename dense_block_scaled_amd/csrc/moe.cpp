@@ -59,22 +59,26 @@ dbs_status run_product(dbs::MoeGemm p, hipStream_t stream)
     if (st != DBS_OK) return (dbs_status)st;
     p.vec = p.ncols % 8 == 0 && aligned(p.D, 16);
     if ((p.M / 64 + p.E) * ((p.ncols + 31) / 32) >= kTwoGiB) return fail(DBS_EUNSUPPORTED, "too many output tiles");
-    // 64-row or 256-row tiles: the rounds that either takes over the CUs, for
-    // groups of M / E rows on average (half a tile of each is waste), at the
-    // time a stage of it was measured to take: 0.37 us against 1.5 (K-major),
-    // 0.9 against 1.5 (MN-major, twice as wide).  8 experts of 4096 x 4096, 64
-    // rows each: 61 us against 70, 128 rows 94 against 86; 128 experts of
-    // 1536 x 4096, 32 rows 301 against 346; 64 experts of 2816 x 2048, 32 rows
-    // 147 against 172, 64 rows 183 against 165; MN-major 2048 x 2816, 4 tokens
-    // of 8 experts 52 against 68, 32 rows per expert 141 against 133.
-    const int64_t met = p.M < p.E ? p.M : p.E;
-    auto rounds = [&](int64_t tm, int64_t tn) {
+    // 64-row or 256-row tiles, by the stages that either takes on the busiest CU
+    // for groups of M / E rows on average (half a tile of each is waste; few
+    // rows leave some experts without any).  A stage of a 256-row tile takes
+    // 0.9 .. 1.5 us, of a 64-row one 0.26 of that (K-major) or 0.52 (MN-major,
+    // twice as wide); large tiles come in whole rounds over the CUs, small ones
+    // even out.  8 experts of 4096 x 4096, 64 rows each: 60 us against 72, 128
+    // rows 86 against 84; 16 of them behind the gate, 32 rows 133 against 97;
+    // 128 of 1536 x 4096, 16 rows 290 against 269; 64 of 2816 x 2048, 16 rows
+    // 127 against 133, 64 rows 170 against 143; MN-major 8 of 2048 x 7168, 192
+    // rows 91 against 146, 9 of 4048 x 2016, 192 rows 60 against 57.
+    const int64_t M = p.M, E = p.E, likely = (3 * M * E + 3 * M + E - 1) / (3 * M + E), met = M < likely ? M : likely;
+    auto tiles = [&](int64_t tm, int64_t tn) {
         int64_t rows = p.M / tm + met / 2;
         rows = rows > met ? rows : met;
-        return (rows * ((p.ncols + tn - 1) / tn) + cus - 1) / cus;
+        return rows * ((p.ncols + tn - 1) / tn);
     };
-    const int64_t few = rounds(64, p.wmn ? 128 : p.gate ? 32 : 64), many = rounds(256, p.gate ? 128 : 256);
-    return done(dbs::launch_moe_tiles(p, (p.wmn ? 5 : 2) * few <= 8 * many ? 64 : 256, cus, stream));
+    const int64_t few = tiles(64, p.wmn ? 128 : p.gate ? 32 : 64);
+    const int64_t rounds = (tiles(256, p.gate ? 128 : 256) + cus - 1) / cus;
+    const int height = (p.wmn ? 52 : 26) * few <= 100 * rounds * cus ? 64 : 256;
+    return done(dbs::launch_moe_tiles(p, height, cus, stream));
 }
 
 dbs::MoeGemm product(const void *X, const void *W, void *D, const int32_t *offsets, const int32_t *rows, int64_t T,
