@@ -7,8 +7,8 @@
 //
 // The groups' row offsets are read on the device: a workgroup turns them
 // into a table of first tiles in LDS, so a router's output needs no copy to
-// the host.  The stages, their swizzles and fragment reads are those of the
-// BF16 GEMM (gemm_kernel.h); what differs is where rows come from.
+// the host.  Many rows per expert are bound by the matrix cores (256 x 256
+// tiles: 1.3 PFLOP/s), few by the reading of W (64-row tiles: up to 7 TB/s).
 //
 // * Rows.  A gathered row's byte offset is taken from `rows` once per output
 //   tile and lives in one register per wave-load, so gathering costs one add
@@ -34,7 +34,7 @@ namespace {
 
 // Results are stored through the caches: a wave's pieces are half lines, which
 // L2 puts together (32768 x 2048 results over 32 experts: 451 us with
-// streaming stores, 413 without).
+// streaming stores, 413 without, in even groups).
 constexpr int kStoreCached = 0;
 constexpr uint32_t kRowOOB = 0xFF000000u;        // + a row's bytes (at most 2^22) still lies past every resource
 
@@ -156,29 +156,34 @@ __device__ __forceinline__ int first_tile()
 // --------------------------------------------------- the 256 x 256 x 64 core
 
 // 256 x 256 output tiles over stages of 64, 8 waves (2 x 4, two per SIMD),
-// each owning 128 x 64.  A stage is four parts of
-// 16 KiB -- A's rows (or columns) 0 .. 127 and 128 .. 255, B's likewise -- in
-// one of two LDS slots, and is computed as four quadrants of 64 x 32.  A
-// wave reads one part whole into registers per quadrant,
-// so the part's place in the slot is free again at once, and its refill for
-// the stage after next starts a turn later: loads get six turns of the eight
-// that two stages take to land, with two slots.  (Rows that nothing else has
-// touched come from HBM: with loads of one stage's lead, waited for in full
-// at its end, the same tiles took a quarter longer.)
+// each owning 128 x 64.  A stage is four parts of 16 KiB -- A's rows (or
+// columns) 0 .. 127 and 128 .. 255, B's likewise -- in one of two LDS slots,
+// and is computed in two turns of 32 MFMAs a wave.  A wave reads the parts of
+// a turn whole into registers, so their places in the slot are free again at
+// once, and their refill for the stage after next starts a turn later: loads
+// get at least two turns of the four that two stages take to land, with two
+// slots.  (Rows that nothing else has touched come from HBM: with loads of one
+// stage's lead, waited for in full at its end, the same tiles took a quarter
+// longer.)
 //
-// The two waves of a SIMD take turns: while one reads its next part and
-// issues two wave-loads, the other runs its quadrant's MFMAs, a workgroup barrier
-// between turns.  Waves 4 .. 7 start one turn late.
+// The two waves of a SIMD take turns: while one reads its parts and issues
+// its loads, the other runs its MFMAs, a workgroup barrier between.  Waves
+// 4 .. 7 start one turn late.
 //
-//   turn   reads              loads issued            MFMAs of the turn after
-//   0      A lo               B lo of stage s + 2     (lo, lo)
-//   1      B hi               A lo of stage s + 2     (lo, hi)
-//   2      A hi               B hi of stage s + 2     (hi, hi)
-//   3      B lo of s + 1      A hi of stage s + 2     (hi, lo)
+//   turn   reads                  loads issued                      MFMAs
+//   0      A lo, B lo, B hi       A hi of stage s + 1               A lo (B lo, B hi)
+//   1      A hi                   A lo, B lo, B hi of stage s + 2   A hi (B hi, B lo)
 //
-// At the end of every turn a wave waits for its loads of the part read in the
-// turn after: kInFlight newer wave-loads may be under way by then.  Its own
-// reads are complete before the barrier that lets others refill their place.
+// At the end of a turn's reads a wave waits for its loads of the parts read in
+// the turn after: the newer kInFlight wave-loads may be under way by then (the
+// turn's own and one turn's before it: 2 + 6).  Its own reads are complete
+// before the barrier that lets others refill their place.
+//
+// What bounds it is the clock that the power leaves and, close behind, the
+// 64 KiB a stage that come into LDS: 32768 rows over 32 experts, 4096 x 2048,
+// in even groups take 430 us (1.28 PFLOP/s), on zeros 358, their loads alone
+// 320.  A tile costs 1.5 us a stage and 6 us of storing, in which all CUs write
+// at once.
 constexpr int kPart = 128 * kRowBytes, kSlot = 4 * kPart, kInFlight = 8;
 enum PartId : int { kALo = 0, kAHi = 1, kBLo = 2, kBHi = 3 };
 constexpr int kStage = 2 * kSlot;              // LDS offset of the waves' output buffers, 2 KiB each
@@ -337,6 +342,9 @@ __device__ __forceinline__ void core_stage(Acc &acc, const uint8_t *lds, uint32_
 // One 32 x 32 block of results as bf16 rows r0 .. mend-1, columns n0 ..
 // ncols-1 of D (ld columns), through the wave's 2 KiB buffer and in 16-byte
 // pieces (vec) or by element; value(u, v, q): register q of 16 x 16 block (u, v).
+// Neighbouring lanes then write neighbouring pieces of a row: exchanged
+// between lanes instead (v_permlane16_swap), with 16 rows to the 16 lanes next to
+// each other, dW of 32 experts took 564 us where this takes 541.
 template <class VALUE>
 __device__ __forceinline__ void store_block(uint8_t *buf, uint8_t *D, int64_t ld, int r0, int mend, int n0, int ncols,
                                             int vec, Lane c, VALUE &&value)
@@ -841,6 +849,11 @@ __device__ __forceinline__ int sort_groups(uint16_t *order, const int32_t *first
     return n;
 }
 
+// Tile columns along N handed out together: the 32 tiles that an XCD's
+// workgroups hold together then read 8 + 4 parts of dY and X where all of 16
+// and 2 took more (32 experts of 4096 x 2048, 1024 rows each: 556 -> 535 us).
+constexpr int kDwBand = 8;
+
 // GATHER: rows of X through p.rows.  F32: dW holds fp32.
 //
 // Gathered rows: a wave loads eight K-rows of X a stage.  Their indices reach
@@ -883,8 +896,10 @@ __global__ __launch_bounds__(512, 1) void moe_dw(MoeGemmDw p)
         r.lo = __builtin_amdgcn_readfirstlane(first[r.g]);
         r.hi = __builtin_amdgcn_readfirstlane(first[r.g + 1]);
         const int local = id % per;
-        r.n0 = local % tiles_n * 256;
-        r.k0 = local / tiles_n * 256;
+        const int band = local / (kDwBand * tiles_k), wide = min(kDwBand, tiles_n - band * kDwBand);
+        const int in = local - band * kDwBand * tiles_k;
+        r.n0 = (band * kDwBand + in % wide) * 256;
+        r.k0 = in / wide * 256;
         // the loads run up to two stages ahead: two at least
         r.nk = max(2, (r.hi - r.lo + 63) / 64);
         return r;
@@ -1021,8 +1036,9 @@ __global__ __launch_bounds__(512, 1) void moe_dw(MoeGemmDw p)
 }
 
 // 64 (N) x 128 (K) tiles over a ring of five slots of 24 KiB, for calls of so
-// few 256 x 256 tiles that the longest sums decide: a stage costs 0.2 us there
-// where the large tiles' costs 1.3.  8 waves (4 x 2) of 16 x 64.
+// few 256 x 256 tiles that the longest sums decide: a stage costs 0.3 .. 0.55 us
+// where the large tiles' costs 1.3 .. 2.3 for eight times the results.  8 waves
+// (4 x 2) of 16 x 64.
 //
 // dY's part of a slot: 64 K-rows of 64 columns (128 bytes), wave-load w covers
 // K-rows 8 w .. 8 w + 7; the transposed reads of two groups take 32 bytes of
