@@ -484,6 +484,12 @@ __device__ __forceinline__ float gated(float g, float u)
 }
 
 // 256-row tiles.  BMN: W MN-major; GATE: see the head of the file.
+//
+// 32768 rows of 32 uneven experts, 4096 x 2048 MN-major: 500 us (1.10
+// PFLOP/s): 4.1 tiles' work a CU, of which the busiest have 4.7, with rests
+// that cost more than their share; in even groups 440.  24594 rows of 64 very
+// uneven experts, 1416 x 2048: 182 us (0.78 PFLOP/s), where groups of 1.5
+// tile rows leave a third of the tiles partly empty.
 template <bool BMN, bool GATE>
 __global__ __launch_bounds__(512, 1) void moe_tiles_256(MoeGemm p)
 {
@@ -661,7 +667,9 @@ __global__ __launch_bounds__(512, 1) void moe_tiles_256(MoeGemm p)
 // half of the columns.  With the gate a wave's 32 rows of W are 16 gate rows
 // and the 16 up rows that meet them.
 //
-// Against 64 x 256 tiles over three slots (0.7 us a stage): 8 experts of
+// 384 rows on 128 experts behind the gate, 768 x 4096: 216 us for 1.5 GB (7
+// TB/s); one token on 8 experts, 1408 x 2048: 21 us for 92 MB (4.3 TB/s: 352
+// tiles on 256 CUs, and the way into the kernel).  Against 64 x 256 tiles over three slots (0.7 us a stage): 8 experts of
 // 4096 x 4096, 4 rows 42 us against 45, 32 rows 44 against 63; 64 experts of
 // 2816 x 2048, 16 rows 143 against 169.
 template <bool BMN>
@@ -860,6 +868,11 @@ constexpr int kDwBand = 8;
 // LDS for eight stages at a time by one dword load of the wave's own (it
 // waits for them by its own count, no barrier), into a buffer per parity of
 // the tile for a tile's first eight stages and two in turn for later ones.
+//
+// 32768 rows of 32 uneven experts, 4096 x 2048: 550 us to bf16 (1.0 PFLOP/s)
+// at 47 % of the matrix cores' cycles: 1.7 us a stage, and 5 us for each of a
+// CU's 16 tiles, when all CUs write at once.  One expert of 16384 rows,
+// 4096 x 4096: 414 us (1.33 PFLOP/s).
 template <bool GATHER, bool F32>
 __global__ __launch_bounds__(512, 1) void moe_dw(MoeGemmDw p)
 {
