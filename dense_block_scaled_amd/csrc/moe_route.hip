@@ -27,7 +27,7 @@
 // which is what a decoding step's latency asks for: one token of 64 experts
 // 3.9 us, nearly all of it the launch and two trips to memory.
 //
-// 32768 tokens, 8 of 128 experts, fp32: 12 us of selection, 4.3 of sums and 5.9
+// 32768 tokens, 8 of 128 experts, fp32: 12 us of selection, 4 of sums and 5.8
 // of placing, for 21 MB.  Selection is bound by its vector instructions (73 a
 // choice and wave of four tokens, 9 us of issue on 1024 SIMDs), not by the
 // logits (1.4 TB/s).  The gradient streams: 16384 tokens of 160 experts, bf16,
@@ -263,14 +263,17 @@ __global__ __launch_bounds__(1024) void route_columns(int32_t *counts, int64_t n
     }
     seg[s][col] = sum;
     __syncthreads();
-    if (threadIdx.x < 16) {
-        int run = 0;
-        for (int i = 0; i < 64; ++i) {
-            const int v = seg[i][threadIdx.x];
-            seg[i][threadIdx.x] = run;
-            run += v;
+    {
+        // a wave per column, a lane per segment
+        const int lane = threadIdx.x & 63, c = threadIdx.x >> 6, v = seg[lane][c];
+        int inc = v;
+#pragma unroll
+        for (int d = 1; d < 64; d *= 2) {
+            const int o = __shfl_up(inc, d);
+            if (lane >= d) inc += o;
         }
-        if (blockIdx.x * 16 + (int)threadIdx.x < E) counts[nb * E + blockIdx.x * 16 + threadIdx.x] = run;
+        seg[lane][c] = inc - v;
+        if (lane == 63 && blockIdx.x * 16 + c < E) counts[nb * E + blockIdx.x * 16 + c] = inc;
     }
     __syncthreads();
     if (e < E) {

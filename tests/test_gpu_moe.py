@@ -163,6 +163,43 @@ SHAPES = [
 ]
 
 
+# rows and columns enough for the 256-row tiles in every form: rests of one to
+# four blocks, column starts past 2048, one to a few stages, no whole pieces
+LARGE = [
+    (1300, 1300, 2, 4360, 72, "ragged"), (600, 3000, 5, 4360, 136, "ragged"), (2000, 6000, 3, 2304, 200, "ragged"),
+    (5000, None, 40, 1032, 264, "ragged"), (64000, None, 3, 33, 40, "ragged"), (64500, None, 2, 72, 8, "one"),
+    (9000, None, 6, 2312, 104, "none"), (4000, 9000, 7, 2312, 328, "short"), (300, 4097, 1, 4099, 64, "even"),
+    (1, 2600, 2, 4104, 128, "even"),
+]
+
+
+def test_large_shapes_reach_the_large_tiles():
+    """The rule of moe.cpp, on the 256 CUs it counts here, sends every shape of
+    LARGE to 256-row tiles in the forms that the tests run, and SHAPES has
+    some for the 64-row tiles."""
+    def height(M, E, cols, mn, gate):
+        met = min(M, -(-3 * M * E // (3 * M + E)))
+        tiles = lambda tm, tn: max(M // tm + met // 2, met) * -(-cols // tn)
+        few, rounds = tiles(64, 128 if mn else 32 if gate else 64), -(-tiles(256, 128 if gate else 256) // 256)
+        return 64 if (52 if mn else 26) * few <= 100 * rounds * 256 else 256
+    for T, M, E, N, K, _ in LARGE:
+        assert height(M or T, E, N, False, False) == 256 and height(M or T, E, N, False, True) == 256
+        if N % 8 == 0 and N > 1000:
+            assert height(M or T, E, N, True, False) == 256
+    assert any(height(M or T, E, N, False, False) == 64 for T, M, E, N, K, _ in SHAPES)
+
+
+def test_dw_shapes_reach_both_tiles():
+    """As above, for the rule of gemm_moe_dw_bf16."""
+    def narrow(M, E, N, K):
+        rounds = lambda tn, tk: -(-E * -(-N // tn) * -(-K // tk) // 256)
+        return M >= 192 * E and rounds(64, 128) <= (4 if E >= 12 else 3) * rounds(256, 256)
+    for T, M, E, N, K, _ in NARROW:
+        assert narrow(M or T, E, N, K)
+    for T, M, E, N, K, _ in WIDE:
+        assert not narrow(M or T, E, N, K)
+
+
 def _case(T, M, E, K, groups, seed):
     g = _gen(seed)
     X = _bf16(g, T, K)
@@ -177,7 +214,7 @@ def _gpu(X, off, rows):
     return X.cuda(), torch.tensor(off, dtype=torch.int32).cuda(), None if rows is None else rows.cuda()
 
 
-@pytest.mark.parametrize("T,M,E,N,K,groups", SHAPES)
+@pytest.mark.parametrize("T,M,E,N,K,groups", SHAPES + LARGE)
 def test_product(T, M, E, N, K, groups):
     g, X, off, rows = _case(T, M, E, K, groups, N + K)
     W = _bf16(g, E, N, K)
@@ -190,7 +227,7 @@ def test_product(T, M, E, N, K, groups):
     assert np.all(got[off[-1]:] == 0)
 
 
-@pytest.mark.parametrize("T,M,E,N,K,groups", [s for s in SHAPES if s[3] % 8 == 0])
+@pytest.mark.parametrize("T,M,E,N,K,groups", [s for s in SHAPES + LARGE if s[3] % 8 == 0])
 def test_product_transposed(T, M, E, N, K, groups):
     g, X, off, rows = _case(T, M, E, K, groups, N + K + 1)
     W = _bf16(g, E, K, N)
@@ -202,7 +239,7 @@ def test_product_transposed(T, M, E, N, K, groups):
     assert np.all(got[off[-1]:] == 0)
 
 
-@pytest.mark.parametrize("T,M,E,F,K,groups", SHAPES)
+@pytest.mark.parametrize("T,M,E,F,K,groups", SHAPES + LARGE)
 def test_product_gated(T, M, E, F, K, groups):
     g, X, off, rows = _case(T, M, E, K, groups, F + K + 2)
     W = _bf16(g, E, 2 * F, K, scale=K ** -0.5 * 2)
@@ -221,11 +258,17 @@ NARROW = [
     (300, 192, 1, 8, 8, "even"), (300, 193, 1, 72, 136, "even"), (100, 4000, 4, 64, 128, "ragged"),
     (2000, 2000, 5, 200, 264, "short"), (500, 3000, 3, 48, 1032, "one"), (700, 2400, 12, 264, 648, "none"),
     (4000, None, 12, 136, 520, "ragged"), (1030, None, 5, 56, 1160, "ragged"), (900, 12000, 60, 56, 1544, "ragged"),
-    (700, 10000, 50, 320, 640, "ragged"), (64, 13000, 60, 320, 392, "one"),
+    (700, 10000, 50, 320, 640, "ragged"),
+]
+
+# long groups and several tiles per workgroup of the 256 x 256 ones
+WIDE = [
+    (700, 3000, 6, 1032, 1288, "ragged"), (3000, None, 6, 1032, 1288, "one"), (5000, None, 40, 1032, 264, "ragged"),
+    (150, 2600, 21, 1040, 648, "short"), (64, 13000, 60, 320, 392, "one"),
 ]
 
 
-@pytest.mark.parametrize("T,M,E,N,K,groups", [s for s in SHAPES if s[3] % 8 == 0] + NARROW)
+@pytest.mark.parametrize("T,M,E,N,K,groups", [s for s in SHAPES if s[3] % 8 == 0] + NARROW + WIDE)
 @pytest.mark.parametrize("out", ["bf16", "f32", "add"])
 def test_dw(T, M, E, N, K, groups, out):
     g, X, off, rows = _case(T, M, E, K, groups, N + K + 3)
@@ -299,6 +342,33 @@ def test_row_indices_outside_x_are_zero_rows():
     D, S = _moe.dw(_moe.f64(dY), _moe.f64(X), off, rows.numpy())
     got = _moe.f64(dbs.gemm_moe_dw_bf16(dY.cuda(), x, o, r))
     assert np.all(np.abs(got - D) <= _moe.product_bound(D, S, 30))
+
+
+def test_large_tiles_keep_foreign_rows_out():
+    """Infinities behind the last group, in an expert without rows and in rows
+    of X that no index names; indices outside X."""
+    g = _gen(33)
+    T, E, N, K = 700, 3, 4360, 136
+    off = np.array([0, 1201, 1201, 2600])
+    M, bad = 3000, float("inf")
+    X, W = _bf16(g, T, K), _bf16(g, E, N, K)
+    rows = torch.randint(0, T - 1, (M,), generator=g, dtype=torch.int32)
+    rows[5], rows[1200], rows[1201], rows[2599] = -1, T, 1 << 30, -(1 << 31)
+    X[T - 1], W[1] = bad, bad
+    rows[2600:] = T - 1
+    Xc, Wc = _moe.f64(X), _moe.f64(W)
+    Xc[T - 1], Wc[1] = 0, 0
+    x, o, r = _gpu(X, off, rows)
+    D, S = _moe.product(Xc, Wc, off, rows.numpy(), False)
+    got = _moe.f64(dbs.gemm_moe_bf16(x, W.cuda(), o, r))
+    assert np.all(np.abs(got - D) <= _moe.product_bound(D, S, K))
+    assert np.all(got[2600:] == 0) and np.all(got[[5, 1200, 1201, 2599]] == 0)
+    got = _moe.f64(dbs.gemm_moe_bf16(x, W.transpose(1, 2).contiguous().cuda(), o, r, lw=dbs.MN_MAJOR))
+    assert np.all(np.abs(got - D) <= _moe.product_bound(D, S, K)) and np.all(got[2600:] == 0)
+    a, u, acc = D[:, :N // 2], D[:, N // 2:], K * 2.0 ** -23 * S
+    got = _moe.f64(dbs.gemm_moe_swiglu_bf16(x, W.cuda(), o, r))
+    assert np.all(np.abs(got - _moe.silu(a) * u) <= _moe.gate_bound(a, u, acc[:, :N // 2], acc[:, N // 2:]))
+    assert np.all(got[2600:] == 0)
 
 
 def test_dw_against_differences():

@@ -125,7 +125,9 @@ def test_graph_replays_on_new_inputs():
 
 
 CASES = [(300, 700, 4, 264, 136), (2000, 5000, 3, 520, 328), (48, 300, 64, 96, 200), (700, 1500, 5, 776, 1032),
-         (2500, 2500, 2, 512, 256)]
+         (2500, 2500, 2, 512, 256),
+         # 256-row tiles in every form, and 64 x 128 tiles of dW over several rounds
+         (1500, 2600, 3, 4400, 2312), (3000, 3000, 7, 4096, 2120), (900, 12000, 60, 320, 1544)]
 
 
 def _inputs(T, M, E, N, K, seed):
@@ -161,7 +163,7 @@ def test_poison_build_gives_the_same_bits(T, M, E, N, K):
         assert torch.equal(u, v)
 
 
-@pytest.mark.parametrize("T,M,E,N,K", CASES[:3])
+@pytest.mark.parametrize("T,M,E,N,K", CASES[:3] + CASES[5:])
 def test_calls_repeat_bit_for_bit(T, M, E, N, K):
     a = _inputs(T, M, E, N, K, N)
     want = _all(*a)
@@ -184,6 +186,18 @@ def test_one_row_has_the_same_bits_in_any_company():
     c = dbs.gemm_moe_bf16(X, W, whole)
     d = dbs.gemm_moe_bf16(X[:3001].contiguous(), W, torch.tensor([0, 3001, 3001, 3001, 3001], dtype=torch.int32).cuda())
     assert torch.equal(c[:3001], d)
+
+
+def test_one_row_has_the_same_bits_in_any_company_under_large_tiles():
+    g = _gen(9)
+    E, N, K = 2, 4360, 72
+    X, W = _bf16(g, 1400, K).cuda(), _bf16(g, E, N, K).cuda()
+    o = lambda *v: torch.tensor(v, dtype=torch.int32).cuda()
+    a = dbs.gemm_moe_bf16(X, W, o(0, 1400, 1400))
+    b = dbs.gemm_moe_bf16(X[:1301].contiguous(), W, o(0, 1301, 1301))
+    assert torch.equal(a[:1301], b)
+    c = dbs.gemm_moe_bf16(X, W, o(0, 1400, 1400), torch.arange(1399, -1, -1, dtype=torch.int32).cuda())
+    assert torch.equal(c.flip(0), a)
 
 
 def test_offsets_that_are_no_offsets_stay_inside():
