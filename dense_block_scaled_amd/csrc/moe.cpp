@@ -198,18 +198,7 @@ dbs_status gemm_moe_dw_bf16(dbs_real type, const void *dY, const void *X, void *
     if (e != DBS_OK) return (dbs_status)e;
     dbs::MoeGemmDw p{static_cast<const uint8_t *>(dY), static_cast<const uint8_t *>(X), static_cast<uint8_t *>(dW),
                      offsets, rows, T, (int)M, (int)E, (int)N, (int)K, type == DBS_F32, accumulate};
-    // 64 x 128 tiles where they take at most three times the rounds over the
-    // CUs that 256 x 256 tiles take: few or thin matrices, whose large tiles
-    // leave CUs idle or half empty.  (16 experts of 768 x 512, 2048 rows each on
-    // average: even groups 58 us with either, groups that differ by e^0.5 80
-    // against 138; 12 of 264 x 1168, 512 rows: 22 against 28.)  At four times
-    // the rounds it is the longest group that decides, and of many groups one
-    // is long: 32 of 512 x 512, 1024 rows 49 against 72, but 4 of 1024 x 2048
-    // 44 against 40.  Below 192 rows per expert the large tiles are never behind (12 of
-    // 264 x 1168, 128 rows: 15 against 13).
-    auto rounds = [&](int64_t tn, int64_t tk) { return (E * ((N + tn - 1) / tn) * ((K + tk - 1) / tk) + cus - 1) / cus; };
-    const bool narrow = M >= 192 * E && rounds(64, 128) <= (E >= 12 ? 4 : 3) * rounds(256, 256);
-    return done(dbs::launch_moe_dw(p, narrow, cus, stream));
+    return done(dbs::launch_moe_dw(p, cus, stream));
 }
 
 dbs_status swiglu_bf16(const void *H, void *A, int64_t M, int64_t F, hipStream_t stream)

@@ -42,8 +42,7 @@ struct MoeGemmDw {
 
 // rows: 64 or 256 per output tile
 hipError_t launch_moe_tiles(const MoeGemm &p, int rows, int cus, hipStream_t stream);
-// narrow: 64 x 128 tiles, else 256 x 256
-hipError_t launch_moe_dw(const MoeGemmDw &p, bool narrow, int cus, hipStream_t stream);
+hipError_t launch_moe_dw(const MoeGemmDw &p, int cus, hipStream_t stream);
 
 struct MoeRoute {
     const void *logits;       // T x E, fp32 or bf16

@@ -874,27 +874,13 @@ constexpr int kDwBand = 8;
 // CU's 16 tiles, when all CUs write at once.  One expert of 16384 rows,
 // 4096 x 4096: 414 us (1.33 PFLOP/s).
 template <bool GATHER, bool F32>
-__global__ __launch_bounds__(512, 1) void moe_dw(MoeGemmDw p)
+__device__ __forceinline__ void dw_large(const MoeGemmDw &p, const Lane &c, uint8_t *lds, const int32_t *first,
+                                         const uint16_t *order, int groups, uint32_t *rowbuf)
 {
-    __shared__ __attribute__((aligned(1024))) uint8_t lds[kCoreLds];
-    __shared__ int32_t first[kMoeMaxExperts + 1];
-    __shared__ uint16_t order[kMoeMaxExperts + 1];     // groups with tiles, the longest sums first
-    __shared__ int32_t count;
-    __shared__ uint32_t rowbuf[GATHER ? 8 * 256 : 1];
     constexpr int kStores = F32 ? 32 : 16;             // store instructions of a tile
-
-    const Lane c = lane_of();
     const int lda = p.N * 2, ldb = p.K * 2;            // bytes of a row of dY, of X
     const int tiles_n = (p.N + 255) / 256, tiles_k = (p.K + 255) / 256, per = tiles_n * tiles_k;
-    if (c.w == 0) {
-        // (the table's second part, rows before a group, is not used)
-        group_table<true>(first, order, p.offsets, p.E, p.M, c, [](int) { return 0; });
-        __builtin_amdgcn_wave_barrier();
-        const int n = sort_groups(order, first, p.E, !p.accumulate, c);
-        if (c.lane == 0) count = n;
-    }
-    __syncthreads();
-    const int ntiles = __builtin_amdgcn_readfirstlane(count) * per, nwg = gridDim.x, self = first_tile();
+    const int ntiles = groups * per, nwg = gridDim.x, self = first_tile();
     if (self >= ntiles) return;
 
     struct Ref {
@@ -1048,7 +1034,7 @@ __global__ __launch_bounds__(512, 1) void moe_dw(MoeGemmDw p)
     asm volatile("s_waitcnt vmcnt(0)" ::: "memory");   // nothing is left to land in LDS
 }
 
-// 64 (N) x 128 (K) tiles over a ring of five slots of 24 KiB, for calls of so
+// 64 (N) x 128 (K) tiles over a ring of five slots of 24 KiB, where there are so
 // few 256 x 256 tiles that the longest sums decide: a stage costs 0.3 .. 0.55 us
 // where the large tiles' costs 1.3 .. 2.3 for eight times the results.  8 waves
 // (4 x 2) of 16 x 64.
@@ -1056,32 +1042,22 @@ __global__ __launch_bounds__(512, 1) void moe_dw(MoeGemmDw p)
 // dY's part of a slot: 64 K-rows of 64 columns (128 bytes), wave-load w covers
 // K-rows 8 w .. 8 w + 7; the transposed reads of two groups take 32 bytes of
 // four K-rows each, groups 8 or 16 K-rows apart, and two K-rows share a bank
-// line.  X's part as in the core.  Row indices as in moe_dw, but a tile's
+// line.  X's part as in the core.  Row indices as in dw_large, but a tile's
 // first eight stages two tiles ahead: the loads run four stages ahead.
 __device__ __forceinline__ constexpr int narrow_swz(int r) { return 2 * ((r >> 1) & 1) ^ 4 * (((r >> 3) ^ (r >> 4)) & 1); }
 
-template <bool GATHER, bool F32>
-__global__ __launch_bounds__(512, 1) void moe_dw_64(MoeGemmDw p)
-{
-    constexpr int NS = 5, kA = 64 * kRowBytes, kSlotD = kA + 128 * kRowBytes, kWait = (NS - 2) * 3;
-    __shared__ __attribute__((aligned(1024))) uint8_t lds[NS * kSlotD];
-    __shared__ int32_t first[kMoeMaxExperts + 1];
-    __shared__ uint16_t order[kMoeMaxExperts + 1];     // groups with tiles, the longest sums first
-    __shared__ int32_t count;
-    __shared__ uint32_t rowbuf[GATHER ? 8 * 5 * 64 : 1];
+constexpr int kDwSlots = 5, kDwSlot = 64 * kRowBytes + 128 * kRowBytes;
 
-    const Lane c = lane_of();
+template <bool GATHER, bool F32>
+__device__ __forceinline__ void dw_small(const MoeGemmDw &p, const Lane &c, uint8_t *lds, const int32_t *first,
+                                         const uint16_t *order, int groups)
+{
+    constexpr int NS = kDwSlots, kA = 64 * kRowBytes, kSlotD = kDwSlot, kWait = (NS - 2) * 3;
+    uint32_t *rowbuf = reinterpret_cast<uint32_t *>(lds + NS * kSlotD);
     const int wm = c.w >> 1, wn = c.w & 1, j = c.lane & 15, g4 = c.lane >> 4;
     const int lda = p.N * 2, ldb = p.K * 2;            // bytes of a row of dY, of X
     const int tiles_n = (p.N + 63) / 64, tiles_k = (p.K + 127) / 128, per = tiles_n * tiles_k;
-    if (c.w == 0) {
-        group_table<true>(first, order, p.offsets, p.E, p.M, c, [](int) { return 0; });
-        __builtin_amdgcn_wave_barrier();
-        const int n = sort_groups(order, first, p.E, !p.accumulate, c);
-        if (c.lane == 0) count = n;
-    }
-    __syncthreads();
-    const int ntiles = __builtin_amdgcn_readfirstlane(count) * per, nwg = gridDim.x, self = first_tile();
+    const int ntiles = groups * per, nwg = gridDim.x, self = first_tile();
     if (self >= ntiles) return;
 
     struct Ref {
@@ -1223,6 +1199,58 @@ __global__ __launch_bounds__(512, 1) void moe_dw_64(MoeGemmDw p)
     asm volatile("s_waitcnt vmcnt(0)" ::: "memory");   // nothing is left to land in LDS
 }
 
+// Which of the two: the stages and tiles of the busiest workgroup, in tenths
+// of a microsecond as measured -- 1.6 us a stage of a large tile with all CUs
+// at work, 1.3 along one long group, 5 to store it (9 in fp32) against 0.5,
+// 0.35 and 1.  The groups decide: 19 experts of 848 x 632, 1024 rows each on
+// average, even groups 43 us with large tiles and 56 with small ones, groups
+// that differ by e^0.5 92 against 70; 8 of 1024 x 1024, 1024 rows, even 35 against 42,
+// exponential 75 against 47; 32 of 4096 x 2048, 1024 rows 540 against 1180.  So
+// it is made here, by every workgroup from the same offsets.
+template <bool GATHER, bool F32>
+__global__ __launch_bounds__(512, 1) void moe_dw(MoeGemmDw p)
+{
+    __shared__ __attribute__((aligned(1024))) uint8_t lds[kCoreLds];
+    static_assert(kDwSlots * kDwSlot + 8 * 5 * 256 <= kCoreLds, "the small tiles' ring and row indices");
+    __shared__ int32_t first[kMoeMaxExperts + 1];
+    __shared__ uint16_t order[kMoeMaxExperts + 1];     // groups with tiles, the longest sums first
+    __shared__ int32_t count, small;
+    __shared__ uint32_t rowbuf[GATHER ? 8 * 256 : 1];
+    const Lane c = lane_of();
+    if (c.w == 0) {
+        // (the table's second part, rows before a group, is not used)
+        group_table<true>(first, order, p.offsets, p.E, p.M, c, [](int) { return 0; });
+        __builtin_amdgcn_wave_barrier();
+        const int n = sort_groups(order, first, p.E, !p.accumulate, c);
+        int longest = 0, two = 0, four = 0;            // stages, at least two or four to a tile
+        for (int i = c.lane; i < n; i += 64) {
+            const int g = order[i], stages = (first[g + 1] - first[g] + 63) / 64;
+            longest = max(longest, stages);
+            two += max(stages, 2);
+            four += max(stages, 4);
+        }
+#pragma unroll
+        for (int d = 32; d; d /= 2) {
+            longest = max(longest, __shfl_xor(longest, d));
+            two += __shfl_xor(two, d);
+            four += __shfl_xor(four, d);
+        }
+        const float wgs = (float)gridDim.x;
+        const float many = (float)(((p.N + 255) / 256) * ((p.K + 255) / 256)) / wgs;    // tiles of a group a workgroup
+        const float few = (float)(((p.N + 63) / 64) * ((p.K + 127) / 128)) / wgs;
+        const float large = (F32 ? 90.0f : 50.0f) * ceilf(many * n) + fmaxf(13.0f * longest, 16.0f * many * two);
+        const float little = 10.0f * ceilf(few * n) + fmaxf(3.5f * longest, 5.0f * few * four);
+        if (c.lane == 0) {
+            count = n;
+            small = little < large;
+        }
+    }
+    __syncthreads();
+    const int groups = __builtin_amdgcn_readfirstlane(count);
+    if (__builtin_amdgcn_readfirstlane(small)) dw_small<GATHER, F32>(p, c, lds, first, order, groups);
+    else dw_large<GATHER, F32>(p, c, lds, first, order, groups, rowbuf);
+}
+
 // At most as many workgroups as there can be tiles of tm rows and tno columns.
 dim3 tile_grid(const MoeGemm &p, int tm, int tno, int cus)
 {
@@ -1249,15 +1277,12 @@ hipError_t launch_moe_tiles(const MoeGemm &p, int rows, int cus, hipStream_t str
     return hipGetLastError();
 }
 
-hipError_t launch_moe_dw(const MoeGemmDw &p, bool narrow, int cus, hipStream_t stream)
+hipError_t launch_moe_dw(const MoeGemmDw &p, int cus, hipStream_t stream)
 {
-    const int tm = narrow ? 64 : 256, tn = narrow ? 128 : 256;
-    const int64_t tiles = (int64_t)p.E * ((p.N + tm - 1) / tm) * ((p.K + tn - 1) / tn);
+    const int64_t tiles = (int64_t)p.E * ((p.N + 63) / 64) * ((p.K + 127) / 128);      // small ones: the more
     const dim3 grid((uint32_t)(tiles < cus ? tiles : cus)), block(512);
     auto go = [&](auto gather, auto f32) {
-        constexpr bool G = decltype(gather)::value, F = decltype(f32)::value;
-        if (narrow) hipLaunchKernelGGL((moe_dw_64<G, F>), grid, block, 0, stream, p);
-        else hipLaunchKernelGGL((moe_dw<G, F>), grid, block, 0, stream, p);
+        hipLaunchKernelGGL((moe_dw<decltype(gather)::value, decltype(f32)::value>), grid, block, 0, stream, p);
         return hipGetLastError();
     };
     if (p.rows) return p.f32 ? go(std::true_type{}, std::true_type{}) : go(std::true_type{}, std::false_type{});

@@ -190,14 +190,20 @@ def test_large_shapes_reach_the_large_tiles():
 
 
 def test_dw_shapes_reach_both_tiles():
-    """As above, for the rule of gemm_moe_dw_bf16."""
-    def narrow(M, E, N, K):
-        rounds = lambda tn, tk: -(-E * -(-N // tn) * -(-K // tk) // 256)
-        return M >= 192 * E and rounds(64, 128) <= (4 if E >= 12 else 3) * rounds(256, 256)
-    for T, M, E, N, K, _ in NARROW:
-        assert narrow(M or T, E, N, K)
-    for T, M, E, N, K, _ in WIDE:
-        assert not narrow(M or T, E, N, K)
+    """As above, for the rule of moe_dw on the groups that test_dw makes."""
+    def small(off, N, K, accumulate, f32):
+        rows = np.diff(off)
+        rows = rows[rows > 0] if accumulate else rows
+        stages = -(-rows // 64)
+        few, many = -(-N // 64) * -(-K // 128), -(-N // 256) * -(-K // 256)
+        wgs, n = min(256, (len(off) - 1) * few), len(rows)
+        longest = stages.max(initial=0)
+        large = (90 if f32 else 50) * np.ceil(many * n / wgs) + max(
+            13 * longest, 16 * many * np.maximum(stages, 2).sum() / wgs)
+        return 10 * np.ceil(few * n / wgs) + max(3.5 * longest, 5 * few * np.maximum(stages, 4).sum() / wgs) < large
+    for shapes, want in ((NARROW, True), (WIDE, False)):
+        for T, M, E, N, K, groups in shapes:
+            assert small(_groups(groups, E, M or T, N + K + 3), N, K, False, False) == want, (T, M, E, N, K, groups)
 
 
 def _case(T, M, E, K, groups, seed):
@@ -258,13 +264,13 @@ NARROW = [
     (300, 192, 1, 8, 8, "even"), (300, 193, 1, 72, 136, "even"), (100, 4000, 4, 64, 128, "ragged"),
     (2000, 2000, 5, 200, 264, "short"), (500, 3000, 3, 48, 1032, "one"), (700, 2400, 12, 264, 648, "none"),
     (4000, None, 12, 136, 520, "ragged"), (1030, None, 5, 56, 1160, "ragged"), (900, 12000, 60, 56, 1544, "ragged"),
-    (700, 10000, 50, 320, 640, "ragged"),
+    (700, 10000, 50, 320, 640, "ragged"), (64, 13000, 60, 320, 392, "one"), (700, 3000, 6, 1032, 1288, "ragged"),
+    (3000, None, 6, 1032, 1288, "one"),
 ]
-
-# long groups and several tiles per workgroup of the 256 x 256 ones
+# the larger ones: long groups, several tiles per workgroup, a stage or two per group
 WIDE = [
-    (700, 3000, 6, 1032, 1288, "ragged"), (3000, None, 6, 1032, 1288, "one"), (5000, None, 40, 1032, 264, "ragged"),
-    (150, 2600, 21, 1040, 648, "short"), (64, 13000, 60, 320, 392, "one"),
+    (5000, None, 40, 1032, 264, "ragged"), (150, 2600, 21, 1040, 648, "short"), (200, 1300, 130, 520, 264, "ragged"),
+    (700, 5200, 4, 1032, 2056, "even"), (5200, None, 4, 1032, 2056, "even"),
 ]
 
 
