@@ -4,6 +4,8 @@
 
 #include <hip/hip_runtime.h>
 
+#include <algorithm>
+#include <cmath>
 #include <cstdio>
 
 #include "dbs.h"
@@ -59,25 +61,30 @@ dbs_status run_product(dbs::MoeGemm p, hipStream_t stream)
     if (st != DBS_OK) return (dbs_status)st;
     p.vec = p.ncols % 8 == 0 && aligned(p.D, 16);
     if ((p.M / 64 + p.E) * ((p.ncols + 31) / 32) >= kTwoGiB) return fail(DBS_EUNSUPPORTED, "too many output tiles");
-    // 64-row or 256-row tiles, by the stages that either takes on the busiest CU
-    // for groups of M / E rows on average (half a tile of each is waste; few
-    // rows leave some experts without any).  A stage of a 256-row tile takes
-    // 0.9 .. 1.5 us, of a 64-row one 0.26 of that (K-major) or 0.52 (MN-major,
-    // twice as wide); large tiles come in whole rounds over the CUs, small ones
-    // even out.  8 experts of 4096 x 4096, 64 rows each: 60 us against 72, 128
-    // rows 86 against 84; 16 of them behind the gate, 32 rows 133 against 97;
-    // 128 of 1536 x 4096, 16 rows 290 against 269; 64 of 2816 x 2048, 16 rows
-    // 127 against 133, 64 rows 170 against 143; MN-major 8 of 2048 x 7168, 192
-    // rows 91 against 146, 9 of 4048 x 2016, 192 rows 60 against 57.
-    const int64_t M = p.M, E = p.E, likely = (3 * M * E + 3 * M + E - 1) / (3 * M + E), met = M < likely ? M : likely;
-    auto tiles = [&](int64_t tm, int64_t tn) {
-        int64_t rows = p.M / tm + met / 2;
-        rows = rows > met ? rows : met;
-        return rows * ((p.ncols + tn - 1) / tn);
+    // Tiles of 64, 128 or 256 rows, by the time of the busiest CU in stages of a
+    // 256-row tile (1.3 us), for groups of M / E rows on average (half a tile
+    // of each is waste; few rows leave some experts without any).  A stage
+    // takes 0.22 of that (64 rows, K-major), 0.39 (MN-major, twice as wide), 0.85
+    // (128 rows), and reads W at the memory's rate, one of 256 rows of it per
+    // CU; large tiles come in whole rounds over the CUs, small ones even out.
+    // us with 64 / 128 / 256 rows: 8 experts of 4096 x 4096, 512 rows in all
+    // 56 / 66 / 69, 8192 rows 531 / 313 / 250; 8 of 1408 x 2048, 4096 rows 54 / 39 /
+    // 50; one of 2048 x 4096, 2048 rows 70 / 68 / 84; 128 of 1536 x 4096 behind the
+    // gate, 192 rows on 49 experts 123 / 152 / 156, 1536 rows on all 291 / 268 / 271;
+    // MN-major 18 of 776 x 2840, 4096 rows 43 / 55 / 68, 8192 rows 78 / 97 / 71.
+    const int64_t M = p.M, E = p.E, likely = (2 * M * E + 2 * M + E - 1) / (2 * M + E), met = std::min(M, likely);
+    auto per_cu = [&](int64_t tm, int64_t tn) {
+        const int64_t rows = std::max(M / tm + met / 2, met);
+        return double(rows * ((p.ncols + tn - 1) / tn)) / cus;
     };
-    const int64_t few = tiles(64, p.wmn ? 128 : p.gate ? 32 : 64);
-    const int64_t rounds = (tiles(256, p.gate ? 128 : 256) + cus - 1) / cus;
-    const int height = (p.wmn ? 52 : 26) * few <= 100 * rounds * cus ? 64 : 256;
+    const double w = double(met) * p.N / 256 / cus;
+    auto rounds = [&](int64_t tm, double stage) {
+        const double n = per_cu(tm, p.gate ? 128 : 256), full = std::floor(n);
+        return full * std::max(stage, w / n) + (n > full ? stage : 0.0);
+    };
+    const double t64 = std::max((p.wmn ? 0.39 : 0.22) * per_cu(64, p.wmn ? 128 : p.gate ? 32 : 64), 1.1 * w);
+    const double t128 = rounds(128, 0.85), t256 = rounds(256, 1.0);
+    const int height = t64 <= t128 && t64 <= t256 ? 64 : t128 < t256 ? 128 : 256;
     return done(dbs::launch_moe_tiles(p, height, cus, stream));
 }
 

@@ -40,7 +40,7 @@ struct MoeGemmDw {
     int accumulate;           // 1: add to dW (fp32 only)
 };
 
-// rows: 64 or 256 per output tile
+// rows: 64, 128 or 256 per output tile
 hipError_t launch_moe_tiles(const MoeGemm &p, int rows, int cus, hipStream_t stream);
 hipError_t launch_moe_dw(const MoeGemmDw &p, int cus, hipStream_t stream);
 

@@ -483,18 +483,20 @@ __device__ __forceinline__ float gated(float g, float u)
     return g * __builtin_amdgcn_rcpf(1.0f + __expf(-g)) * u;
 }
 
-// 256-row tiles.  BMN: W MN-major; GATE: see the head of the file.
+// 256-row tiles, or of 128 rows (TM) where a call has too few of the large ones
+// for the CUs: the same stages with half of A's parts left out, 1.1 us in place
+// of 1.3.  BMN: W MN-major; GATE: see the head of the file.
 //
 // 32768 rows of 32 uneven experts, 4096 x 2048 MN-major: 500 us (1.10
 // PFLOP/s): 4.1 tiles' work a CU, of which the busiest have 4.7, with rests
 // that cost more than their share; in even groups 440.  24594 rows of 64 very
 // uneven experts, 1416 x 2048: 182 us (0.78 PFLOP/s), where groups of 1.5
 // tile rows leave a third of the tiles partly empty.
-template <bool BMN, bool GATE>
-__global__ __launch_bounds__(512, 1) void moe_tiles_256(MoeGemm p)
+template <int TM, bool BMN, bool GATE>
+__global__ __launch_bounds__(512, 1) void moe_tiles(MoeGemm p)
 {
     __shared__ __attribute__((aligned(1024))) uint8_t lds[kCoreLds];
-    __shared__ Table<256> tab;
+    __shared__ Table<TM> tab;
     __shared__ uint32_t rowbuf[256];
     static_assert(!(GATE && BMN), "the gate takes K-major matrices");
     constexpr int TNO = GATE ? 128 : 256;              // output columns of a tile
@@ -527,7 +529,7 @@ __global__ __launch_bounds__(512, 1) void moe_tiles_256(MoeGemm p)
     // group's end load zeros, which aim does not use)
     auto fetch = [&](const RowTile &r) {
         const int n = max(r.mend - r.m0, 0);
-        const i32x4 rr = words_of(p.rows ? p.rows + r.m0 : nullptr, p.rows ? (uint32_t)min(n, 256) * 4u : 0u);
+        const i32x4 rr = words_of(p.rows ? p.rows + r.m0 : nullptr, p.rows ? (uint32_t)min(n, TM) * 4u : 0u);
         dma<4>(rr, reinterpret_cast<uint8_t *>(rowbuf), (c.w & 3) * 256, (uint32_t)((c.w & 3) * 256 + c.lane * 4));
     };
     auto aim = [&](const RowTile &r) {
@@ -551,7 +553,7 @@ __global__ __launch_bounds__(512, 1) void moe_tiles_256(MoeGemm p)
             rb = words_of(wg, (uint32_t)wbytes);
         else
             rb = words_of(wg + (int64_t)r.n0 * lda, (uint32_t)(min(p.N - r.n0, 256) * lda));
-        const int left = min(r.mend - r.m0, 256);
+        const int left = min(r.mend - r.m0, TM);
         const uint32_t have = p.rows ? (uint32_t)p.T : (uint32_t)left;
         ra = words_of(p.rows ? p.X : p.X + (int64_t)r.m0 * lda, have * (uint32_t)lda);
 #pragma unroll
@@ -649,8 +651,8 @@ __global__ __launch_bounds__(512, 1) void moe_tiles_256(MoeGemm p)
     using I2 = std::integral_constant<int, 2>;
     for (;;) {
         next = find(++round);
-        if (cur.blocks == 4) run(I2{}, I2{});
-        else if (cur.blocks == 3) run(I2{}, I1{});
+        if (TM == 256 && cur.blocks == 4) run(I2{}, std::integral_constant<int, TM == 256 ? 2 : 0>{});
+        else if (TM == 256 && cur.blocks == 3) run(I2{}, std::integral_constant<int, TM == 256>{});
         else if (cur.blocks == 2) run(I2{}, I0{});
         else run(I1{}, I0{});
         if (next.blocks == 0) break;
@@ -717,7 +719,7 @@ __global__ __launch_bounds__(512, 1) void moe_tiles_64(MoeGemm p)
             ra = rb = words_of(nullptr, 0);
             return;
         }
-        // (first stage, as in moe_tiles_256, but per tile: a group's few rows of X
+        // (first stage, as in moe_tiles, but per tile: a group's few rows of X
         // stay in L2.  16 experts of 4096 x 4096, 16 rows each: 109 -> 94 us)
         rot = BMN ? 0 : r.n0 / TNO % nk;
         const int64_t wbytes = (int64_t)p.N * p.K * 2;
@@ -1269,10 +1271,15 @@ hipError_t launch_moe_tiles(const MoeGemm &p, int rows, int cus, hipStream_t str
         else if (p.gate) hipLaunchKernelGGL((moe_tiles_64<false, true>), grid, block, 0, stream, p);
         else hipLaunchKernelGGL((moe_tiles_64<false, false>), grid, block, 0, stream, p);
     } else {
-        const dim3 grid = tile_grid(p, 256, p.gate ? 128 : 256, cus);
-        if (p.wmn) hipLaunchKernelGGL((moe_tiles_256<true, false>), grid, block, 0, stream, p);
-        else if (p.gate) hipLaunchKernelGGL((moe_tiles_256<false, true>), grid, block, 0, stream, p);
-        else hipLaunchKernelGGL((moe_tiles_256<false, false>), grid, block, 0, stream, p);
+        auto go = [&](auto tm) {
+            constexpr int TM = decltype(tm)::value;
+            const dim3 grid = tile_grid(p, TM, p.gate ? 128 : 256, cus);
+            if (p.wmn) hipLaunchKernelGGL((moe_tiles<TM, true, false>), grid, block, 0, stream, p);
+            else if (p.gate) hipLaunchKernelGGL((moe_tiles<TM, false, true>), grid, block, 0, stream, p);
+            else hipLaunchKernelGGL((moe_tiles<TM, false, false>), grid, block, 0, stream, p);
+        };
+        if (rows == 256) go(std::integral_constant<int, 256>{});
+        else go(std::integral_constant<int, 128>{});
     }
     return hipGetLastError();
 }

@@ -163,30 +163,47 @@ SHAPES = [
 ]
 
 
-# rows and columns enough for the 256-row tiles in every form: rests of one to
-# four blocks, column starts past 2048, one to a few stages, no whole pieces
+# rows and columns enough for the 256-row tiles: rests of one to four blocks,
+# column starts past 2048, one to a few stages, no whole pieces
 LARGE = [
-    (1300, 1300, 2, 4360, 72, "ragged"), (600, 3000, 5, 4360, 136, "ragged"), (2000, 6000, 3, 2304, 200, "ragged"),
-    (5000, None, 40, 1032, 264, "ragged"), (64000, None, 3, 33, 40, "ragged"), (64500, None, 2, 72, 8, "one"),
+    (600, 3000, 5, 4360, 136, "ragged"), (2000, 6000, 3, 2304, 200, "ragged"),
+    (5000, None, 40, 1032, 264, "ragged"), (64000, None, 3, 97, 40, "ragged"), (64500, None, 2, 72, 8, "one"),
     (9000, None, 6, 2312, 104, "none"), (4000, 9000, 7, 2312, 328, "short"), (300, 4097, 1, 4099, 64, "even"),
     (1, 2600, 2, 4104, 128, "even"),
 ]
 
 
-def test_large_shapes_reach_the_large_tiles():
-    """The rule of moe.cpp, on the 256 CUs it counts here, sends every shape of
-    LARGE to 256-row tiles in the forms that the tests run, and SHAPES has
-    some for the 64-row tiles."""
-    def height(M, E, cols, mn, gate):
-        met = min(M, -(-3 * M * E // (3 * M + E)))
-        tiles = lambda tm, tn: max(M // tm + met // 2, met) * -(-cols // tn)
-        few, rounds = tiles(64, 128 if mn else 32 if gate else 64), -(-tiles(256, 128 if gate else 256) // 256)
-        return 64 if (52 if mn else 26) * few <= 100 * rounds * 256 else 256
-    for T, M, E, N, K, _ in LARGE:
-        assert height(M or T, E, N, False, False) == 256 and height(M or T, E, N, False, True) == 256
-        if N % 8 == 0 and N > 1000:
-            assert height(M or T, E, N, True, False) == 256
-    assert any(height(M or T, E, N, False, False) == 64 for T, M, E, N, K, _ in SHAPES)
+# for the 128-row tiles
+MID = [
+    (900, 2048, 2, 2056, 200, "ragged"), (500, 4000, 8, 1032, 40, "ragged"), (4000, None, 1, 1033, 264, "even"),
+    (8200, None, 5, 608, 328, "ragged"), (1300, 1300, 2, 4360, 72, "ragged"), (3800, None, 3, 1352, 136, "short"),
+    (1200, None, 3, 4096, 104, "ragged"), (700, 8300, 5, 600, 72, "ragged"), (2900, None, 2, 1544, 328, "ragged"),
+]
+HALF = [(T, M, E, N // 2, K, groups) for T, M, E, N, K, groups in MID]      # the same behind the gate
+
+
+def test_shapes_reach_every_tile_height():
+    """The rule of moe.cpp on 256 CUs: LARGE goes to 256-row tiles and MID to
+    128-row tiles of a K-major product, and in every form the shapes of the tests
+    reach every height three times at least."""
+    def height(M, E, N, mn, gate):
+        cols, met = N // 2 if gate else N, min(M, -(-2 * M * E // (2 * M + E)))
+        per_cu = lambda tm, tn: max(M // tm + met // 2, met) * -(-cols // tn) / 256
+        w = met * N / 65536
+
+        def rounds(tm, stage):
+            n = per_cu(tm, 128 if gate else 256)
+            return n // 1 * max(stage, w / n) + (stage if n % 1 else 0.0)
+        small = max((0.39 if mn else 0.22) * per_cu(64, 128 if mn else 32 if gate else 64), 1.1 * w)
+        mid, large = rounds(128, 0.85), rounds(256, 1.0)
+        return 64 if small <= mid and small <= large else 128 if mid < large else 256
+    for shapes, want in ((LARGE, 256), (MID, 128)):
+        for T, M, E, N, K, groups in shapes:
+            assert height(M or T, E, N, False, False) == want, (T, M, E, N, K, groups)
+    for mn, gate in ((False, False), (False, True), (True, False)):
+        reached = [height(M or T, E, 2 * N if gate else N, mn, gate)
+                   for T, M, E, N, K, _ in SHAPES + MID + LARGE + (HALF if gate else []) if not mn or N % 8 == 0]
+        assert all(reached.count(h) >= 3 for h in (64, 128, 256)), (mn, gate, reached)
 
 
 def test_dw_shapes_reach_both_tiles():
@@ -220,7 +237,7 @@ def _gpu(X, off, rows):
     return X.cuda(), torch.tensor(off, dtype=torch.int32).cuda(), None if rows is None else rows.cuda()
 
 
-@pytest.mark.parametrize("T,M,E,N,K,groups", SHAPES + LARGE)
+@pytest.mark.parametrize("T,M,E,N,K,groups", SHAPES + MID + LARGE)
 def test_product(T, M, E, N, K, groups):
     g, X, off, rows = _case(T, M, E, K, groups, N + K)
     W = _bf16(g, E, N, K)
@@ -233,7 +250,7 @@ def test_product(T, M, E, N, K, groups):
     assert np.all(got[off[-1]:] == 0)
 
 
-@pytest.mark.parametrize("T,M,E,N,K,groups", [s for s in SHAPES + LARGE if s[3] % 8 == 0])
+@pytest.mark.parametrize("T,M,E,N,K,groups", [s for s in SHAPES + MID + LARGE if s[3] % 8 == 0])
 def test_product_transposed(T, M, E, N, K, groups):
     g, X, off, rows = _case(T, M, E, K, groups, N + K + 1)
     W = _bf16(g, E, K, N)
@@ -245,7 +262,7 @@ def test_product_transposed(T, M, E, N, K, groups):
     assert np.all(got[off[-1]:] == 0)
 
 
-@pytest.mark.parametrize("T,M,E,F,K,groups", SHAPES + LARGE)
+@pytest.mark.parametrize("T,M,E,F,K,groups", SHAPES + MID + LARGE + HALF)
 def test_product_gated(T, M, E, F, K, groups):
     g, X, off, rows = _case(T, M, E, K, groups, F + K + 2)
     W = _bf16(g, E, 2 * F, K, scale=K ** -0.5 * 2)

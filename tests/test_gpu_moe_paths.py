@@ -127,7 +127,9 @@ def test_graph_replays_on_new_inputs():
 CASES = [(300, 700, 4, 264, 136), (2000, 5000, 3, 520, 328), (48, 300, 64, 96, 200), (700, 1500, 5, 776, 1032),
          (2500, 2500, 2, 512, 256),
          # 256-row tiles in every form, and 64 x 128 tiles of dW over several rounds
-         (1500, 2600, 3, 4400, 2312), (3000, 3000, 7, 4096, 2120), (900, 12000, 60, 320, 1544)]
+         (1500, 2600, 3, 4400, 2312), (3000, 3000, 7, 4096, 2120), (900, 12000, 60, 320, 1544),
+         # 128-row tiles: K-major, and of the last MN-major and gated
+         (900, 2048, 2, 2056, 200), (2000, 2900, 2, 2056, 1544)]
 
 
 def _inputs(T, M, E, N, K, seed):
