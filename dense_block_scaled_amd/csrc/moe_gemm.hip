@@ -487,10 +487,10 @@ __device__ __forceinline__ float gated(float g, float u)
 // for the CUs: the same stages with half of A's parts left out, 1.1 us in place
 // of 1.3.  BMN: W MN-major; GATE: see the head of the file.
 //
-// 32768 rows of 32 uneven experts, 4096 x 2048 MN-major: 500 us (1.10
+// 32768 rows of 32 uneven experts, 4096 x 2048 MN-major: 490 us (1.12
 // PFLOP/s): 4.1 tiles' work a CU, of which the busiest have 4.7, with rests
-// that cost more than their share; in even groups 440.  24594 rows of 64 very
-// uneven experts, 1416 x 2048: 182 us (0.78 PFLOP/s), where groups of 1.5
+// that cost more than their share; in even groups 430.  24594 rows of 64 very
+// uneven experts, 1416 x 2048: 177 us (0.8 PFLOP/s), where groups of 1.5
 // tile rows leave a third of the tiles partly empty.
 template <int TM, bool BMN, bool GATE>
 __global__ __launch_bounds__(512, 1) void moe_tiles(MoeGemm p)
@@ -669,7 +669,7 @@ __global__ __launch_bounds__(512, 1) void moe_tiles(MoeGemm p)
 // half of the columns.  With the gate a wave's 32 rows of W are 16 gate rows
 // and the 16 up rows that meet them.
 //
-// 384 rows on 128 experts behind the gate, 768 x 4096: 216 us for 1.5 GB (7
+// 384 rows on 128 experts behind the gate, 768 x 4096: 212 us for 1.5 GB (7
 // TB/s); one token on 8 experts, 1408 x 2048: 21 us for 92 MB (4.3 TB/s: 352
 // tiles on 256 CUs, and the way into the kernel).  Against 64 x 256 tiles over three slots (0.7 us a stage): 8 experts of
 // 4096 x 4096, 4 rows 42 us against 45, 32 rows 44 against 63; 64 experts of
@@ -871,8 +871,8 @@ constexpr int kDwBand = 8;
 // waits for them by its own count, no barrier), into a buffer per parity of
 // the tile for a tile's first eight stages and two in turn for later ones.
 //
-// 32768 rows of 32 uneven experts, 4096 x 2048: 550 us to bf16 (1.0 PFLOP/s)
-// at 47 % of the matrix cores' cycles: 1.7 us a stage, and 5 us for each of a
+// 32768 rows of 32 uneven experts, 4096 x 2048: 542 us to bf16 (1.0 PFLOP/s)
+// at 46 % of the matrix cores' cycles: 1.7 us a stage, and 5 us for each of a
 // CU's 16 tiles, when all CUs write at once.  One expert of 16384 rows,
 // 4096 x 4096: 414 us (1.33 PFLOP/s).
 template <bool GATHER, bool F32>

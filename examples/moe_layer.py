@@ -83,7 +83,8 @@ def reference(layer: MoeLayer, x: torch.Tensor, router, w13, w2) -> torch.Tensor
 
 
 def relative(a: torch.Tensor, b: torch.Tensor) -> float:
-    return float((a.double() - b.double()).norm() / b.double().norm())
+    a, b = a.detach().double(), b.detach().double()
+    return float((a - b).norm() / b.norm())
 
 
 def run(tokens: int, hidden: int, ffn: int, experts: int, k: int, seed: int = 0) -> dict:
