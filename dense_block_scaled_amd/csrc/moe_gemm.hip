@@ -96,54 +96,78 @@ __device__ __forceinline__ Lane lane_of()
 // first[g] = first row of group g (g <= E; offsets clamped to 0 .. M and made
 // ascending; with FIRST), and at[g] = units of work before group g, per(rows)
 // of them in a group: by one wave, the others wait at the caller's barrier.
+// A lane has ceil(E / 64) groups in a row, so that all loads are under way
+// together (1024 experts: 16 trips to memory one after the other before).
 template <bool FIRST, class T, class PER>
 __device__ __forceinline__ void group_table(int32_t *first, T *at, const int32_t *offsets, int E, int M, const Lane &c,
                                             PER &&per)
 {
-    int hi = 0, sum = 0;                       // last row and work before this chunk of 64 groups
-    if (c.lane == 0) {
-        hi = min(max(offsets[0], 0), M);
-        if constexpr (FIRST) first[0] = hi;
-        at[0] = 0;
+    constexpr int kMost = kMoeMaxExperts / 64;
+    const int S = (E + 63) / 64, g0 = c.lane * S;
+    int end[kMost];
+#pragma unroll
+    for (int i = 0; i < kMost; ++i) {
+        if (i == S) break;
+        end[i] = offsets[min(g0 + i + 1, E)];
     }
-    hi = __shfl(hi, 0);
-    for (int g0 = 0; g0 < E; g0 += 64) {
-        const int g = g0 + c.lane;
-        int end = g < E ? min(max(offsets[g + 1], 0), M) : 0;
-        end = max(end, hi);
+    const int start = min(max(offsets[0], 0), M);
+    int top = start;
 #pragma unroll
-        for (int d = 1; d < 64; d *= 2) {
-            const int o = __shfl_up(end, d);
-            if (c.lane >= d) end = max(end, o);
-        }
-        const int prev = __shfl_up(end, 1);
-        const int rows = end - (c.lane == 0 ? hi : prev);
-        int n = g < E ? per(rows) : 0;
+    for (int i = 0; i < kMost; ++i) {
+        if (i == S) break;
+        end[i] = min(max(end[i], 0), M);
+        top = max(top, end[i]);
+    }
 #pragma unroll
-        for (int d = 1; d < 64; d *= 2) {
-            const int o = __shfl_up(n, d);
-            if (c.lane >= d) n += o;
+    for (int d = 1; d < 64; d *= 2) {
+        const int o = __shfl_up(top, d);
+        if (c.lane >= d) top = max(top, o);
+    }
+    int lo = __shfl_up(top, 1);                // the lane's first row
+    lo = c.lane == 0 ? start : lo;
+    int sum = 0, row = lo;
+#pragma unroll
+    for (int i = 0; i < kMost; ++i) {
+        if (i == S) break;
+        end[i] = max(end[i], row);
+        sum += g0 + i < E ? per(end[i] - row) : 0;
+        row = end[i];
+    }
+    int work = sum;
+#pragma unroll
+    for (int d = 1; d < 64; d *= 2) {
+        const int o = __shfl_up(work, d);
+        if (c.lane >= d) work += o;
+    }
+    work -= sum;
+    row = lo;
+#pragma unroll
+    for (int i = 0; i < kMost; ++i) {
+        if (i == S) break;
+        if (g0 + i < E) {
+            if constexpr (FIRST) first[g0 + i] = row;
+            at[g0 + i] = (T)work;
+            work += per(end[i] - row);
+            row = end[i];
+            if (g0 + i == E - 1) {
+                if constexpr (FIRST) first[E] = row;
+                at[E] = (T)work;
+            }
         }
-        if (g < E) {
-            if constexpr (FIRST) first[g + 1] = end;
-            at[g + 1] = (T)(sum + n);
-        }
-        hi = __shfl(end, 63);
-        sum += __shfl(n, 63);
     }
 }
 
 // The last group g with at[g] <= id (groups without work have equal
-// neighbours): 64 entries a step, one LDS read each.
+// neighbours): every ceil(E / 64)-th entry, then those behind the last of them.
 template <class T>
 __device__ __forceinline__ int group_of(const T *at, int E, int id, const Lane &c)
 {
-    int n = 0;
-    for (int g0 = 0; g0 < E; g0 += 64) {
-        const int g = g0 + c.lane;
-        n += __popcll(__ballot(g < E && (int)at[g] <= id));
-    }
-    return __builtin_amdgcn_readfirstlane(n - 1);
+    const int S = (E + 63) / 64;
+    int g = c.lane * S;
+    const int block = __builtin_amdgcn_readfirstlane((__popcll(__ballot(g < E && (int)at[min(g, E)] <= id)) - 1) * S);
+    if (S == 1) return block;
+    g = block + c.lane;
+    return block + __builtin_amdgcn_readfirstlane(__popcll(__ballot(c.lane < S && g < E && (int)at[min(g, E)] <= id)) - 1);
 }
 
 __device__ __forceinline__ int first_tile()
@@ -827,34 +851,27 @@ __global__ __launch_bounds__(512, 1) void moe_tiles_64(MoeGemm p)
 // ---------------------------------------------------------------------- dw
 
 // The groups of E with work (all, or those with rows) into order, by their
-// number of rows in steps of half an octave, the longest first: tiles are
-// handed out in a snake, as the products' are, and end together the better
-// the smaller the last ones are.  By one wave; returns how many.
+// number of stages in steps of half an octave (two at least), the longest
+// first: tiles are handed out in a snake, as the products' are, and end
+// together the better the smaller the last ones are.  By one wave; returns how
+// many.
 __device__ __forceinline__ int sort_groups(uint16_t *order, const int32_t *first, int E, bool all, const Lane &c)
 {
-    auto step = [](int rows) { return rows > 0 ? (int)(__builtin_bit_cast(uint32_t, (float)rows) >> 22) : 0; };
-    int hi = 0, lo = 1 << 30;
-    for (int g = c.lane; g < E; g += 64) {
-        const int k = step(first[g + 1] - first[g]);
-        hi = max(hi, k);
-        lo = min(lo, k > 0 || all ? k : lo);
-    }
+    auto step = [](int rows) { return (int)(__builtin_bit_cast(uint32_t, (float)max((rows + 63) / 64, 2)) >> 22); };
+    int hi = step(0);
+    const int lo = hi;
+    for (int g = c.lane; g < E; g += 64) hi = max(hi, step(first[g + 1] - first[g]));
 #pragma unroll
-    for (int d = 32; d; d /= 2) {
-        hi = max(hi, __shfl_xor(hi, d));
-        lo = min(lo, __shfl_xor(lo, d));
-    }
+    for (int d = 32; d; d /= 2) hi = max(hi, __shfl_xor(hi, d));
     int n = 0;
-    // (from 0, no rows, to the first step, one row, lie steps that no group has)
-    for (int k = hi; k >= lo; k = k == 254 && lo == 0 ? 0 : k - 1) {
+    for (int k = hi; k >= lo; --k) {
         for (int g0 = 0; g0 < E; g0 += 64) {
-            const int g = g0 + c.lane;
-            const bool here = g < E && step(first[g + 1] - first[g]) == k;
+            const int g = g0 + c.lane, rows = g < E ? first[g + 1] - first[g] : 0;
+            const bool here = g < E && step(rows) == k && (all || rows > 0);
             const uint64_t who = __ballot(here);
             if (here) order[n + __popcll(who & (((uint64_t)1 << c.lane) - 1))] = (uint16_t)g;
             n += __popcll(who);
         }
-        if (k == 0) break;
     }
     return n;
 }
