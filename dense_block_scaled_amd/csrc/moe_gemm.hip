@@ -695,9 +695,9 @@ __global__ __launch_bounds__(512, 1) void moe_tiles(MoeGemm p)
 //
 // 384 rows on 128 experts behind the gate, 768 x 4096: 212 us for 1.5 GB (7
 // TB/s); one token on 8 experts, 1408 x 2048: 21 us for 92 MB (4.3 TB/s: 352
-// tiles on 256 CUs, and the way into the kernel).  Against 64 x 256 tiles over three slots (0.7 us a stage): 8 experts of
-// 4096 x 4096, 4 rows 42 us against 45, 32 rows 44 against 63; 64 experts of
-// 2816 x 2048, 16 rows 143 against 169.
+// tiles on 256 CUs, and the way into the kernel).  Against 64 x 256 tiles over
+// three slots (0.7 us a stage): 8 experts of 4096 x 4096, 4 rows 42 us against
+// 45, 32 rows 44 against 63; 64 experts of 2816 x 2048, 16 rows 143 against 169.
 template <bool BMN>
 struct Deep {
     static constexpr int TN = BMN ? 128 : 64, NS = BMN ? 6 : 8, NB = TN / 32, QB = TN / 64;
