@@ -54,6 +54,10 @@ __device__ __forceinline__ i32x4 words_of(const void *base, uint32_t bytes)
 // are built on.  They wait by count themselves, at every barrier.  Lane i's
 // bytes land at lds + dst + BYTES i; nothing is returned to registers.  (M0, which
 // holds the destination, is a register the compiler sets before its own uses.)
+// A descriptor's words come from v_readfirstlane or, respilled, v_readlane, and
+// a vector load may read an SGPR that a vector instruction wrote only five wait
+// states later (M0 one after it is set).  The compiler does not count them for
+// a load inside asm, so they stand here: one move and four of s_nop 3.
 template <int BYTES>
 __device__ __forceinline__ void dma(const i32x4 &words, uint8_t *lds, uint32_t dst, uint32_t voff)
 {
@@ -68,10 +72,10 @@ __device__ __forceinline__ void dma(const i32x4 &words, uint8_t *lds, uint32_t d
 #endif
     const uint32_t m0 = (uint32_t)(uintptr_t)(lds_void *)lds + dst;
     if constexpr (BYTES == 4)
-        asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dword %1, %2, 0 offen lds" ::"s"(m0), "v"(voff), "s"(words)
+        asm volatile("s_mov_b32 m0, %0\n\ts_nop 3\n\tbuffer_load_dword %1, %2, 0 offen lds" ::"s"(m0), "v"(voff), "s"(words)
                      : "memory");
     else
-        asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dwordx4 %1, %2, 0 offen lds" ::"s"(m0), "v"(voff), "s"(words)
+        asm volatile("s_mov_b32 m0, %0\n\ts_nop 3\n\tbuffer_load_dwordx4 %1, %2, 0 offen lds" ::"s"(m0), "v"(voff), "s"(words)
                      : "memory");
 }
 

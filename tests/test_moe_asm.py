@@ -65,3 +65,87 @@ def test_mfma_results_are_read_after_their_wait_states(listings, unit):
     assert len(re.findall(r"^\s*v_mfma", text, flags=re.M)) > 100
     _, short = hazards.scan(text)
     assert not short, f"{len(short)} MFMA results read too early, e.g. {short[0]}"
+
+
+# An SGPR that a vector instruction has written may be read by a vector memory
+# instruction only five wait states later.  The compiler keeps them for its
+# own instructions, not for those inside inline asm, which the direct-to-LDS
+# loads of these kernels are.
+SGPR_WAIT = 5
+
+
+def _sgprs(tok):
+    m = re.match(r"s\[(\d+):(\d+)\]$", tok)
+    if m:
+        return set(range(int(m.group(1)), int(m.group(2)) + 1))
+    m = re.match(r"s(\d+)$", tok)
+    return {int(m.group(1))} if m else set()
+
+
+def _sgpr_results(op, ops):
+    """SGPRs that a vector instruction writes."""
+    if op.startswith(("v_readfirstlane", "v_readlane", "v_cmp")):
+        return _sgprs(ops[0])
+    if op.startswith(("v_add_co", "v_sub_co", "v_subrev_co", "v_addc_co", "v_subb_co", "v_subbrev_co", "v_div_scale",
+                      "v_mad_u64", "v_mad_i64")):
+        return _sgprs(ops[1])
+    return set()
+
+
+def _early_sgpr_reads(text):
+    """(vector instructions that write SGPRs, [(wait states, writer, reader)] below SGPR_WAIT), on every path."""
+    lines = []
+    for raw in text.splitlines():
+        s = raw.split(";")[0].strip()
+        if s and (not s.startswith(".") or s.endswith(":")):
+            lines.append(s)
+    label = {s[:-1]: i for i, s in enumerate(lines) if s.endswith(":")}
+    writers, early = 0, []
+    for i, s in enumerate(lines):
+        p = s.replace(",", " ").split()
+        dst = _sgpr_results(p[0], p[1:])
+        if not dst:
+            continue
+        writers += 1
+        paths = [(i + 1, 0, dst)]
+        while paths:
+            j, ws, live = paths.pop()
+            while j < len(lines) and ws < SGPR_WAIT and live:
+                t = lines[j]
+                j += 1
+                if t.endswith(":"):
+                    continue
+                q = t.replace(",", " ").split()
+                if q[0] == "s_nop":
+                    ws += int(q[1], 0) + 1
+                    continue
+                if q[0].startswith(("buffer_", "global_", "flat_", "scratch_")):
+                    if any(live & _sgprs(a) for a in q[1:]):
+                        early.append((ws, s, t))
+                        break
+                elif q[0].startswith("s_cbranch"):
+                    paths.append((label[q[1]], ws + 1, live))
+                elif q[0].startswith("s_") and len(q) > 1:
+                    live = live - _sgprs(q[1])             # a scalar result takes its place
+                if q[0] == "s_branch":
+                    j = label[q[1]]
+                if q[0] in ("s_endpgm", "s_setpc_b64"):
+                    break
+                ws += 1
+    return writers, early
+
+
+def test_the_scan_finds_an_early_read_of_an_sgpr():
+    early = "v_readfirstlane_b32 s6, v1\ns_mov_b32 s7, 0\ns_nop 2\nbuffer_load_dword v1, v0, s[4:7], 0 offen lds\n"
+    assert _early_sgpr_reads(early) == (1, [(4, "v_readfirstlane_b32 s6, v1",
+                                             "buffer_load_dword v1, v0, s[4:7], 0 offen lds")])
+    assert _early_sgpr_reads(early.replace("s_nop 2", "s_nop 3")) == (1, [])
+    assert _early_sgpr_reads(early.replace("s_mov_b32 s7", "s_mov_b32 s6")) == (1, [])
+
+
+@pytest.mark.parametrize("unit", UNITS)
+@pytest.mark.parametrize("poisoned", [False, True])
+def test_loads_read_their_descriptors_after_the_wait_states(listings, unit, poisoned):
+    writers, early = _early_sgpr_reads(listings[(unit, poisoned)])
+    assert writers > 100
+    assert not early, f"{len(early)} SGPRs read too early, e.g. {early[0]}"
