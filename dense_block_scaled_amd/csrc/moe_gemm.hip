@@ -79,6 +79,54 @@ __device__ __forceinline__ void dma(const i32x4 &words, uint8_t *lds, uint32_t d
                      : "memory");
 }
 
+// Two wave-loads to neighbouring KiB, or four, the second two `apart` bytes
+// behind the first, from one descriptor, at offsets max(at, least): `least` is 0
+// or, where a lane has nothing to load, an offset out of bounds.  The maxima
+// stand in the descriptor's wait states.  32 experts of 4096 x 2048, 32768 rows,
+// MN-major: 519 us, 532 with the loads one by one and s_nop 3 before each.
+template <int N>
+__device__ __forceinline__ void dma_group(const i32x4 &words, uint8_t *lds, uint32_t dst, const uint32_t (&at)[N],
+                                          const uint32_t (&least)[N], uint32_t apart = 0)
+{
+    static_assert(N == 2 || N == 4, "one pair or two");
+#if DBS_LDS_POISON
+#pragma unroll
+    for (int i = 0; i < N; ++i)
+        dma<16>(words, lds, dst + (i & 1) * 1024 + (i >> 1) * apart, max(at[i], least[i]));
+#else
+    const uint32_t m0 = (uint32_t)(uintptr_t)(lds_void *)lds + dst;
+    uint32_t off[N];
+    if constexpr (N == 2)
+        asm volatile("s_mov_b32 m0, %2\n\t"
+                     "v_max_u32 %0, %3, %5\n\t"
+                     "v_max_u32 %1, %4, %6\n\t"
+                     "s_nop 1\n\t"
+                     "buffer_load_dwordx4 %0, %7, 0 offen lds\n\t"
+                     "s_add_u32 m0, m0, 0x400\n\ts_nop 0\n\t"
+                     "buffer_load_dwordx4 %1, %7, 0 offen lds"
+                     : "=&v"(off[0]), "=&v"(off[1])
+                     : "s"(m0), "v"(at[0]), "v"(at[1]), "v"(least[0]), "v"(least[1]), "s"(words)
+                     : "memory", "scc");
+    else
+        asm volatile("s_mov_b32 m0, %4\n\t"
+                     "v_max_u32 %0, %5, %9\n\t"
+                     "v_max_u32 %1, %6, %10\n\t"
+                     "v_max_u32 %2, %7, %11\n\t"
+                     "v_max_u32 %3, %8, %12\n\t"
+                     "buffer_load_dwordx4 %0, %13, 0 offen lds\n\t"
+                     "s_add_u32 m0, m0, 0x400\n\ts_nop 0\n\t"
+                     "buffer_load_dwordx4 %1, %13, 0 offen lds\n\t"
+                     "s_add_u32 m0, m0, %14\n\ts_nop 0\n\t"
+                     "buffer_load_dwordx4 %2, %13, 0 offen lds\n\t"
+                     "s_add_u32 m0, m0, 0x400\n\ts_nop 0\n\t"
+                     "buffer_load_dwordx4 %3, %13, 0 offen lds"
+                     : "=&v"(off[0]), "=&v"(off[1]), "=&v"(off[2]), "=&v"(off[3])
+                     : "s"(m0), "v"(at[0]), "v"(at[1]), "v"(at[2]), "v"(at[3]), "v"(least[0]), "v"(least[1]),
+                       "v"(least[2]), "v"(least[3]), "s"(words), "s"(apart - 1024)
+                     : "memory", "scc");
+#endif
+}
+
 struct Lane {
     int lane, h, lr, w, wm, wn;
 };
@@ -315,7 +363,8 @@ __device__ __forceinline__ void read_b(bf16x8 (&b)[4], const uint8_t *lds, uint3
 
 // One stage out of slot `slot`.  NLO, NHI: blocks per wave in the two halves
 // of A (fewer than 2 where a group ends).  advance() moves the loads on to the
-// next stage, load(part, slot) issues the two wave-loads of a part of it.
+// next stage, load(part, slot) issues the two wave-loads of a part of A, or
+// (kBLo) the four of both parts of B.
 // extra: STORES stores of the last tile's results went out between the loads
 // awaited here and now, and may still be under way.
 template <bool AMN, bool BMN, int NLO, int NHI, class LOAD, class ADVANCE, int STORES>
@@ -359,7 +408,6 @@ __device__ __forceinline__ void core_stage(Acc &acc, const uint8_t *lds, uint32_
     advance();
     load(kALo, slot);
     load(kBLo, slot);
-    load(kBHi, slot);
     wait();
     __builtin_amdgcn_s_setprio(1);
     math(1, 1, NHI, b1);
@@ -592,30 +640,38 @@ __global__ __launch_bounds__(512, 1) void moe_tiles(MoeGemm p)
         }
     };
     auto load = [&](int part, int slot) {
-        const int k0 = lk * kRowBytes;
+        const uint32_t dst = slot * kSlot + part * kPart + c.w * 2048;
+        // the lane's bytes of a K-major row, and the least offset they lead to (past the row's end out of bounds)
+        uint32_t kc[2], least[2];
 #pragma unroll
         for (int q = 0; q < 2; ++q) {
-            const int L = c.w * 2 + q;
-            const uint32_t dst = slot * kSlot + part * kPart + L * 1024;
-            const int kc = (int)(x4 ^ (uint32_t)((L & 7) << 4)) + k0;
-            if (part == kALo || part == kAHi) {
-                dma<16>(ra, lds, dst, kc < lda ? aoff[(part == kAHi ? 2 : 0) + q] + kc : kRowOOB);
+            kc[q] = (x4 ^ (uint32_t)(((c.w * 2 + q) & 7) << 4)) + (uint32_t)(lk * kRowBytes);
+            least[q] = kc[q] < (uint32_t)lda ? 0u : kRowOOB;
+        }
+        if (part == kALo || part == kAHi) {
+            const int i = part == kAHi ? 2 : 0;
+            dma_group<2>(ra, lds, dst, {aoff[i] + kc[0], aoff[i + 1] + kc[1]}, least);
+            return;
+        }
+        uint32_t x[4], y[4];                   // [2 j + q]: part j of B
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const int j = i >> 1, L = c.w * 2 + (i & 1);
+            if constexpr (BMN) {
+                const uint32_t row = (uint32_t)(lk * 64 + L * 4);          // four K-rows a wave-load
+                x[i] = lb + row * (uint32_t)ldb + j * 256;
+                y[i] = row < (uint32_t)p.K ? 0u : kOOB;
+            } else if constexpr (GATE) {
+                const int f = f0 + L * 8;                                  // of matrix j
+                x[i] = lb + (uint32_t)(j * p.ncols + f) * (uint32_t)lda + kc[i & 1];
+                y[i] = f + (c.lane >> 3) < p.ncols ? least[i & 1] : kOOB;
             } else {
-                const int j = part == kBHi;
-                if constexpr (BMN) {
-                    const uint32_t row = (uint32_t)(lk * 64 + L * 4);          // four K-rows a wave-load
-                    dma<16>(rb, lds, dst, row < (uint32_t)p.K ? lb + row * (uint32_t)ldb + j * 256 : kOOB);
-                } else if constexpr (GATE) {
-                    const int f = f0 + L * 8;                                  // of matrix j
-                    dma<16>(rb, lds, dst, kc < lda && f + (c.lane >> 3) < p.ncols
-                                             ? lb + (uint32_t)((j * p.ncols + f) * lda) + kc : kOOB);
-                } else {
-                    // wave column L / 4's rows: 32 of its 64
-                    const int n = (L >> 2) * 64 + j * 32 + (L & 3) * 8;
-                    dma<16>(rb, lds, dst, kc < lda ? lb + (uint32_t)(n * lda) + kc : kOOB);
-                }
+                // wave column L / 4's rows: 32 of its 64
+                x[i] = lb + (uint32_t)(((L >> 2) * 64 + j * 32 + (L & 3) * 8) * lda) + kc[i & 1];
+                y[i] = least[i & 1];
             }
         }
+        dma_group<4>(rb, lds, dst, x, y, kPart);
     };
 
     RowTile cur = find(0), next = cur;
@@ -628,12 +684,10 @@ __global__ __launch_bounds__(512, 1) void moe_tiles(MoeGemm p)
     aim(cur);
     load(kALo, 0);
     load(kBLo, 0);
-    load(kBHi, 0);
     load(kAHi, 0);
     advance();
     load(kALo, 1);
     load(kBLo, 1);
-    load(kBHi, 1);
     uint32_t fa = part_base<false>(c, c.wm), fb = part_base<BMN>(c, c.wn);
     uint8_t *buf = lds + kStage + c.w * 2048;
     turn_end<kInFlight>();
@@ -963,16 +1017,15 @@ __device__ __forceinline__ void dw_large(const MoeGemmDw &p, const Lane &c, uint
         }
     };
     auto load = [&](int part, int slot) {
-        const bool a = part == kALo || part == kAHi;
-        const int col = part == kAHi || part == kBHi ? 256 : 0;
-#pragma unroll
-        for (int q = 0; q < 2; ++q) {
-            const int L = c.w * 2 + q;
-            const uint32_t dst = slot * kSlot + part * kPart + L * 1024;
-            if (a) dma<16>(wa, lds, dst, la + (uint32_t)(L * 4 * lda + col));
-            else if (GATHER) dma<16>(wb, lds, dst, boff[q] + col);
-            else dma<16>(wb, lds, dst, lb + (uint32_t)(L * 4 * ldb + col));
+        const uint32_t dst = slot * kSlot + part * kPart + c.w * 2048;
+        if (part == kALo || part == kAHi) {
+            const uint32_t at = la + (uint32_t)(c.w * 8 * lda) + (part == kAHi ? 256 : 0);
+            dma_group<2>(wa, lds, dst, {at, at + (uint32_t)(4 * lda)}, {0, 0});
+            return;
         }
+        const uint32_t b0 = GATHER ? boff[0] : lb + (uint32_t)(c.w * 8 * ldb);
+        const uint32_t b1 = GATHER ? boff[1] : b0 + (uint32_t)(4 * ldb);
+        dma_group<4>(wb, lds, dst, {b0, b1, b0 + 256, b1 + 256}, {0, 0, 0, 0}, kPart);
     };
 
     batch(cur, 0, 0);
@@ -980,13 +1033,11 @@ __device__ __forceinline__ void dw_large(const MoeGemmDw &p, const Lane &c, uint
     aim();
     load(kALo, 0);
     load(kBLo, 0);
-    load(kBHi, 0);
     load(kAHi, 0);
     lk = 1;
     aim();
     load(kALo, 1);
     load(kBLo, 1);
-    load(kBHi, 1);
     uint32_t fa = part_base<true>(c, c.wm), fb = part_base<true>(c, c.wn);
     uint8_t *buf = lds + kStage + c.w * 2048;
     turn_end<kInFlight>();
