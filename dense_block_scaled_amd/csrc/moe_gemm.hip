@@ -52,8 +52,8 @@ __device__ __forceinline__ i32x4 words_of(const void *base, uint32_t bytes)
 // written out: the compiler follows the builtin's loads and waits for all of
 // them before any LDS read, which would end the overlap this file's kernels
 // are built on.  They wait by count themselves, at every barrier.  Lane i's
-// bytes land at lds + dst + BYTES i; nothing is returned to registers.  (M0, which
-// holds the destination, is a register the compiler sets before its own uses.)
+// bytes land at lds + dst + BYTES i; nothing is returned to registers.  M0 holds
+// the destination; the compiler learns that it is written as an output.
 // A descriptor's words come from v_readfirstlane or, respilled, v_readlane, and
 // a vector load may read an SGPR that a vector instruction wrote only five wait
 // states later (M0 one after it is set).  The compiler does not count them for
@@ -70,12 +70,17 @@ __device__ __forceinline__ void dma(const i32x4 &words, uint8_t *lds, uint32_t d
         *reinterpret_cast<i32x4 *>(lds + dst + 16 * lane) = i32x4{-1, -1, -1, -1};
     asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
 #endif
-    const uint32_t m0 = (uint32_t)(uintptr_t)(lds_void *)lds + dst;
+    const uint32_t to = (uint32_t)(uintptr_t)(lds_void *)lds + dst;
+    uint32_t m0;
     if constexpr (BYTES == 4)
-        asm volatile("s_mov_b32 m0, %0\n\ts_nop 3\n\tbuffer_load_dword %1, %2, 0 offen lds" ::"s"(m0), "v"(voff), "s"(words)
+        asm volatile("s_mov_b32 m0, %1\n\ts_nop 3\n\tbuffer_load_dword %2, %3, 0 offen lds"
+                     : "=&{m0}"(m0)
+                     : "s"(to), "v"(voff), "s"(words)
                      : "memory");
     else
-        asm volatile("s_mov_b32 m0, %0\n\ts_nop 3\n\tbuffer_load_dwordx4 %1, %2, 0 offen lds" ::"s"(m0), "v"(voff), "s"(words)
+        asm volatile("s_mov_b32 m0, %1\n\ts_nop 3\n\tbuffer_load_dwordx4 %2, %3, 0 offen lds"
+                     : "=&{m0}"(m0)
+                     : "s"(to), "v"(voff), "s"(words)
                      : "memory");
 }
 
@@ -94,34 +99,34 @@ __device__ __forceinline__ void dma_group(const i32x4 &words, uint8_t *lds, uint
     for (int i = 0; i < N; ++i)
         dma<16>(words, lds, dst + (i & 1) * 1024 + (i >> 1) * apart, max(at[i], least[i]));
 #else
-    const uint32_t m0 = (uint32_t)(uintptr_t)(lds_void *)lds + dst;
-    uint32_t off[N];
+    const uint32_t to = (uint32_t)(uintptr_t)(lds_void *)lds + dst;
+    uint32_t m0, off[N];
     if constexpr (N == 2)
-        asm volatile("s_mov_b32 m0, %2\n\t"
-                     "v_max_u32 %0, %3, %5\n\t"
+        asm volatile("s_mov_b32 m0, %3\n\t"
                      "v_max_u32 %1, %4, %6\n\t"
+                     "v_max_u32 %2, %5, %7\n\t"
                      "s_nop 1\n\t"
-                     "buffer_load_dwordx4 %0, %7, 0 offen lds\n\t"
+                     "buffer_load_dwordx4 %1, %8, 0 offen lds\n\t"
                      "s_add_u32 m0, m0, 0x400\n\ts_nop 0\n\t"
-                     "buffer_load_dwordx4 %1, %7, 0 offen lds"
-                     : "=&v"(off[0]), "=&v"(off[1])
-                     : "s"(m0), "v"(at[0]), "v"(at[1]), "v"(least[0]), "v"(least[1]), "s"(words)
+                     "buffer_load_dwordx4 %2, %8, 0 offen lds"
+                     : "=&{m0}"(m0), "=&v"(off[0]), "=&v"(off[1])
+                     : "s"(to), "v"(at[0]), "v"(at[1]), "v"(least[0]), "v"(least[1]), "s"(words)
                      : "memory", "scc");
     else
-        asm volatile("s_mov_b32 m0, %4\n\t"
-                     "v_max_u32 %0, %5, %9\n\t"
+        asm volatile("s_mov_b32 m0, %5\n\t"
                      "v_max_u32 %1, %6, %10\n\t"
                      "v_max_u32 %2, %7, %11\n\t"
                      "v_max_u32 %3, %8, %12\n\t"
-                     "buffer_load_dwordx4 %0, %13, 0 offen lds\n\t"
+                     "v_max_u32 %4, %9, %13\n\t"
+                     "buffer_load_dwordx4 %1, %14, 0 offen lds\n\t"
                      "s_add_u32 m0, m0, 0x400\n\ts_nop 0\n\t"
-                     "buffer_load_dwordx4 %1, %13, 0 offen lds\n\t"
-                     "s_add_u32 m0, m0, %14\n\ts_nop 0\n\t"
-                     "buffer_load_dwordx4 %2, %13, 0 offen lds\n\t"
+                     "buffer_load_dwordx4 %2, %14, 0 offen lds\n\t"
+                     "s_add_u32 m0, m0, %15\n\ts_nop 0\n\t"
+                     "buffer_load_dwordx4 %3, %14, 0 offen lds\n\t"
                      "s_add_u32 m0, m0, 0x400\n\ts_nop 0\n\t"
-                     "buffer_load_dwordx4 %3, %13, 0 offen lds"
-                     : "=&v"(off[0]), "=&v"(off[1]), "=&v"(off[2]), "=&v"(off[3])
-                     : "s"(m0), "v"(at[0]), "v"(at[1]), "v"(at[2]), "v"(at[3]), "v"(least[0]), "v"(least[1]),
+                     "buffer_load_dwordx4 %4, %14, 0 offen lds"
+                     : "=&{m0}"(m0), "=&v"(off[0]), "=&v"(off[1]), "=&v"(off[2]), "=&v"(off[3])
+                     : "s"(to), "v"(at[0]), "v"(at[1]), "v"(at[2]), "v"(at[3]), "v"(least[0]), "v"(least[1]),
                        "v"(least[2]), "v"(least[3]), "s"(words), "s"(apart - 1024)
                      : "memory", "scc");
 #endif

@@ -149,3 +149,22 @@ def test_loads_read_their_descriptors_after_the_wait_states(listings, unit, pois
     writers, early = _early_sgpr_reads(listings[(unit, poisoned)])
     assert writers > 100
     assert not early, f"{len(early)} SGPRs read too early, e.g. {early[0]}"
+
+
+@pytest.mark.parametrize("poisoned", [False, True])
+def test_the_compiler_knows_what_the_loads_do_to_m0(poisoned, tmp_path):
+    """M0, which holds a load's destination, is written inside inline asm: each
+    such statement has it as an output, or the compiler might take a value of
+    its own to be still there (in the IR: {m0} among the asm's outputs)."""
+    if not Path(poison.HIPCC).exists():
+        pytest.skip("hipcc not available")
+    out = tmp_path / "moe_gemm.ll"
+    subprocess.run([poison.HIPCC, "--offload-arch=gfx950", "-O3", "-std=c++17", f"-I{poison.ROOT / 'include'}",
+                    f"-I{poison.CSRC}", "-Xclang", "-target-feature", "-Xclang", "-packed-fp32-ops", "--cuda-device-only",
+                    "-S", "-emit-llvm", *(["-DDBS_LDS_POISON=1"] if poisoned else []),
+                    str(poison.CSRC / "moe_gemm.hip"), "-o", str(out)], check=True, capture_output=True)
+    writes = [x for x in out.read_text().splitlines() if " asm " in x and re.search(r"s_\w+ m0,", x)]
+    assert len(writes) > 100
+    for x in writes:
+        constraints = re.findall(r'"([^"]*)"', x[x.index(" asm "):])[1]
+        assert "{m0}" in [c.lstrip("=&") for c in constraints.split(",") if c.startswith("=")], x.strip()[:300]
