@@ -28,6 +28,7 @@
 //   accumulating, nothing).
 #include "gemm_kernel.h"
 #include "moe.h"
+#include "moe_device.h"
 
 namespace dbs {
 namespace {
@@ -437,12 +438,14 @@ __device__ __forceinline__ void store_block(uint8_t *buf, uint8_t *D, int64_t ld
     // block g's four values of consecutive columns lie at row and column
     const int row0 = c.lane & 15, col0 = 4 * (c.lane >> 4);
     if (vec) {
+        wave_handover();                     // (the block before has been read)
 #pragma unroll
         for (int g = 0; g < 4; ++g) {
             const int u = g >> 1, v = g & 1, row = 16 * u + row0, col = 16 * v + col0;
             *reinterpret_cast<u32x2 *>(buf + row * 64 + (((col >> 3) ^ ((row >> 1) & 3)) << 4) + 2 * (col & 4)) =
                 u32x2{pack_bf16(value(u, v, 0), value(u, v, 1)), pack_bf16(value(u, v, 2), value(u, v, 3))};
         }
+        wave_handover();
 #pragma unroll
         for (int q = 0; q < 2; ++q) {
             const int r = q * 16 + (c.lane >> 2), ch = c.lane & 3, n = n0 + ch * 8;
@@ -1299,8 +1302,9 @@ __global__ __launch_bounds__(512, 1) void moe_dw(MoeGemmDw p)
     if (c.w == 0) {
         // (the table's second part, rows before a group, is not used)
         group_table<true>(first, order, p.offsets, p.E, p.M, c, [](int) { return 0; });
-        __builtin_amdgcn_wave_barrier();
+        wave_handover();
         const int n = sort_groups(order, first, p.E, !p.accumulate, c);
+        wave_handover();
         int longest = 0, two = 0, four = 0;            // stages, at least two or four to a tile
         for (int i = c.lane; i < n; i += 64) {
             const int g = order[i], stages = (first[g + 1] - first[g] + 63) / 64;

@@ -39,6 +39,7 @@
 #include <type_traits>
 
 #include "moe.h"
+#include "moe_device.h"
 
 namespace dbs {
 namespace {
@@ -333,7 +334,7 @@ __global__ __launch_bounds__(kThreads) void route_place(MoeRoute p, int64_t nb)
 // elsewhere.  16 lanes a token, as in route_select; lane j has the j-th
 // choice, and the chosen experts' gradients reach the lanes that hold those
 // experts through a row of E floats in LDS (zeroed, written and read by the
-// token's own lanes of one wave, whose LDS operations keep their order).
+// token's own lanes of one wave, with a handover between).
 template <int VPL, int C, bool BF16>
 __global__ __launch_bounds__(kThreads) void route_bwd(const void *logits, int64_t T, int E, int k, int renorm,
                                                       const int32_t *experts, const float *dweights, void *dlogits)
@@ -384,9 +385,9 @@ __global__ __launch_bounds__(kThreads) void route_bwd(const void *logits, int64_
     const float scale = renorm ? 0.0f : dot * inv;
 #pragma unroll
     for (int i = 0; i < VPL; ++i) row[expert_of<C>(i, l)] = 0.0f;
-    __builtin_amdgcn_wave_barrier();
+    wave_handover();
     if (e >= 0) row[e] = renorm ? p * (u - dot) : p * u;
-    __builtin_amdgcn_wave_barrier();
+    wave_handover();
 #pragma unroll
     for (int i = 0; i < VPL; i += C) {
         const int first = expert_of<C>(i, l);

@@ -168,3 +168,65 @@ def test_the_compiler_knows_what_the_loads_do_to_m0(poisoned, tmp_path):
     for x in writes:
         constraints = re.findall(r'"([^"]*)"', x[x.index(" asm "):])[1]
         assert "{m0}" in [c.lstrip("=&") for c in constraints.split(",") if c.startswith("=")], x.strip()[:300]
+
+
+# ---- values handed from lane to lane through LDS inside a wave ------------------
+
+def _device(src, out, *flags):
+    subprocess.run([poison.HIPCC, "--offload-arch=gfx950", "-O3", "-std=c++17", f"-I{poison.ROOT / 'include'}",
+                    f"-I{poison.CSRC}", "-Xclang", "-target-feature", "-Xclang", "-packed-fp32-ops", "--cuda-device-only",
+                    "-S", *flags, str(src), "-o", str(out)], check=True, capture_output=True)
+    return out.read_text()
+
+
+HANDED = """#include <hip/hip_runtime.h>
+#include "moe_device.h"
+__global__ void by_nothing(float *out, const int *to, const float *x) {
+    __shared__ float row[64];
+    row[threadIdx.x] = 0.0f;
+    out[threadIdx.x] = row[threadIdx.x];
+}
+__global__ void by_handover(float *out, const int *to, const float *x) {
+    __shared__ float row[64];
+    row[threadIdx.x] = 0.0f;
+    dbs::wave_handover();
+    out[threadIdx.x] = row[threadIdx.x];
+}
+"""
+
+
+def test_a_handover_reads_lds_again(tmp_path):
+    """What a lane stored may be another lane's by the time it is read: the
+    compiler may not answer the read with the lane's own value, as it does
+    where nothing stands between."""
+    if not Path(poison.HIPCC).exists():
+        pytest.skip("hipcc not available")
+    src = tmp_path / "handed.hip"
+    src.write_text(HANDED)
+    kernels = dict(_kernels(_device(src, tmp_path / "handed.s")))
+    reads = {name: "ds_read" in body for name, body in kernels.items()}
+    assert [v for k, v in sorted(reads.items()) if "by_nothing" in k] == [False]
+    assert [v for k, v in sorted(reads.items()) if "by_handover" in k] == [True]
+
+
+@pytest.mark.parametrize("unit,kernel,handovers", [
+    ("moe_route.hip", "route_bwd", 2),           # zeros, chosen experts' gradients
+    ("moe_gemm.hip", "moe_dw", 2),               # table of rows, order of groups
+    ("moe_gemm.hip", "moe_tilesI", 2),           # a block of results in and out of the wave's buffer
+])
+def test_lanes_hand_over_through_a_fence(unit, kernel, handovers, tmp_path):
+    if not Path(poison.HIPCC).exists():
+        pytest.skip("hipcc not available")
+    found = 0
+    for part in re.split(r"^(?=define )", _device(poison.CSRC / unit, tmp_path / "u.ll", "-emit-llvm"), flags=re.M):
+        if not part.startswith("define ") or "amdgpu_kernel" not in part[:200] or kernel not in part[:400]:
+            continue
+        found += 1
+        assert len(re.findall(r'fence syncscope\("wavefront"\) acquire', part)) >= handovers, part[:200]
+        assert len(re.findall(r'fence syncscope\("wavefront"\) release', part)) >= handovers, part[:200]
+    assert found
+
+
+def test_no_bare_wave_barrier():
+    for f in sorted(poison.CSRC.glob("moe_*.hip")):
+        assert "__builtin_amdgcn_wave_barrier" not in f.read_text(), f.name
