@@ -114,7 +114,7 @@ dbs_status check_route(dbs_real type, const void *logits, int64_t T, int64_t E, 
     if (E > dbs::kMoeMaxExperts) return fail(DBS_EINVAL, "more than 1024 experts");
     if (k > E) return fail(DBS_EINVAL, "k above the number of experts");
     if (k > dbs::kMoeMaxK) return fail(DBS_EUNSUPPORTED, "more than 16 experts per token");
-    if (T * k > kMaxRows) return fail(DBS_EINVAL, "T * k above 2^25");
+    if (T > kMaxRows / k) return fail(DBS_EINVAL, "T * k above 2^25");
     if (!aligned(logits, type == DBS_F32 ? 4 : 2)) return fail(DBS_EINVAL, "misaligned logits");
     return DBS_OK;
 }

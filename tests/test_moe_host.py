@@ -154,6 +154,15 @@ def test_binding_refuses_what_is_not_on_the_gpu():
         dbs.gemm_moe_dw_bf16(x, x, i, out_dtype=torch.float16)
 
 
+@pytest.mark.parametrize("T", [(1 << 60) + 16, 1 << 60, (1 << 63) - 1, (1 << 25) + 1])
+def test_routing_refuses_more_pairs_than_64_bits_count(T):
+    """T k passes 2^64 here: it must not come back as a small number."""
+    big = 1 << 62
+    _refused("moe_route", (0, P, T, 64, 16, 1, P, P, P, P, P, P, big), EINVAL)
+    _refused("moe_route_bwd", (0, P, T, 64, 16, 1, P, P, P), EINVAL)
+    assert dbs.lib().moe_route_workspace(T, 64, 16) == 0
+
+
 # ------------------------------------------------- the plain forms themselves
 
 def test_plain_routing_and_gradient():
