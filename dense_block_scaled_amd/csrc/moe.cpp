@@ -33,6 +33,7 @@ constexpr int64_t kMaxRows = int64_t(1) << 25;      // rows of the sorted order
 constexpr int64_t kMaxWidth = int64_t(1) << 21;     // N and K
 constexpr int64_t kGatherLimit = 0xFF000000;        // bytes of a gathered X
 constexpr int64_t kTwoGiB = int64_t(1) << 31;
+constexpr int64_t kMostTiles = int64_t(1) << 30;
 
 // What gemm_moe_bf16, gemm_moe_swiglu_bf16 and gemm_moe_dw_bf16 share.
 dbs_status check_product(const void *X, const void *other, const void *out, const int32_t *offsets,
@@ -56,11 +57,13 @@ dbs_status check_product(const void *X, const void *other, const void *out, cons
 
 dbs_status run_product(dbs::MoeGemm p, hipStream_t stream)
 {
+    // the kernels number their tiles (64 x 32 the smallest) in int, with a round of workgroups to spare
+    if (((int64_t)p.M / 64 + p.E) * (((int64_t)p.ncols + 31) / 32) >= kMostTiles)
+        return fail(DBS_EUNSUPPORTED, "too many output tiles");
     int cus = 0;
     const int st = dbs::device_compute_units(&cus);
     if (st != DBS_OK) return (dbs_status)st;
     p.vec = p.ncols % 8 == 0 && aligned(p.D, 16);
-    if ((p.M / 64 + p.E) * ((p.ncols + 31) / 32) >= kTwoGiB) return fail(DBS_EUNSUPPORTED, "too many output tiles");
     // Tiles of 64, 128 or 256 rows, by the time of the busiest CU in stages of a
     // 256-row tile (1.3 us), for groups of M / E rows on average (half a tile
     // of each is waste; few rows leave some experts without any).  A stage

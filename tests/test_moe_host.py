@@ -94,6 +94,17 @@ def test_product_refusals(args, want):
         _refused("gemm_moe_swiglu_bf16", args[:-1], want)
 
 
+@pytest.mark.parametrize("name,args", [
+    ("gemm_moe_bf16", (P, P, P, P, N0, 1 << 25, 1 << 25, 1, 1 << 18, 8, 0)),            # 2^19 x 2^13 tiles of 64 x 32
+    ("gemm_moe_bf16", (P, P, P, P, P, 8, 1 << 25, 1024, 1 << 21, 8, 1)),                # 2^19 x 2^16
+    ("gemm_moe_swiglu_bf16", (P, P, P, P, N0, 1 << 25, 1 << 25, 1, 1 << 17, 8)),        # 2^19 x 2^12
+])
+def test_products_refuse_more_tiles_than_32_bits_count(name, args):
+    """Refused for the count itself, before any device is asked for."""
+    _refused(name, args, EUNSUP)
+    assert "tiles" in dbs.lib().dbs_last_error().decode()
+
+
 def test_swiglu_product_width():
     _refused("gemm_moe_swiglu_bf16", (P, P, P, P, P, 4, 8, 2, (1 << 20) + 1, 16), EINVAL)
 
