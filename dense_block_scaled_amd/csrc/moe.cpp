@@ -202,7 +202,8 @@ dbs_status gemm_moe_dw_bf16(dbs_real type, const void *dY, const void *X, void *
     if (accumulate != 0 && accumulate != 1) return fail(DBS_EINVAL, "accumulate must be 0 or 1");
     if (accumulate && type != DBS_F32) return fail(DBS_EUNSUPPORTED, "accumulation needs an fp32 dW");
     if (!aligned(dW, 16)) return fail(DBS_EINVAL, "dW must be 16-byte aligned");
-    if (E * ((N + 255) / 256) * ((K + 255) / 256) >= kTwoGiB) return fail(DBS_EUNSUPPORTED, "too many output tiles");
+    // (the kernel numbers its tiles, 64 x 128 the smaller ones, in int: N K < 2^30 and widths up to 2^21
+    // make fewer than 2^17 + 2^15 + 2^14 + 2 of an expert, 2^28 over 1024 experts)
     int cus = 0;
     const int e = dbs::device_compute_units(&cus);
     if (e != DBS_OK) return (dbs_status)e;

@@ -367,8 +367,8 @@ dbs_status quant_bf16(const float *x, int64_t n, void *out, hipStream_t stream);
  *
  * Limits: N and K at most 2^21 (F 2^20), an expert's matrix below 2 GiB and a
  * gathered X below 4 GiB - 16 MiB, and (M / 64 + E) (columns of D / 32) below
- * 2^30 (DBS_EUNSUPPORTED).  D, dW, dY and the
- * other outputs must not alias inputs.
+ * 2^30 (DBS_EUNSUPPORTED).  D, dW, dY and the other outputs must not alias
+ * inputs.
  */
 typedef enum {
     DBS_F32 = 0,
