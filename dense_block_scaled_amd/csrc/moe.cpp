@@ -146,6 +146,8 @@ dbs_status moe_route(dbs_real type, const void *logits, int64_t T, int64_t E, in
     dbs_status st = check_route(type, logits, T, E, k);
     if (st != DBS_OK) return st;
     if (!experts || !weights || !offsets || !rows || !slots) return fail(DBS_EINVAL, "null pointer argument");
+    if (!aligned(experts, 4) || !aligned(weights, 4) || !aligned(offsets, 4) || !aligned(rows, 4) || !aligned(slots, 4))
+        return fail(DBS_EINVAL, "misaligned output");
     if (renormalize != 0 && renormalize != 1) return fail(DBS_EINVAL, "renormalize must be 0 or 1");
     const int64_t need = dbs::moe_route_workspace_bytes(T, E);
     if (need > 0 && (!workspace || !aligned(workspace, 4) || workspace_bytes < (size_t)need))
@@ -161,6 +163,8 @@ dbs_status moe_route_bwd(dbs_real type, const void *logits, int64_t T, int64_t E
     dbs_status st = check_route(type, logits, T, E, k);
     if (st != DBS_OK) return st;
     if (!experts || !dweights || !dlogits) return fail(DBS_EINVAL, "null pointer argument");
+    if (!aligned(experts, 4) || !aligned(dweights, 4) || !aligned(dlogits, type == DBS_F32 ? 4 : 2))
+        return fail(DBS_EINVAL, "misaligned array");
     if (renormalize != 0 && renormalize != 1) return fail(DBS_EINVAL, "renormalize must be 0 or 1");
     return done(dbs::launch_moe_route_bwd(logits, type == DBS_BF16, T, (int)E, (int)k, renormalize, experts, dweights,
                                           dlogits, stream));

@@ -174,6 +174,20 @@ def test_routing_refuses_more_pairs_than_64_bits_count(T):
     assert dbs.lib().moe_route_workspace(T, 64, 16) == 0
 
 
+@pytest.mark.parametrize("place,bad", [(6, P2), (7, P2), (8, P1), (9, P2), (10, P2)])
+def test_route_refuses_misaligned_outputs(place, bad):
+    args = [1, P, 4, 8, 2, 1, P, P, P, P, P, N0, 0]
+    args[place] = bad
+    _refused("moe_route", tuple(args), EINVAL)
+
+
+@pytest.mark.parametrize("kind,place,bad", [(0, 6, P2), (0, 7, P2), (0, 8, P2), (1, 8, P1)])
+def test_route_bwd_refuses_misaligned_arrays(kind, place, bad):
+    args = [kind, P, 4, 8, 2, 1, P, P, P]
+    args[place] = bad
+    _refused("moe_route_bwd", tuple(args), EINVAL)
+
+
 # ------------------------------------------------- the plain forms themselves
 
 def test_plain_routing_and_gradient():
