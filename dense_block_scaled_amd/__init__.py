@@ -555,7 +555,7 @@ def moe_route(logits: torch.Tensor, k: int, renormalize: bool = True) -> MoeRout
     T, E = _dims(logits, "logits", 2)
     dev = logits.device
     pl = _arg(logits, "logits", _REAL, (T, E), dev)
-    kk = max(int(k), 0)
+    kk = min(max(int(k), 0), E)               # (the library refuses other k; nothing is sized by them)
     need = int(lib().moe_route_workspace(T, E, kk))
     experts = torch.empty((T, kk), dtype=torch.int32, device=dev)
     weights = torch.empty_like(experts, dtype=torch.float32)

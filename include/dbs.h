@@ -326,10 +326,10 @@ dbs_status quant_bf16(const float *x, int64_t n, void *out, hipStream_t stream);
  *
  * all int32 in DEVICE memory: nothing is copied to the host between the calls
  * of a layer, so they can be captured in a HIP graph.  Arrays are dense, rows
- * contiguous; int32 and fp32 arrays are 4-byte aligned, logits and their
- * gradients as their type is, other bf16 arrays to 16 bytes unless stated.  Sums, softmax
- * and gate are fp32 and rounded once.  Every result is the same from run to
- * run (no floating-point atomics).  T k at most 2^25.
+ * contiguous; int32 arrays, weights and their gradients are aligned to 4 bytes,
+ * logits and their gradients as their type is, the others to 16 unless stated.
+ * Sums, softmax and gate are fp32 and rounded once.  Every result is the same
+ * from run to run (no floating-point atomics).  T k at most 2^25.
  *
  * moe_route: experts and weights of every token from its logits (T x E of
  *   `type`): the k largest, ties to the lower expert; weights = softmax over

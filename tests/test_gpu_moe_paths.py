@@ -220,6 +220,16 @@ def test_offsets_that_are_no_offsets_stay_inside():
                                               torch.tensor([3, 3, 3, 8, 8, 8], dtype=torch.int32).cuda()))
 
 
+@pytest.mark.parametrize("k", [1 << 40, 9, 0, -1, -(1 << 40)])
+def test_route_refuses_k_without_sizing_outputs_by_it(k):
+    x = torch.zeros(4, 8, device="cuda")
+    before = torch.cuda.memory_allocated()
+    torch.cuda.reset_peak_memory_stats()
+    with pytest.raises(dbs.DbsError):
+        dbs.moe_route(x, k)
+    assert torch.cuda.max_memory_allocated() - before <= 1 << 16
+
+
 def test_example_layer():
     """The layer's results against its plain form in 32 bits: intermediate
     rounding to bf16 (2^-8 each, five in a row at most in a gradient) keeps them
