@@ -27,6 +27,7 @@ from __future__ import annotations
 
 import contextlib
 import ctypes
+import operator
 from pathlib import Path
 from typing import NamedTuple
 
@@ -552,10 +553,11 @@ def moe_route(logits: torch.Tensor, k: int, renormalize: bool = True) -> MoeRout
     with renormalize=False) and the stable order of the pairs by expert.
     Logits of -inf or NaN close an expert to the token; ties go to the lower
     expert."""
+    k = operator.index(k)
     T, E = _dims(logits, "logits", 2)
     dev = logits.device
     pl = _arg(logits, "logits", _REAL, (T, E), dev)
-    kk = min(max(int(k), 0), E)               # (the library refuses other k; nothing is sized by them)
+    kk = min(max(k, 0), E)                    # (the library refuses other k; nothing is sized by them)
     need = int(lib().moe_route_workspace(T, E, kk))
     experts = torch.empty((T, kk), dtype=torch.int32, device=dev)
     weights = torch.empty_like(experts, dtype=torch.float32)
@@ -563,7 +565,7 @@ def moe_route(logits: torch.Tensor, k: int, renormalize: bool = True) -> MoeRout
     rows = torch.empty(T * kk, dtype=torch.int32, device=dev)
     slots = torch.empty_like(experts)
     ws = torch.empty(need, dtype=torch.uint8, device=dev) if need else None
-    _call("moe_route", dev, _REAL[logits.dtype], pl, T, E, int(k), int(bool(renormalize)), experts.data_ptr(),
+    _call("moe_route", dev, _REAL[logits.dtype], pl, T, E, k, int(bool(renormalize)), experts.data_ptr(),
           weights.data_ptr(), offsets.data_ptr(), rows.data_ptr(), slots.data_ptr(),
           None if ws is None else ws.data_ptr(), need)
     return MoeRouting(experts, weights, offsets, rows, slots)

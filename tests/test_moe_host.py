@@ -188,6 +188,13 @@ def test_route_bwd_refuses_misaligned_arrays(kind, place, bad):
     _refused("moe_route_bwd", tuple(args), EINVAL)
 
 
+@pytest.mark.parametrize("k", [2.5, "2", None])
+def test_route_takes_whole_numbers_of_experts(k):
+    """Not cut to a whole number without a word."""
+    with pytest.raises(TypeError):
+        dbs.moe_route(torch.zeros(4, 8), k)
+
+
 # ------------------------------------------------- the plain forms themselves
 
 def test_plain_routing_and_gradient():
