@@ -21,7 +21,8 @@ import dense_block_scaled_amd as dbs  # noqa: E402
 
 
 class MoeFunction(torch.autograd.Function):
-    """out = layer(x, logits, w13, w2); gradients of all four."""
+    """out = layer(x, logits, w13, w2); gradients of all four (first ones: the
+    operators have no second derivatives)."""
 
     @staticmethod
     def forward(ctx, x, logits, w13, w2, k):
@@ -34,6 +35,8 @@ class MoeFunction(torch.autograd.Function):
 
     @staticmethod
     def backward(ctx, dout):
+        if torch.is_grad_enabled():                # (create_graph=True)
+            raise RuntimeError("MoeFunction has no second derivatives: its gradients would be taken for constants")
         x, logits, w13, w2, h, a, y, *r = ctx.saved_tensors
         r = dbs.MoeRouting(*r)
         dy, dweights = dbs.moe_combine_backward(dout.contiguous(), y, r.slots, r.weights, r.offsets)

@@ -244,3 +244,24 @@ def test_example_layer():
     far = m.run(512, 256, 128, 16, 4)
     _say(far)
     assert all(v <= 5 * 2.0 ** -8 for v in far.values())
+
+
+def _example():
+    import importlib.util
+    from pathlib import Path
+
+    path = Path(__file__).resolve().parent.parent / "examples" / "moe_layer.py"
+    spec = importlib.util.spec_from_file_location("moe_layer", path)
+    m = importlib.util.module_from_spec(spec)
+    spec.loader.exec_module(m)
+    return m
+
+
+@pytest.mark.parametrize("loss", [lambda out: out.float().sum(), lambda out: out.float().square().sum()])
+def test_example_layer_has_no_second_derivative(loss):
+    """A gradient's gradient is an error, not the gradient of a constant."""
+    layer = _example().MoeLayer(64, 32, 4, 2)
+    x = torch.randn(8, 64, device="cuda", dtype=torch.bfloat16, requires_grad=True)
+    with pytest.raises(RuntimeError, match="second derivatives"):
+        torch.autograd.grad(loss(layer(x)), x, create_graph=True)
+    torch.autograd.grad(loss(layer(x)), x)
