@@ -21,8 +21,8 @@ import dense_block_scaled_amd as dbs  # noqa: E402
 
 
 class MoeFunction(torch.autograd.Function):
-    """out = layer(x, logits, w13, w2); gradients of all four (first ones: the
-    operators have no second derivatives)."""
+    """out = layer(x, logits, w13, w2); gradients of those of the four that need
+    one (first ones: the operators have no second derivatives)."""
 
     @staticmethod
     def forward(ctx, x, logits, w13, w2, k):
@@ -38,15 +38,22 @@ class MoeFunction(torch.autograd.Function):
         if torch.is_grad_enabled():                # (create_graph=True)
             raise RuntimeError("MoeFunction has no second derivatives: its gradients would be taken for constants")
         x, logits, w13, w2, h, a, y, *r = ctx.saved_tensors
+        need_x, need_logits, need_w13, need_w2, _ = ctx.needs_input_grad
         r = dbs.MoeRouting(*r)
+        dx = dlogits = dw13 = dw2 = None
         dy, dweights = dbs.moe_combine_backward(dout.contiguous(), y, r.slots, r.weights, r.offsets)
-        dw2 = dbs.gemm_moe_dw_bf16(dy, a, r.offsets)
-        da = dbs.gemm_moe_bf16(dy, w2, r.offsets, lw=dbs.MN_MAJOR)        # w2 (E, H, F) as K x N
-        dh = dbs.swiglu_backward(da, h)
-        dw13 = dbs.gemm_moe_dw_bf16(dh, x, r.offsets, r.rows)
-        dxs = dbs.gemm_moe_bf16(dh, w13, r.offsets, lw=dbs.MN_MAJOR)
-        dx = dbs.moe_combine(dxs, r.slots)                                # a token's rows, summed
-        dlogits = dbs.moe_route_backward(logits, r.experts, dweights)
+        if need_w2:
+            dw2 = dbs.gemm_moe_dw_bf16(dy, a, r.offsets)
+        if need_x or need_w13:
+            da = dbs.gemm_moe_bf16(dy, w2, r.offsets, lw=dbs.MN_MAJOR)    # w2 (E, H, F) as K x N
+            dh = dbs.swiglu_backward(da, h)
+        if need_w13:
+            dw13 = dbs.gemm_moe_dw_bf16(dh, x, r.offsets, r.rows)
+        if need_x:
+            dxs = dbs.gemm_moe_bf16(dh, w13, r.offsets, lw=dbs.MN_MAJOR)
+            dx = dbs.moe_combine(dxs, r.slots)                            # a token's rows, summed
+        if need_logits:
+            dlogits = dbs.moe_route_backward(logits, r.experts, dweights)
         return dx, dlogits, dw13, dw2, None
 
 

@@ -265,3 +265,27 @@ def test_example_layer_has_no_second_derivative(loss):
     with pytest.raises(RuntimeError, match="second derivatives"):
         torch.autograd.grad(loss(layer(x)), x, create_graph=True)
     torch.autograd.grad(loss(layer(x)), x)
+
+
+@pytest.mark.parametrize("need", ["x", "router", "w13", "w2"])
+def test_example_layer_computes_the_gradients_that_are_needed(need, monkeypatch):
+    """One at a time: the same bits as with all of them, and no matrices'
+    gradients where the matrices are frozen."""
+    m = _example()
+    torch.manual_seed(1)
+    layer = m.MoeLayer(128, 64, 8, 2)
+    x = torch.randn(40, 128, device="cuda", dtype=torch.bfloat16)
+    leaves = {"x": x.requires_grad_(), "router": layer.router, "w13": layer.w13, "w2": layer.w2}
+    dout = torch.randn_like(x)
+    layer(x).backward(dout)
+    want = {n: t.grad.clone() for n, t in leaves.items()}
+    calls = []
+    dw = m.dbs.gemm_moe_dw_bf16
+    monkeypatch.setattr(m.dbs, "gemm_moe_dw_bf16", lambda *a, **k: calls.append(1) or dw(*a, **k))
+    for n, t in leaves.items():
+        t.grad = None
+        t.requires_grad_(n == need)
+    layer(x).backward(dout)
+    assert torch.equal(leaves[need].grad, want[need])
+    assert all(t.grad is None for n, t in leaves.items() if n != need)
+    assert len(calls) == (need in ("w13", "w2"))
