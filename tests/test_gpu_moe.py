@@ -58,6 +58,27 @@ def test_route(T, E, k, dtype, renorm, closed):
     assert np.all(np.abs(_moe.f64(r.weights) - weights) <= (E + 28) * 2.0 ** -23 * weights + 1e-30)
 
 
+# both sides of the switch to three kernels (2048 tokens), experts over several
+# workgroups of the column sums (16 each) and a rest, one to nine rows of counts a segment
+MANY = [(2048, 33, 4), (2049, 33, 4), (2049, 16, 2), (4500, 160, 6), (4097, 17, 16), (2113, 600, 8), (2500, 1024, 3),
+        (9000, 48, 8), (33000, 21, 2)]
+
+
+@pytest.mark.parametrize("T,E,k", MANY)
+@pytest.mark.parametrize("dtype,renorm,closed", [(torch.float32, True, 0.0), (torch.bfloat16, False, 0.6)])
+def test_route_of_many_tokens(T, E, k, dtype, renorm, closed):
+    x = _logits(T, E, dtype, T + 7 * E, closed)
+    _say("route", T, E, k, dtype, renorm, closed)
+    r = dbs.moe_route(x.cuda(), k, renormalize=renorm)
+    experts, weights = _moe.route(_moe.f64(x), k, renorm)
+    offsets, rows, slots = _moe.routing(experts, E)
+    assert np.array_equal(r.experts.cpu().numpy(), experts)
+    assert np.array_equal(r.offsets.cpu().numpy(), offsets)
+    assert np.array_equal(r.rows.cpu().numpy(), rows)
+    assert np.array_equal(r.slots.cpu().numpy(), slots)
+    assert np.all(np.abs(_moe.f64(r.weights) - weights) <= (E + 28) * 2.0 ** -23 * weights + 1e-30)
+
+
 def test_route_special_logits():
     inf, nan, low = float("inf"), float("nan"), torch.finfo(torch.float32).min
     x = torch.tensor([[1.0, inf, inf, 0.0, -1.0],       # two infinities share
