@@ -562,11 +562,6 @@ __device__ __forceinline__ void zero_rows(const MoeGemm &p, int64_t from, int64_
         for (int64_t o = me * 2; o < bytes; o += all * 2) *reinterpret_cast<uint16_t *>(z + o) = 0;
 }
 
-__device__ __forceinline__ float gated(float g, float u)
-{
-    return g * __builtin_amdgcn_rcpf(1.0f + __expf(-g)) * u;
-}
-
 // 256-row tiles, or of 128 rows (TM) where a call has too few of the large ones
 // for the CUs: the same stages with half of A's parts left out, 1.1 us in place
 // of 1.3.  BMN: W MN-major; GATE: see the head of the file.

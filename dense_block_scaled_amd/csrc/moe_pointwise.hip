@@ -22,6 +22,7 @@
 #include <type_traits>
 
 #include "moe.h"
+#include "moe_device.h"
 
 namespace dbs {
 namespace {
@@ -91,9 +92,6 @@ __device__ __forceinline__ void store(uint16_t *x, int64_t i, const Piece<V> &p)
     }
 }
 
-// 1 / (1 + e^-g); 0 where e^-g overflows
-__device__ __forceinline__ float sigmoid(float g) { return __builtin_amdgcn_rcpf(1.0f + __expf(-g)); }
-
 // One piece of V outputs a thread: piece c of row m.
 template <int V>
 __global__ __launch_bounds__(kThreads) void swiglu_kernel(const uint16_t *H, uint16_t *A, int64_t pieces, int64_t F)
@@ -104,7 +102,7 @@ __global__ __launch_bounds__(kThreads) void swiglu_kernel(const uint16_t *H, uin
         unpack<V>(load<V>(H, m * 2 * F + c), g);
         unpack<V>(load<V>(H, m * 2 * F + F + c), u);
 #pragma unroll
-        for (int q = 0; q < V; ++q) a[q] = g[q] * sigmoid(g[q]) * u[q];
+        for (int q = 0; q < V; ++q) a[q] = gated(g[q], u[q]);
         store<V>(A, m * F + c, pack<V>(a));
     }
 }
@@ -121,9 +119,10 @@ __global__ __launch_bounds__(kThreads) void swiglu_bwd_kernel(const uint16_t *dA
         unpack<V>(load<V>(dA, m * F + c), d);
 #pragma unroll
         for (int q = 0; q < V; ++q) {
-            const float s = sigmoid(g[q]);
-            dg[q] = d[q] * u[q] * s * (1.0f + g[q] * (1.0f - s));
-            du[q] = d[q] * g[q] * s;
+            const Sigmoid s = sigmoid(g[q]);
+            const float ds = d[q] * s.p * s.r;
+            dg[q] = ds * (u[q] * s.p) * (1.0f + g[q] * s.rest);
+            du[q] = ds * (g[q] * s.p);
         }
         store<V>(dH, m * 2 * F + c, pack<V>(dg));
         store<V>(dH, m * 2 * F + F + c, pack<V>(du));

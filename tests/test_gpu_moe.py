@@ -460,6 +460,46 @@ def test_swiglu(M, F):
     assert np.all(np.abs(got[:, F:] - du) <= (rel + _moe.HALF_STEP * (1 + rel)) * np.abs(du) + _moe.TINY)
 
 
+def _far_below():
+    """Gates where e^-g leaves fp32's normal range or fp32, and what they meet:
+    silu(g) u is a normal number for some of them."""
+    g = torch.arange(-120, -70, 0.5)
+    u = torch.tensor([1.0, -3.0, 2.0 ** 40, -2.0 ** 100])
+    return g.repeat(4).to(torch.bfloat16), u.repeat_interleave(len(g)).to(torch.bfloat16)
+
+
+def test_swiglu_far_below_zero():
+    g, u = _far_below()
+    a, b = _moe.f64(g), _moe.f64(u)
+    H = torch.cat([g, u]).view(1, -1)
+    got = _moe.f64(dbs.swiglu(H.cuda()))[0]
+    assert np.all(np.abs(got - _moe.silu(a) * b) <= _moe.gate_bound(a, b, 0.0, 0.0))
+    d = torch.tensor([0.75, -2.0]).repeat(len(g) // 2).to(torch.bfloat16)
+    got = _moe.f64(dbs.swiglu_backward(d.view(1, -1).cuda(), H.cuda()))[0]
+    dd, s = _moe.f64(d), 1 / (1 + np.exp(-a))
+    da, du = dd * b * s * (1 + a * (1 - s)), dd * a * s
+    # (bounds of test_swiglu)
+    rel = (16 + np.abs(a)) * 2.0 ** -22
+    slack = rel * np.abs(dd * b * s) * (1 + np.abs(a) * (1 - s) * (1 + np.abs(a)))
+    assert np.all(np.abs(got[:len(a)] - da) <= slack + _moe.HALF_STEP * (np.abs(da) + slack) + _moe.TINY)
+    assert np.all(np.abs(got[len(a):] - du) <= (rel + _moe.HALF_STEP * (1 + rel)) * np.abs(du) + _moe.TINY)
+
+
+@pytest.mark.parametrize("M", [1, 200, 60000])
+def test_product_gated_far_below_zero(M):
+    """The same out of the product's registers: one term per sum."""
+    g, u = _far_below()
+    a, b = _moe.f64(g), _moe.f64(u)
+    F = len(g)
+    X, W = torch.zeros(M, 8, dtype=torch.bfloat16), torch.zeros(1, 2 * F, 8, dtype=torch.bfloat16)
+    X[:, 3] = 1.0
+    W[0, :, 3] = torch.cat([g, u])
+    got = dbs.gemm_moe_swiglu_bf16(X.cuda(), W.cuda(), torch.tensor([0, M], dtype=torch.int32).cuda())
+    first = _moe.f64(got[0])
+    assert np.all(np.abs(first - _moe.silu(a) * b) <= _moe.gate_bound(a, b, 0.0, 0.0))
+    assert bool((got == got[0]).all())
+
+
 def test_swiglu_gradient_against_differences():
     g = _gen(51)
     M, F, h = 3, 8, 0.5
