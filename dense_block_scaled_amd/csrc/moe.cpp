@@ -11,6 +11,62 @@
 #include "dbs.h"
 #include "launch.h"
 
+namespace dbs {
+
+// Tiles of 64, 128 or 256 rows, by the time of the busiest CU in stages of a
+// 256-row tile (1.3 us), for groups of M / E rows on average (half a tile
+// of each is waste; few rows leave some experts without any).  A stage
+// takes 0.22 of that (64 rows, K-major), 0.39 (MN-major, twice as wide), 0.85
+// (128 rows), and reads W at the memory's rate, one of 256 rows of it per
+// CU; large tiles come in whole rounds over the CUs, small ones even out.
+// us with 64 / 128 / 256 rows: 8 experts of 4096 x 4096, 512 rows in all
+// 56 / 66 / 69, 8192 rows 531 / 313 / 250; 8 of 1408 x 2048, 4096 rows 54 / 39 /
+// 50; one of 2048 x 4096, 2048 rows 70 / 68 / 84; 128 of 1536 x 4096 behind the
+// gate, 192 rows on 49 experts 123 / 152 / 156, 1536 rows on all 291 / 268 / 271;
+// MN-major 18 of 776 x 2840, 4096 rows 43 / 55 / 68, 8192 rows 78 / 97 / 71.
+int moe_tile_rows(int64_t M, int64_t E, int64_t N, int64_t ncols, bool wmn, bool gate, int cus)
+{
+    const int64_t likely = (2 * M * E + 2 * M + E - 1) / (2 * M + E), met = std::min(M, likely);
+    auto per_cu = [&](int64_t tm, int64_t tn) {
+        const int64_t rows = std::max(M / tm + met / 2, met);
+        return double(rows * ((ncols + tn - 1) / tn)) / cus;
+    };
+    const double w = double(met) * N / 256 / cus;
+    auto rounds = [&](int64_t tm, double stage) {
+        const double n = per_cu(tm, gate ? 128 : 256), full = std::floor(n);
+        return full * std::max(stage, w / n) + (n > full ? stage : 0.0);
+    };
+    const double t64 = std::max((wmn ? 0.39 : 0.22) * per_cu(64, wmn ? 128 : gate ? 32 : 64), 1.1 * w);
+    const double t128 = rounds(128, 0.85), t256 = rounds(256, 1.0);
+    return t64 <= t128 && t64 <= t256 ? 64 : t128 < t256 ? 128 : 256;
+}
+
+int moe_dw_grid(int64_t E, int64_t N, int64_t K, int cus)
+{
+    const int64_t tiles = E * ((N + 63) / 64) * ((K + 127) / 128);      // small ones: the more
+    return (int)std::min<int64_t>(tiles, cus);
+}
+
+}  // namespace dbs
+
+extern "C" int dbs_moe_tile_rows(int64_t M, int64_t E, int64_t N, int wmn, int gate, int cus)
+{
+    return dbs::moe_tile_rows(M, E, N, gate ? N / 2 : N, wmn, gate, cus);
+}
+
+extern "C" int dbs_moe_dw_small(const int32_t *stages, int E, int N, int K, int f32, int accumulate, int cus)
+{
+    int groups = 0, longest = 0, two = 0, four = 0;
+    for (int e = 0; e < E; ++e) {
+        if (accumulate && stages[e] == 0) continue;
+        ++groups;
+        longest = std::max(longest, stages[e]);
+        two += std::max(stages[e], 2);
+        four += std::max(stages[e], 4);
+    }
+    return dbs::moe_dw_small(groups, longest, two, four, N, K, f32, dbs::moe_dw_grid(E, N, K, cus));
+}
+
 namespace {
 
 dbs_status fail(dbs_status st, const char *msg)
@@ -64,30 +120,7 @@ dbs_status run_product(dbs::MoeGemm p, hipStream_t stream)
     const int st = dbs::device_compute_units(&cus);
     if (st != DBS_OK) return (dbs_status)st;
     p.vec = p.ncols % 8 == 0 && aligned(p.D, 16);
-    // Tiles of 64, 128 or 256 rows, by the time of the busiest CU in stages of a
-    // 256-row tile (1.3 us), for groups of M / E rows on average (half a tile
-    // of each is waste; few rows leave some experts without any).  A stage
-    // takes 0.22 of that (64 rows, K-major), 0.39 (MN-major, twice as wide), 0.85
-    // (128 rows), and reads W at the memory's rate, one of 256 rows of it per
-    // CU; large tiles come in whole rounds over the CUs, small ones even out.
-    // us with 64 / 128 / 256 rows: 8 experts of 4096 x 4096, 512 rows in all
-    // 56 / 66 / 69, 8192 rows 531 / 313 / 250; 8 of 1408 x 2048, 4096 rows 54 / 39 /
-    // 50; one of 2048 x 4096, 2048 rows 70 / 68 / 84; 128 of 1536 x 4096 behind the
-    // gate, 192 rows on 49 experts 123 / 152 / 156, 1536 rows on all 291 / 268 / 271;
-    // MN-major 18 of 776 x 2840, 4096 rows 43 / 55 / 68, 8192 rows 78 / 97 / 71.
-    const int64_t M = p.M, E = p.E, likely = (2 * M * E + 2 * M + E - 1) / (2 * M + E), met = std::min(M, likely);
-    auto per_cu = [&](int64_t tm, int64_t tn) {
-        const int64_t rows = std::max(M / tm + met / 2, met);
-        return double(rows * ((p.ncols + tn - 1) / tn)) / cus;
-    };
-    const double w = double(met) * p.N / 256 / cus;
-    auto rounds = [&](int64_t tm, double stage) {
-        const double n = per_cu(tm, p.gate ? 128 : 256), full = std::floor(n);
-        return full * std::max(stage, w / n) + (n > full ? stage : 0.0);
-    };
-    const double t64 = std::max((p.wmn ? 0.39 : 0.22) * per_cu(64, p.wmn ? 128 : p.gate ? 32 : 64), 1.1 * w);
-    const double t128 = rounds(128, 0.85), t256 = rounds(256, 1.0);
-    const int height = t64 <= t128 && t64 <= t256 ? 64 : t128 < t256 ? 128 : 256;
+    const int height = dbs::moe_tile_rows(p.M, p.E, p.N, p.ncols, p.wmn, p.gate, cus);
     return done(dbs::launch_moe_tiles(p, height, cus, stream));
 }
 

@@ -3,7 +3,8 @@
 // moe_pointwise.hip).  Not installed; callers use include/dbs.h.
 #pragma once
 
-#include <hip/hip_runtime_api.h>
+#include <hip/hip_runtime.h>
+#include <math.h>
 #include <stdint.h>
 
 namespace dbs {
@@ -40,9 +41,29 @@ struct MoeGemmDw {
     int accumulate;           // 1: add to dW (fp32 only)
 };
 
+// Rows of an output tile (64, 128 or 256) for M rows over E experts on `cus`
+// compute units, by the time of the busiest one (the rule and what it rests
+// on: moe.cpp).
+int moe_tile_rows(int64_t M, int64_t E, int64_t N, int64_t ncols, bool wmn, bool gate, int cus);
+
+// Whether dW of `groups` experts is computed in 64 x 128 tiles (else 256 x 256)
+// by `wgs` workgroups: the longest group's stages (64 rows), and the sums of
+// all groups' with at least two and four to a group (what it rests on: at
+// moe_dw in moe_gemm.hip).
+__host__ __device__ inline bool moe_dw_small(int groups, int longest, int two, int four, int N, int K, bool f32, int wgs)
+{
+    const float many = (float)(((N + 255) / 256) * ((K + 255) / 256)) / (float)wgs;    // tiles of a group a workgroup
+    const float few = (float)(((N + 63) / 64) * ((K + 127) / 128)) / (float)wgs;
+    const float large = (f32 ? 90.0f : 50.0f) * ceilf(many * groups) + fmaxf(13.0f * longest, 16.0f * many * two);
+    const float little = 10.0f * ceilf(few * groups) + fmaxf(3.5f * longest, 5.0f * few * four);
+    return little < large;
+}
+
 // rows: 64, 128 or 256 per output tile
 hipError_t launch_moe_tiles(const MoeGemm &p, int rows, int cus, hipStream_t stream);
 hipError_t launch_moe_dw(const MoeGemmDw &p, int cus, hipStream_t stream);
+// workgroups of moe_dw
+int moe_dw_grid(int64_t E, int64_t N, int64_t K, int cus);
 
 struct MoeRoute {
     const void *logits;       // T x E, fp32 or bf16
@@ -74,3 +95,8 @@ hipError_t launch_moe_combine_bwd(const void *dO, const void *Y, const int32_t *
 int device_compute_units(int *cus);
 
 }  // namespace dbs
+
+// For the tests that say which kernel a size reaches (not in include/dbs.h):
+// the rules above; stages: each expert's number of 64-row stages.
+extern "C" int dbs_moe_tile_rows(int64_t M, int64_t E, int64_t N, int wmn, int gate, int cus);
+extern "C" int dbs_moe_dw_small(const int32_t *stages, int E, int N, int K, int f32, int accumulate, int cus);

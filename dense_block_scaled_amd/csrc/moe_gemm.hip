@@ -1276,7 +1276,7 @@ __device__ __forceinline__ void dw_small(const MoeGemmDw &p, const Lane &c, uint
     asm volatile("s_waitcnt vmcnt(0)" ::: "memory");   // nothing is left to land in LDS
 }
 
-// Which of the two: the stages and tiles of the busiest workgroup, in tenths
+// Which of the two (moe_dw_small in moe.h): the stages and tiles of the busiest workgroup, in tenths
 // of a microsecond as measured -- 1.6 us a stage of a large tile with all CUs
 // at work, 1.3 along one long group, 5 to store it (9 in fp32) against 0.5,
 // 0.35 and 1.  The groups decide: 19 experts of 848 x 632, 1024 rows each on
@@ -1313,14 +1313,9 @@ __global__ __launch_bounds__(512, 1) void moe_dw(MoeGemmDw p)
             two += __shfl_xor(two, d);
             four += __shfl_xor(four, d);
         }
-        const float wgs = (float)gridDim.x;
-        const float many = (float)(((p.N + 255) / 256) * ((p.K + 255) / 256)) / wgs;    // tiles of a group a workgroup
-        const float few = (float)(((p.N + 63) / 64) * ((p.K + 127) / 128)) / wgs;
-        const float large = (F32 ? 90.0f : 50.0f) * ceilf(many * n) + fmaxf(13.0f * longest, 16.0f * many * two);
-        const float little = 10.0f * ceilf(few * n) + fmaxf(3.5f * longest, 5.0f * few * four);
         if (c.lane == 0) {
             count = n;
-            small = little < large;
+            small = moe_dw_small(n, longest, two, four, p.N, p.K, F32, (int)gridDim.x);
         }
     }
     __syncthreads();
@@ -1362,8 +1357,7 @@ hipError_t launch_moe_tiles(const MoeGemm &p, int rows, int cus, hipStream_t str
 
 hipError_t launch_moe_dw(const MoeGemmDw &p, int cus, hipStream_t stream)
 {
-    const int64_t tiles = (int64_t)p.E * ((p.N + 63) / 64) * ((p.K + 127) / 128);      // small ones: the more
-    const dim3 grid((uint32_t)(tiles < cus ? tiles : cus)), block(512);
+    const dim3 grid((uint32_t)moe_dw_grid(p.E, p.N, p.K, cus)), block(512);
     auto go = [&](auto gather, auto f32) {
         hipLaunchKernelGGL((moe_dw<decltype(gather)::value, decltype(f32)::value>), grid, block, 0, stream, p);
         return hipGetLastError();

@@ -12,6 +12,7 @@ import torch
 
 import dense_block_scaled_amd as dbs
 from tests import _moe
+from tests import test_gpu_moe as shapes
 
 P = ctypes.c_void_p(1 << 20)          # 16-byte aligned, never dereferenced
 P2 = ctypes.c_void_p((1 << 20) + 2)   # 2-byte aligned
@@ -218,6 +219,34 @@ def test_plain_routing_and_gradient():
     off, rows, slots = _moe.routing(np.array([[1, 0], [-1, 1], [0, 2]]), 3)
     assert list(off) == [0, 2, 4, 5] and list(rows) == [0, 2, 0, 1, 2, -1]
     assert slots.tolist() == [[2, 0], [-1, 3], [1, 4]]
+
+
+# ------------------------------------- which kernel a size goes to: the library's rules
+
+def _tile_rows(T, M, E, N, mn, gate):
+    return dbs.lib().dbs_moe_tile_rows(*map(ctypes.c_int64, (M or T, E, N)), int(mn), int(gate), 256)
+
+
+def test_the_gpu_tests_shapes_reach_every_tile_height():
+    """The library's own rule on 256 CUs: LARGE is for 256-row tiles, MID for
+    128-row ones, and every form reaches each height three times."""
+    g = shapes
+    for which, want in ((g.LARGE, 256), (g.MID, 128)):
+        for T, M, E, N, K, groups in which:
+            assert _tile_rows(T, M, E, N, False, False) == want, (T, M, E, N, K, groups)
+    for mn, gate in ((False, False), (False, True), (True, False)):
+        reached = [_tile_rows(T, M, E, 2 * N if gate else N, mn, gate)
+                   for T, M, E, N, K, _ in g.SHAPES + g.MID + g.LARGE + (g.HALF if gate else []) if not mn or N % 8 == 0]
+        assert all(reached.count(h) >= 3 for h in (64, 128, 256)), (mn, gate, reached)
+
+
+def test_the_gpu_tests_shapes_reach_both_tiles_of_dw():
+    g = shapes
+    for which, want in ((g.NARROW, 1), (g.WIDE, 0)):
+        for T, M, E, N, K, groups in which:
+            off = g._groups(groups, E, M or T, N + K + 3)
+            stages = (ctypes.c_int32 * E)(*[-(-int(n) // 64) for n in np.diff(off)])
+            assert dbs.lib().dbs_moe_dw_small(stages, E, N, K, 0, 0, 256) == want, (T, M, E, N, K, groups)
 
 
 # ----------------------------------------- order of the products' output tiles
