@@ -29,6 +29,7 @@
 #include "gemm_kernel.h"
 #include "moe.h"
 #include "moe_device.h"
+#include "moe_tiles.h"
 
 namespace dbs {
 namespace {
@@ -287,15 +288,8 @@ constexpr int kCoreLds = kStage + 8 * 2048;
 // groups 0 and 2 (or 1 and 3) together, which then read neighbouring chunks
 // of their rows, apart under the swizzle (chunks two apart were not: half of
 // the LDS cycles were conflicts).
-__device__ __forceinline__ constexpr int kgroup(int g) { return (g >> 1) | (g & 1) << 1; }
-
 constexpr int kMnRow = 256;
 typedef __attribute__((ext_vector_type(4))) float f32x4;
-
-// MN-major swizzle of K-row r, in 16-byte chunks: the transposed reads of 32
-// lanes take 32 bytes of four K-rows of two groups, 8 or 16 K-rows apart: rows
-// 1 apart move by 64 bytes, rows 8 or 16 apart by 32.
-__device__ __forceinline__ constexpr int mn_swz(int r) { return 4 * (r & 3) ^ 2 * (((r >> 3) ^ (r >> 4)) & 1); }
 
 // The lane's byte offset in wave-loads 2 w and 2 w + 1 of an MN-major part
 // whose K-rows lie ld bytes apart in memory (8 w .. 8 w + 7 share the bits above 2).
@@ -470,84 +464,14 @@ __device__ __forceinline__ void store_block(uint8_t *buf, uint8_t *D, int64_t ld
 
 // ------------------------------------------------------------------- tiles
 
-// A group of r rows has r / TM whole tile rows and a rest, computed with the
-// ceil(rest / 64) blocks per wave that hold it.  Tiles are handed out by
-// descending cost -- all groups' whole tile rows (and rests that need every
-// block), then the rests by blocks -- in a snake over the workgroups, so
-// that those with a tile less of one kind come first for the next.
-template <int TM>
-struct Table {
-    static constexpr int kRests = TM / 64 - 1;
-    int32_t first[kMoeMaxExperts + 1], whole[kMoeMaxExperts + 1];   // tile rows before a group
-    uint16_t rest[kRests > 0 ? kRests : 1][kMoeMaxExperts + 1];     // rests of b + 1 blocks before a group
-};
-
-constexpr int kBand = 4;              // tile rows of a group handed out together
-
-struct RowTile {
-    int m0, mend, n0, g, blocks;      // blocks 0: nothing
-};
-
 template <int TM>
 __device__ __forceinline__ void fill_table(Table<TM> &tab, const MoeGemm &p, const Lane &c)
 {
-    constexpr int MB = TM / 64;
-    const auto blocks = [](int rows) { return (rows % TM + 63) / 64; };   // of a group's rest
     if (c.w == 0)
-        group_table<true>(tab.first, tab.whole, p.offsets, p.E, p.M, c,
-                          [&](int rows) { return rows / TM + (blocks(rows) == MB); });
-    else if (c.w < MB)
+        group_table<true>(tab.first, tab.whole, p.offsets, p.E, p.M, c, [](int rows) { return Table<TM>::whole_of(rows); });
+    else if (c.w < TM / 64)
         group_table<false>(tab.first, tab.rest[c.w - 1], p.offsets, p.E, p.M, c,
-                           [&](int rows) { return (int)(blocks(rows) == c.w); });
-}
-
-template <int TM>
-__device__ __forceinline__ int count_tiles(const Table<TM> &tab, int E, int tiles_n)
-{
-    int n = __builtin_amdgcn_readfirstlane(tab.whole[E]);
-#pragma unroll
-    for (int b = 0; b < Table<TM>::kRests; ++b) n += __builtin_amdgcn_readfirstlane((int)tab.rest[b][E]);
-    return n * tiles_n;
-}
-
-// Output tile id of the order above, tno columns wide.
-template <int TM>
-__device__ __forceinline__ RowTile find_tile(const Table<TM> &tab, int E, int ntiles, int tiles_n, int tno, int id,
-                                             const Lane &c)
-{
-    constexpr int MB = TM / 64;
-    RowTile r{};
-    if (id >= ntiles) return r;
-    const int whole = __builtin_amdgcn_readfirstlane(tab.whole[E]) * tiles_n;
-    if (id < whole) {
-        r.g = group_of(tab.whole, E, id / tiles_n, c);
-        const int before = __builtin_amdgcn_readfirstlane(tab.whole[r.g]);
-        const int n = __builtin_amdgcn_readfirstlane(tab.whole[r.g + 1]) - before;
-        // bands of kBand tile rows, columns outside them: the tiles that one
-        // XCD's workgroups hold together share rows of X and of W in its L2
-        const int local = id - before * tiles_n, band = local / (kBand * tiles_n);
-        const int rows = min(n - band * kBand, kBand), in = local - band * kBand * tiles_n;
-        r.m0 = (band * kBand + in % rows) * TM;
-        r.n0 = in / rows * tno;
-        r.blocks = MB;
-    } else {
-        id -= whole;
-#pragma unroll
-        for (int b = MB - 1; b >= 1; --b) {
-            const int n = __builtin_amdgcn_readfirstlane((int)tab.rest[b - 1][E]) * tiles_n;
-            if (r.blocks == 0 && id < n) {
-                r.g = group_of(tab.rest[b - 1], E, id / tiles_n, c);
-                r.n0 = id % tiles_n * tno;
-                r.blocks = b;
-            }
-            id -= r.blocks == 0 ? n : 0;
-        }
-    }
-    const int lo = __builtin_amdgcn_readfirstlane(tab.first[r.g]);
-    r.mend = __builtin_amdgcn_readfirstlane(tab.first[r.g + 1]);
-    if (r.blocks < MB) r.m0 = (r.mend - lo) / TM * TM;
-    r.m0 += lo;
-    return r;
+                           [&](int rows) { return Table<TM>::rest_of(rows, c.w); });
 }
 
 // Rows from .. to-1 of D are zero (those before the first group and behind the last).
@@ -595,7 +519,8 @@ __global__ __launch_bounds__(512, 1) void moe_tiles(MoeGemm p)
     // indices land within a tile (see rowbuf)
     const int nk = max((p.K + 63) / 64, 3);
     auto find = [&](int round) {
-        return find_tile(tab, p.E, ntiles, tiles_n, TNO, round * nwg + (round & 1 ? nwg - 1 - self : self), c);
+        return find_tile(tab, p.E, ntiles, tiles_n, TNO, snake(round, nwg, self),
+                         [&](const auto *at, int id) { return group_of(at, p.E, id, c); });
     };
 
     // What the loads read: stage lk of the tile behind ra and rb.
@@ -788,7 +713,10 @@ __global__ __launch_bounds__(512, 1) void moe_tiles_64(MoeGemm p)
     int tile = first_tile();
     if (tile >= ntiles) return;
     const int nk = max((p.K + 63) / 64, S::NS - 1);
-    auto find = [&](int id) { return find_tile(tab, p.E, ntiles, tiles_n, TNO, id, c); };
+    auto find = [&](int id) {
+        return find_tile(tab, p.E, ntiles, tiles_n, TNO, id,
+                         [&](const auto *at, int n) { return group_of(at, p.E, n, c); });
+    };
 
     // wave w loads rows 8 w .. of A and of W (K-rows of an MN-major W)
     i32x4 ra, rb;
@@ -983,7 +911,7 @@ __device__ __forceinline__ void dw_large(const MoeGemmDw &p, const Lane &c, uint
         r.nk = max(2, (r.hi - r.lo + 63) / 64);
         return r;
     };
-    auto tile_of = [&](int round) { return round * nwg + (round & 1 ? nwg - 1 - self : self); };
+    auto tile_of = [&](int round) { return snake(round, nwg, self); };
     Ref cur = find(self), next = cur;
 
     // What the loads read: stage lk of tile src, rows behind wa and wb.
@@ -1121,8 +1049,6 @@ __device__ __forceinline__ void dw_large(const MoeGemmDw &p, const Lane &c, uint
 // four K-rows each, groups 8 or 16 K-rows apart, and two K-rows share a bank
 // line.  X's part as in the core.  Row indices as in dw_large, but a tile's
 // first eight stages two tiles ahead: the loads run four stages ahead.
-__device__ __forceinline__ constexpr int narrow_swz(int r) { return 2 * ((r >> 1) & 1) ^ 4 * (((r >> 3) ^ (r >> 4)) & 1); }
-
 constexpr int kDwSlots = 5, kDwSlot = 64 * kRowBytes + 128 * kRowBytes;
 
 template <bool GATHER, bool F32>
@@ -1144,7 +1070,7 @@ __device__ __forceinline__ void dw_small(const MoeGemmDw &p, const Lane &c, uint
     auto find = [&](int round) {
         Ref r{};
         r.nk = NS - 1;
-        const int id = round * nwg + (round & 1 ? nwg - 1 - self : self);
+        const int id = snake(round, nwg, self);
         if (id >= ntiles) return r;
         r.g = __builtin_amdgcn_readfirstlane((int)order[id / per]);
         r.lo = __builtin_amdgcn_readfirstlane(first[r.g]);
@@ -1268,7 +1194,7 @@ __device__ __forceinline__ void dw_small(const MoeGemmDw &p, const Lane &c, uint
                                                       rd, at, 0, kStoreCached);
             }
         }
-        if ((round + 1) * nwg + ((round + 1) & 1 ? nwg - 1 - self : self) >= ntiles) break;
+        if (snake(round + 1, nwg, self) >= ntiles) break;
         cur = next;
         next = after;
         ++round;
