@@ -87,50 +87,56 @@ __device__ __forceinline__ void dma(const i32x4 &words, uint8_t *lds, uint32_t d
 }
 
 // Two wave-loads to neighbouring KiB, or four, the second two `apart` bytes
-// behind the first, from one descriptor, at offsets max(at, least): `least` is 0
-// or, where a lane has nothing to load, an offset out of bounds.  The maxima
-// stand in the descriptor's wait states.  32 experts of 4096 x 2048, 32768 rows,
-// MN-major: 519 us, 532 with the loads one by one and s_nop 3 before each.
-template <int N>
-__device__ __forceinline__ void dma_group(const i32x4 &words, uint8_t *lds, uint32_t dst, const uint32_t (&at)[N],
-                                          const uint32_t (&least)[N], uint32_t apart = 0)
+// behind the first, from one descriptor, at offsets max(x, y) -- y is 0 or, where
+// a lane has nothing to load, an offset out of bounds -- or, with SUM, x + y, y
+// the same in every lane.  The arithmetic stands in the descriptor's wait
+// states.  32 experts of 4096 x 2048, 32768 rows, MN-major: 519 us, 532 with the
+// loads one by one and s_nop 3 before each.
+#define DBS_LOAD_PAIR(OP, Y)                                                                                   \
+    asm volatile("s_mov_b32 m0, %3\n\t"                                                                        \
+                 OP " %1, %6, %4\n\t"                                                                          \
+                 OP " %2, %7, %5\n\t"                                                                          \
+                 "s_nop 1\n\t"                                                                                 \
+                 "buffer_load_dwordx4 %1, %8, 0 offen lds\n\t"                                                 \
+                 "s_add_u32 m0, m0, 0x400\n\ts_nop 0\n\t"                                                     \
+                 "buffer_load_dwordx4 %2, %8, 0 offen lds"                                                     \
+                 : "=&{m0}"(m0), "=&v"(off[0]), "=&v"(off[1])                                                  \
+                 : "s"(to), "v"(x[0]), "v"(x[1]), Y(y[0]), Y(y[1]), "s"(words)                                 \
+                 : "memory", "scc")
+#define DBS_LOAD_FOUR(OP, Y)                                                                                   \
+    asm volatile("s_mov_b32 m0, %5\n\t"                                                                        \
+                 OP " %1, %10, %6\n\t"                                                                         \
+                 OP " %2, %11, %7\n\t"                                                                         \
+                 OP " %3, %12, %8\n\t"                                                                         \
+                 OP " %4, %13, %9\n\t"                                                                         \
+                 "buffer_load_dwordx4 %1, %14, 0 offen lds\n\t"                                                \
+                 "s_add_u32 m0, m0, 0x400\n\ts_nop 0\n\t"                                                     \
+                 "buffer_load_dwordx4 %2, %14, 0 offen lds\n\t"                                                \
+                 "s_add_u32 m0, m0, %15\n\ts_nop 0\n\t"                                                       \
+                 "buffer_load_dwordx4 %3, %14, 0 offen lds\n\t"                                                \
+                 "s_add_u32 m0, m0, 0x400\n\ts_nop 0\n\t"                                                     \
+                 "buffer_load_dwordx4 %4, %14, 0 offen lds"                                                    \
+                 : "=&{m0}"(m0), "=&v"(off[0]), "=&v"(off[1]), "=&v"(off[2]), "=&v"(off[3])                    \
+                 : "s"(to), "v"(x[0]), "v"(x[1]), "v"(x[2]), "v"(x[3]), Y(y[0]), Y(y[1]), Y(y[2]), Y(y[3]),    \
+                   "s"(words), "s"(apart - 1024)                                                               \
+                 : "memory", "scc")
+
+template <bool SUM, int N>
+__device__ __forceinline__ void dma_group(const i32x4 &words, uint8_t *lds, uint32_t dst, const uint32_t (&x)[N],
+                                          const uint32_t (&y)[N], uint32_t apart = 0)
 {
     static_assert(N == 2 || N == 4, "one pair or two");
 #if DBS_LDS_POISON
 #pragma unroll
     for (int i = 0; i < N; ++i)
-        dma<16>(words, lds, dst + (i & 1) * 1024 + (i >> 1) * apart, max(at[i], least[i]));
+        dma<16>(words, lds, dst + (i & 1) * 1024 + (i >> 1) * apart, SUM ? x[i] + y[i] : max(x[i], y[i]));
 #else
     const uint32_t to = (uint32_t)(uintptr_t)(lds_void *)lds + dst;
     uint32_t m0, off[N];
-    if constexpr (N == 2)
-        asm volatile("s_mov_b32 m0, %3\n\t"
-                     "v_max_u32 %1, %4, %6\n\t"
-                     "v_max_u32 %2, %5, %7\n\t"
-                     "s_nop 1\n\t"
-                     "buffer_load_dwordx4 %1, %8, 0 offen lds\n\t"
-                     "s_add_u32 m0, m0, 0x400\n\ts_nop 0\n\t"
-                     "buffer_load_dwordx4 %2, %8, 0 offen lds"
-                     : "=&{m0}"(m0), "=&v"(off[0]), "=&v"(off[1])
-                     : "s"(to), "v"(at[0]), "v"(at[1]), "v"(least[0]), "v"(least[1]), "s"(words)
-                     : "memory", "scc");
-    else
-        asm volatile("s_mov_b32 m0, %5\n\t"
-                     "v_max_u32 %1, %6, %10\n\t"
-                     "v_max_u32 %2, %7, %11\n\t"
-                     "v_max_u32 %3, %8, %12\n\t"
-                     "v_max_u32 %4, %9, %13\n\t"
-                     "buffer_load_dwordx4 %1, %14, 0 offen lds\n\t"
-                     "s_add_u32 m0, m0, 0x400\n\ts_nop 0\n\t"
-                     "buffer_load_dwordx4 %2, %14, 0 offen lds\n\t"
-                     "s_add_u32 m0, m0, %15\n\ts_nop 0\n\t"
-                     "buffer_load_dwordx4 %3, %14, 0 offen lds\n\t"
-                     "s_add_u32 m0, m0, 0x400\n\ts_nop 0\n\t"
-                     "buffer_load_dwordx4 %4, %14, 0 offen lds"
-                     : "=&{m0}"(m0), "=&v"(off[0]), "=&v"(off[1]), "=&v"(off[2]), "=&v"(off[3])
-                     : "s"(to), "v"(at[0]), "v"(at[1]), "v"(at[2]), "v"(at[3]), "v"(least[0]), "v"(least[1]),
-                       "v"(least[2]), "v"(least[3]), "s"(words), "s"(apart - 1024)
-                     : "memory", "scc");
+    if constexpr (N == 2 && SUM) DBS_LOAD_PAIR("v_add_u32", "s");
+    else if constexpr (N == 2) DBS_LOAD_PAIR("v_max_u32", "v");
+    else if constexpr (SUM) DBS_LOAD_FOUR("v_add_u32", "s");
+    else DBS_LOAD_FOUR("v_max_u32", "v");
 #endif
 }
 
@@ -578,7 +584,7 @@ __global__ __launch_bounds__(512, 1) void moe_tiles(MoeGemm p)
         }
         if (part == kALo || part == kAHi) {
             const int i = part == kAHi ? 2 : 0;
-            dma_group<2>(ra, lds, dst, {aoff[i] + kc[0], aoff[i + 1] + kc[1]}, least);
+            dma_group<false, 2>(ra, lds, dst, {aoff[i] + kc[0], aoff[i + 1] + kc[1]}, least);
             return;
         }
         uint32_t x[4], y[4];                   // [2 j + q]: part j of B
@@ -599,7 +605,7 @@ __global__ __launch_bounds__(512, 1) void moe_tiles(MoeGemm p)
                 y[i] = least[i & 1];
             }
         }
-        dma_group<4>(rb, lds, dst, x, y, kPart);
+        dma_group<false, 4>(rb, lds, dst, x, y, kPart);
     };
 
     RowTile cur = find(0), next = cur;
@@ -950,13 +956,16 @@ __device__ __forceinline__ void dw_large(const MoeGemmDw &p, const Lane &c, uint
     auto load = [&](int part, int slot) {
         const uint32_t dst = slot * kSlot + part * kPart + c.w * 2048;
         if (part == kALo || part == kAHi) {
-            const uint32_t at = la + (uint32_t)(c.w * 8 * lda) + (part == kAHi ? 256 : 0);
-            dma_group<2>(wa, lds, dst, {at, at + (uint32_t)(4 * lda)}, {0, 0});
+            const uint32_t at = (uint32_t)(c.w * 8 * lda) + (part == kAHi ? 256 : 0);
+            dma_group<true, 2>(wa, lds, dst, {la, la}, {at, at + (uint32_t)(4 * lda)});
             return;
         }
-        const uint32_t b0 = GATHER ? boff[0] : lb + (uint32_t)(c.w * 8 * ldb);
-        const uint32_t b1 = GATHER ? boff[1] : b0 + (uint32_t)(4 * ldb);
-        dma_group<4>(wb, lds, dst, {b0, b1, b0 + 256, b1 + 256}, {0, 0, 0, 0}, kPart);
+        if constexpr (GATHER) {
+            dma_group<true, 4>(wb, lds, dst, {boff[0], boff[1], boff[0], boff[1]}, {0, 0, 256, 256}, kPart);
+        } else {
+            const uint32_t at = (uint32_t)(c.w * 8 * ldb), next = at + (uint32_t)(4 * ldb);
+            dma_group<true, 4>(wb, lds, dst, {lb, lb, lb, lb}, {at, next, at + 256, next + 256}, kPart);
+        }
     };
 
     batch(cur, 0, 0);
