@@ -8,7 +8,7 @@
 // The groups' row offsets are read on the device: a workgroup turns them
 // into a table of first tiles in LDS, so a router's output needs no copy to
 // the host.  Many rows per expert are bound by the matrix cores (256 x 256
-// tiles: 1.3 PFLOP/s), few by the reading of W (64-row tiles: up to 7 TB/s).
+// tiles: 1.3 PFLOP/s), few by the reading of W (64-row tiles: up to 5.8 TB/s).
 //
 // * Rows.  A gathered row's byte offset is taken from `rows` once per output
 //   tile and lives in one register per wave-load, so gathering costs one add
@@ -270,9 +270,8 @@ __device__ __forceinline__ int first_tile()
 //
 // What bounds it is the clock that the power leaves and, close behind, the
 // 64 KiB a stage that come into LDS: 32768 rows over 32 experts, 4096 x 2048,
-// in even groups take 430 us (1.28 PFLOP/s), on zeros 358, their loads alone
-// 320.  A tile costs 1.5 us a stage and 6 us of storing, in which all CUs write
-// at once.
+// in even groups take 427 us (1.29 PFLOP/s), on zeros 340.  A tile costs 1.5 us
+// a stage and 6 us of storing, in which all CUs write at once.
 constexpr int kPart = 128 * kRowBytes, kSlot = 4 * kPart, kInFlight = 8;
 enum PartId : int { kALo = 0, kAHi = 1, kBLo = 2, kBHi = 3 };
 constexpr int kStage = 2 * kSlot;              // LDS offset of the waves' output buffers, 2 KiB each
@@ -283,10 +282,9 @@ constexpr int kCoreLds = kStage + 8 * 2048;
 // of 128 columns (256 bytes), wave-load L covers K-rows 4 L .. 4 L + 3.  Wave
 // w issues wave-loads 2 w and 2 w + 1.
 //
-// The math is v_mfma_f32_16x16x32_bf16: with random data in the registers it
-// runs at 2.06 PFLOP/s where 32x32x16 runs at 1.82 (both at 2.45 with zeros:
-// it is the power that differs, an accumulator being read and written half
-// as often), and these kernels are bound by the clock that power leaves.  Its
+// The math is v_mfma_f32_16x16x32_bf16: the products of even groups ran at 1.30
+// PFLOP/s with it and at 1.22 with 32x32x16, both bound by the clock that
+// power leaves (an accumulator is read and written half as often).  Its
 // lane l holds row (or column) l % 16 and eight K of a 16 x 32 operand block,
 // and of the result, with B's block as the first operand, row l % 16 of A's
 // and columns 4 (l / 16) .. + 3 of B's.  The lane's K are 8 kgroup(l / 16) ..,
@@ -493,13 +491,13 @@ __device__ __forceinline__ void zero_rows(const MoeGemm &p, int64_t from, int64_
 }
 
 // 256-row tiles, or of 128 rows (TM) where a call has too few of the large ones
-// for the CUs: the same stages with half of A's parts left out, 1.1 us in place
-// of 1.3.  BMN: W MN-major; GATE: see the head of the file.
+// for the CUs: the same stages, A's upper half filled with zeros and not
+// multiplied, 1.1 us in place of 1.3.  BMN: W MN-major; GATE: see the head of the file.
 //
-// 32768 rows of 32 uneven experts, 4096 x 2048 MN-major: 490 us (1.12
+// 32768 rows of 32 uneven experts, 4096 x 2048 MN-major: 488 us (1.13
 // PFLOP/s): 4.1 tiles' work a CU, of which the busiest have 4.7, with rests
-// that cost more than their share; in even groups 430.  24594 rows of 64 very
-// uneven experts, 1416 x 2048: 177 us (0.8 PFLOP/s), where groups of 1.5
+// that cost more than their share; in even groups 427.  24594 rows of 64 very
+// uneven experts, 1416 x 2048: 185 us (0.77 PFLOP/s), where groups of 1.5
 // tile rows leave a third of the tiles partly empty.
 template <int TM, bool BMN, bool GATE>
 __global__ __launch_bounds__(512, 1) void moe_tiles(MoeGemm p)
@@ -685,9 +683,9 @@ __global__ __launch_bounds__(512, 1) void moe_tiles(MoeGemm p)
 // half of the columns.  With the gate a wave's 32 rows of W are 16 gate rows
 // and the 16 up rows that meet them.
 //
-// 384 rows on 128 experts behind the gate, 768 x 4096: 212 us for 1.5 GB (7
-// TB/s); one token on 8 experts, 1408 x 2048: 21 us for 92 MB (4.3 TB/s: 352
-// tiles on 256 CUs, and the way into the kernel).  Against 64 x 256 tiles over
+// 384 rows on 96 of 128 experts behind the gate, 768 x 4096: 209 us for 1.2 GB
+// (5.8 TB/s); one token on 8 experts, 1408 x 2048: 22.6 us for 92 MB (4.1 TB/s:
+// 352 tiles on 256 CUs, and the way into the kernel).  Against 64 x 256 tiles over
 // three slots (0.7 us a stage): 8 experts of 4096 x 4096, 4 rows 42 us against
 // 45, 32 rows 44 against 63; 64 experts of 2816 x 2048, 16 rows 143 against 169.
 template <bool BMN>
@@ -883,10 +881,10 @@ constexpr int kDwBand = 8;
 // waits for them by its own count, no barrier), into a buffer per parity of
 // the tile for a tile's first eight stages and two in turn for later ones.
 //
-// 32768 rows of 32 uneven experts, 4096 x 2048: 542 us to bf16 (1.0 PFLOP/s)
+// 32768 rows of 32 uneven experts, 4096 x 2048: 540 us to bf16 (1.02 PFLOP/s)
 // at 46 % of the matrix cores' cycles: 1.7 us a stage, and 5 us for each of a
 // CU's 16 tiles, when all CUs write at once.  One expert of 16384 rows,
-// 4096 x 4096: 414 us (1.33 PFLOP/s).
+// 4096 x 4096: 409 us (1.35 PFLOP/s).
 template <bool GATHER, bool F32>
 __device__ __forceinline__ void dw_large(const MoeGemmDw &p, const Lane &c, uint8_t *lds, const int32_t *first,
                                          const uint16_t *order, int groups, uint32_t *rowbuf)

@@ -8,10 +8,10 @@
 //     combine        out_t = sum_j w_tj Y[slot_tj]  (slots of -1 add nothing)
 //     combine_bwd    dY[slot_tj] = w_tj dO_t,       dw_tj = <dO_t, Y[slot_tj]>
 //
-// Measured, where a copy of 1 GiB reaches 5.0 TB/s: swiglu 32768 x 2048 68 us
-// (5.9 TB/s, two bytes read for one written), swiglu_bwd 49999 x 1416 129 us (5.5),
-// combine 8192 tokens x 8 rows x 4096 115 us (5.3), combine_bwd 8191 x 6 x 2056
-// 90 us (4.7, as much written as read).
+// Measured, where a copy of 1 GiB reaches 5.0 TB/s: swiglu 32768 x 2048 69 us
+// (5.8 TB/s, two bytes read for one written), swiglu_bwd 49999 x 1416 129 us (5.5),
+// combine 8192 tokens x 8 rows x 4096 116 us (5.2), combine_bwd 8191 x 6 x 2056
+// 87 us (4.9, as much written as read).
 //
 // Every kernel has a form of 16-byte pieces (8 elements; row lengths that are
 // multiples of 8, base addresses on 16 bytes) and one of single elements.

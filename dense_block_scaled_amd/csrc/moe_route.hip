@@ -7,7 +7,7 @@
 // and the stable order of the T k pairs (t, j) by expert.  A logit of -inf or
 // NaN closes an expert to the token; a token with fewer than k open experts
 // has experts -1 (weight 0) behind them, and such pairs have no place in the
-// order.  +inf counts as the largest finite value.
+// order.  +inf counts as the largest finite fp32 value.
 //
 // Selection.  16 lanes hold one token's logits in registers, so the
 // cross-lane steps of a maximum are four DPP moves inside a row of 16 and one
@@ -25,13 +25,13 @@
 // every workgroup sums the expert totals for itself -- and, up to 2048 tokens,
 // the columns too, so that two kernels do.  Up to 64 tokens take one kernel,
 // which is what a decoding step's latency asks for: one token of 64 experts
-// 3.9 us, nearly all of it the launch and two trips to memory.
+// 3.8 us, nearly all of it the launch and two trips to memory.
 //
-// 32768 tokens, 8 of 128 experts, fp32: 12 us of selection, 4 of sums and 5.8
+// 32768 tokens, 8 of 128 experts, fp32: 11.7 us of selection, 4.1 of sums and 5.6
 // of placing, for 21 MB.  Selection is bound by its vector instructions (73 a
 // choice and wave of four tokens, 9 us of issue on 1024 SIMDs), not by the
 // logits (1.4 TB/s).  The gradient streams: 16384 tokens of 160 experts, bf16,
-// 6.0 us (1.9 TB/s, a third of it the launch).
+// 6.1 us (1.9 TB/s).
 #include <hip/hip_runtime.h>
 #include <float.h>
 #include <stdint.h>

@@ -335,7 +335,8 @@ dbs_status quant_bf16(const float *x, int64_t n, void *out, hipStream_t stream);
  *   `type`): the k largest, ties to the lower expert; weights = softmax over
  *   all E logits, or, with renormalize = 1, over the chosen ones.  A logit of
  *   -inf or NaN closes its expert to the token (weight 0, never chosen); a
- *   token may have no open expert.  +inf counts as the largest finite value.
+ *   token may have no open expert.  +inf counts as the largest finite
+ *   fp32 value.
  *   workspace: device memory of moe_route_workspace(T, E, k) bytes (0 up to
  *   64 tokens), 4-byte aligned, the caller's; calls that share one must not
  *   overlap.  One kernel up to 64 tokens, two or three above.
