@@ -90,21 +90,22 @@ __device__ __forceinline__ void dma(const i32x4 &words, uint8_t *lds, uint32_t d
 // behind the first, from one descriptor, at offsets max(x, y) -- y is 0 or, where
 // a lane has nothing to load, an offset out of bounds -- or, with SUM, x + y, y
 // the same in every lane.  The arithmetic stands in the descriptor's wait
-// states.  32 experts of 4096 x 2048, 32768 rows, MN-major: 519 us, 532 with the
-// loads one by one and s_nop 3 before each.
+// states; a vector instruction may read an SGPR two states after one wrote it.
+// 32 experts of 4096 x 2048, 32768 rows, MN-major: 519 us, 532 with the loads
+// one by one and s_nop 3 before each.
 #define DBS_LOAD_PAIR(OP, Y)                                                                                   \
-    asm volatile("s_mov_b32 m0, %3\n\t"                                                                        \
+    asm volatile("s_mov_b32 m0, %3\n\ts_nop 0\n\t"                                                            \
                  OP " %1, %6, %4\n\t"                                                                          \
                  OP " %2, %7, %5\n\t"                                                                          \
-                 "s_nop 1\n\t"                                                                                 \
+                 "s_nop 0\n\t"                                                                                 \
                  "buffer_load_dwordx4 %1, %8, 0 offen lds\n\t"                                                 \
                  "s_add_u32 m0, m0, 0x400\n\ts_nop 0\n\t"                                                     \
                  "buffer_load_dwordx4 %2, %8, 0 offen lds"                                                     \
                  : "=&{m0}"(m0), "=&v"(off[0]), "=&v"(off[1])                                                  \
                  : "s"(to), "v"(x[0]), "v"(x[1]), Y(y[0]), Y(y[1]), "s"(words)                                 \
                  : "memory", "scc")
-#define DBS_LOAD_FOUR(OP, Y)                                                                                   \
-    asm volatile("s_mov_b32 m0, %5\n\t"                                                                        \
+#define DBS_LOAD_FOUR(FIRST, OP, Y)                                                                            \
+    asm volatile("s_mov_b32 m0, %5\n\t" FIRST                                                                  \
                  OP " %1, %10, %6\n\t"                                                                         \
                  OP " %2, %11, %7\n\t"                                                                         \
                  OP " %3, %12, %8\n\t"                                                                         \
@@ -135,8 +136,8 @@ __device__ __forceinline__ void dma_group(const i32x4 &words, uint8_t *lds, uint
     uint32_t m0, off[N];
     if constexpr (N == 2 && SUM) DBS_LOAD_PAIR("v_add_u32", "s");
     else if constexpr (N == 2) DBS_LOAD_PAIR("v_max_u32", "v");
-    else if constexpr (SUM) DBS_LOAD_FOUR("v_add_u32", "s");
-    else DBS_LOAD_FOUR("v_max_u32", "v");
+    else if constexpr (SUM) DBS_LOAD_FOUR("s_nop 0\n\t", "v_add_u32", "s");
+    else DBS_LOAD_FOUR("", "v_max_u32", "v");
 #endif
 }
 

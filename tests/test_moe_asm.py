@@ -230,3 +230,33 @@ def test_lanes_hand_over_through_a_fence(unit, kernel, handovers, tmp_path):
 def test_no_bare_wave_barrier():
     for f in sorted(poison.CSRC.glob("moe_*.hip")):
         assert "__builtin_amdgcn_wave_barrier" not in f.read_text(), f.name
+
+
+@pytest.mark.parametrize("unit", UNITS)
+@pytest.mark.parametrize("poisoned", [False, True])
+def test_every_load_statement_keeps_the_wait_states_itself(listings, unit, poisoned):
+    """Whatever the compiler puts right before one: inside the statement a
+    vector instruction reads an SGPR after two wait states at the earliest, a
+    load after five, and a load comes one after M0 is written."""
+    statements = 0
+    for block in re.findall(r";+#ASMSTART\n(.*?);+#ASMEND", listings[(unit, poisoned)], flags=re.S):
+        lines = [x.split(";")[0].strip() for x in block.splitlines()]
+        if not any(poison.DMA.match(x) for x in lines):
+            continue
+        statements += 1
+        ws, m0 = 0, None
+        for x in lines:
+            if not x:
+                continue
+            q = x.replace(",", " ").split()
+            if q[0] == "s_nop":
+                ws += int(q[1], 0) + 1
+                continue
+            if q[0].startswith("buffer_load"):
+                assert ws >= SGPR_WAIT and m0 is not None and ws - m0 >= 1, block
+            elif q[0].startswith("v_") and any(_sgprs(a) for a in q[2:]):
+                assert ws >= 2, block
+            ws += 1
+            if q[0].startswith("s_") and q[1] == "m0":
+                m0 = ws
+    assert statements > 100
