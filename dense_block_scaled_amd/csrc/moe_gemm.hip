@@ -271,7 +271,7 @@ __device__ __forceinline__ int first_tile()
 //
 // What bounds it is the clock that the power leaves and, close behind, the
 // 64 KiB a stage that come into LDS: 32768 rows over 32 experts, 4096 x 2048,
-// in even groups take 427 us (1.29 PFLOP/s), on zeros 340.  A tile costs 1.5 us
+// in even groups take 431 us (1.28 PFLOP/s), on zeros 343.  A tile costs 1.5 us
 // a stage and 6 us of storing, in which all CUs write at once.
 constexpr int kPart = 128 * kRowBytes, kSlot = 4 * kPart, kInFlight = 8;
 enum PartId : int { kALo = 0, kAHi = 1, kBLo = 2, kBHi = 3 };
@@ -495,10 +495,10 @@ __device__ __forceinline__ void zero_rows(const MoeGemm &p, int64_t from, int64_
 // for the CUs: the same stages, A's upper half filled with zeros and not
 // multiplied, 1.1 us in place of 1.3.  BMN: W MN-major; GATE: see the head of the file.
 //
-// 32768 rows of 32 uneven experts, 4096 x 2048 MN-major: 488 us (1.13
+// 32768 rows of 32 uneven experts, 4096 x 2048 MN-major: 491 us (1.12
 // PFLOP/s): 4.1 tiles' work a CU, of which the busiest have 4.7, with rests
-// that cost more than their share; in even groups 427.  24594 rows of 64 very
-// uneven experts, 1416 x 2048: 185 us (0.77 PFLOP/s), where groups of 1.5
+// that cost more than their share; in even groups 431.  24594 rows of 64 very
+// uneven experts, 1416 x 2048: 186 us (0.77 PFLOP/s), where groups of 1.5
 // tile rows leave a third of the tiles partly empty.
 template <int TM, bool BMN, bool GATE>
 __global__ __launch_bounds__(512, 1) void moe_tiles(MoeGemm p)
@@ -882,10 +882,10 @@ constexpr int kDwBand = 8;
 // waits for them by its own count, no barrier), into a buffer per parity of
 // the tile for a tile's first eight stages and two in turn for later ones.
 //
-// 32768 rows of 32 uneven experts, 4096 x 2048: 540 us to bf16 (1.02 PFLOP/s)
+// 32768 rows of 32 uneven experts, 4096 x 2048: 542 us to bf16 (1.01 PFLOP/s)
 // at 46 % of the matrix cores' cycles: 1.7 us a stage, and 5 us for each of a
 // CU's 16 tiles, when all CUs write at once.  One expert of 16384 rows,
-// 4096 x 4096: 409 us (1.35 PFLOP/s).
+// 4096 x 4096: 413 us (1.33 PFLOP/s).
 template <bool GATHER, bool F32>
 __device__ __forceinline__ void dw_large(const MoeGemmDw &p, const Lane &c, uint8_t *lds, const int32_t *first,
                                          const uint16_t *order, int groups, uint32_t *rowbuf)

@@ -25,9 +25,9 @@
 // every workgroup sums the expert totals for itself -- and, up to 2048 tokens,
 // the columns too, so that two kernels do.  Up to 64 tokens take one kernel,
 // which is what a decoding step's latency asks for: one token of 64 experts
-// 3.8 us, nearly all of it the launch and two trips to memory.
+// 3.6 us, nearly all of it the launch and two trips to memory.
 //
-// 32768 tokens, 8 of 128 experts, fp32: 11.7 us of selection, 4.1 of sums and 5.6
+// 32768 tokens, 8 of 128 experts, fp32: 11.5 us of selection, 4.1 of sums and 5.5
 // of placing, for 21 MB.  Selection is bound by its vector instructions (73 a
 // choice and wave of four tokens, 9 us of issue on 1024 SIMDs), not by the
 // logits (1.4 TB/s).  The gradient streams: 16384 tokens of 160 experts, bf16,
