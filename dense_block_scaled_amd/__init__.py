@@ -35,6 +35,7 @@ import torch
 
 __all__ = ["gemm_bf16", "gemm_bf16_decoupled", "gemm_mx", "gemm_mx_mixed", "gemm_nvfp4", "gemm_nvfp4_fp8", "gemm_nvfp4_fp8_noalloc", "nvfp4_fp8_workspace_bytes", "gemm_nvfp4_fp6", "nvfp4_fp6_workspace_bytes", "gemm_grouped_bf16", "gemm_grouped_mx", "gemm_grouped_nvfp4", "quant_mx", "quant_nvfp4", "quant_bf16",
            "MoeRouting", "moe_route", "moe_route_backward", "gemm_moe_bf16", "gemm_moe_swiglu_bf16", "gemm_moe_dw_bf16",
+           "moe_route_grouped", "moe_route_grouped_backward", "quant_i8", "gemm_i8", "gemm_moe_i8", "gemm_moe_swiglu_i8",
            "swiglu", "swiglu_backward", "moe_combine", "moe_combine_backward", "lib", "LIB_PATH", "DbsError", "load_poison_library", "using_library",
            "DBS_OK", "DBS_EINVAL", "DBS_EUNSUPPORTED", "DBS_EHIP", "K_MAJOR", "MN_MAJOR",
            "E4M3", "E5M2", "E2M3", "E3M2", "E2M1", "status_str"]
@@ -151,6 +152,19 @@ def _declare(L: ctypes.CDLL) -> None:
     L.moe_combine_bf16.restype = I
     L.moe_combine_bwd_bf16.argtypes = [P, P, P, P, P, I64, P, P, I64, I64, I64, P]
     L.moe_combine_bwd_bf16.restype = I
+    F = ctypes.c_float
+    L.moe_route_grouped.argtypes = [I, P, P, I64, I64, I64, I, I64, I64, I64, I, F, P, P, P, P, P, P, SZ, P]
+    L.moe_route_grouped.restype = I
+    L.moe_route_grouped_bwd.argtypes = [I, P, I64, I64, I64, I, I, F, P, P, P, P]
+    L.moe_route_grouped_bwd.restype = I
+    L.quant_i8.argtypes = [I, P, I64, I64, P, P, P]
+    L.quant_i8.restype = I
+    L.gemm_i8.argtypes = [I, P, P, P, P, P, I64, I64, I64, P]
+    L.gemm_i8.restype = I
+    L.gemm_moe_i8.argtypes = [P, P, P, P, P, P, P, I64, I64, I64, I64, I64, P]
+    L.gemm_moe_i8.restype = I
+    L.gemm_moe_swiglu_i8.argtypes = [P, P, P, P, P, P, P, I64, I64, I64, I64, I64, P]
+    L.gemm_moe_swiglu_i8.restype = I
     L.dbs_status_str.argtypes = [I]
     L.dbs_status_str.restype = ctypes.c_char_p
     L.dbs_last_error.argtypes = []
@@ -547,6 +561,17 @@ def _given(out: torch.Tensor | None, shape, dtype, device: torch.device) -> torc
     return out
 
 
+def _routing(T: int, E: int, k: int, device: torch.device):
+    """Outputs of a router, and its workspace (bytes, tensor or None)."""
+    kk = min(max(k, 0), E)                    # (the library refuses other k; nothing is sized by them)
+    need = int(lib().moe_route_workspace(T, E, kk))
+    experts = torch.empty((T, kk), dtype=torch.int32, device=device)
+    r = MoeRouting(experts, torch.empty_like(experts, dtype=torch.float32),
+                   torch.empty(E + 1, dtype=torch.int32, device=device),
+                   torch.empty(T * kk, dtype=torch.int32, device=device), torch.empty_like(experts))
+    return r, need, torch.empty(need, dtype=torch.uint8, device=device) if need else None
+
+
 def moe_route(logits: torch.Tensor, k: int, renormalize: bool = True) -> MoeRouting:
     """Router: the k best of E experts for each of T tokens from logits (T, E)
     fp32 or bf16, their softmax weights (over the chosen experts, or over all
@@ -557,18 +582,62 @@ def moe_route(logits: torch.Tensor, k: int, renormalize: bool = True) -> MoeRout
     T, E = _dims(logits, "logits", 2)
     dev = logits.device
     pl = _arg(logits, "logits", _REAL, (T, E), dev)
-    kk = min(max(k, 0), E)                    # (the library refuses other k; nothing is sized by them)
-    need = int(lib().moe_route_workspace(T, E, kk))
-    experts = torch.empty((T, kk), dtype=torch.int32, device=dev)
-    weights = torch.empty_like(experts, dtype=torch.float32)
-    offsets = torch.empty(E + 1, dtype=torch.int32, device=dev)
-    rows = torch.empty(T * kk, dtype=torch.int32, device=dev)
-    slots = torch.empty_like(experts)
-    ws = torch.empty(need, dtype=torch.uint8, device=dev) if need else None
-    _call("moe_route", dev, _REAL[logits.dtype], pl, T, E, k, int(bool(renormalize)), experts.data_ptr(),
-          weights.data_ptr(), offsets.data_ptr(), rows.data_ptr(), slots.data_ptr(),
+    r, need, ws = _routing(T, E, k, dev)
+    _call("moe_route", dev, _REAL[logits.dtype], pl, T, E, k, int(bool(renormalize)), r.experts.data_ptr(),
+          r.weights.data_ptr(), r.offsets.data_ptr(), r.rows.data_ptr(), r.slots.data_ptr(),
           None if ws is None else ws.data_ptr(), need)
-    return MoeRouting(experts, weights, offsets, rows, slots)
+    return r
+
+
+_SCORE = {"softmax": 0, "sigmoid": 1}
+
+
+def _score(scores: str) -> int:
+    if scores not in _SCORE:
+        raise ValueError(f"scores: {scores!r} not in {tuple(_SCORE)}")
+    return _SCORE[scores]
+
+
+def moe_route_grouped(logits: torch.Tensor, k: int, bias: torch.Tensor | None = None, groups: int = 1,
+                      kept_groups: int | None = None, group_best: int = 2, scores: str = "sigmoid",
+                      renormalize: bool = True, scale: float = 1.0) -> MoeRouting:
+    """Router by groups of experts: scores of the logits (T, E) fp32 or bf16 by
+    'sigmoid' or 'softmax'; by score plus ``bias`` (E,) fp32 the best
+    ``kept_groups`` (default: all) of ``groups`` runs of E / groups experts are
+    kept, by the sum of their ``group_best`` (1 or 2) largest, and the k best
+    experts of those chosen.  Weights are ``scale`` times the chosen scores,
+    divided by their sum with renormalize=True; the bias is not in them.
+    Logits (or biases) of -inf or NaN close an expert; ties go to the lower one."""
+    k, groups = operator.index(k), operator.index(groups)
+    kept = groups if kept_groups is None else operator.index(kept_groups)
+    T, E = _dims(logits, "logits", 2)
+    dev = logits.device
+    pl = _arg(logits, "logits", _REAL, (T, E), dev)
+    pb = None if bias is None else _arg(bias, "bias", _F32, (E,), dev)
+    code = _score(scores)
+    r, need, ws = _routing(T, E, k, dev)
+    _call("moe_route_grouped", dev, _REAL[logits.dtype], pl, pb, T, E, k, code, groups, kept, operator.index(group_best),
+          int(bool(renormalize)), float(scale), r.experts.data_ptr(), r.weights.data_ptr(), r.offsets.data_ptr(),
+          r.rows.data_ptr(), r.slots.data_ptr(), None if ws is None else ws.data_ptr(), need)
+    return r
+
+
+def moe_route_grouped_backward(logits: torch.Tensor, experts: torch.Tensor, dweights: torch.Tensor,
+                               scores: str = "sigmoid", renormalize: bool = True, scale: float = 1.0) -> torch.Tensor:
+    """Gradient of moe_route_grouped's weights with respect to its logits (T, E):
+    experts (T, k) as moe_route_grouped gave them, dweights (T, k) fp32.  (The
+    choice, and with it the bias, has none.)"""
+    T, E = _dims(logits, "logits", 2)
+    k = _dims(experts, "experts", 2)[1]
+    dev = logits.device
+    pl = _arg(logits, "logits", _REAL, (T, E), dev)
+    pe = _arg(experts, "experts", _I32, (T, k), dev)
+    pw = _arg(dweights, "dweights", _F32, (T, k), dev)
+    code = _score(scores)
+    out = torch.empty_like(logits)
+    _call("moe_route_grouped_bwd", dev, _REAL[logits.dtype], pl, T, E, k, code, int(bool(renormalize)), float(scale), pe,
+          pw, out.data_ptr())
+    return out
 
 
 def moe_route_backward(logits: torch.Tensor, experts: torch.Tensor, dweights: torch.Tensor,
@@ -708,3 +777,95 @@ def moe_combine_backward(dO: torch.Tensor, Y: torch.Tensor, slots: torch.Tensor,
     dweights = torch.empty_like(weights)
     _call("moe_combine_bwd_bf16", dev, pd, py, ps, pw, po, E, dY.data_ptr(), dweights.data_ptr(), T, k, H)
     return dY, dweights
+
+
+# ---- products in 8-bit integers ---------------------------------------------------
+#
+# A matrix product with int8 codes and a scale for each row (token) of A and each
+# row (channel) of B, and a routed layer served that way:
+#
+#     qw, sw = quant_i8(W)                                    once
+#     qx, sx = quant_i8(x)
+#     y = gemm_i8(qx, sx, qw, sw)
+#
+#     r = moe_route_grouped(logits, k, bias, groups, kept_groups)
+#     a = gemm_moe_swiglu_i8(qx, sx, q13, s13, r.offsets, r.rows)
+#     qa, sa = quant_i8(a)
+#     out = moe_combine(gemm_moe_i8(qa, sa, q2, s2, r.offsets), r.slots, r.weights)
+
+_I8 = (torch.int8,)
+
+
+def quant_i8(x: torch.Tensor) -> tuple[torch.Tensor, torch.Tensor]:
+    """Rows x (M, K) fp32 or bf16 -> (codes (M, K) int8, scales (M,) fp32): scale =
+    amax / 127, codes the nearest whole numbers to 127 x / amax (ties to even).
+    A row of zeros has scale 0, one with an infinity or a NaN scale NaN."""
+    M, K = _dims(x, "x", 2)
+    dev = x.device
+    px = _arg(x, "x", _REAL, (M, K), dev)
+    codes = torch.empty((M, K), dtype=torch.int8, device=dev)
+    scales = torch.empty((M,), dtype=torch.float32, device=dev)
+    _call("quant_i8", dev, _REAL[x.dtype], px, M, K, codes.data_ptr(), scales.data_ptr())
+    return codes, scales
+
+
+def gemm_i8(A: torch.Tensor, sA: torch.Tensor, B: torch.Tensor, sB: torch.Tensor, out: torch.Tensor | None = None,
+            out_dtype: torch.dtype = torch.bfloat16) -> torch.Tensor:
+    """D[m, n] = sA[m] * sB[n] * sum over k of A[m, k] * B[n, k]: codes A (M, K) and B
+    (N, K) int8, scales sA (M,) and sB (N,) fp32; the sum in whole numbers; D (M, N)
+    bf16 or fp32 (or ``out``'s type)."""
+    M, K = _dims(A, "A", 2)
+    N = _dims(B, "B", 2)[0]
+    dev = A.device
+    pa, psa = _arg(A, "A", _I8, (M, K), dev), _arg(sA, "sA", _F32, (M,), dev)
+    pb, psb = _arg(B, "B", _I8, (N, K), dev), _arg(sB, "sB", _F32, (N,), dev)
+    if out is not None and isinstance(out, torch.Tensor):
+        out_dtype = out.dtype if out.dtype in _REAL else out_dtype
+    if out_dtype not in _REAL:
+        raise TypeError(f"out_dtype: {out_dtype} not in {tuple(_REAL)}")
+    out = _given(out, (M, N), out_dtype, dev)
+    _call("gemm_i8", dev, _REAL[out_dtype], pa, psa, pb, psb, out.data_ptr(), M, N, K)
+    return out
+
+
+def _sorted_i8(X, sX, offsets, rows, E):
+    """Checked addresses of X, sX, offsets and rows, with T, M and K."""
+    T, K = _dims(X, "X", 2)
+    dev = X.device
+    px, ps = _arg(X, "X", _I8, (T, K), dev), _arg(sX, "sX", _F32, (T,), dev)
+    po = _arg(offsets, "offsets", _I32, (E + 1,), dev)
+    if rows is None:
+        return px, ps, po, None, T, T, K
+    M = _dims(rows, "rows", 1)[0]
+    return px, ps, po, _arg(rows, "rows", _I32, (M,), dev), T, M, K
+
+
+def gemm_moe_i8(X: torch.Tensor, sX: torch.Tensor, W: torch.Tensor, sW: torch.Tensor, offsets: torch.Tensor,
+                rows: torch.Tensor | None = None, out: torch.Tensor | None = None) -> torch.Tensor:
+    """gemm_moe_bf16 in 8-bit integers: D[i] = sX[r] * sW[g] * (X[r] @ W[g].T), r =
+    rows[i], for the sorted rows i of expert g.  X (T, K) int8 gathered through
+    rows (M,) int32, or sorted already (rows=None), sX (T,) fp32; W (E, N, K)
+    int8, sW (E, N) fp32; D (M, N) bf16.  Rows of D past offsets[E] are zero."""
+    E, N, _ = _dims(W, "W", 3)
+    px, ps, po, pr, T, M, K = _sorted_i8(X, sX, offsets, rows, E)
+    dev = X.device
+    pw, pt = _arg(W, "W", _I8, (E, N, K), dev), _arg(sW, "sW", _F32, (E, N), dev)
+    out = _given(out, (M, N), torch.bfloat16, dev)
+    _call("gemm_moe_i8", dev, px, ps, pw, pt, out.data_ptr(), po, pr, T, M, E, N, K)
+    return out
+
+
+def gemm_moe_swiglu_i8(X: torch.Tensor, sX: torch.Tensor, W: torch.Tensor, sW: torch.Tensor, offsets: torch.Tensor,
+                       rows: torch.Tensor | None = None, out: torch.Tensor | None = None) -> torch.Tensor:
+    """gemm_moe_i8 with the gate applied on the way out: W (E, 2F, K) holds every
+    expert's gate matrix (first F rows) and up matrix; returns silu(gate) * up,
+    (M, F) bf16."""
+    E, N, _ = _dims(W, "W", 3)
+    if N % 2:
+        raise ValueError(f"W: {N} rows per expert, expected an even number (gate and up matrices)")
+    px, ps, po, pr, T, M, K = _sorted_i8(X, sX, offsets, rows, E)
+    dev = X.device
+    pw, pt = _arg(W, "W", _I8, (E, N, K), dev), _arg(sW, "sW", _F32, (E, N), dev)
+    out = _given(out, (M, N // 2), torch.bfloat16, dev)
+    _call("gemm_moe_swiglu_i8", dev, px, ps, pw, pt, out.data_ptr(), po, pr, T, M, E, N // 2, K)
+    return out

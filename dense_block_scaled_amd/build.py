@@ -5,8 +5,8 @@
 hipcc compiles the kernel translation units (csrc/gemm_*.hip: one per group
 of formats, all instantiating the template in csrc/gemm_kernel.h), the
 launcher (csrc/gemm.hip), the quantisers (csrc/quant.hip), the
-mixture-of-experts kernels (csrc/moe_*.hip) and the ABI layer (csrc/dbs.cpp,
-csrc/moe.cpp) to objects in parallel, then links them, in-tree; no GPU is
+mixture-of-experts kernels (csrc/moe_*.hip), the 8-bit integer kernels
+(csrc/i8_*.hip) and the ABI layer (csrc/dbs.cpp, csrc/moe.cpp, csrc/i8.cpp) to objects in parallel, then links them, in-tree; no GPU is
 needed to build.  Packed-fp32 VALU instructions are turned off for the
 device code.  build(poison=True) builds the same sources with
 DBS_LDS_POISON=1 into libdbs_poison.so, a debug library whose direct-to-LDS
@@ -35,8 +35,8 @@ DEVICE_FLAGS = ["-Xclang", "-target-feature", "-Xclang", "-packed-fp32-ops"]
 
 # largest first, so the longest compile starts first
 SOURCES = ["gemm_mx8_fp4.hip", "gemm_mxfp8.hip", "gemm_mx8_e5m2.hip", "gemm_nvfp4.hip", "gemm_mxfp4.hip", "gemm_mxfp6.hip",
-           "gemm_bf16.hip", "moe_gemm.hip", "gemm_bf16_ea.hip", "quant.hip", "moe_route.hip", "moe_pointwise.hip", "gemm.hip",
-           "scratch.hip", "dbs.cpp", "moe.cpp"]
+           "gemm_bf16.hip", "moe_gemm.hip", "i8_gemm.hip", "moe_route.hip", "gemm_bf16_ea.hip", "quant.hip", "moe_pointwise.hip", "i8_quant.hip",
+           "gemm.hip", "scratch.hip", "dbs.cpp", "moe.cpp", "i8.cpp"]
 
 
 def _jobs() -> int:

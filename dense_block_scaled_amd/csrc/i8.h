@@ -1,0 +1,37 @@
+// i8.h -- internal interface between the C ABI of the 8-bit integer operators
+// (i8.cpp) and their gfx950 kernels (i8_gemm.hip, i8_quant.hip).  Not
+// installed; callers use include/dbs.h.
+#pragma once
+
+#include <hip/hip_runtime.h>
+#include <stdint.h>
+
+namespace dbs {
+
+// Products of codes, summed as 32-bit integers, times a scale per row of X and one per row
+// of W.  Dense: offsets and rows null, E = 1, T = M.  Otherwise group g
+// owns rows offsets[g] .. offsets[g+1]-1 of the sorted order, as in MoeGemm.
+struct I8Gemm {
+    const uint8_t *X;         // T x K codes (gathered through rows) or M x K
+    const uint8_t *W;         // E x N x K codes
+    const float *sX;          // T
+    const float *sW;          // E x N
+    uint8_t *D;               // M x ncols, bf16 or fp32
+    const int32_t *offsets;   // E + 1, or null
+    const int32_t *rows;      // M, or null
+    int64_t T;                // rows of X
+    int M, E, N, K;
+    int ncols;                // columns of D: N, or N / 2 behind the gate
+    int gate;                 // 1: D = silu(first N/2 columns) * last N/2 columns
+    int f32;                  // 1: D holds fp32 (without the gate)
+    int vec;                  // 1 if D rows take 16-byte stores
+};
+
+// rows: 64, 128 or 256 per output tile
+hipError_t launch_i8_tiles(const I8Gemm &p, int rows, int cus, hipStream_t stream);
+
+// Row scales and codes of x (M x K, fp32 or bf16).
+hipError_t launch_quant_i8(const void *x, int bf16, int64_t M, int64_t K, int8_t *codes, float *scales,
+                           hipStream_t stream);
+
+}  // namespace dbs

@@ -155,6 +155,26 @@ dbs_status check_route(dbs_real type, const void *logits, int64_t T, int64_t E, 
     return DBS_OK;
 }
 
+dbs_status check_route_outputs(int64_t T, int64_t E, const int32_t *experts, const float *weights, const int32_t *offsets,
+                               const int32_t *rows, const int32_t *slots, const void *workspace, size_t workspace_bytes)
+{
+    if (!experts || !weights || !offsets || !rows || !slots) return fail(DBS_EINVAL, "null pointer argument");
+    if (!aligned(experts, 4) || !aligned(weights, 4) || !aligned(offsets, 4) || !aligned(rows, 4) || !aligned(slots, 4))
+        return fail(DBS_EINVAL, "misaligned output");
+    const int64_t need = dbs::moe_route_workspace_bytes(T, E);
+    if (need > 0 && (!workspace || !aligned(workspace, 4) || workspace_bytes < (size_t)need))
+        return fail(DBS_EINVAL, "workspace missing, misaligned or too small");
+    return DBS_OK;
+}
+
+dbs_status check_score(dbs_score score, int renormalize, float scale)
+{
+    if (score != DBS_SOFTMAX && score != DBS_SIGMOID) return fail(DBS_EINVAL, "unknown score");
+    if (renormalize != 0 && renormalize != 1) return fail(DBS_EINVAL, "renormalize must be 0 or 1");
+    if (!std::isfinite(scale)) return fail(DBS_EINVAL, "scale must be finite");
+    return DBS_OK;
+}
+
 dbs_status check_rows(int64_t rows, int64_t width)
 {
     if (rows <= 0 || width <= 0) return fail(DBS_EINVAL, "sizes must be positive");
@@ -178,13 +198,9 @@ dbs_status moe_route(dbs_real type, const void *logits, int64_t T, int64_t E, in
 {
     dbs_status st = check_route(type, logits, T, E, k);
     if (st != DBS_OK) return st;
-    if (!experts || !weights || !offsets || !rows || !slots) return fail(DBS_EINVAL, "null pointer argument");
-    if (!aligned(experts, 4) || !aligned(weights, 4) || !aligned(offsets, 4) || !aligned(rows, 4) || !aligned(slots, 4))
-        return fail(DBS_EINVAL, "misaligned output");
     if (renormalize != 0 && renormalize != 1) return fail(DBS_EINVAL, "renormalize must be 0 or 1");
-    const int64_t need = dbs::moe_route_workspace_bytes(T, E);
-    if (need > 0 && (!workspace || !aligned(workspace, 4) || workspace_bytes < (size_t)need))
-        return fail(DBS_EINVAL, "workspace missing, misaligned or too small");
+    if ((st = check_route_outputs(T, E, experts, weights, offsets, rows, slots, workspace, workspace_bytes)) != DBS_OK)
+        return st;
     dbs::MoeRoute p{logits, type == DBS_BF16, T, (int)E, (int)k, renormalize, experts, weights, offsets, rows, slots,
                     static_cast<int32_t *>(workspace)};
     return done(dbs::launch_moe_route(p, stream));
@@ -199,8 +215,52 @@ dbs_status moe_route_bwd(dbs_real type, const void *logits, int64_t T, int64_t E
     if (!aligned(experts, 4) || !aligned(dweights, 4) || !aligned(dlogits, type == DBS_F32 ? 4 : 2))
         return fail(DBS_EINVAL, "misaligned array");
     if (renormalize != 0 && renormalize != 1) return fail(DBS_EINVAL, "renormalize must be 0 or 1");
-    return done(dbs::launch_moe_route_bwd(logits, type == DBS_BF16, T, (int)E, (int)k, renormalize, experts, dweights,
+    return done(dbs::launch_moe_route_bwd(logits, type == DBS_BF16, T, (int)E, (int)k, 0, renormalize, 1.0f, experts, dweights,
                                           dlogits, stream));
+}
+
+dbs_status moe_route_grouped(dbs_real type, const void *logits, const float *bias, int64_t T, int64_t E, int64_t k,
+                             dbs_score score, int64_t groups, int64_t kept_groups, int64_t group_best, int renormalize,
+                             float scale, int32_t *experts, float *weights, int32_t *offsets, int32_t *rows,
+                             int32_t *slots, void *workspace, size_t workspace_bytes, hipStream_t stream)
+{
+    dbs_status st = check_route(type, logits, T, E, k);
+    if (st != DBS_OK) return st;
+    if ((st = check_score(score, renormalize, scale)) != DBS_OK) return st;
+    if (groups <= 0 || groups > E || E % groups) return fail(DBS_EINVAL, "groups must divide the number of experts");
+    if (kept_groups <= 0 || kept_groups > groups) return fail(DBS_EINVAL, "kept_groups outside 1 .. groups");
+    if (group_best != 1 && group_best != 2) return fail(DBS_EINVAL, "group_best must be 1 or 2");
+    if (k > kept_groups * (E / groups)) return fail(DBS_EINVAL, "k above the number of experts in the kept groups");
+    if (groups > dbs::kMoeMaxGroups) return fail(DBS_EUNSUPPORTED, "more than 16 groups");
+    if (dbs::moe_route_grouped_lane(E, groups, true) > dbs::kMoeLaneExperts)
+        return fail(DBS_EUNSUPPORTED, "groups too large: more than 64 experts of one to a lane");
+    if ((st = check_route_outputs(T, E, experts, weights, offsets, rows, slots, workspace, workspace_bytes)) != DBS_OK)
+        return st;
+    if (!aligned(bias, 4)) return fail(DBS_EINVAL, "misaligned bias");
+    dbs::MoeRouteGrouped g{};
+    g.r = dbs::MoeRoute{logits, type == DBS_BF16, T, (int)E, (int)k, renormalize, experts, weights, offsets, rows, slots,
+                        static_cast<int32_t *>(workspace)};
+    g.bias = bias;
+    g.sigmoid = score == DBS_SIGMOID;
+    g.groups = (int)groups;
+    g.kept = (int)kept_groups;
+    g.best = (int)group_best;
+    g.scale = scale;
+    return done(dbs::launch_moe_route_grouped(g, stream));
+}
+
+dbs_status moe_route_grouped_bwd(dbs_real type, const void *logits, int64_t T, int64_t E, int64_t k, dbs_score score,
+                                 int renormalize, float scale, const int32_t *experts, const float *dweights,
+                                 void *dlogits, hipStream_t stream)
+{
+    dbs_status st = check_route(type, logits, T, E, k);
+    if (st != DBS_OK) return st;
+    if ((st = check_score(score, renormalize, scale)) != DBS_OK) return st;
+    if (!experts || !dweights || !dlogits) return fail(DBS_EINVAL, "null pointer argument");
+    if (!aligned(experts, 4) || !aligned(dweights, 4) || !aligned(dlogits, type == DBS_F32 ? 4 : 2))
+        return fail(DBS_EINVAL, "misaligned array");
+    return done(dbs::launch_moe_route_bwd(logits, type == DBS_BF16, T, (int)E, (int)k, score == DBS_SIGMOID, renormalize,
+                                          scale, experts, dweights, dlogits, stream));
 }
 
 dbs_status gemm_moe_bf16(const void *X, const void *W, void *D, const int32_t *offsets, const int32_t *rows,

@@ -79,7 +79,23 @@ struct MoeRoute {
 };
 int64_t moe_route_workspace_bytes(int64_t T, int64_t E);
 hipError_t launch_moe_route(const MoeRoute &p, hipStream_t stream);
-hipError_t launch_moe_route_bwd(const void *logits, int bf16, int64_t T, int E, int k, int renorm,
+
+// The choice by groups: scores from sigmoid or softmax, the best `kept` of
+// `groups` groups by the sum of their `best` (1 or 2) largest scores.
+struct MoeRouteGrouped {
+    MoeRoute r;
+    const float *bias;        // E, or null
+    int sigmoid, groups, kept, best;
+    float scale;              // of the weights
+    int lanes, q;             // set by the launcher: lanes of a token per group, experts per lane
+};
+constexpr int kMoeMaxGroups = 16;        // a lane of a 16-lane token group each
+constexpr int kMoeLaneExperts = 64;
+int moe_route_grouped_lane(int64_t E, int64_t groups, bool fours);
+hipError_t launch_moe_route_grouped(MoeRouteGrouped p, hipStream_t stream);
+
+// factor: multiplies the weights' gradients
+hipError_t launch_moe_route_bwd(const void *logits, int bf16, int64_t T, int E, int k, int sigmoid, int renorm, float factor,
                                 const int32_t *experts, const float *dweights, void *dlogits, hipStream_t stream);
 
 hipError_t launch_swiglu(const void *H, void *A, int64_t M, int64_t F, hipStream_t stream);

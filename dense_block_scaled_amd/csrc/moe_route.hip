@@ -249,6 +249,291 @@ __global__ __launch_bounds__((select_threads<VPL, ONE>())) void route_select(Moe
     }
 }
 
+// ------------------------------------------------------- selection by groups
+//
+//     s_e = sigmoid(logits[t, e])  or  softmax(logits[t, :])_e
+//     c_e = s_e + bias_e                     what the choice goes by
+//     group's score                          the sum of its best one or two c
+//     experts[t, 0 .. k-1]                   the k largest c of the kept groups with the largest scores
+//     weights[t, j]                          scale s at those experts, or scale s / (the sum of s over them)
+//
+// Choices must not hang on a rounding: c is computed in fp64 (vector fp64 runs at
+// fp32's rate here).  The expert's index lies in the ten lowest bits of
+// its c, so keys differ, ties go to the lower index, and sorting needs no second
+// register: two instructions for every exchange of a lane's network.  Scores that
+// agree to 2^-42 count as equal.  After the sort a lane's best are its
+// first, groups' sums come from neighbouring lanes, and a choice is one maximum
+// over the 16 lanes' heads and one step of the winner's list, where
+// route_select goes through all of a lane's logits three times.
+//
+// Lanes.  The 16 lanes of a token are cut into as many runs as the groups'
+// count rounded up to a power of two, one run a group; a lane has Q experts in a
+// row (see launch_moe_route_grouped).
+
+template <int STEP>
+__device__ __forceinline__ double row_move64(double v)
+{
+    const uint64_t b = __builtin_bit_cast(uint64_t, v);
+    const uint32_t lo = row_move<STEP>((uint32_t)b), hi = row_move<STEP>((uint32_t)(b >> 32));
+    return __builtin_bit_cast(double, (uint64_t)hi << 32 | lo);
+}
+
+__device__ __forceinline__ double row_max64(double v)
+{
+    v = fmax(v, row_move64<0>(v));
+    v = fmax(v, row_move64<1>(v));
+    v = fmax(v, row_move64<2>(v));
+    return fmax(v, row_move64<3>(v));
+}
+
+__device__ __forceinline__ double row_sum64(double v)
+{
+    v += row_move64<0>(v);
+    v += row_move64<1>(v);
+    v += row_move64<2>(v);
+    return v + row_move64<3>(v);
+}
+
+// e^x for -708 <= x <= 708 to about 2^-46: x = n ln 2 + r with ln 2 as the sum of
+// two fp64 numbers, |r| <= 0.3466, and the exponential series to r^11 / 11! (the
+// next term is 6.4e-15)
+__device__ __forceinline__ double exp64(double x)
+{
+    const double n = __builtin_rint(x * 1.4426950408889634);
+    const double r = __builtin_fma(n, -2.3190468138462996e-17, __builtin_fma(n, -0.6931471805599453, x));
+    double p = 1.0 / 39916800;
+#pragma unroll
+    for (int i = 0; i < 11; ++i) {
+        constexpr double inv[11] = {1.0 / 3628800, 1.0 / 362880, 1.0 / 40320, 1.0 / 5040, 1.0 / 720, 1.0 / 120,
+                                    1.0 / 24,      1.0 / 6,      1.0 / 2,     1.0,        1.0};
+        p = __builtin_fma(p, r, inv[i]);
+    }
+    return __builtin_ldexp(p, (int)n);
+}
+
+// 1 / x, x a normal number: v_rcp_f64 and two Newton steps
+__device__ __forceinline__ double inverse64(double x)
+{
+    double y = __builtin_amdgcn_rcp(x);
+    y = __builtin_fma(__builtin_fma(-x, y, 1.0), y, y);
+    return __builtin_fma(__builtin_fma(-x, y, 1.0), y, y);
+}
+
+constexpr uint64_t kIndexBits = 1023;           // kMoeMaxExperts - 1
+
+// c with index e in its lowest bits: larger for a larger c, then for a lower e
+__device__ __forceinline__ double keyed(double c, int e)
+{
+    const uint64_t b = __builtin_bit_cast(uint64_t, c);
+    const uint32_t low = (uint32_t)((int64_t)b < 0 ? e : (int)kIndexBits - e);
+    return __builtin_bit_cast(double, (b & ~kIndexBits) | low);
+}
+
+__device__ __forceinline__ double unkeyed(double key)
+{
+    return __builtin_bit_cast(double, __builtin_bit_cast(uint64_t, key) & ~kIndexBits);
+}
+
+__device__ __forceinline__ int key_index(double key)
+{
+    const uint64_t b = __builtin_bit_cast(uint64_t, key);
+    const int low = (int)(b & kIndexBits);
+    return (int64_t)b < 0 ? low : (int)kIndexBits - low;
+}
+
+// Odd-even merge sort of v[0 .. N-1], descending
+template <int LO, int N, int R, int VPL>
+__device__ __forceinline__ void merge_sorted(double (&v)[VPL])
+{
+    auto order = [&](int a, int b) {
+        const double hi = fmax(v[a], v[b]), lo = fmin(v[a], v[b]);
+        v[a] = hi;
+        v[b] = lo;
+    };
+    if constexpr (2 * R < N) {
+        merge_sorted<LO, N, 2 * R>(v);
+        merge_sorted<LO + R, N, 2 * R>(v);
+#pragma unroll
+        for (int i = LO + R; i + R < LO + N; i += 2 * R) order(i, i + R);
+    } else {
+        order(LO, LO + R);
+    }
+}
+
+template <int LO, int N, int VPL>
+__device__ __forceinline__ void sort_down(double (&v)[VPL])
+{
+    if constexpr (N > 1) {
+        sort_down<LO, N / 2>(v);
+        sort_down<LO + N / 2, N / 2>(v);
+        merge_sorted<LO, N, 1>(v);
+    }
+}
+
+// The experts of a token, chosen by its 16 lanes (l: lane of the 16): lane j
+// returns the j-th choice (-1: none) and its weight.  VPL: keys a lane has
+// registers for (p.q used); C: as in load_logits.
+template <int VPL, int C, bool BF16>
+__device__ __forceinline__ void choose(const MoeRouteGrouped &p, int64_t tok, int l, int &expert, float &weight)
+{
+    typedef __attribute__((ext_vector_type(4))) float f32x4;
+    typedef __attribute__((ext_vector_type(2))) uint32_t u32x2;
+    const int per = p.r.E / p.groups, group = l / p.lanes, at0 = l % p.lanes * p.q;    // first of the lane's in its group
+    const int have = group < p.groups ? max(min(per - at0, p.q), 0) : 0, e0 = group * per + at0;
+    const float *logits32 = reinterpret_cast<const float *>(p.r.logits) + tok * p.r.E;
+    const uint16_t *logits16 = reinterpret_cast<const uint16_t *>(p.r.logits) + tok * p.r.E;
+    float x[VPL];
+#pragma unroll
+    for (int i = 0; i < VPL; i += C) {
+        float y[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+        if (i < have) {                          // (C = 4: have is a multiple of 4)
+            if constexpr (BF16 && C == 4) {
+                const u32x2 w = *reinterpret_cast<const u32x2 *>(logits16 + e0 + i);
+                y[0] = __builtin_bit_cast(float, w[0] << 16);
+                y[1] = __builtin_bit_cast(float, w[0] & 0xFFFF0000u);
+                y[2] = __builtin_bit_cast(float, w[1] << 16);
+                y[3] = __builtin_bit_cast(float, w[1] & 0xFFFF0000u);
+            } else if constexpr (BF16) {
+                y[0] = __builtin_bit_cast(float, (uint32_t)logits16[e0 + i] << 16);
+            } else if constexpr (C == 4) {
+                const f32x4 w = *reinterpret_cast<const f32x4 *>(logits32 + e0 + i);
+#pragma unroll
+                for (int c = 0; c < 4; ++c) y[c] = w[c];
+            } else {
+                y[0] = logits32[e0 + i];
+            }
+        }
+#pragma unroll
+        for (int c = 0; c < C; ++c) x[i + c] = open_logit(y[c]);
+    }
+    float top = 0.0f;
+    double whole = 1.0, v[VPL];
+    if (p.sigmoid) {
+#pragma unroll
+        for (int i = 0; i < VPL; ++i) v[i] = inverse64(1.0 + exp64((double)fminf(fmaxf(-x[i], -708.0f), 708.0f)));
+    } else {
+        top = x[0];
+#pragma unroll
+        for (int i = 1; i < VPL; ++i) top = fmaxf(top, x[i]);
+        top = row_max(top);
+        const float from = top > -INFINITY ? top : 0.0f;
+        whole = 0.0;
+#pragma unroll
+        for (int i = 0; i < VPL; ++i) {
+            // (the difference in fp64: it need not be an fp32 number)
+            const double d = fmax((double)x[i] - (double)from, -708.0);
+            v[i] = x[i] > -INFINITY ? exp64(d) : 0.0;
+            whole += v[i];
+        }
+        whole = row_sum64(whole);
+        const double inv = top > -INFINITY ? inverse64(whole) : 0.0;
+#pragma unroll
+        for (int i = 0; i < VPL; ++i) v[i] *= inv;
+    }
+#pragma unroll
+    for (int i = 0; i < VPL; ++i) {
+        float b = 0.0f;
+        if (p.bias && i < have) b = open_logit(p.bias[e0 + i]);
+        v[i] = x[i] > -INFINITY && b > -INFINITY ? keyed(v[i] + (double)b, e0 + i) : -(double)INFINITY;
+    }
+    sort_down<0, VPL>(v);
+
+    if (p.kept < p.groups) {
+        // the group's best two, from its lanes' best two
+        double one = v[0], two = v[1];
+        auto join = [&](double o1, double o2) {
+            two = fmax(fmin(one, o1), fmax(two, o2));
+            one = fmax(one, o1);
+        };
+        if (p.lanes > 1) join(row_move64<0>(one), row_move64<0>(two));
+        if (p.lanes > 2) join(row_move64<1>(one), row_move64<1>(two));
+        if (p.lanes > 4) join(row_move64<2>(one), row_move64<2>(two));
+        double score = -(double)INFINITY;
+        if (one > -(double)INFINITY) {
+            score = unkeyed(one);
+            if (p.best == 2 && two > -(double)INFINITY) score += unkeyed(two);
+            score = keyed(score, group);
+        }
+        bool keep = false;
+        for (int j = 0; j < p.kept; ++j) {
+            const double b = row_max64(score);
+            if (b == -(double)INFINITY) break;
+            const bool mine = score == b;
+            keep = keep || mine;
+            score = mine ? -(double)INFINITY : score;
+        }
+        v[0] = keep ? v[0] : -(double)INFINITY;
+    }
+
+    expert = -1;
+    for (int j = 0; j < p.r.k; ++j) {
+        const double b = row_max64(v[0]);
+        if (b == -(double)INFINITY) break;       // no open expert is left
+        expert = l == j ? key_index(b) : expert;
+        const bool mine = v[0] == b;
+#pragma unroll
+        for (int i = 0; i < (VPL < kMoeMaxK ? VPL : kMoeMaxK); ++i)
+            v[i] = mine ? (i + 1 < VPL ? v[i + 1] : -(double)INFINITY) : v[i];
+    }
+
+    // the weights, from the chosen logits: sigmoid(y) = e^min(y, 0) / (1 + e^-|y|), of which
+    // renormalising cancels the largest e^min(y, 0)
+    float y = -INFINITY;
+    if (expert >= 0) {
+        if constexpr (BF16) y = __builtin_bit_cast(float, (uint32_t)logits16[expert] << 16);
+        else y = logits32[expert];
+        y = open_logit(y);
+    }
+    float s = 0.0f, from = p.sigmoid ? 0.0f : top;
+    if (p.r.renorm) from = row_max(p.sigmoid ? fminf(y, 0.0f) : y);
+    if (expert >= 0) s = p.sigmoid ? expf(fminf(y, 0.0f) - from) / (1.0f + expf(-fabsf(y))) : expf(y - from);
+    const float total = p.r.renorm ? row_sum(s) : p.sigmoid ? 1.0f : (float)whole;
+    weight = expert >= 0 ? s / total * p.scale : 0.0f;
+}
+
+// As route_select, with the choice above.
+template <int VPL, bool ONE>
+constexpr int choose_threads() { return ONE ? 256 : VPL > 16 ? 512 : 1024; }
+
+template <int VPL, int C, bool BF16, bool ONE>
+__global__ __launch_bounds__((choose_threads<VPL, ONE>())) void route_choose(MoeRouteGrouped g)
+{
+    __shared__ uint64_t mask[kMoeMaxExperts];
+    __shared__ int32_t chosen[ONE ? kRouteTokens * kMoeMaxK : 1];
+    __shared__ int32_t base[ONE ? kMoeMaxExperts + 1 : 1];
+    __shared__ int32_t part[4];
+    constexpr int kThreads = choose_threads<VPL, ONE>();
+    const MoeRoute &p = g.r;
+    const int t = threadIdx.x, l = t & (kLanes - 1);
+    for (int e = t; e < p.E; e += kThreads) mask[e] = 0;
+    __syncthreads();
+    const int64_t t0 = (int64_t)blockIdx.x * kRouteTokens;
+    for (int tl = t / kLanes; tl < kRouteTokens; tl += kThreads / kLanes) {
+        const int64_t tok = t0 + tl;
+        if (tok >= p.T) break;                   // (uniform in the token's 16 lanes)
+        int e;
+        float w;
+        choose<VPL, C, BF16>(g, tok, l, e, w);
+        if (l < p.k) {
+            p.experts[tok * p.k + l] = e;
+            p.weights[tok * p.k + l] = w;
+            if (e >= 0) atomicOr(reinterpret_cast<unsigned long long *>(&mask[e]), 1ull << tl);
+            if constexpr (ONE) chosen[tl * p.k + l] = e;
+        }
+    }
+    __syncthreads();
+    if constexpr (ONE) {
+        for (int e = t; e < p.E; e += kThreads) base[e] = __popcll(mask[e]);
+        __syncthreads();
+        int32_t *b = base;
+        scan_experts(b, p.E, b, part);
+        for (int e = t; e <= p.E; e += kThreads) p.offsets[e] = base[e];
+        place(p, 0, 0, p.T * p.k, mask, base, nullptr, chosen);
+    } else {
+        for (int e = t; e < p.E; e += kThreads) p.counts[(int64_t)blockIdx.x * p.E + e] = __popcll(mask[e]);
+    }
+}
+
 // Exclusive sums down the columns of counts (nb rows of E), in place, and the
 // column totals behind them: 16 columns a workgroup, 64 segments of rows.
 __global__ __launch_bounds__(1024) void route_columns(int32_t *counts, int64_t nb, int E)
@@ -330,13 +615,13 @@ __global__ __launch_bounds__(kThreads) void route_place(MoeRoute p, int64_t nb)
 }
 
 // dlogits = p (u - sum p u): p the softmax over all experts, or over the
-// chosen ones (renorm), u the weights' gradients at the chosen experts and 0
+// chosen ones (renorm), u the weights' gradients (times `factor`) at the chosen experts and 0
 // elsewhere.  16 lanes a token, as in route_select; lane j has the j-th
 // choice, and the chosen experts' gradients reach the lanes that hold those
 // experts through a row of E floats in LDS (zeroed, written and read by the
 // token's own lanes of one wave, with a handover between).
 template <int VPL, int C, bool BF16>
-__global__ __launch_bounds__(kThreads) void route_bwd(const void *logits, int64_t T, int E, int k, int renorm,
+__global__ __launch_bounds__(kThreads) void route_bwd(const void *logits, int64_t T, int E, int k, int renorm, float factor,
                                                       const int32_t *experts, const float *dweights, void *dlogits)
 {
     // lane l's values lie together, C at a time: [token][i / C][l][i % C]
@@ -353,7 +638,7 @@ __global__ __launch_bounds__(kThreads) void route_bwd(const void *logits, int64_
         e = experts[tok * k + l];
         e = e < E ? e : -1;
         if (e >= 0) {
-            u = dweights[tok * k + l];
+            u = dweights[tok * k + l] * factor;
             const int64_t at = tok * E + e;
             if constexpr (BF16)
                 x = open_logit(__builtin_bit_cast(float, (uint32_t) reinterpret_cast<const uint16_t *>(logits)[at] << 16));
@@ -407,6 +692,74 @@ __global__ __launch_bounds__(kThreads) void route_bwd(const void *logits, int64_
     }
 }
 
+// The gradient through sigmoid scores, at the chosen experts alone:
+//
+//     renorm:  w_j (u_j - sum_i w_i u_i) (1 - s_j)      w the weights, of sum 1
+//     else:    u_j s_j (1 - s_j)
+//
+// with u the weights' gradients times `factor`.  Only the chosen logits are
+// read; a token's row of zeros and k values goes out through LDS.
+template <int VPL, int C, bool BF16>
+__global__ __launch_bounds__(kThreads) void route_sigmoid_bwd(const void *logits, int64_t T, int E, int k, int renorm,
+                                                              float factor, const int32_t *experts, const float *dweights,
+                                                              void *dlogits)
+{
+    __shared__ __attribute__((aligned(16))) float at_chosen[kThreads / kLanes][16 * VPL];
+    const int l = threadIdx.x & (kLanes - 1);
+    const int64_t tok = (int64_t)blockIdx.x * (kThreads / kLanes) + threadIdx.x / kLanes;
+    if (tok >= T) return;                        // (uniform in the token's 16 lanes)
+    float *row = at_chosen[threadIdx.x / kLanes];
+    int e = -1;
+    float u = 0.0f, x = -INFINITY;
+    if (l < k) {
+        e = experts[tok * k + l];
+        e = e < E ? e : -1;
+        if (e >= 0) {
+            u = dweights[tok * k + l] * factor;
+            const int64_t at = tok * E + e;
+            if constexpr (BF16)
+                x = open_logit(__builtin_bit_cast(float, (uint32_t) reinterpret_cast<const uint16_t *>(logits)[at] << 16));
+            else
+                x = open_logit(reinterpret_cast<const float *>(logits)[at]);
+        }
+    }
+#pragma unroll
+    for (int i = 0; i < VPL; ++i) row[expert_of<C>(i, l)] = 0.0f;
+    wave_handover();
+    // (1 - s = e^-x / (1 + e^-x); an expert closed since then has no gradient)
+    const bool open = x > -INFINITY;
+    const float low = expf(-fabsf(x)), half = 1.0f / (1.0f + low);
+    const float rest = x >= 0.0f ? low * half : half;
+    float d;
+    if (renorm) {
+        const float from = row_max(fminf(x, 0.0f));
+        const float s = open ? expf(fminf(x, 0.0f) - from) * half : 0.0f;
+        const float total = row_sum(s), w = open ? s / total : 0.0f;
+        d = w * (u - row_sum(w * u)) * rest;
+    } else {
+        d = u * (x >= 0.0f ? half : low * half) * rest;
+    }
+    if (e >= 0) row[e] = open ? d : 0.0f;
+    wave_handover();
+#pragma unroll
+    for (int i = 0; i < VPL; i += C) {
+        const int first = expert_of<C>(i, l);
+        if (first >= E) continue;
+        const int64_t at = tok * E + first;
+        if constexpr (BF16) {
+            __bf16 w[C];
+#pragma unroll
+            for (int c = 0; c < C; ++c) w[c] = (__bf16)row[first + c];
+            __builtin_memcpy(reinterpret_cast<__bf16 *>(dlogits) + at, w, sizeof(w));
+        } else {
+            float w[C];
+#pragma unroll
+            for (int c = 0; c < C; ++c) w[c] = row[first + c];
+            __builtin_memcpy(reinterpret_cast<float *>(dlogits) + at, w, sizeof(w));
+        }
+    }
+}
+
 // F(VPL, C) for the smallest number of logits per lane that holds E experts;
 // C = 4 if every row starts on a whole load and ends with one.
 template <class F>
@@ -436,6 +789,20 @@ int64_t moe_route_workspace_bytes(int64_t T, int64_t E)
     return T <= kRouteTokens ? 0 : (blocks_of(T) + 1) * E * (int64_t)sizeof(int32_t);
 }
 
+// The order of the pairs behind the selecting kernel's counts.
+static hipError_t launch_place(const MoeRoute &p, int64_t nb, hipStream_t stream)
+{
+    if (nb <= kDirect) {
+        hipLaunchKernelGGL((route_place<true>), dim3(nb), dim3(kThreads), 0, stream, p, nb);
+        return hipGetLastError();
+    }
+    hipLaunchKernelGGL(route_columns, dim3((p.E + 15) / 16), dim3(1024), 0, stream, p.counts, nb, p.E);
+    hipError_t e = hipGetLastError();
+    if (e != hipSuccess) return e;
+    hipLaunchKernelGGL((route_place<false>), dim3(nb), dim3(kThreads), 0, stream, p, nb);
+    return hipGetLastError();
+}
+
 hipError_t launch_moe_route(const MoeRoute &p, hipStream_t stream)
 {
     const int64_t nb = blocks_of(p.T);
@@ -452,29 +819,67 @@ hipError_t launch_moe_route(const MoeRoute &p, hipStream_t stream)
         return hipGetLastError();
     });
     if (e != hipSuccess || one) return e;
-    if (nb <= kDirect) {
-        hipLaunchKernelGGL((route_place<true>), dim3(nb), dim3(kThreads), 0, stream, p, nb);
-        return hipGetLastError();
-    }
-    hipLaunchKernelGGL(route_columns, dim3((p.E + 15) / 16), dim3(1024), 0, stream, p.counts, nb, p.E);
-    if ((e = hipGetLastError()) != hipSuccess) return e;
-    hipLaunchKernelGGL((route_place<false>), dim3(nb), dim3(kThreads), 0, stream, p, nb);
-    return hipGetLastError();
+    return launch_place(p, nb, stream);
 }
 
-hipError_t launch_moe_route_bwd(const void *logits, int bf16, int64_t T, int E, int k, int renorm,
+// A lane's experts: at most 64 of a group's, in whole loads of four where every
+// group's logits are whole ones.
+int moe_route_grouped_lane(int64_t E, int64_t groups, bool fours)
+{
+    int runs = 1;
+    while (runs < groups) runs *= 2;
+    const int64_t lanes = kLanes / runs, per = E / groups;
+    int64_t q = (per + lanes - 1) / lanes;
+    if (fours) q = (q + 3) / 4 * 4;
+    return (int)q;
+}
+
+hipError_t launch_moe_route_grouped(MoeRouteGrouped g, hipStream_t stream)
+{
+    const MoeRoute &p = g.r;
+    const int64_t nb = blocks_of(p.T);
+    const bool one = p.T <= kRouteTokens;
+    const bool fours = p.E / g.groups % 4 == 0 && (reinterpret_cast<uintptr_t>(p.logits) & 15) == 0;
+    int runs = 1;
+    while (runs < g.groups) runs *= 2;
+    g.lanes = kLanes / runs;
+    g.q = moe_route_grouped_lane(p.E, g.groups, fours);
+    auto go = [&](auto vpl, auto c, auto bf16, auto whole) {
+        constexpr int V = decltype(vpl)::value, C = decltype(c)::value;
+        constexpr bool B = decltype(bf16)::value, ONE = decltype(whole)::value;
+        hipLaunchKernelGGL((route_choose<V, C, B, ONE>), dim3(ONE ? 1 : nb), dim3(choose_threads<V, ONE>()), 0, stream, g);
+        return hipGetLastError();
+    };
+    auto by_type = [&](auto vpl, auto c) {
+        if (one) return p.bf16 ? go(vpl, c, std::true_type{}, std::true_type{}) : go(vpl, c, std::false_type{}, std::true_type{});
+        return p.bf16 ? go(vpl, c, std::true_type{}, std::false_type{}) : go(vpl, c, std::false_type{}, std::false_type{});
+    };
+    auto by_load = [&](auto vpl) {
+        return fours ? by_type(vpl, std::integral_constant<int, 4>{}) : by_type(vpl, std::integral_constant<int, 1>{});
+    };
+    hipError_t e;
+    if (g.q <= 4) e = by_load(std::integral_constant<int, 4>{});
+    else if (g.q <= 8) e = by_load(std::integral_constant<int, 8>{});
+    else if (g.q <= 16) e = by_load(std::integral_constant<int, 16>{});
+    else if (g.q <= 32) e = by_load(std::integral_constant<int, 32>{});
+    else e = by_load(std::integral_constant<int, 64>{});
+    if (e != hipSuccess || one) return e;
+    return launch_place(p, nb, stream);
+}
+
+hipError_t launch_moe_route_bwd(const void *logits, int bf16, int64_t T, int E, int k, int sigmoid, int renorm, float factor,
                                 const int32_t *experts, const float *dweights, void *dlogits, hipStream_t stream)
 {
     const dim3 grid((T + kThreads / kLanes - 1) / (kThreads / kLanes));
     return by_experts(E, logits, dlogits, [&](auto vpl, auto c) {
         constexpr int V = decltype(vpl)::value, C = decltype(c)::value;
-        if (bf16)
-            hipLaunchKernelGGL((route_bwd<V, C, true>), grid, dim3(kThreads), 0, stream, logits, T, E, k, renorm,
-                               experts, dweights, dlogits);
-        else
-            hipLaunchKernelGGL((route_bwd<V, C, false>), grid, dim3(kThreads), 0, stream, logits, T, E, k, renorm,
-                               experts, dweights, dlogits);
-        return hipGetLastError();
+        auto go = [&](auto *kernel) {
+            hipLaunchKernelGGL(kernel, grid, dim3(kThreads), 0, stream, logits, T, E, k, renorm, factor, experts, dweights,
+                               dlogits);
+            return hipGetLastError();
+        };
+        if (sigmoid) return bf16 ? go(&route_sigmoid_bwd<V, C, true>) : go(&route_sigmoid_bwd<V, C, false>);
+        return bf16 ? go(&route_bwd<V, C, true>) : go(&route_bwd<V, C, false>);
     });
 }
 

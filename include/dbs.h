@@ -383,6 +383,44 @@ dbs_status moe_route(dbs_real type, const void *logits, int64_t T, int64_t E, in
                      void *workspace, size_t workspace_bytes, hipStream_t stream);
 dbs_status moe_route_bwd(dbs_real type, const void *logits, int64_t T, int64_t E, int64_t k, int renormalize,
                          const int32_t *experts, const float *dweights, void *dlogits, hipStream_t stream);
+
+/*
+ * The router by groups of experts.  From the logits come scores s (DBS_SOFTMAX:
+ * over all E logits; DBS_SIGMOID: of each by itself) and c = s + bias (E fp32
+ * values; null: none), which only the choice goes by.  The experts are cut
+ * into `groups` runs of E / groups; a group's score is the sum of its
+ * group_best (1 or 2) largest c; among the experts of the kept_groups best groups
+ * the k with the largest c are chosen.  (kept_groups = groups: no limit by
+ * groups.)  weights = scale s, or, with renormalize = 1, scale s / (the sum of
+ * s over the chosen ones).
+ *
+ * Closed experts are moe_route's (a logit of -inf or NaN); a bias of -inf or NaN
+ * closes its expert to every token, +inf counts as the largest finite value.  A
+ * closed expert adds nothing to its group; a group with none open is not kept.
+ * c is computed in fp64; values that agree to 2^-42 of their size are
+ * ties, which go to the lower expert (group).  Outputs and workspace
+ * (moe_route_workspace) are moe_route's.  At most 16 groups, and at most 64
+ * experts of a group to each of the 16 / (groups rounded up to a power of two)
+ * lanes that a token has for it (DBS_EUNSUPPORTED; any E up to 512).
+ * moe_route_grouped_bwd: dlogits from the weights' gradients, with the experts
+ * that moe_route_grouped chose (no expert twice in a token): moe_route_bwd's for
+ * softmax scores; for sigmoid ones, w the weights over scale and u = scale
+ * dweights, w (u - sum w u) (1 - s) renormalised and u s (1 - s) otherwise, 0 at the
+ * experts that are not chosen.  The bias has no gradient.
+ */
+typedef enum {
+    DBS_SOFTMAX = 0,
+    DBS_SIGMOID = 1
+} dbs_score;
+
+dbs_status moe_route_grouped(dbs_real type, const void *logits, const float *bias, int64_t T, int64_t E, int64_t k,
+                             dbs_score score, int64_t groups, int64_t kept_groups, int64_t group_best, int renormalize,
+                             float scale, int32_t *experts, float *weights, int32_t *offsets, int32_t *rows,
+                             int32_t *slots, void *workspace, size_t workspace_bytes, hipStream_t stream);
+dbs_status moe_route_grouped_bwd(dbs_real type, const void *logits, int64_t T, int64_t E, int64_t k, dbs_score score,
+                                 int renormalize, float scale, const int32_t *experts, const float *dweights,
+                                 void *dlogits, hipStream_t stream);
+
 dbs_status gemm_moe_bf16(const void *X, const void *W, void *D, const int32_t *offsets, const int32_t *rows,
                          int64_t T, int64_t M, int64_t E, int64_t N, int64_t K, dbs_layout lw, hipStream_t stream);
 dbs_status gemm_moe_swiglu_bf16(const void *X, const void *W, void *D, const int32_t *offsets, const int32_t *rows,
@@ -397,6 +435,41 @@ dbs_status moe_combine_bf16(const void *Y, const int32_t *slots, const float *we
 dbs_status moe_combine_bwd_bf16(const void *dO, const void *Y, const int32_t *slots, const float *weights,
                                 const int32_t *offsets, int64_t E, void *dY, float *dweights, int64_t T, int64_t k,
                                 int64_t H, hipStream_t stream);
+
+/*
+ * Products in 8-bit integers, with a scale for each row of both operands (for
+ * each token and channel).  Codes are int8, rows of K contiguous, 16-byte
+ * aligned; scales fp32; K a multiple of 16, at most 131056, so that sums of
+ * products of any codes are exact in 32 bits.
+ *
+ * quant_i8: a row x (fp32 or bf16, M x K, any K) becomes scales[m] = amax / 127 and
+ *   codes[m] = the whole numbers nearest to 127 x / amax (ties to even), amax the
+ *   row's largest magnitude.  A row of zeros has scale 0; a row with an infinity
+ *   or a NaN has scale NaN and codes 0, which makes its products NaN.
+ *   codes need no alignment (8 bytes, with K a multiple of 8 and x on 16 bytes,
+ *   for the faster form).
+ * gemm_i8: D[m, n] = sA[m] sB[n] sum_k A[m, k] B[n, k]: A M x K, B N x K, D M x N of
+ *   `type` (aligned to it).
+ * gemm_moe_i8, gemm_moe_swiglu_i8: gemm_moe_bf16 (K-major) and
+ *   gemm_moe_swiglu_bf16 on codes X (T x K) with scales sX (T) and W (E x N x K; E x
+ *   2F x K) with scales sW (E x N; E x 2F): offsets, rows, clamping and zero rows as
+ *   there; D bf16, 2-byte aligned.
+ *
+ * A sum becomes fp32 (rounded above 2^24), then times the row's scale, then times the
+ * column's; the gate is fp32; a bf16 result is rounded once more.  Limits: N at
+ * most 2^21 (F 2^20), at most 2^25 rows, an expert's gate and up matrices below 2 GiB
+ * together, a gathered X below 4 GiB - 16 MiB, and (M / 64 + E) (columns of D / 32)
+ * below 2^30 (DBS_EUNSUPPORTED).  Outputs must not alias inputs.
+ */
+dbs_status quant_i8(dbs_real type, const void *x, int64_t M, int64_t K, int8_t *codes, float *scales,
+                    hipStream_t stream);
+dbs_status gemm_i8(dbs_real type, const void *A, const float *sA, const void *B, const float *sB, void *D, int64_t M,
+                   int64_t N, int64_t K, hipStream_t stream);
+dbs_status gemm_moe_i8(const void *X, const float *sX, const void *W, const float *sW, void *D, const int32_t *offsets,
+                       const int32_t *rows, int64_t T, int64_t M, int64_t E, int64_t N, int64_t K, hipStream_t stream);
+dbs_status gemm_moe_swiglu_i8(const void *X, const float *sX, const void *W, const float *sW, void *D,
+                              const int32_t *offsets, const int32_t *rows, int64_t T, int64_t M, int64_t E, int64_t F,
+                              int64_t K, hipStream_t stream);
 
 /* Static text for a status code. */
 const char *dbs_status_str(dbs_status st);
