@@ -4,11 +4,84 @@
 
 #include <hip/hip_runtime.h>
 
+#include <algorithm>
+#include <cmath>
 #include <cstdio>
 
 #include "dbs.h"
 #include "launch.h"
 #include "moe.h"
+
+namespace dbs {
+
+// The tile with the least estimated time, in us: a first round of tiles over the
+// CUs (the walk along K, `k` times 1024 long, behind the way into the kernel and
+// out of it), further rounds at what a busy machine takes, or the reading of W at
+// 5.5 TB/s where that is more.  Groups (E > 1) are known on the device only: M / E rows of
+// each, half a tile of each is waste, some may have none; tiles then even out,
+// and rounds are counted in parts.  us of the dense product with tiles of 16 x 16 /
+// 64 x 16 / 64 x 32 / 64 x 64 / 128 x 128 / 128 x 256 / 256 x 256:
+//
+//      1 x 4096 x 4096     5.0   7.5   8.9  10.6    23    35    38
+//     16 x 8192 x 4096    10.2  12.4   9.5  11.0
+//     48 x 4096 x 4096    17.8   8.0   9.3  11.0
+//    128 x 8192 x 4096      63    22  15.7  11.9    24    36    39
+//    512 x 8192 x 1024     113    42    26  16.5  11.8  15.0  19.5
+//   1024 x 4096 x 4096                  54    36    25    35    46
+//   2048 x 4096 x 4096                  94    66    46    41    47
+//   4096 x 4096 x 4096                 180   127    85    75    57
+//
+// and of 64 .. 8191 rows each to 4 of 32 experts of 2056 x 4096, with the last four, 57 / 71 /
+// 63 / 67 for 64 rows, 77 / 75 / 73 / 77 for 512, 110 / 95 / 85 / 83 for 1024, 563 / 401 / 361 / 282
+// for 8191.
+I8Tile i8_tile(int64_t M, int64_t E, int64_t N, int64_t ncols, int64_t K, bool gate, int cus)
+{
+    const double k = K / 1024.0, n = cus;
+    const int64_t likely = (2 * M * E + 2 * M + E - 1) / (2 * M + E), met = E == 1 ? 1 : std::min(M, likely);
+    auto tiles = [&](int64_t tm, int64_t tn) {
+        const int64_t rows = E == 1 ? (M + tm - 1) / tm : std::max(M / tm + met / 2, met);
+        const int64_t wide = gate ? tn / 2 : tn;
+        return double(rows * ((ncols + wide - 1) / wide));
+    };
+    auto more = [&](double x) { return E == 1 ? std::max(std::ceil(x) - 1, 0.0) : std::max(x - 1, 0.0); };
+    const double w = 4 + double(met) * N * K / 5.5e6;
+    I8Tile best{64, 64};
+    double least = 1e30;
+    auto offer = [&](int rows, int cols, double t) {
+        t = std::max(t, w) + 0.2 * t;
+        if (t < least) {
+            least = t;
+            best = I8Tile{rows, cols};
+        }
+    };
+    {
+        // (not for more than the two tiles that a CU works on together)
+        const double x = tiles(16, gate ? 32 : 16) / n, m = std::min(double(M) / met, 16.0) / 16, c = gate ? 1.6 : 1.0;
+        if (x <= 2) offer(16, 16, 3.6 + c * k * (x <= 1 ? 0.36 + 0.37 * m : 0.95 + 0.7 * m));
+    }
+    auto deep = [&](int cols, double first, double next) {
+        const double x = tiles(64, cols) / n;
+        offer(64, cols, 5.2 + first * k + more(x) * (1.9 + next * k));
+    };
+    if (!gate) deep(16, 0.6, 0.75);
+    deep(32, 0.95, 1.05);
+    deep(64, 1.42, 1.55);
+    double x = tiles(128, 128) / n;
+    offer(128, 128, 7 + 3.9 * k + more(x) * (3.2 + 4.4 * k));
+    x = tiles(128, 256) / n;
+    offer(128, 256, 7 + (7 + 1.3 * std::min(x, 1.0)) * k + more(x) * (4 + 7.9 * k));
+    x = tiles(256, 256) / n;
+    offer(256, 256, 10 + (8.6 + 3.1 * std::min(x, 1.0)) * k + more(x) * (7 + 12.2 * k));
+    return best;
+}
+
+}  // namespace dbs
+
+extern "C" int dbs_i8_tile(int64_t M, int64_t E, int64_t N, int64_t K, int gate, int cus)
+{
+    const dbs::I8Tile t = dbs::i8_tile(M, E, N, gate ? N / 2 : N, K, gate, cus);
+    return 1000 * t.rows + t.cols;
+}
 
 namespace {
 
@@ -70,15 +143,15 @@ dbs::I8Gemm product(const void *X, const float *sX, const void *W, const float *
 
 dbs_status run_product(dbs::I8Gemm p, hipStream_t stream)
 {
-    // the kernels number their tiles (64 x 32 the smallest) in int, with a round of workgroups to spare
+    // the kernels number their tiles in int, with a round of workgroups to spare (smaller ones than 64 x 32 only
+    // where there are few)
     if (((int64_t)p.M / 64 + p.E) * (((int64_t)p.ncols + 31) / 32) >= kMostTiles)
         return fail(DBS_EUNSUPPORTED, "too many output tiles");
     int cus = 0;
     const int st = dbs::device_compute_units(&cus);
     if (st != DBS_OK) return (dbs_status)st;
     p.vec = p.ncols % (p.f32 ? 4 : 8) == 0 && aligned(p.D, 16);
-    const int height = dbs::moe_tile_rows(p.M, p.E, p.N, p.ncols, false, p.gate, cus);
-    return done(dbs::launch_i8_tiles(p, height, cus, stream));
+    return done(dbs::launch_i8_tiles(p, dbs::i8_tile(p.M, p.E, p.N, p.ncols, p.K, p.gate, cus), cus, stream));
 }
 
 // What the experts' products check beyond check_product.

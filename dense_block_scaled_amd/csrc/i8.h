@@ -27,11 +27,21 @@ struct I8Gemm {
     int vec;                  // 1 if D rows take 16-byte stores
 };
 
-// rows: 64, 128 or 256 per output tile
-hipError_t launch_i8_tiles(const I8Gemm &p, int rows, int cus, hipStream_t stream);
+// An output tile: 16 rows by 16 columns; 64 by the columns of 64, 32 or (without
+// the gate) 16 rows of W; 128 by those of 128; 128 or 256 by those of 256.
+struct I8Tile {
+    int rows, cols;
+};
+// The tile for M rows over E groups on `cus` compute units (the rule and what it
+// rests on: i8.cpp)
+I8Tile i8_tile(int64_t M, int64_t E, int64_t N, int64_t ncols, int64_t K, bool gate, int cus);
+hipError_t launch_i8_tiles(const I8Gemm &p, I8Tile tile, int cus, hipStream_t stream);
 
 // Row scales and codes of x (M x K, fp32 or bf16).
 hipError_t launch_quant_i8(const void *x, int bf16, int64_t M, int64_t K, int8_t *codes, float *scales,
                            hipStream_t stream);
 
 }  // namespace dbs
+
+// For the tests that say which kernel a size reaches (not in include/dbs.h): 1000 rows + cols of the tile
+extern "C" int dbs_i8_tile(int64_t M, int64_t E, int64_t N, int64_t K, int gate, int cus);

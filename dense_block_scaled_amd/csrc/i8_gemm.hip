@@ -64,6 +64,18 @@ __device__ __forceinline__ void zero_rows(const I8Gemm &p, int64_t from, int64_t
         for (int64_t o = me * 2; o < bytes; o += all * 2) *reinterpret_cast<uint16_t *>(z + o) = 0;
 }
 
+// The workgroups that the tiles are spread over: no more than there are tiles,
+// by eights, so that every XCD has its share of few (a grid is sized before the
+// groups are known; 256 tiles by a grid of 512 kept to four XCDs: 11 us, not 7).
+__device__ __forceinline__ int spread(int ntiles) { return min((int)gridDim.x, (ntiles + 7) & ~7); }
+
+// As first_tile, over n workgroups; those behind them have no tile
+__device__ __forceinline__ int first_of(int n, int ntiles)
+{
+    const int wg = blockIdx.x;
+    return wg >= n ? ntiles : (n & 7) == 0 ? (wg & 7) * (n >> 3) + (wg >> 3) : wg;
+}
+
 // Four consecutive columns n .. n + 3 of a row as the type of D, at byte offset
 // `at` (of column n) behind rd; columns past ncols are dropped.
 template <bool F32>
@@ -94,34 +106,56 @@ __device__ __forceinline__ void store_four(__amdgpu_buffer_rsrc_t rd, const floa
 }
 
 // 16 rows r0 .. (up to mend) and 32 columns n0 .. of results, value(v, q): the
-// lane's row l % 16, columns 16 v + 4 (l / 16) + q.  bf16 rows that take
-// 16-byte stores go through the wave's 1 KiB buffer (see store_block).
+// lane's row l % 16, columns 16 v + 4 (l / 16) + q.  They go through the wave's
+// 1 KiB buffer, 64 bytes of each row at a time (32 bf16, 16 fp32), so that a store
+// takes whole pieces of 16 bytes, or neighbouring lanes write neighbouring columns
+// (2047 x 4102 fp32 results, whose rows do not start on 16 bytes, element by
+// element from the lanes that have them: 68 us where 2048 x 4096 take 48).
 template <bool F32, class VALUE>
 __device__ __forceinline__ void store_rows(uint8_t *buf, const I8Gemm &p, int r0, int mend, int n0, Lane c, VALUE &&value)
 {
-    constexpr int SZ = F32 ? 4 : 2;
+    constexpr int SZ = F32 ? 4 : 2, kCols = 64 / SZ;
     asm volatile("" : "+v"(c.lane));
     const int left = __builtin_amdgcn_readfirstlane(max(0, min(16, mend - r0)));
     const __amdgpu_buffer_rsrc_t rd = make_rsrc(p.D + (int64_t)r0 * p.ncols * SZ, (uint32_t)left * (uint32_t)p.ncols * (uint32_t)SZ);
-    const int row = c.lane & 15, col0 = 4 * (c.lane >> 4);
-    if (!F32 && p.vec) {
-        wave_handover();                     // (the rows before have been read)
+    const int row = c.lane & 15, g = c.lane >> 4;
 #pragma unroll
-        for (int v = 0; v < 2; ++v) {
-            const int col = 16 * v + col0;
-            *reinterpret_cast<u32x2 *>(buf + row * 64 + (((col >> 3) ^ ((row >> 1) & 3)) << 4) + 2 * (col & 4)) =
-                u32x2{pack_bf16(value(v, 0), value(v, 1)), pack_bf16(value(v, 2), value(v, 3))};
+    for (int h = 0; h < (F32 ? 2 : 1); ++h) {
+        const int nh = n0 + 16 * h;
+        if (F32 && p.vec) {
+            const float w[4] = {value(h, 0), value(h, 1), value(h, 2), value(h, 3)};
+            store_four<true>(rd, w, nh + 4 * g, p.ncols, (uint32_t)(row * p.ncols + nh + 4 * g) * 4u, 1);
+            continue;
+        }
+        wave_handover();                     // (the rows before have been read)
+        if constexpr (F32) {
+            *reinterpret_cast<f32x4 *>(buf + row * 64 + ((g ^ ((row >> 1) & 3)) << 4)) =
+                f32x4{value(h, 0), value(h, 1), value(h, 2), value(h, 3)};
+        } else {
+#pragma unroll
+            for (int v = 0; v < 2; ++v) {
+                const int col = 16 * v + 4 * g;
+                *reinterpret_cast<u32x2 *>(buf + row * 64 + (((col >> 3) ^ ((row >> 1) & 3)) << 4) + 2 * (col & 4)) =
+                    u32x2{pack_bf16(value(v, 0), value(v, 1)), pack_bf16(value(v, 2), value(v, 3))};
+            }
         }
         wave_handover();
-        const int r = c.lane >> 2, ch = c.lane & 3, n = n0 + ch * 8;
-        const i32x4 v = *reinterpret_cast<const i32x4 *>(buf + r * 64 + 16 * (ch ^ ((r >> 1) & 3)));
-        __builtin_amdgcn_raw_buffer_store_b128(v, rd, n < p.ncols ? (uint32_t)(r * p.ncols + n) * 2u : kOOB, 0, kStoreCached);
-    } else {
+        if (!F32 && p.vec) {
+            const int r = c.lane >> 2, ch = c.lane & 3, n = nh + ch * 8;
+            const i32x4 v = *reinterpret_cast<const i32x4 *>(buf + r * 64 + 16 * (ch ^ ((r >> 1) & 3)));
+            __builtin_amdgcn_raw_buffer_store_b128(v, rd, n < p.ncols ? (uint32_t)(r * p.ncols + n) * 2u : kOOB, 0, kStoreCached);
+        } else {
+            // lanes along the columns: 4 (fp32) or 2 (bf16) rows a store
+            const int e = c.lane % kCols, n = nh + e;
 #pragma unroll
-        for (int v = 0; v < 2; ++v) {
-            const int n = n0 + 16 * v + col0;
-            const float w[4] = {value(v, 0), value(v, 1), value(v, 2), value(v, 3)};
-            store_four<F32>(rd, w, n, p.ncols, (uint32_t)(row * p.ncols + n) * (uint32_t)SZ, p.vec);
+            for (int q = 0; q < kCols / 4; ++q) {
+                const int r = q * (64 / kCols) + c.lane / kCols, at = r * 64 + (((e * SZ >> 4) ^ ((r >> 1) & 3)) << 4) + (e * SZ & 15);
+                const uint32_t to = n < p.ncols ? (uint32_t)(r * p.ncols + n) * (uint32_t)SZ : kOOB;
+                if constexpr (F32)
+                    __builtin_amdgcn_raw_buffer_store_b32(*reinterpret_cast<const uint32_t *>(buf + at), rd, to, 0, kStoreCached);
+                else
+                    __builtin_amdgcn_raw_buffer_store_b16(*reinterpret_cast<const uint16_t *>(buf + at), rd, to, 0, kStoreCached);
+            }
         }
     }
 }
@@ -148,7 +182,7 @@ __global__ __launch_bounds__(512, 1) void i8_tiles(I8Gemm p)
     zero_rows(p, 0, tab.first[0]);
     zero_rows(p, tab.first[p.E], p.M);
     const int ntiles = count_tiles(tab, p.E, tiles_n);
-    const int nwg = gridDim.x, self = first_tile();
+    const int nwg = spread(ntiles), self = first_of(nwg, ntiles);
     if (self >= ntiles) return;
     // at least three stages (the surplus reads zeros): the next tile's row
     // indices and scales land within a tile
@@ -317,25 +351,61 @@ __global__ __launch_bounds__(512, 1) void i8_tiles(I8Gemm p)
     asm volatile("s_waitcnt vmcnt(0)" ::: "memory");   // nothing is left to land in LDS
 }
 
-// 64-row tiles of 64 columns over a deep ring (see moe_tiles_64), for a few rows
-// per group: the time is the reading of W.  8 waves (4 x 2) of 16 x 32; with the
-// gate a wave's 32 rows of W are 16 gate rows and the 16 up rows that meet
-// them.  A tile's row indices are loaded two tiles ahead, its scales as in
-// i8_tiles, all into LDS: the loads of the ring are waited for by count, and a
-// load into registers would end that.
-constexpr int kDeep = 8, kDeepPart = 64 * kRowBytes, kDeepSlot = 2 * kDeepPart, kDeepWait = (kDeep - 2) * 2;
+// Tiles over a deep ring (see moe_tiles_64).  64 rows by TN = 64, 32 or 16 rows of W for
+// a few rows per group, where the time is the reading of W: what a CU can have
+// under way is its LDS, over a latency of 1.2 us about 100 GB/s, so narrower
+// tiles pay where wide ones leave CUs idle, although each reads all of X's rows.
+// 128 rows by 128 where the large tiles are too few for the CUs.
+//
+// A stage is H times 128 bytes of every row.  8 waves: WM along the rows, the others
+// along the columns or (KS = 2, where there are not enough of those to share
+// out) taking every second 128 bytes, to be added at the end.  With the gate 16
+// gate rows of W and the 16 up rows that meet them alternate, and a wave has
+// both.  Where the products count (PIPE) a wave reads a stage's blocks from LDS
+// while it multiplies those of the stage before, whose slot is refilled at once
+// (1024 x 4096 x 4096: one after the other 25.6 us).  A tile's row
+// indices are loaded two tiles ahead, its scales as in i8_tiles, all into LDS:
+// the loads of the ring are waited for by count, and a load into registers would
+// end that.
+template <int TM_, int TN_, bool GATE>
+struct Deep {
+    static constexpr int TM = TM_, TN = TN_, H = TM == 128 ? 1 : TN == 16 ? 4 : 2;
+    static constexpr int WM = TM == 128 ? 2 : 4, RB = TM / 16 / WM;            // waves along the rows, blocks of 16 of each
+    static constexpr int NB = TN >= 64 || GATE ? 2 : 1, WN = TN / 16 / NB, KS = 8 / WM / WN;
+    static constexpr int kSteps = 2 * H / KS;                                  // k-steps of 64 bytes of a wave
+    static constexpr int kA = TM * kRowBytes, kHalf = kA + TN * kRowBytes, kSlot = H * kHalf, kStageBytes = H * kRowBytes;
+    static constexpr int NS = 131072 / kSlot;
+    static constexpr bool PIPE = TM == 128;
+    static constexpr int kAhead = PIPE ? NS : NS - 1;                          // stages that the loads are ahead
+    static constexpr int kLoadsA = TM / 64, kLoadsW = H * TN / 64, kLoads = H * kLoadsA + kLoadsW, kWait = (NS - 2) * kLoads;
+    static constexpr int kRowsW = TN > 64 ? TN / 64 : 1;                       // wave-loads of W at rows of their own
+    static constexpr int TNO = GATE ? TN / 2 : TN;
+    static_assert(KS == 1 || KS == 2, "one or two waves along K");
+    static_assert(KS * WN * WM == 8 && H % KS == 0 && NS >= 3, "");
+};
 
-template <bool GATE, bool F32>
-__global__ __launch_bounds__(512, 1) void i8_tiles_64(I8Gemm p)
+// k-step kk (64 bytes) of the 16 rows 16 i further down than the lane's base: those
+// change bits 1 and 2 of the swizzle
+__device__ __forceinline__ bf16x8 deep_frag(const uint8_t *lds, uint32_t base, int kk, int i)
 {
-    __shared__ __attribute__((aligned(1024))) uint8_t lds[kDeep * kDeepSlot];
-    __shared__ Table<64> tab;
-    __shared__ uint32_t rowbuf[2][64];
-    __shared__ __attribute__((aligned(16))) float scales[2][2][64];    // [parity of the tile][0: rows, 1: rows of W]
-    constexpr int TNO = GATE ? 32 : 64, SZ = F32 ? 4 : 2;
+    return lds_read<bf16x8>(lds, (base ^ (uint32_t)((kk << 6) ^ ((i & 3) << 5))) + (uint32_t)(16 * i * kRowBytes));
+}
+
+template <int TM, int TN, bool GATE, bool F32>
+__global__ __launch_bounds__(512, 1) void i8_tiles_deep(I8Gemm p)
+{
+    using S = Deep<TM, TN, GATE>;
+    constexpr int RB = S::RB, NB = S::NB, KS = S::KS, H = S::H, TNO = S::TNO, SZ = F32 ? 4 : 2;
+    __shared__ __attribute__((aligned(1024))) uint8_t lds[S::NS * S::kSlot];
+    __shared__ Table<TM> tab;
+    __shared__ uint32_t rowbuf[2][TM];
+    // [parity of the tile]: rows' scales, then those of the tile's rows of W
+    constexpr int kScales = TM + (TN > 64 ? TN : 64);
+    __shared__ __attribute__((aligned(16))) float scales[2][kScales];
+    __shared__ __attribute__((aligned(16))) i32x4 part[TM == 128 ? 8 : KS == 2 ? 4 * NB : 1][64];
 
     const Lane c = lane_of();
-    const int wm = c.w >> 1, wn = c.w & 1, j = c.lane & 15, g = c.lane >> 4;
+    const int wm = c.w / (S::WN * KS), wn = c.w / KS % S::WN, ks2 = KS == 2 ? c.w & 1 : 0, j = c.lane & 15, g = c.lane >> 4;
     const int lda = p.K;
     const int tiles_n = (p.ncols + TNO - 1) / TNO;
     fill_table(tab, p, c);
@@ -343,28 +413,30 @@ __global__ __launch_bounds__(512, 1) void i8_tiles_64(I8Gemm p)
     zero_rows(p, 0, tab.first[0]);
     zero_rows(p, tab.first[p.E], p.M);
     const int ntiles = count_tiles(tab, p.E, tiles_n);
-    const int nwg = gridDim.x;
-    int tile = first_tile();
+    const int nwg = spread(ntiles);
+    int tile = first_of(nwg, ntiles);
     if (tile >= ntiles) return;
-    // at least as many stages as slots: the loads turn to the next tile behind a
-    // barrier of this one, when the tile before's scales have been read
-    const int nk = max((p.K + kRowBytes - 1) / kRowBytes, kDeep);
+    // more stages than the loads are ahead: they turn to the next tile behind a
+    // barrier of this one, when the tile before's scales have been read.  (PIPE:
+    // an even number, the two sets of registers take turns)
+    int nk = max((p.K + S::kStageBytes - 1) / S::kStageBytes, S::kAhead + 1);
+    if (S::PIPE) nk += nk & 1;
     auto find = [&](int id) {
         return find_tile(tab, p.E, ntiles, tiles_n, TNO, id,
                          [&](const auto *at, int n) { return group_of(at, p.E, n, c); });
     };
 
-    // wave w loads rows 8 w .. of A and of W
+    // wave w loads rows 8 w .. (and 64 further down) of A; wave-load w + 8 q of W's: eight rows of one of the H parts
     i32x4 ra, rb;
-    const int lrow = 8 * c.w + (c.lane >> 3);
+    const int arow = 8 * c.w + (c.lane >> 3), wrow = 8 * (c.w % (TN / 8)) + (c.lane >> 3);
     int rot = 0;
-    uint32_t aoff = 0, boff = 0;
-    uint32_t kx = (uint32_t)(((c.lane & 7) ^ swz(lrow)) << 4);     // the lane's chunk of its row
-    // (one wave, one load: the others' count of loads under way is one less, which waits for no fewer)
+    uint32_t aoff[S::kLoadsA], boff[S::kRowsW];
+    uint32_t ax = (uint32_t)(((c.lane & 7) ^ swz(arow)) << 4), bx = (uint32_t)(((c.lane & 7) ^ swz(wrow)) << 4);   // the lane's chunks
+    // (64 rows a wave; that the other waves have a load less under way waits for no fewer)
     auto fetch = [&](const RowTile &r, int place) {
-        if (c.w != 0 || !p.rows) return;
-        dma<4>(words_of(p.rows + r.m0, (uint32_t)max(min(r.mend - r.m0, 64), 0) * 4u),
-               reinterpret_cast<uint8_t *>(rowbuf), place * 256, (uint32_t)c.lane * 4u);
+        if (c.w >= TM / 64 || !p.rows) return;
+        dma<4>(words_of(p.rows + r.m0, (uint32_t)max(min(r.mend - r.m0, TM), 0) * 4u), reinterpret_cast<uint8_t *>(rowbuf),
+               (place * TM + c.w * 64) * 4, (uint32_t)(c.w * 64 + c.lane) * 4u);
     };
     auto aim = [&](const RowTile &r, int place) {
         if (r.blocks == 0) {
@@ -375,38 +447,54 @@ __global__ __launch_bounds__(512, 1) void i8_tiles_64(I8Gemm p)
         rot = r.n0 / TNO % nk;
         const int64_t wbytes = (int64_t)p.N * p.K;
         const uint8_t *wg = p.W + r.g * wbytes;
-        const int left = min(r.mend - r.m0, 64);
+        const int left = min(r.mend - r.m0, TM);
         const uint32_t have = p.rows ? (uint32_t)p.T : (uint32_t)left;
-        const uint32_t row = p.rows ? rowbuf[place][lrow] : (uint32_t)lrow;
         ra = words_of(p.rows ? p.X : p.X + (int64_t)r.m0 * lda, have * (uint32_t)lda);
-        aoff = lrow < left && row < have ? row * (uint32_t)lda : kRowOOB;
-        if constexpr (GATE) {
-            // rows 32 wn + 16 u + q of the slot: row n0 + 16 wn + q of matrix u
-            const int f = r.n0 + (lrow >> 5) * 16 + (lrow & 15);
-            rb = words_of(wg, (uint32_t)wbytes);
-            boff = f < p.ncols ? (uint32_t)((((lrow >> 4) & 1) * p.ncols + f) * lda) : kRowOOB;
-        } else {
-            rb = words_of(wg + (int64_t)r.n0 * lda, (uint32_t)(min(p.N - r.n0, 64) * lda));
-            boff = (uint32_t)(lrow * lda);
+#pragma unroll
+        for (int q = 0; q < S::kLoadsA; ++q) {
+            const int m = arow + 64 * q;
+            const uint32_t row = p.rows ? rowbuf[place][m] : (uint32_t)m;
+            aoff[q] = m < left && row < have ? row * (uint32_t)lda : kRowOOB;
         }
-        if (c.w == 0) {
-            const uint32_t at = p.rows ? rowbuf[place][c.lane] : (uint32_t)c.lane;
-            dma<4>(words_of(p.rows ? p.sX : p.sX + r.m0, have * 4u), reinterpret_cast<uint8_t *>(scales), place * 512,
-                   at < have ? at * 4u : kRowOOB);
-        } else if (c.w == 1) {
-            const int at = GATE ? ((c.lane >> 4) & 1) * p.ncols + r.n0 + (c.lane >> 5) * 16 + (c.lane & 15) : r.n0 + c.lane;
+        rb = GATE ? words_of(wg, (uint32_t)wbytes) : words_of(wg + (int64_t)r.n0 * lda, (uint32_t)(min(p.N - r.n0, TN) * lda));
+        // rows 32 i + 16 u + q of the slot, with the gate: row n0 + 16 i + q of matrix u
+        auto row_of_w = [&](int e) { return ((e >> 4) & 1) * p.ncols + r.n0 + (e >> 5) * 16 + (e & 15); };
+        auto there = [&](int e) { return r.n0 + (e >> 5) * 16 + (e & 15) < p.ncols; };
+#pragma unroll
+        for (int q = 0; q < S::kRowsW; ++q) {
+            const int e = wrow + 64 * q;
+            if constexpr (GATE) boff[q] = there(e) ? (uint32_t)(row_of_w(e) * lda) : kRowOOB;
+            else boff[q] = (uint32_t)(e * lda);
+        }
+        if (c.w < TM / 64) {
+            const int m = c.w * 64 + c.lane;
+            const uint32_t at = p.rows ? rowbuf[place][m] : (uint32_t)m;
+            dma<4>(words_of(p.rows ? p.sX : p.sX + r.m0, have * 4u), reinterpret_cast<uint8_t *>(scales),
+                   (place * kScales + c.w * 64) * 4, at < have ? at * 4u : kRowOOB);
+        } else if (c.w < TM / 64 + (TN + 63) / 64) {
+            const int e = (c.w - TM / 64) * 64 + c.lane, at = GATE ? row_of_w(e) : r.n0 + e;
             dma<4>(words_of(p.sW + (int64_t)r.g * p.N, (uint32_t)p.N * 4u), reinterpret_cast<uint8_t *>(scales),
-                   place * 512 + 256, at < p.N ? (uint32_t)at * 4u : kRowOOB);
+                   (place * kScales + c.w * 64) * 4, e < TN && at < p.N ? (uint32_t)at * 4u : kRowOOB);
         }
     };
     auto load = [&](int slot, int ks) {
         ks += rot;
         ks -= ks >= nk ? nk : 0;
-        const uint32_t dst = slot * kDeepSlot;
-        const int kc = (int)kx + ks * kRowBytes;
-        const bool in = kc < lda;
-        dma<16>(ra, lds, dst + c.w * 1024, in ? aoff + kc : kRowOOB);
-        dma<16>(rb, lds, dst + kDeepPart + c.w * 1024, in ? boff + kc : kRowOOB);
+        const uint32_t dst = slot * S::kSlot;
+        const int k0 = ks * S::kStageBytes;
+#pragma unroll
+        for (int h = 0; h < H; ++h) {
+            const int kc = (int)ax + k0 + h * kRowBytes;
+#pragma unroll
+            for (int q = 0; q < S::kLoadsA; ++q)
+                dma<16>(ra, lds, dst + h * S::kHalf + (c.w + 8 * q) * 1024, kc < lda ? aoff[q] + kc : kRowOOB);
+        }
+#pragma unroll
+        for (int q = 0; q < S::kLoadsW; ++q) {
+            const int i = c.w + 8 * q, h = i / (TN / 8), kc = (int)bx + k0 + h * kRowBytes;
+            dma<16>(rb, lds, dst + h * S::kHalf + S::kA + i % (TN / 8) * 1024,
+                    kc < lda ? boff[S::kRowsW > 1 ? q : 0] + kc : kRowOOB);
+        }
     };
 
     int parity = 0;
@@ -416,60 +504,122 @@ __global__ __launch_bounds__(512, 1) void i8_tiles_64(I8Gemm p)
     turn_end<0>();
     aim(cur, 0);
 #pragma unroll
-    for (int f = 0; f < kDeep - 1; ++f) load(f, f);
-    const int ar = 16 * wm + j;
-    uint32_t fa = (uint32_t)(ar * kRowBytes + ((kgroup(g) ^ swz(ar)) << 4)), fb = kDeepPart + part_base<false>(c, wn);
-    stage_barrier<kDeepWait>();
+    for (int f = 0; f < S::kAhead; ++f) load(f, f);
+    const int ar = 16 * RB * wm + j, br = 16 * NB * wn + j;
+    uint32_t fa = (uint32_t)(ar * kRowBytes + ((kgroup(g) ^ swz(ar)) << 4));
+    uint32_t fb = (uint32_t)(S::kA + br * kRowBytes + ((kgroup(g) ^ swz(br)) << 4));
+    struct Blocks {
+        bf16x8 a[S::kSteps][RB], b[S::kSteps][NB];
+    };
+    auto read = [&](Blocks &f, int slot) {
+#pragma unroll
+        for (int kk = 0; kk < S::kSteps; ++kk) {
+            const uint32_t from = (uint32_t)(slot * S::kSlot + (KS * (kk >> 1) + ks2) * S::kHalf);
+#pragma unroll
+            for (int i = 0; i < RB; ++i) f.a[kk][i] = deep_frag(lds, fa + from, kk & 1, i);
+#pragma unroll
+            for (int u = 0; u < NB; ++u) f.b[kk][u] = deep_frag(lds, fb + from, kk & 1, u);
+        }
+    };
+    Blocks even, odd;
+    if constexpr (S::PIPE) {
+        stage_barrier<(S::NS - 1) * S::kLoads>();
+        read(even, 0);
+    }
+    stage_barrier<S::kWait>();
 
-    int rs = 0;               // slot the next stage reads
+    int rs = 0;               // slot of the stage
     for (;;) {
         tile += nwg;
         // (this tile's row indices have been read: their place is the tile's after the next one)
         const RowTile after = find(tile + nwg);
         fetch(after, parity);
-        i32x4 acc[2] = {};
-        for (int s = 0; s < nk; ++s) {
-            int ks = s + kDeep - 1;
+        const bool busy = cur.m0 + 16 * RB * wm < cur.mend;        // the wave has rows
+        i32x4 acc[RB][NB];
+#pragma unroll
+        for (int i = 0; i < RB; ++i)
+#pragma unroll
+            for (int u = 0; u < NB; ++u) acc[i][u] = i32x4{};
+        auto multiply = [&](const Blocks &f) {
+#pragma unroll
+            for (int kk = 0; kk < S::kSteps; ++kk)
+#pragma unroll
+                for (int i = 0; i < RB; ++i)
+#pragma unroll
+                    for (int u = 0; u < NB; ++u) acc[i][u] = MulI8::mul(f.b[kk][u], f.a[kk][i], acc[i][u]);
+        };
+        auto ahead = [&](int s) {
+            int ks = s + S::kAhead;
             if (ks >= nk) {
                 ks -= nk;
                 if (ks == 0) aim(next, parity ^ 1);
             }
-            asm volatile("" : "+v"(kx), "+v"(fa), "+v"(fb));
-            const uint32_t so = (uint32_t)(rs * kDeepSlot);
-            bf16x8 a[2], b[2][2];
-#pragma unroll
-            for (int kk = 0; kk < 2; ++kk) {
-                a[kk] = lds_read<bf16x8>(lds, (fa ^ (uint32_t)(kk << 6)) + so);
-#pragma unroll
-                for (int u = 0; u < 2; ++u) b[kk][u] = part_frag<false>(lds, fb + so, kk, 0, u);
+            asm volatile("" : "+v"(ax), "+v"(bx), "+v"(fa), "+v"(fb));
+            return ks;
+        };
+        if constexpr (S::PIPE) {
+            auto stage = [&](const Blocks &now, Blocks &then, int s) {
+                const int ks = ahead(s), after_rs = rs + 1 == S::NS ? 0 : rs + 1;
+                read(then, after_rs);
+                load(rs, ks);
+                DBS_FENCE();
+                if (busy) multiply(now);
+                stage_barrier<S::kWait>();
+                rs = after_rs;
+            };
+            for (int s = 0; s < nk; s += 2) {
+                stage(even, odd, s);
+                stage(odd, even, s + 1);
             }
-            load(rs == 0 ? kDeep - 1 : rs - 1, ks);
-#pragma unroll
-            for (int kk = 0; kk < 2; ++kk)
-#pragma unroll
-                for (int u = 0; u < 2; ++u) acc[u] = MulI8::mul(b[kk][u], a[kk], acc[u]);
-            stage_barrier<kDeepWait>();
-            rs = rs + 1 == kDeep ? 0 : rs + 1;
+        } else {
+            for (int s = 0; s < nk; ++s) {
+                const int ks = ahead(s);
+                read(even, rs);
+                load(rs == 0 ? S::NS - 1 : rs - 1, ks);
+                multiply(even);
+                stage_barrier<S::kWait>();
+                rs = rs + 1 == S::NS ? 0 : rs + 1;
+            }
         }
-        // lane: row 16 wm + l % 16, four columns of each block
-        const int r0 = cur.m0 + 16 * wm, left = __builtin_amdgcn_readfirstlane(max(0, min(16, cur.mend - r0)));
-        const __amdgpu_buffer_rsrc_t rd =
-            make_rsrc(p.D + (int64_t)r0 * p.ncols * SZ, (uint32_t)left * (uint32_t)p.ncols * (uint32_t)SZ);
-        const float sx = scales[parity][0][ar];
-        f32x4 h[2];
+        if constexpr (KS == 2) {
+            // (read before the next tile's stages end, written behind them)
+            if (ks2) {
 #pragma unroll
-        for (int u = 0; u < 2; ++u) {
-            const f32x4 sw = *reinterpret_cast<const f32x4 *>(&scales[parity][1][32 * wn + 16 * u + 4 * g]);
+                for (int u = 0; u < NB; ++u) part[NB * wm + u][c.lane] = acc[0][u];
+            }
+            asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory");
+            if (!ks2) {
 #pragma unroll
-            for (int q = 0; q < 4; ++q) h[u][q] = (float)acc[u][q] * sx * sw[q];
+                for (int u = 0; u < NB; ++u) acc[0][u] += part[NB * wm + u][c.lane];
+            }
         }
+        if (!ks2 && busy) {
+            // lane: rows l % 16 of each block, four columns of each
+            f32x4 sw[NB];
 #pragma unroll
-        for (int u = 0; u < (GATE ? 1 : 2); ++u) {
-            float v[4];
+            for (int u = 0; u < NB; ++u)
+                sw[u] = *reinterpret_cast<const f32x4 *>(&scales[parity][TM + 16 * NB * wn + 16 * u + 4 * g]);
 #pragma unroll
-            for (int q = 0; q < 4; ++q) v[q] = GATE ? gated(h[0][q], h[1][q]) : h[u][q];
-            const int n = cur.n0 + (GATE ? 16 : 32) * wn + 16 * u + 4 * g;
-            store_four<F32>(rd, v, n, p.ncols, (uint32_t)(j * p.ncols + n) * (uint32_t)SZ, p.vec);
+            for (int i = 0; i < RB; ++i) {
+                const int r0 = cur.m0 + 16 * (RB * wm + i);
+                const float sx = scales[parity][ar + 16 * i];
+                auto scaled = [&](int u, int q) { return (float)acc[i][u][q] * sx * sw[u][q]; };
+                if constexpr (TM == 128 && !GATE) {
+                    store_rows<F32>(reinterpret_cast<uint8_t *>(part[c.w]), p, r0, cur.mend, cur.n0 + 32 * wn, c, scaled);
+                } else {
+                    const int left = __builtin_amdgcn_readfirstlane(max(0, min(16, cur.mend - r0)));
+                    const __amdgpu_buffer_rsrc_t rd =
+                        make_rsrc(p.D + (int64_t)r0 * p.ncols * SZ, (uint32_t)left * (uint32_t)p.ncols * (uint32_t)SZ);
+#pragma unroll
+                    for (int u = 0; u < (GATE ? 1 : NB); ++u) {
+                        float v[4];
+#pragma unroll
+                        for (int q = 0; q < 4; ++q) v[q] = GATE ? gated(scaled(0, q), scaled(NB - 1, q)) : scaled(u, q);
+                        const int n = cur.n0 + (GATE ? 16 : 16 * NB) * wn + 16 * u + 4 * g;
+                        store_four<F32>(rd, v, n, p.ncols, (uint32_t)(j * p.ncols + n) * (uint32_t)SZ, p.vec);
+                    }
+                }
+            }
         }
         if (next.blocks == 0) break;
         cur = next;
@@ -477,6 +627,164 @@ __global__ __launch_bounds__(512, 1) void i8_tiles_64(I8Gemm p)
         parity ^= 1;
     }
     asm volatile("s_waitcnt vmcnt(0)" ::: "memory");   // nothing is left to land in LDS
+}
+
+// Few rows: 16 rows and 16 columns a workgroup (with the gate 16 gate columns and
+// the 16 up columns that meet them), whose 8 waves share out K: every wave sums
+// its part, from fragments loaded straight into registers (no wave reads what
+// another does, so LDS would only be a detour), and the parts meet in LDS at the
+// end, exact in whatever order.  So a matrix of a few thousand rows occupies
+// every CU, and a walk along K is an eighth as long.  Two workgroups a CU fill
+// each other's pauses, and the loads of the next tile go out before this one's
+// parts meet.
+constexpr int kRowsUnroll = 4;                   // k-steps of 64 bytes loaded together, twice
+
+template <bool GATE, bool F32>
+__global__ __launch_bounds__(512, 4) void i8_rows(I8Gemm p)
+{
+    constexpr int U = GATE ? 3 : kRowsUnroll, C = GATE ? 2 : 1, SZ = F32 ? 4 : 2;
+    __shared__ __attribute__((aligned(16))) i32x4 part[C][8][64];
+    __shared__ int32_t first[kMoeMaxExperts + 1], at[kMoeMaxExperts + 1];
+    const Lane c = lane_of();
+    const int j = c.lane & 15, g = c.lane >> 4;
+    const int tiles_n = (p.ncols + 15) / 16;
+    auto tiles_of = [](int rows) { return (rows + 15) / 16; };
+    if (!p.offsets) {
+        if (threadIdx.x == 0) {
+            first[0] = at[0] = 0;
+            first[1] = p.M;
+            at[1] = tiles_of(p.M);
+        }
+    } else if (c.w == 0) {
+        group_table<true>(first, at, p.offsets, p.E, p.M, c, tiles_of);
+    }
+    __syncthreads();
+    zero_rows(p, 0, first[0]);
+    zero_rows(p, first[p.E], p.M);
+    const int ntiles = same(at[p.E]) * tiles_n, nwg = spread(ntiles);
+    int tile = first_of(nwg, ntiles);
+    if (tile >= ntiles) return;
+    // the wave's k-steps; the lane's end of them
+    const int steps = (p.K + 63) / 64, each = (steps + 7) / 8, s0 = c.w * each, s1 = min(s0 + each, steps);
+    const int kend = min(s1 * 64, p.K - 16 * g);
+
+    struct Ref {
+        int m0, left, n0, grp;
+        uint32_t row;                            // the lane's row of X
+    };
+    auto find = [&](int id) {
+        Ref t{};
+        if (id >= ntiles) return t;
+        const int row_tile = id / tiles_n;
+        t.n0 = (id - row_tile * tiles_n) * 16;
+        t.grp = p.offsets ? group_of(at, p.E, row_tile, c) : 0;
+        t.m0 = same(first[t.grp]) + (row_tile - same(at[t.grp])) * 16;
+        t.left = min(same(first[t.grp + 1]) - t.m0, 16);
+        t.row = j < t.left ? (p.rows ? (uint32_t)p.rows[t.m0 + j] : (uint32_t)j) : ~0u;
+        return t;
+    };
+    // What the loads read: the tile behind ra and rb.
+    __amdgpu_buffer_rsrc_t ra, rb;
+    uint32_t aoff, boff[C];
+    auto aim = [&](const Ref &t) {
+        const int64_t wbytes = (int64_t)p.N * p.K;
+        const uint8_t *wg = p.W + t.grp * wbytes;
+        const uint32_t have = p.rows ? (uint32_t)p.T : (uint32_t)t.left;
+        ra = make_rsrc(p.rows ? p.X : p.X + (int64_t)t.m0 * p.K, have * (uint32_t)p.K);
+        rb = GATE ? make_rsrc(wg, (uint32_t)wbytes)
+                  : make_rsrc(wg + (int64_t)t.n0 * p.K, (uint32_t)max(min(p.N - t.n0, 16), 0) * (uint32_t)p.K);
+        aoff = t.row < have ? t.row * (uint32_t)p.K + 16 * g : kRowOOB;
+#pragma unroll
+        for (int i = 0; i < C; ++i) {
+            if constexpr (GATE) boff[i] = t.n0 + j < p.ncols ? (uint32_t)(i * p.ncols + t.n0 + j) * (uint32_t)p.K + 16 * g : kRowOOB;
+            else boff[i] = (uint32_t)j * (uint32_t)p.K + 16 * g;
+        }
+    };
+    bf16x8 a[2][U], b[2][U][C];
+    auto load = [&](int place, int s) {
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            const int k = (s + u) * 64;
+            const bool in = k < kend;            // (past the wave's part or the row's end: out of bounds, zero)
+#pragma unroll
+            for (int i = 0; i < C; ++i)
+                b[place][u][i] =
+                    __builtin_bit_cast(bf16x8, __builtin_amdgcn_raw_buffer_load_b128(rb, in ? boff[i] + k : kRowOOB, 0, 0));
+            a[place][u] = __builtin_bit_cast(bf16x8, __builtin_amdgcn_raw_buffer_load_b128(ra, in ? aoff + k : kRowOOB, 0, 0));
+        }
+        DBS_FENCE();                             // (all of them before the products of those before)
+    };
+    i32x4 acc[C];
+    auto mul = [&](int place) {
+#pragma unroll
+        for (int u = 0; u < U; ++u)
+#pragma unroll
+            for (int i = 0; i < C; ++i) acc[i] = MulI8::mul(b[place][u][i], a[place][u], acc[i]);
+        DBS_FENCE();
+    };
+
+    Ref cur = find(tile);
+    aim(cur);
+    load(0, s0);
+    for (;;) {
+        tile += nwg;
+        const bool more = tile < ntiles;
+        const Ref next = find(tile);
+        // the scales that the results of this tile meet (by the first wave)
+        const int n = cur.n0 + 4 * g;
+        const uint32_t have = p.rows ? (uint32_t)p.T : (uint32_t)cur.left;
+        float sx = 0.0f, sw[C][4] = {};
+        if (c.w == 0) {
+            const __amdgpu_buffer_rsrc_t rx = make_rsrc(p.rows ? p.sX : p.sX + cur.m0, have * 4u);
+            const __amdgpu_buffer_rsrc_t rw = make_rsrc(p.sW + (int64_t)cur.grp * p.N, (uint32_t)p.N * 4u);
+            sx = __builtin_bit_cast(float, __builtin_amdgcn_raw_buffer_load_b32(rx, cur.row < have ? cur.row * 4u : kRowOOB, 0, 0));
+#pragma unroll
+            for (int h = 0; h < C; ++h)
+#pragma unroll
+                for (int q = 0; q < 4; ++q)
+                    sw[h][q] = __builtin_bit_cast(float, __builtin_amdgcn_raw_buffer_load_b32(
+                                                             rw, n + q < p.ncols ? (uint32_t)(h * p.ncols + n + q) * 4u : kRowOOB, 0, 0));
+        }
+#pragma unroll
+        for (int i = 0; i < C; ++i) acc[i] = i32x4{};
+        int s = s0;
+        for (; s + 2 * U < s1; s += 2 * U) {
+            load(1, s + U);
+            mul(0);
+            load(0, s + 2 * U);
+            mul(1);
+        }
+        load(1, s + U);
+        mul(0);
+        if (more) {
+            aim(next);
+            load(0, s0);
+        }
+        mul(1);
+#pragma unroll
+        for (int i = 0; i < C; ++i) part[i][c.w][c.lane] = acc[i];
+        __syncthreads();
+        if (c.w == 0) {
+            float h[C][4];
+#pragma unroll
+            for (int i = 0; i < C; ++i) {
+                i32x4 sum = {};
+#pragma unroll
+                for (int w = 0; w < 8; ++w) sum += part[i][w][c.lane];
+#pragma unroll
+                for (int q = 0; q < 4; ++q) h[i][q] = (float)sum[q] * sx * sw[i][q];
+            }
+            float v[4];
+#pragma unroll
+            for (int q = 0; q < 4; ++q) v[q] = GATE ? gated(h[0][q], h[C - 1][q]) : h[0][q];
+            const __amdgpu_buffer_rsrc_t rd =
+                make_rsrc(p.D + (int64_t)cur.m0 * p.ncols * SZ, (uint32_t)cur.left * (uint32_t)p.ncols * (uint32_t)SZ);
+            store_four<F32>(rd, v, n, p.ncols, (uint32_t)(j * p.ncols + n) * (uint32_t)SZ, p.vec);
+        }
+        if (!more) break;
+        __syncthreads();                         // (the parts have been read)
+        cur = next;
+    }
 }
 
 // At most as many workgroups as there can be tiles of tm rows and tno columns.
@@ -488,14 +796,33 @@ dim3 tile_grid(const I8Gemm &p, int tm, int tno, int cus)
 
 }  // namespace
 
-hipError_t launch_i8_tiles(const I8Gemm &p, int rows, int cus, hipStream_t stream)
+hipError_t launch_i8_tiles(const I8Gemm &p, I8Tile t, int cus, hipStream_t stream)
 {
     const dim3 block(512);
-    if (rows == 64) {
-        const dim3 grid = tile_grid(p, 64, p.gate ? 32 : 64, cus);
-        if (p.gate) hipLaunchKernelGGL((i8_tiles_64<true, false>), grid, block, 0, stream, p);
-        else if (p.f32) hipLaunchKernelGGL((i8_tiles_64<false, true>), grid, block, 0, stream, p);
-        else hipLaunchKernelGGL((i8_tiles_64<false, false>), grid, block, 0, stream, p);
+    if (t.rows == 16) {
+        const dim3 grid = tile_grid(p, 16, 16, 2 * cus);
+        if (p.gate) hipLaunchKernelGGL((i8_rows<true, false>), grid, block, 0, stream, p);
+        else if (p.f32) hipLaunchKernelGGL((i8_rows<false, true>), grid, block, 0, stream, p);
+        else hipLaunchKernelGGL((i8_rows<false, false>), grid, block, 0, stream, p);
+    } else if (t.cols <= 128) {
+        auto go = [&](auto tm, auto tn) {
+            constexpr int TM = decltype(tm)::value, TN = decltype(tn)::value;
+            const dim3 grid = tile_grid(p, TM, p.gate ? TN / 2 : TN, cus);
+            if constexpr (TN >= 32) {
+                if (p.gate) {
+                    hipLaunchKernelGGL((i8_tiles_deep<TM, TN, true, false>), grid, block, 0, stream, p);
+                    return;
+                }
+            }
+            if (p.f32) hipLaunchKernelGGL((i8_tiles_deep<TM, TN, false, true>), grid, block, 0, stream, p);
+            else hipLaunchKernelGGL((i8_tiles_deep<TM, TN, false, false>), grid, block, 0, stream, p);
+        };
+        using I64 = std::integral_constant<int, 64>;
+        using I128 = std::integral_constant<int, 128>;
+        if (t.rows == 128) go(I128{}, I128{});
+        else if (t.cols == 64) go(I64{}, I64{});
+        else if (t.cols == 32 || p.gate) go(I64{}, std::integral_constant<int, 32>{});
+        else go(I64{}, std::integral_constant<int, 16>{});
     } else {
         auto go = [&](auto tm) {
             constexpr int TM = decltype(tm)::value;
@@ -504,7 +831,7 @@ hipError_t launch_i8_tiles(const I8Gemm &p, int rows, int cus, hipStream_t strea
             else if (p.f32) hipLaunchKernelGGL((i8_tiles<TM, false, true>), grid, block, 0, stream, p);
             else hipLaunchKernelGGL((i8_tiles<TM, false, false>), grid, block, 0, stream, p);
         };
-        if (rows == 256) go(std::integral_constant<int, 256>{});
+        if (t.rows == 256) go(std::integral_constant<int, 256>{});
         else go(std::integral_constant<int, 128>{});
     }
     return hipGetLastError();

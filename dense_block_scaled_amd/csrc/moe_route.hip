@@ -325,8 +325,9 @@ constexpr uint64_t kIndexBits = 1023;           // kMoeMaxExperts - 1
 __device__ __forceinline__ double keyed(double c, int e)
 {
     const uint64_t b = __builtin_bit_cast(uint64_t, c);
-    const uint32_t low = (uint32_t)((int64_t)b < 0 ? e : (int)kIndexBits - e);
-    return __builtin_bit_cast(double, (b & ~kIndexBits) | low);
+    const uint32_t hi = (uint32_t)(b >> 32), flip = ~(uint32_t)((int32_t)hi >> 31) & (uint32_t)kIndexBits;
+    const uint32_t lo = ((uint32_t)b & ~(uint32_t)kIndexBits) | ((uint32_t)e ^ flip);      // e, or 1023 - e
+    return __builtin_bit_cast(double, (uint64_t)hi << 32 | lo);
 }
 
 __device__ __forceinline__ double unkeyed(double key)
@@ -370,42 +371,61 @@ __device__ __forceinline__ void sort_down(double (&v)[VPL])
     }
 }
 
+// C consecutive values of an array as fp32: to[i ..]
+template <int C, int N>
+__device__ __forceinline__ void load_some(float (&to)[N], int i, const float *from)
+{
+    typedef __attribute__((ext_vector_type(4))) float f32x4;
+    if constexpr (C == 4) {
+        const f32x4 w = *reinterpret_cast<const f32x4 *>(from);
+#pragma unroll
+        for (int c = 0; c < 4; ++c) to[i + c] = w[c];
+    } else {
+        to[i] = *from;
+    }
+}
+
+template <int C, int N>
+__device__ __forceinline__ void load_some(float (&to)[N], int i, const uint16_t *from)
+{
+    typedef __attribute__((ext_vector_type(2))) uint32_t u32x2;
+    if constexpr (C == 4) {
+        const u32x2 w = *reinterpret_cast<const u32x2 *>(from);
+#pragma unroll
+        for (int c = 0; c < 4; ++c)
+            to[i + c] = __builtin_bit_cast(float, c & 1 ? w[c >> 1] & 0xFFFF0000u : w[c >> 1] << 16);
+    } else {
+        to[i] = __builtin_bit_cast(float, (uint32_t)*from << 16);
+    }
+}
+
 // The experts of a token, chosen by its 16 lanes (l: lane of the 16): lane j
 // returns the j-th choice (-1: none) and its weight.  VPL: keys a lane has
 // registers for (p.q used); C: as in load_logits.
 template <int VPL, int C, bool BF16>
 __device__ __forceinline__ void choose(const MoeRouteGrouped &p, int64_t tok, int l, int &expert, float &weight)
 {
-    typedef __attribute__((ext_vector_type(4))) float f32x4;
-    typedef __attribute__((ext_vector_type(2))) uint32_t u32x2;
     const int per = p.r.E / p.groups, group = l / p.lanes, at0 = l % p.lanes * p.q;    // first of the lane's in its group
-    const int have = group < p.groups ? max(min(per - at0, p.q), 0) : 0, e0 = group * per + at0;
+    const int have = group < p.groups ? max(min(per - at0, p.q), 0) : 0, e0 = have ? group * per + at0 : 0;
     const float *logits32 = reinterpret_cast<const float *>(p.r.logits) + tok * p.r.E;
     const uint16_t *logits16 = reinterpret_cast<const uint16_t *>(p.r.logits) + tok * p.r.E;
-    float x[VPL];
+    // All loads are under way together: what a lane has no expert for reads its last one's again
+    float x[VPL], bias[VPL];
+    const int last = max(have - C, 0);           // (C = 4: have is a multiple of 4)
 #pragma unroll
     for (int i = 0; i < VPL; i += C) {
-        float y[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
-        if (i < have) {                          // (C = 4: have is a multiple of 4)
-            if constexpr (BF16 && C == 4) {
-                const u32x2 w = *reinterpret_cast<const u32x2 *>(logits16 + e0 + i);
-                y[0] = __builtin_bit_cast(float, w[0] << 16);
-                y[1] = __builtin_bit_cast(float, w[0] & 0xFFFF0000u);
-                y[2] = __builtin_bit_cast(float, w[1] << 16);
-                y[3] = __builtin_bit_cast(float, w[1] & 0xFFFF0000u);
-            } else if constexpr (BF16) {
-                y[0] = __builtin_bit_cast(float, (uint32_t)logits16[e0 + i] << 16);
-            } else if constexpr (C == 4) {
-                const f32x4 w = *reinterpret_cast<const f32x4 *>(logits32 + e0 + i);
-#pragma unroll
-                for (int c = 0; c < 4; ++c) y[c] = w[c];
-            } else {
-                y[0] = logits32[e0 + i];
-            }
-        }
-#pragma unroll
-        for (int c = 0; c < C; ++c) x[i + c] = open_logit(y[c]);
+        const int e = e0 + min(i, last);
+        if constexpr (BF16) load_some<C>(x, i, logits16 + e);
+        else load_some<C>(x, i, logits32 + e);
     }
+    auto load_bias = [&] {
+        if (!p.bias) return;
+#pragma unroll
+        for (int i = 0; i < VPL; i += C) load_some<C>(bias, i, p.bias + e0 + min(i, last));
+    };
+    if constexpr (VPL <= 16) load_bias();
+#pragma unroll
+    for (int i = 0; i < VPL; ++i) x[i] = i < have ? open_logit(x[i]) : -INFINITY;
     float top = 0.0f;
     double whole = 1.0, v[VPL];
     if (p.sigmoid) {
@@ -422,7 +442,8 @@ __device__ __forceinline__ void choose(const MoeRouteGrouped &p, int64_t tok, in
         for (int i = 0; i < VPL; ++i) {
             // (the difference in fp64: it need not be an fp32 number)
             const double d = fmax((double)x[i] - (double)from, -708.0);
-            v[i] = x[i] > -INFINITY ? exp64(d) : 0.0;
+            const double e = exp64(d);
+            v[i] = x[i] > -INFINITY ? e : 0.0;
             whole += v[i];
         }
         whole = row_sum64(whole);
@@ -430,11 +451,12 @@ __device__ __forceinline__ void choose(const MoeRouteGrouped &p, int64_t tok, in
 #pragma unroll
         for (int i = 0; i < VPL; ++i) v[i] *= inv;
     }
+    if constexpr (VPL > 16) load_bias();         // (more of them have no registers until now)
 #pragma unroll
     for (int i = 0; i < VPL; ++i) {
-        float b = 0.0f;
-        if (p.bias && i < have) b = open_logit(p.bias[e0 + i]);
-        v[i] = x[i] > -INFINITY && b > -INFINITY ? keyed(v[i] + (double)b, e0 + i) : -(double)INFINITY;
+        const float b = p.bias ? open_logit(bias[i]) : 0.0f;
+        const double key = keyed(v[i] + (double)b, e0 + i);
+        v[i] = fminf(x[i], b) > -INFINITY ? key : -(double)INFINITY;
     }
     sort_down<0, VPL>(v);
 
@@ -470,10 +492,21 @@ __device__ __forceinline__ void choose(const MoeRouteGrouped &p, int64_t tok, in
         const double b = row_max64(v[0]);
         if (b == -(double)INFINITY) break;       // no open expert is left
         expert = l == j ? key_index(b) : expert;
+        // the winner's list moves up, as far as the choices left can reach
         const bool mine = v[0] == b;
+        auto up = [&](auto n) {
+            constexpr int N = decltype(n)::value < VPL ? decltype(n)::value : VPL;
 #pragma unroll
-        for (int i = 0; i < (VPL < kMoeMaxK ? VPL : kMoeMaxK); ++i)
-            v[i] = mine ? (i + 1 < VPL ? v[i + 1] : -(double)INFINITY) : v[i];
+            for (int i = 0; i < N; ++i) {
+                double below = i + 1 < VPL ? v[i + 1] : -(double)INFINITY;
+                asm("" : "+v"(below));           // (or the list is taken for one that is indexed by what a lane won)
+                v[i] = mine ? below : v[i];
+            }
+        };
+        const int left = p.r.k - 1 - j;
+        if (left <= 4) up(std::integral_constant<int, 4>{});
+        else if (left <= 8) up(std::integral_constant<int, 8>{});
+        else up(std::integral_constant<int, 16>{});
     }
 
     // the weights, from the chosen logits: sigmoid(y) = e^min(y, 0) / (1 + e^-|y|), of which
@@ -839,7 +872,8 @@ hipError_t launch_moe_route_grouped(MoeRouteGrouped g, hipStream_t stream)
     const MoeRoute &p = g.r;
     const int64_t nb = blocks_of(p.T);
     const bool one = p.T <= kRouteTokens;
-    const bool fours = p.E / g.groups % 4 == 0 && (reinterpret_cast<uintptr_t>(p.logits) & 15) == 0;
+    const bool fours = p.E / g.groups % 4 == 0 &&
+                       ((reinterpret_cast<uintptr_t>(p.logits) | reinterpret_cast<uintptr_t>(g.bias)) & 15) == 0;
     int runs = 1;
     while (runs < g.groups) runs *= 2;
     g.lanes = kLanes / runs;

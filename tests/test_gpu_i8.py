@@ -98,7 +98,7 @@ def test_quant_rows_on_odd_addresses():
 DENSE = [(1, 1, 16), (1, 64, 128), (1, 8192, 4096), (2, 33, 48), (5, 100, 144), (16, 256, 1024), (17, 1000, 2064),
          (48, 4096, 512), (63, 65, 912), (64, 2050, 1040), (65, 64, 16), (100, 300, 3200), (200, 4097, 272),
          (256, 256, 384), (300, 520, 4096), (513, 2047, 528), (1024, 1024, 1024), (700, 8200, 256), (2047, 4102, 400),
-         (4096, 4100, 128), (8192, 513, 160)]
+         (4096, 4100, 128), (8192, 513, 160), (64, 8170, 528), (512, 8170, 512), (1030, 4099, 784)]
 
 
 @pytest.mark.parametrize("M,N,K", DENSE)
@@ -206,9 +206,37 @@ def test_experts_rows_and_offsets_out_of_range():
     assert np.all(np.abs(_moe.f64(D) - want) <= _i8.product_bound(want, True))
 
 
+# Groups whose rows make more tiles than their number leads to expect, so that
+# workgroups of the small tiles take several: group sizes, N, K
+RAGGED = [([17, 1] * 4, 1024, 336), ([17, 0, 33, 2] * 4, 700, 1040), ([65] * 4, 640, 2048), ([65] * 4, 1300, 1040),
+          ([1, 129, 0, 70, 64, 3], 1500, 272)]
+
+
+@pytest.mark.parametrize("sizes,N,K", RAGGED)
+@pytest.mark.parametrize("gate", [False, True])
+def test_experts_with_more_tiles_than_expected(sizes, N, K, gate):
+    E, M = len(sizes), sum(sizes)
+    g = _gen(M + N)
+    X, W, sX, sW = _codes(g, 90, K), _codes(g, E, N, K), _scales(g, 90), _scales(g, E, N) / (64 * K ** 0.5)
+    rows = torch.randint(0, 90, (M,), generator=g, dtype=torch.int32)
+    off = np.concatenate([[0], np.cumsum(sizes)])
+    call = dbs.gemm_moe_swiglu_i8 if gate else dbs.gemm_moe_i8
+    args = [t.cuda() for t in (X, sX, W, sW, torch.tensor(off, dtype=torch.int32), rows)]
+    _say("ragged", sizes, N, K, gate)
+    D = call(*args)
+    h = _i8.moe_product(*(_moe.f64(t) for t in (X, sX, W, sW)), off, rows.numpy())
+    if gate:
+        a, u = h[:, : N // 2], h[:, N // 2:]
+        assert np.all(np.abs(_moe.f64(D) - _i8.silu(a) * u) <= _i8.gate_bound(a, u, _i8.scaled_bound(a), _i8.scaled_bound(u)))
+    else:
+        assert np.all(np.abs(_moe.f64(D) - h) <= _i8.product_bound(h, True))
+    with dbs.using_library(dbs.load_poison_library()):
+        assert torch.equal(call(*args), D)
+
+
 @pytest.mark.parametrize("M", [1, 30, 200, 700, 3000])
 def test_experts_of_one_group_are_the_dense_product(M):
-    """The same kernels: bit for bit."""
+    """The same numbers whichever tiles: sums are whole."""
     g = _gen(M)
     A, B, sA, sB = (t.cuda() for t in (_codes(g, M, 320), _codes(g, 600, 320), _scales(g, M), _scales(g, 600)))
     off = torch.tensor([0, M], dtype=torch.int32).cuda()
@@ -284,7 +312,7 @@ def test_other_streams_and_two_calls_at_once():
 
 
 # sizes that reach every kernel, with several tiles to a workgroup
-POISON = [(3, 70000, 200), (900, 33000, 640), (5000, 6000, 400), (9000, 9000, 130), (1500, 2500, 1024), (700, 30000, 260), (2047, 4102, 400)]
+POISON = [(3, 70000, 200), (900, 33000, 640), (5000, 6000, 400), (9000, 9000, 130), (1500, 2500, 1024), (700, 30000, 260), (2047, 4102, 400), (1100, 9000, 768), (64, 30000, 512)]
 
 
 @pytest.mark.parametrize("M,N,K", POISON)
@@ -334,12 +362,3 @@ def test_outputs_beyond_4_gib():
     q, s = dbs.quant_i8(D)
     codes, _ = _i8.quant(_moe.f64(D[r]))
     assert np.array_equal(q[r].cpu().numpy(), codes)
-
-
-def test_sizes_reach_every_kernel():
-    """The rule that the products go by puts the sizes above in every kernel."""
-    rule = dbs.lib().dbs_moe_tile_rows
-    assert {rule(M, 1, N, 0, 0, 256) for M, N, K in DENSE} == {64, 128, 256}
-    assert {rule(M, 1, N, 0, 0, 256) for M, N, K in POISON} == {64, 128, 256}
-    assert {rule(M, E, N, 0, 0, 256) for T, M, E, N, K in EXPERTS} == {64, 128, 256}
-    assert {rule(M, E, 2 * N, 0, 1, 256) for T, M, E, N, K in EXPERTS} == {64, 128, 256}

@@ -12,6 +12,7 @@ import torch
 
 import dense_block_scaled_amd as dbs
 from tests import _i8
+from tests import test_gpu_i8 as shapes
 
 P = ctypes.c_void_p(1 << 20)          # 16-byte aligned, never dereferenced
 P8 = ctypes.c_void_p((1 << 20) + 8)
@@ -210,3 +211,40 @@ def test_plain_gradient_against_differences(kind, renorm):
             z[t, e] -= h
             (wy, _), (wz, _) = (_i8.weights(v, experts, kind, renorm, 1.7) for v in (y, z))
             assert abs(((wy - wz) * d).sum() / (2 * h) - g[t, e]) < 1e-8
+
+
+# ------------------------------------------------------------ sizes and kernels
+
+TILES = {16016, 64016, 64032, 64064, 128128, 128256, 256256}
+
+
+def _tile(M, E, N, K, gate=0):
+    f = dbs.lib().dbs_i8_tile
+    f.argtypes = [ctypes.c_int64] * 4 + [ctypes.c_int] * 2
+    return f(M, E, N, K, gate, 256)
+
+
+def test_gpu_sizes_reach_every_kernel():
+    """The rule that the products go by puts the sizes of the GPU tests in every kernel."""
+    assert {_tile(M, 1, N, K) for M, N, K in shapes.DENSE} == TILES
+    assert {_tile(M, 1, N, K // 16 * 16) for M, N, K in shapes.POISON} >= TILES - {16016, 64016, 64032}
+    ragged = {(tuple(s), N): _tile(sum(s), len(s), N, K) for s, N, K in shapes.RAGGED}
+    assert set(ragged.values()) >= {16016, 64016, 64032}
+    assert {_tile(M, E, N, K) for T, M, E, N, K in shapes.EXPERTS} | set(ragged.values()) == TILES
+    gated = {_tile(M, E, 2 * N, K, 1) for T, M, E, N, K in shapes.EXPERTS}
+    gated |= {_tile(sum(s), len(s), N, K, 1) for s, N, K in shapes.RAGGED}
+    assert gated == TILES - {64016}
+    # small tiles by several to a workgroup: more of them than workgroups
+    for (sizes, N), tile in ragged.items():
+        rows, cols = divmod(tile, 1000)
+        if tile in (16016, 64016, 64032):
+            tiles = sum(-(-n // rows) for n in sizes) * -(-N // cols)
+            assert tiles > (512 if rows == 16 else 256), (sizes, N, tile)
+
+
+def test_the_rule_has_a_tile_for_every_size():
+    rng = np.random.default_rng(5)
+    for _ in range(2000):
+        M, E = int(2 ** rng.uniform(0, 25)), int(2 ** rng.uniform(0, 10))
+        N, K = 2 * int(2 ** rng.uniform(0, 20)), 16 * int(2 ** rng.uniform(0, 12.9))
+        assert _tile(M, E, N, K) in TILES and _tile(M, E, N, K, 1) in TILES - {64016}
