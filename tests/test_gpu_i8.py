@@ -166,7 +166,8 @@ def _split(M, E, seed, first=0, last=0):
 # T, M, E, N, K: gathered rows; sorted ones where T == M
 EXPERTS = [(1, 2, 4, 64, 128), (3, 9, 5, 33, 48), (7, 7, 1, 100, 16), (16, 64, 64, 130, 272), (48, 384, 128, 96, 512),
            (100, 600, 8, 513, 1040), (300, 900, 3, 264, 400), (500, 500, 40, 1000, 96), (600, 2400, 4, 1030, 160),
-           (2000, 8000, 12, 520, 256), (4099, 4099, 6, 2050, 144), (40, 200, 1024, 40, 80)]
+           (2000, 8000, 12, 520, 256), (4099, 4099, 6, 2050, 144), (40, 200, 1024, 40, 80),
+           (3000, 9000, 6, 2050, 528), (300, 1500, 6, 1030, 800)]
 
 
 @pytest.mark.parametrize("T,M,E,N,K", EXPERTS)
