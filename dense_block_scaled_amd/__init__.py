@@ -153,6 +153,8 @@ def _declare(L: ctypes.CDLL) -> None:
     L.moe_combine_bwd_bf16.argtypes = [P, P, P, P, P, I64, P, P, I64, I64, I64, P]
     L.moe_combine_bwd_bf16.restype = I
     F = ctypes.c_float
+    L.moe_route_grouped_workspace.argtypes = [I64, I64, I64]
+    L.moe_route_grouped_workspace.restype = SZ
     L.moe_route_grouped.argtypes = [I, P, P, I64, I64, I64, I, I64, I64, I64, I, F, P, P, P, P, P, P, SZ, P]
     L.moe_route_grouped.restype = I
     L.moe_route_grouped_bwd.argtypes = [I, P, I64, I64, I64, I, I, F, P, P, P, P]
@@ -561,10 +563,10 @@ def _given(out: torch.Tensor | None, shape, dtype, device: torch.device) -> torc
     return out
 
 
-def _routing(T: int, E: int, k: int, device: torch.device):
+def _routing(T: int, E: int, k: int, device: torch.device, workspace):
     """Outputs of a router, and its workspace (bytes, tensor or None)."""
     kk = min(max(k, 0), E)                    # (the library refuses other k; nothing is sized by them)
-    need = int(lib().moe_route_workspace(T, E, kk))
+    need = int(workspace(T, E, kk))
     experts = torch.empty((T, kk), dtype=torch.int32, device=device)
     r = MoeRouting(experts, torch.empty_like(experts, dtype=torch.float32),
                    torch.empty(E + 1, dtype=torch.int32, device=device),
@@ -582,7 +584,7 @@ def moe_route(logits: torch.Tensor, k: int, renormalize: bool = True) -> MoeRout
     T, E = _dims(logits, "logits", 2)
     dev = logits.device
     pl = _arg(logits, "logits", _REAL, (T, E), dev)
-    r, need, ws = _routing(T, E, k, dev)
+    r, need, ws = _routing(T, E, k, dev, lib().moe_route_workspace)
     _call("moe_route", dev, _REAL[logits.dtype], pl, T, E, k, int(bool(renormalize)), r.experts.data_ptr(),
           r.weights.data_ptr(), r.offsets.data_ptr(), r.rows.data_ptr(), r.slots.data_ptr(),
           None if ws is None else ws.data_ptr(), need)
@@ -615,7 +617,7 @@ def moe_route_grouped(logits: torch.Tensor, k: int, bias: torch.Tensor | None = 
     pl = _arg(logits, "logits", _REAL, (T, E), dev)
     pb = None if bias is None else _arg(bias, "bias", _F32, (E,), dev)
     code = _score(scores)
-    r, need, ws = _routing(T, E, k, dev)
+    r, need, ws = _routing(T, E, k, dev, lib().moe_route_grouped_workspace)
     _call("moe_route_grouped", dev, _REAL[logits.dtype], pl, pb, T, E, k, code, groups, kept, operator.index(group_best),
           int(bool(renormalize)), float(scale), r.experts.data_ptr(), r.weights.data_ptr(), r.offsets.data_ptr(),
           r.rows.data_ptr(), r.slots.data_ptr(), None if ws is None else ws.data_ptr(), need)

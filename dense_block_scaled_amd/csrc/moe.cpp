@@ -155,14 +155,14 @@ dbs_status check_route(dbs_real type, const void *logits, int64_t T, int64_t E, 
     return DBS_OK;
 }
 
-dbs_status check_route_outputs(int64_t T, int64_t E, const int32_t *experts, const float *weights, const int32_t *offsets,
-                               const int32_t *rows, const int32_t *slots, const void *workspace, size_t workspace_bytes)
+dbs_status check_route_outputs(const int32_t *experts, const float *weights, const int32_t *offsets,
+                               const int32_t *rows, const int32_t *slots, const void *workspace, size_t workspace_bytes,
+                               int64_t need, uintptr_t alignment)
 {
     if (!experts || !weights || !offsets || !rows || !slots) return fail(DBS_EINVAL, "null pointer argument");
     if (!aligned(experts, 4) || !aligned(weights, 4) || !aligned(offsets, 4) || !aligned(rows, 4) || !aligned(slots, 4))
         return fail(DBS_EINVAL, "misaligned output");
-    const int64_t need = dbs::moe_route_workspace_bytes(T, E);
-    if (need > 0 && (!workspace || !aligned(workspace, 4) || workspace_bytes < (size_t)need))
+    if (need > 0 && (!workspace || !aligned(workspace, alignment) || workspace_bytes < (size_t)need))
         return fail(DBS_EINVAL, "workspace missing, misaligned or too small");
     return DBS_OK;
 }
@@ -199,7 +199,8 @@ dbs_status moe_route(dbs_real type, const void *logits, int64_t T, int64_t E, in
     dbs_status st = check_route(type, logits, T, E, k);
     if (st != DBS_OK) return st;
     if (renormalize != 0 && renormalize != 1) return fail(DBS_EINVAL, "renormalize must be 0 or 1");
-    if ((st = check_route_outputs(T, E, experts, weights, offsets, rows, slots, workspace, workspace_bytes)) != DBS_OK)
+    if ((st = check_route_outputs(experts, weights, offsets, rows, slots, workspace, workspace_bytes,
+                                  dbs::moe_route_workspace_bytes(T, E), 4)) != DBS_OK)
         return st;
     dbs::MoeRoute p{logits, type == DBS_BF16, T, (int)E, (int)k, renormalize, experts, weights, offsets, rows, slots,
                     static_cast<int32_t *>(workspace)};
@@ -219,6 +220,12 @@ dbs_status moe_route_bwd(dbs_real type, const void *logits, int64_t T, int64_t E
                                           dlogits, stream));
 }
 
+size_t moe_route_grouped_workspace(int64_t T, int64_t E, int64_t k)
+{
+    if (T <= 0 || E <= 0 || k <= 0 || E > dbs::kMoeMaxExperts || k > E || k > dbs::kMoeMaxK || T > kMaxRows / k) return 0;
+    return (size_t)dbs::moe_route_grouped_workspace_bytes(T, E);
+}
+
 dbs_status moe_route_grouped(dbs_real type, const void *logits, const float *bias, int64_t T, int64_t E, int64_t k,
                              dbs_score score, int64_t groups, int64_t kept_groups, int64_t group_best, int renormalize,
                              float scale, int32_t *experts, float *weights, int32_t *offsets, int32_t *rows,
@@ -234,7 +241,8 @@ dbs_status moe_route_grouped(dbs_real type, const void *logits, const float *bia
     if (groups > dbs::kMoeMaxGroups) return fail(DBS_EUNSUPPORTED, "more than 16 groups");
     if (dbs::moe_route_grouped_lane(E, groups, true) > dbs::kMoeLaneExperts)
         return fail(DBS_EUNSUPPORTED, "groups too large: more than 64 experts of one to a lane");
-    if ((st = check_route_outputs(T, E, experts, weights, offsets, rows, slots, workspace, workspace_bytes)) != DBS_OK)
+    if ((st = check_route_outputs(experts, weights, offsets, rows, slots, workspace, workspace_bytes,
+                                  dbs::moe_route_grouped_workspace_bytes(T, E), 16)) != DBS_OK)
         return st;
     if (!aligned(bias, 4)) return fail(DBS_EINVAL, "misaligned bias");
     dbs::MoeRouteGrouped g{};

@@ -87,11 +87,13 @@ struct MoeRouteGrouped {
     const float *bias;        // E, or null
     int sigmoid, groups, kept, best;
     float scale;              // of the weights
-    int lanes, q;             // set by the launcher: lanes of a token per group, experts per lane
+    // set by the launcher: lanes of a token per group, experts per lane, counts as bytes, tokens per workgroup
+    int lanes, q, bytes, tokens;
 };
 constexpr int kMoeMaxGroups = 16;        // a lane of a 16-lane token group each
 constexpr int kMoeLaneExperts = 64;
 int moe_route_grouped_lane(int64_t E, int64_t groups, bool fours);
+int64_t moe_route_grouped_workspace_bytes(int64_t T, int64_t E);
 hipError_t launch_moe_route_grouped(MoeRouteGrouped p, hipStream_t stream);
 
 // factor: multiplies the weights' gradients

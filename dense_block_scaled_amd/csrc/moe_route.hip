@@ -294,21 +294,23 @@ __device__ __forceinline__ double row_sum64(double v)
     return v + row_move64<3>(v);
 }
 
-// e^x for -708 <= x <= 708 to about 2^-46: x = n ln 2 + r with ln 2 as the sum of
-// two fp64 numbers, |r| <= 0.3466, and the exponential series to r^11 / 11! (the
-// next term is 6.4e-15)
+// e^x for -708 <= x <= 708 to about 2^-46: x = (n + f) ln 2 with |f| <= 1 / 2, and the
+// series of e^(f ln 2) to its 11th power (the next term is 6.4e-15).  n is
+// taken from the low bits of a sum with 3 2^51, and put in by adding to the exponent
+// (the conversions, v_rndne_f64 and v_ldexp_f64 among them, issue more slowly).
 __device__ __forceinline__ double exp64(double x)
 {
-    const double n = __builtin_rint(x * 1.4426950408889634);
-    const double r = __builtin_fma(n, -2.3190468138462996e-17, __builtin_fma(n, -0.6931471805599453, x));
+    constexpr double kLn2 = 0.6931471805599453, kRound = 6755399441055744.0;
+    const double t = x * 1.4426950408889634, shifted = t + kRound;
+    const double r = (t - (shifted - kRound)) * kLn2;
     double p = 1.0 / 39916800;
+    constexpr double inv[11] = {1.0 / 3628800, 1.0 / 362880, 1.0 / 40320, 1.0 / 5040, 1.0 / 720, 1.0 / 120,
+                                1.0 / 24,      1.0 / 6,      1.0 / 2,     1.0,        1.0};
 #pragma unroll
-    for (int i = 0; i < 11; ++i) {
-        constexpr double inv[11] = {1.0 / 3628800, 1.0 / 362880, 1.0 / 40320, 1.0 / 5040, 1.0 / 720, 1.0 / 120,
-                                    1.0 / 24,      1.0 / 6,      1.0 / 2,     1.0,        1.0};
-        p = __builtin_fma(p, r, inv[i]);
-    }
-    return __builtin_ldexp(p, (int)n);
+    for (int i = 0; i < 11; ++i) p = __builtin_fma(p, r, inv[i]);
+    const uint64_t b = __builtin_bit_cast(uint64_t, p);
+    const uint32_t hi = (uint32_t)(b >> 32) + ((uint32_t)__builtin_bit_cast(uint64_t, shifted) << 20);
+    return __builtin_bit_cast(double, (uint64_t)hi << 32 | (uint32_t)b);
 }
 
 // 1 / x, x a normal number: v_rcp_f64 and two Newton steps
@@ -369,6 +371,50 @@ __device__ __forceinline__ void sort_down(double (&v)[VPL])
         sort_down<LO + N / 2, N / 2>(v);
         merge_sorted<LO, N, 1>(v);
     }
+}
+
+// A descending list of N in every lane becomes that of the N largest of all 16
+// lanes, the same in each: lane by lane the larger of one's list and the
+// other's from its end are the N largest of both, falling and rising, which log2 N
+// steps of exchanges sort.
+template <int STEP, int N, int VPL>
+__device__ __forceinline__ void best_of_both(double (&v)[VPL])
+{
+    double o[N];
+#pragma unroll
+    for (int i = 0; i < N; ++i) o[i] = row_move64<STEP>(v[N - 1 - i]);
+#pragma unroll
+    for (int i = 0; i < N; ++i) v[i] = fmax(v[i], o[i]);
+#pragma unroll
+    for (int d = N / 2; d > 0; d /= 2)
+#pragma unroll
+        for (int i = 0; i < N; ++i)
+            if ((i & d) == 0) {
+                const double hi = fmax(v[i], v[i + d]), lo = fmin(v[i], v[i + d]);
+                v[i] = hi;
+                v[i + d] = lo;
+            }
+}
+
+template <int N, int VPL>
+__device__ __forceinline__ void best_of_row(double (&v)[VPL])
+{
+    best_of_both<0, N>(v);
+    best_of_both<1, N>(v);
+    best_of_both<2, N>(v);
+    best_of_both<3, N>(v);
+}
+
+// How many of the other 15 lanes have a larger value
+template <int BY = 1>
+__device__ __forceinline__ int larger_in_row(double v)
+{
+    const uint64_t b = __builtin_bit_cast(uint64_t, v);
+    const uint32_t lo = __builtin_amdgcn_mov_dpp((int)b, 0x120 + BY, 0xF, 0xF, true);               // row_ror
+    const uint32_t hi = __builtin_amdgcn_mov_dpp((int)(b >> 32), 0x120 + BY, 0xF, 0xF, true);
+    const int n = __builtin_bit_cast(double, (uint64_t)hi << 32 | lo) > v;
+    if constexpr (BY < 15) return n + larger_in_row<BY + 1>(v);
+    return n;
 }
 
 // C consecutive values of an array as fp32: to[i ..]
@@ -476,38 +522,26 @@ __device__ __forceinline__ void choose(const MoeRouteGrouped &p, int64_t tok, in
             if (p.best == 2 && two > -(double)INFINITY) score += unkeyed(two);
             score = keyed(score, group);
         }
-        bool keep = false;
-        for (int j = 0; j < p.kept; ++j) {
-            const double b = row_max64(score);
-            if (b == -(double)INFINITY) break;
-            const bool mine = score == b;
-            keep = keep || mine;
-            score = mine ? -(double)INFINITY : score;
-        }
-        v[0] = keep ? v[0] : -(double)INFINITY;
+        // (a group's lanes all have its score)
+        const bool keep = larger_in_row(score) < p.kept * p.lanes && one > -(double)INFINITY;
+#pragma unroll
+        for (int i = 0; i < (VPL < kMoeMaxK ? VPL : kMoeMaxK); ++i) v[i] = keep ? v[i] : -(double)INFINITY;
     }
 
-    expert = -1;
-    for (int j = 0; j < p.r.k; ++j) {
-        const double b = row_max64(v[0]);
-        if (b == -(double)INFINITY) break;       // no open expert is left
-        expert = l == j ? key_index(b) : expert;
-        // the winner's list moves up, as far as the choices left can reach
-        const bool mine = v[0] == b;
-        auto up = [&](auto n) {
-            constexpr int N = decltype(n)::value < VPL ? decltype(n)::value : VPL;
+    // the k best of all lanes, and the lane's own of them
+    constexpr int N8 = 8, N16 = 16;
+    double w[N16];
 #pragma unroll
-            for (int i = 0; i < N; ++i) {
-                double below = i + 1 < VPL ? v[i + 1] : -(double)INFINITY;
-                asm("" : "+v"(below));           // (or the list is taken for one that is indexed by what a lane won)
-                v[i] = mine ? below : v[i];
-            }
-        };
-        const int left = p.r.k - 1 - j;
-        if (left <= 4) up(std::integral_constant<int, 4>{});
-        else if (left <= 8) up(std::integral_constant<int, 8>{});
-        else up(std::integral_constant<int, 16>{});
+    for (int i = 0; i < N16; ++i) w[i] = i < VPL ? v[i < VPL ? i : 0] : -(double)INFINITY;
+    if (p.r.k <= N8) best_of_row<N8>(w);
+    else best_of_row<N16>(w);
+    double key = w[0];
+#pragma unroll
+    for (int i = 1; i < N16; ++i) {
+        const double other = w[i];
+        key = l == i ? other : key;
     }
+    expert = l < p.r.k && key > -(double)INFINITY ? key_index(key) : -1;
 
     // the weights, from the chosen logits: sigmoid(y) = e^min(y, 0) / (1 + e^-|y|), of which
     // renormalising cancels the largest e^min(y, 0)
@@ -524,26 +558,29 @@ __device__ __forceinline__ void choose(const MoeRouteGrouped &p, int64_t tok, in
     weight = expert >= 0 ? s / total * p.scale : 0.0f;
 }
 
-// As route_select, with the choice above.
-template <int VPL, bool ONE>
-constexpr int choose_threads() { return ONE ? 256 : VPL > 16 ? 512 : 1024; }
+// Rows of counts up to which route_choose leaves them as bytes, and such a row's length
+constexpr int kBytes = 256;
+__host__ __device__ constexpr int byte_row(int E) { return (E + 15) & ~15; }
 
-template <int VPL, int C, bool BF16, bool ONE>
-__global__ __launch_bounds__((choose_threads<VPL, ONE>())) void route_choose(MoeRouteGrouped g)
+// As route_select, with the choice above, g.tokens to a workgroup: 16 while the CUs
+// are not all taken so (1024 tokens of 256 experts on 16 CUs: 15 us), else more.
+template <int VPL, int C, bool BF16, bool ONE, int THREADS>
+__global__ __launch_bounds__(THREADS) void route_choose(MoeRouteGrouped g)
 {
     __shared__ uint64_t mask[kMoeMaxExperts];
     __shared__ int32_t chosen[ONE ? kRouteTokens * kMoeMaxK : 1];
     __shared__ int32_t base[ONE ? kMoeMaxExperts + 1 : 1];
-    __shared__ int32_t part[4];
-    constexpr int kThreads = choose_threads<VPL, ONE>();
+    __shared__ int32_t part[16];
     const MoeRoute &p = g.r;
     const int t = threadIdx.x, l = t & (kLanes - 1);
-    for (int e = t; e < p.E; e += kThreads) mask[e] = 0;
+    for (int e = t; e < p.E; e += THREADS) mask[e] = 0;
     __syncthreads();
-    const int64_t t0 = (int64_t)blockIdx.x * kRouteTokens;
-    for (int tl = t / kLanes; tl < kRouteTokens; tl += kThreads / kLanes) {
+    const int64_t t0 = (int64_t)blockIdx.x * g.tokens;
+    // (256 threads are for 16 tokens, so that those and 1024 have one round, which is no loop)
+    constexpr int kMost = THREADS == 256 ? 16 : kRouteTokens;
+    for (int tl = t / kLanes; tl < kMost; tl += THREADS / kLanes) {
         const int64_t tok = t0 + tl;
-        if (tok >= p.T) break;                   // (uniform in the token's 16 lanes)
+        if (tl >= g.tokens || tok >= p.T) break; // (uniform in the token's 16 lanes)
         int e;
         float w;
         choose<VPL, C, BF16>(g, tok, l, e, w);
@@ -556,14 +593,18 @@ __global__ __launch_bounds__((choose_threads<VPL, ONE>())) void route_choose(Moe
     }
     __syncthreads();
     if constexpr (ONE) {
-        for (int e = t; e < p.E; e += kThreads) base[e] = __popcll(mask[e]);
+        for (int e = t; e < p.E; e += THREADS) base[e] = __popcll(mask[e]);
         __syncthreads();
         int32_t *b = base;
         scan_experts(b, p.E, b, part);
-        for (int e = t; e <= p.E; e += kThreads) p.offsets[e] = base[e];
+        for (int e = t; e <= p.E; e += THREADS) p.offsets[e] = base[e];
         place(p, 0, 0, p.T * p.k, mask, base, nullptr, chosen);
+    } else if (g.bytes) {
+        const int row = byte_row(p.E);
+        uint8_t *counts = reinterpret_cast<uint8_t *>(p.counts) + (int64_t)blockIdx.x * row;
+        for (int e = t; e < row; e += THREADS) counts[e] = e < p.E ? (uint8_t)__popcll(mask[e]) : (uint8_t)0;
     } else {
-        for (int e = t; e < p.E; e += kThreads) p.counts[(int64_t)blockIdx.x * p.E + e] = __popcll(mask[e]);
+        for (int e = t; e < p.E; e += THREADS) p.counts[(int64_t)blockIdx.x * p.E + e] = __popcll(mask[e]);
     }
 }
 
@@ -645,6 +686,81 @@ __global__ __launch_bounds__(kThreads) void route_place(MoeRoute p, int64_t nb)
     }
     __syncthreads();
     place(p, t0, p0, p1, mask, base, DIRECT ? before : p.counts + (int64_t)blockIdx.x * p.E, chosen);
+}
+
+// Up to kBytes rows of counts behind route_choose: they are bytes there (64 tokens
+// make at most 64), rows of whole 16-byte pieces, and every workgroup sums all
+// of them for itself, two launches in place of three (16384 tokens of 256
+// experts: 64 KiB a workgroup, 7.3 us where the two kernels take 9.1 and a launch).  A
+// thread sums 16 experts of every so manyth row as pairs of 16-bit numbers, its
+// wave's lanes and then the waves meet.
+__global__ __launch_bounds__(1024) void route_place_bytes(MoeRoute p, int nb, int tokens)
+{
+    typedef __attribute__((ext_vector_type(4))) uint32_t u32x4;
+    __shared__ uint64_t mask[kMoeMaxExperts];
+    __shared__ int32_t base[kMoeMaxExperts + 1], before[kMoeMaxExperts], total[kMoeMaxExperts];
+    __shared__ uint32_t sums[2][kMoeMaxExperts / 2];       // [0: the rows before, 1: all][16-bit pairs]
+    __shared__ int32_t chosen[kRouteTokens * kMoeMaxK];
+    __shared__ int32_t part[16];
+    const int t = threadIdx.x, lane = t & 63;
+    const int row = byte_row(p.E), pieces = row / 16;
+    int width = 1;                               // threads a row: a power of two up to 64
+    while (width < pieces) width *= 2;
+    const uint8_t *counts = reinterpret_cast<const uint8_t *>(p.counts);
+    const int piece = t & (width - 1), group = t / width, groups = 1024 / width;
+    // (64 tokens have at most 1024 pairs: one a thread)
+    const int64_t t0 = (int64_t)blockIdx.x * tokens;
+    const int64_t p0 = t0 * p.k, p1 = (t0 + tokens < p.T ? t0 + tokens : p.T) * p.k;
+    const int expert = p0 + t < p1 ? p.experts[p0 + t] : -1;
+    for (int e = t; e < kMoeMaxExperts; e += 1024) {
+        mask[e] = 0;
+        if (e < kMoeMaxExperts / 2) sums[0][e] = sums[1][e] = 0;
+    }
+    uint32_t mine[8] = {}, all[8] = {};          // (at most 16 rows a thread: sums of 1024)
+    if (piece < pieces) {
+#pragma unroll 4
+        for (int r = group; r < nb; r += groups) {
+            const u32x4 v = *reinterpret_cast<const u32x4 *>(counts + r * row + 16 * piece);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const uint32_t even = v[i] & 0x00FF00FFu, odd = (v[i] >> 8) & 0x00FF00FFu;
+                all[2 * i] += even;
+                all[2 * i + 1] += odd;
+                mine[2 * i] += r < (int)blockIdx.x ? even : 0;
+                mine[2 * i + 1] += r < (int)blockIdx.x ? odd : 0;
+            }
+        }
+    }
+    for (int d = width; d < 64; d *= 2) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            all[i] += (uint32_t)__shfl_xor((int)all[i], d);
+            mine[i] += (uint32_t)__shfl_xor((int)mine[i], d);
+        }
+    }
+    __syncthreads();
+    if (lane < width && piece < pieces) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            // word i of a piece: experts 4 (i / 2) + i % 2 and two further on
+            atomicAdd(&sums[0][8 * piece + i], mine[i]);
+            atomicAdd(&sums[1][8 * piece + i], all[i]);
+        }
+    }
+    __syncthreads();
+    for (int e = t; e < p.E; e += 1024) {
+        const int w = 8 * (e / 16) + 2 * (e % 16 / 4) + (e & 1), up = (e & 2) * 8;
+        before[e] = (int)(sums[0][w] >> up & 0xFFFF);
+        total[e] = (int)(sums[1][w] >> up & 0xFFFF);
+    }
+    static_assert(kRouteTokens * kMoeMaxK <= 1024, "a pair a thread");
+    if (p0 + t < p1) chosen[t] = expert;
+    if (expert >= 0) atomicOr(reinterpret_cast<unsigned long long *>(&mask[expert]), 1ull << (t / p.k));
+    __syncthreads();
+    scan_experts(total, p.E, base, part);        // (ends with a barrier)
+    if (blockIdx.x == 0)
+        for (int e = t; e <= p.E; e += 1024) p.offsets[e] = base[e];
+    place(p, t0, p0, p1, mask, base, before, chosen);
 }
 
 // dlogits = p (u - sum p u): p the softmax over all experts, or over the
@@ -867,10 +983,24 @@ int moe_route_grouped_lane(int64_t E, int64_t groups, bool fours)
     return (int)q;
 }
 
+// Tokens a workgroup of T: 16, or 32, while there are no more of them than kBytes, else 64
+static int grouped_tokens(int64_t T)
+{
+    return T <= kRouteTokens ? kRouteTokens : T <= 16 * kBytes ? 16 : T <= 32 * kBytes ? 32 : 64;
+}
+
+int64_t moe_route_grouped_workspace_bytes(int64_t T, int64_t E)
+{
+    const int64_t tokens = grouped_tokens(T), nb = (T + tokens - 1) / tokens;
+    if (T <= kRouteTokens) return 0;
+    return nb <= kBytes ? nb * byte_row((int)E) : moe_route_workspace_bytes(T, E);
+}
+
 hipError_t launch_moe_route_grouped(MoeRouteGrouped g, hipStream_t stream)
 {
     const MoeRoute &p = g.r;
-    const int64_t nb = blocks_of(p.T);
+    g.tokens = grouped_tokens(p.T);
+    const int64_t nb = (p.T + g.tokens - 1) / g.tokens;
     const bool one = p.T <= kRouteTokens;
     const bool fours = p.E / g.groups % 4 == 0 &&
                        ((reinterpret_cast<uintptr_t>(p.logits) | reinterpret_cast<uintptr_t>(g.bias)) & 15) == 0;
@@ -878,10 +1008,13 @@ hipError_t launch_moe_route_grouped(MoeRouteGrouped g, hipStream_t stream)
     while (runs < g.groups) runs *= 2;
     g.lanes = kLanes / runs;
     g.q = moe_route_grouped_lane(p.E, g.groups, fours);
+    g.bytes = !one && nb <= kBytes;
+    const bool few = one ? p.T <= 16 : g.tokens == 16;
     auto go = [&](auto vpl, auto c, auto bf16, auto whole) {
-        constexpr int V = decltype(vpl)::value, C = decltype(c)::value;
+        constexpr int V = decltype(vpl)::value, C = decltype(c)::value, MANY = V > 16 ? 512 : 1024;
         constexpr bool B = decltype(bf16)::value, ONE = decltype(whole)::value;
-        hipLaunchKernelGGL((route_choose<V, C, B, ONE>), dim3(ONE ? 1 : nb), dim3(choose_threads<V, ONE>()), 0, stream, g);
+        if (few) hipLaunchKernelGGL((route_choose<V, C, B, ONE, 256>), dim3(nb), dim3(256), 0, stream, g);
+        else hipLaunchKernelGGL((route_choose<V, C, B, ONE, MANY>), dim3(nb), dim3(MANY), 0, stream, g);
         return hipGetLastError();
     };
     auto by_type = [&](auto vpl, auto c) {
@@ -898,7 +1031,9 @@ hipError_t launch_moe_route_grouped(MoeRouteGrouped g, hipStream_t stream)
     else if (g.q <= 32) e = by_load(std::integral_constant<int, 32>{});
     else e = by_load(std::integral_constant<int, 64>{});
     if (e != hipSuccess || one) return e;
-    return launch_place(p, nb, stream);
+    if (!g.bytes) return launch_place(p, nb, stream);
+    hipLaunchKernelGGL(route_place_bytes, dim3(nb), dim3(1024), 0, stream, p, (int)nb, g.tokens);
+    return hipGetLastError();
 }
 
 hipError_t launch_moe_route_bwd(const void *logits, int bf16, int64_t T, int E, int k, int sigmoid, int renorm, float factor,

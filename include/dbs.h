@@ -398,8 +398,9 @@ dbs_status moe_route_bwd(dbs_real type, const void *logits, int64_t T, int64_t E
  * closes its expert to every token, +inf counts as the largest finite value.  A
  * closed expert adds nothing to its group; a group with none open is not kept.
  * c is computed in fp64; values that agree to 2^-42 of their size are
- * ties, which go to the lower expert (group).  Outputs and workspace
- * (moe_route_workspace) are moe_route's.  At most 16 groups, and at most 64
+ * ties, which go to the lower expert (group).  Outputs are moe_route's; the
+ * workspace is moe_route_grouped_workspace(T, E, k) bytes (0 up to 64 tokens) on
+ * 16, and like moe_route's otherwise.  At most 16 groups, and at most 64
  * experts of a group to each of the 16 / (groups rounded up to a power of two)
  * lanes that a token has for it (DBS_EUNSUPPORTED; any E up to 512).
  * moe_route_grouped_bwd: dlogits from the weights' gradients, with the experts
@@ -413,6 +414,7 @@ typedef enum {
     DBS_SIGMOID = 1
 } dbs_score;
 
+size_t moe_route_grouped_workspace(int64_t T, int64_t E, int64_t k);      /* 0 for invalid sizes too */
 dbs_status moe_route_grouped(dbs_real type, const void *logits, const float *bias, int64_t T, int64_t E, int64_t k,
                              dbs_score score, int64_t groups, int64_t kept_groups, int64_t group_best, int renormalize,
                              float scale, int32_t *experts, float *weights, int32_t *offsets, int32_t *rows,

@@ -65,7 +65,10 @@ def test_route(T, E, k, groups, kept, best, dtype, scores, renorm, closed, bias)
     _check(x, k, b, groups, kept, best, scores, renorm, 2.5)
 
 
-@pytest.mark.parametrize("T,E,k,groups,kept", [(2048, 32, 4, 4, 2), (2049, 48, 4, 8, 4), (4500, 160, 6, 8, 3)])
+# 16, 32 and 64 tokens to a workgroup on both sides of each switch, counts of one and of several threads a row
+@pytest.mark.parametrize("T,E,k,groups,kept", [(2048, 32, 4, 4, 2), (2049, 48, 4, 8, 4), (4500, 160, 6, 8, 3), (4096, 17, 3, 1, 1),
+                                               (8192, 24, 16, 2, 2), (8193, 3, 2, 1, 1), (16384, 20, 2, 4, 3),
+                                               (16385, 36, 3, 4, 2), (1100, 1024, 4, 8, 4), (600, 520, 5, 1, 1)])
 @pytest.mark.parametrize("scores", ["sigmoid", "softmax"])
 def test_route_of_many_tokens(T, E, k, groups, kept, scores):
     x = _logits(T, E, torch.float32, T, 0.3)

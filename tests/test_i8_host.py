@@ -94,10 +94,18 @@ def _route(type=0, logits=P, bias=N0, T=4, E=8, k=2, score=1, groups=2, kept=1, 
     (dict(E=1023, groups=11, kept=11), EUNSUP),                         # 93 experts to a lane
     (dict(renorm=2), EINVAL), (dict(scale=float("inf")), EINVAL), (dict(scale=float("nan")), EINVAL),
     (dict(experts=N0), EINVAL), (dict(weights=P2), EINVAL), (dict(slots=N0), EINVAL), (dict(bias=P2), EINVAL),
-    (dict(logits=P2), EINVAL), (dict(T=65), EINVAL), (dict(T=65, ws=P, n=4), EINVAL), (dict(T=65, ws=P2, n=1 << 20), EINVAL),
+    (dict(logits=P2), EINVAL), (dict(T=65), EINVAL), (dict(T=65, ws=P, n=4), EINVAL), (dict(T=65, ws=P8, n=1 << 20), EINVAL),
 ])
 def test_route_grouped_refusals(more, want):
     _refused("moe_route_grouped", _route(**more), want)
+
+
+def test_route_grouped_workspace_sizes():
+    ws = dbs.lib().moe_route_grouped_workspace
+    assert ws(64, 128, 8) == 0 and ws(0, 8, 2) == 0 and ws(100, 8, 9) == 0 and ws(100, 2000, 2) == 0
+    # rows of bytes for 16, 32 or 64 tokens, of 32-bit counts and their totals above 16384
+    assert ws(65, 8, 2) == 5 * 16 and ws(4096, 160, 2) == 256 * 160 and ws(4097, 161, 2) == 129 * 176
+    assert ws(16384, 256, 8) == 256 * 256 and ws(16385, 3, 2) == 258 * 3 * 4
 
 
 # type, logits, T, E, k, score, renorm, scale, experts, dweights, dlogits
