@@ -61,13 +61,13 @@ I8Tile i8_tile(int64_t M, int64_t E, int64_t N, int64_t ncols, int64_t K, bool g
     }
     auto deep = [&](int cols, double first, double next) {
         const double x = tiles(64, cols) / n;
-        offer(64, cols, 5.2 + first * k + more(x) * (1.9 + next * k));
+        offer(64, cols, 4.8 + first * k + more(x) * (1.9 + next * k));
     };
     if (!gate) deep(16, 0.6, 0.75);
     deep(32, 0.95, 1.05);
     deep(64, 1.42, 1.55);
     double x = tiles(128, 128) / n;
-    offer(128, 128, 7 + 3.9 * k + more(x) * (3.2 + 4.4 * k));
+    offer(128, 128, 6.6 + 3.9 * k + more(x) * (3.2 + 4.4 * k));
     x = tiles(128, 256) / n;
     offer(128, 256, 7 + (7 + 1.3 * std::min(x, 1.0)) * k + more(x) * (4 + 7.9 * k));
     x = tiles(256, 256) / n;

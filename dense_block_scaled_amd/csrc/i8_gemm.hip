@@ -30,28 +30,6 @@ struct MulI8 {
     }
 };
 
-template <int TM>
-__device__ __forceinline__ void fill_table(Table<TM> &tab, const I8Gemm &p, const Lane &c)
-{
-    if (!p.offsets) {
-        if (threadIdx.x == 0) {
-            tab.first[0] = tab.whole[0] = 0;
-            tab.first[1] = p.M;
-            tab.whole[1] = Table<TM>::whole_of(p.M);
-#pragma unroll
-            for (int b = 0; b < Table<TM>::kRests; ++b) {
-                tab.rest[b][0] = 0;
-                tab.rest[b][1] = (uint16_t)Table<TM>::rest_of(p.M, b + 1);
-            }
-        }
-    } else if (c.w == 0) {
-        group_table<true>(tab.first, tab.whole, p.offsets, p.E, p.M, c, [](int rows) { return Table<TM>::whole_of(rows); });
-    } else if (c.w < TM / 64) {
-        group_table<false>(tab.first, tab.rest[c.w - 1], p.offsets, p.E, p.M, c,
-                           [&](int rows) { return Table<TM>::rest_of(rows, c.w); });
-    }
-}
-
 // Rows from .. to-1 of D are zero (those before the first group and behind the last).
 __device__ __forceinline__ void zero_rows(const I8Gemm &p, int64_t from, int64_t to)
 {
@@ -63,6 +41,56 @@ __device__ __forceinline__ void zero_rows(const I8Gemm &p, int64_t from, int64_t
     else
         for (int64_t o = me * 2; o < bytes; o += all * 2) *reinterpret_cast<uint16_t *>(z + o) = 0;
 }
+
+// The tiles of a call: of groups by a table in LDS (moe_tiles.h), of the dense
+// product's one group in the same order by arithmetic on its sizes, which saves
+// small calls the way through LDS (three tiles of it before the first loads).
+template <int TM>
+struct Tiles {
+    Table<TM> &tab;
+    const I8Gemm &p;
+    const Lane &c;
+    int tiles_n, tno, count;
+
+    __device__ __forceinline__ Tiles(Table<TM> &t, const I8Gemm &args, const Lane &lane, int width)
+        : tab(t), p(args), c(lane), tiles_n((args.ncols + width - 1) / width), tno(width)
+    {
+        if (!p.offsets) {
+            count = (p.M + TM - 1) / TM * tiles_n;
+            return;
+        }
+        if (c.w == 0)
+            group_table<true>(tab.first, tab.whole, p.offsets, p.E, p.M, c, [](int rows) { return Table<TM>::whole_of(rows); });
+        else if (c.w < TM / 64)
+            group_table<false>(tab.first, tab.rest[c.w - 1], p.offsets, p.E, p.M, c,
+                               [&](int rows) { return Table<TM>::rest_of(rows, c.w); });
+        __syncthreads();
+        zero_rows(p, 0, tab.first[0]);
+        zero_rows(p, tab.first[p.E], p.M);
+        count = count_tiles(tab, p.E, tiles_n);
+    }
+
+    __device__ __forceinline__ RowTile operator()(int id) const
+    {
+        if (p.offsets)
+            return find_tile(tab, p.E, count, tiles_n, tno, id, [&](const auto *at, int n) { return group_of(at, p.E, n, c); });
+        RowTile r{};
+        if (id >= count) return r;
+        const int whole = Table<TM>::whole_of(p.M);
+        r.mend = p.M;
+        if (id < whole * tiles_n) {
+            const int band = id / (kBand * tiles_n), rows = min(whole - band * kBand, kBand), in = id - band * kBand * tiles_n;
+            r.m0 = (band * kBand + in % rows) * TM;
+            r.n0 = in / rows * tno;
+            r.blocks = TM / 64;
+        } else {
+            r.m0 = p.M / TM * TM;
+            r.n0 = (id - whole * tiles_n) * tno;
+            r.blocks = Table<TM>::blocks(p.M);
+        }
+        return r;
+    }
+};
 
 // The workgroups that the tiles are spread over: no more than there are tiles,
 // by eights, so that every XCD has its share of few (a grid is sized before the
@@ -172,25 +200,17 @@ __global__ __launch_bounds__(512, 1) void i8_tiles(I8Gemm p)
     __shared__ uint32_t rowbuf[256];
     __shared__ __attribute__((aligned(16))) float scales[2][2][256];   // [parity of the tile][0: rows, 1: columns]
     constexpr int TNO = GATE ? 128 : 256;              // output columns of a tile
-    constexpr int kStores = GATE ? 8 : F32 ? 32 : 16;  // store instructions of a whole tile (vec)
+    constexpr int kStores = TM / 64 * (GATE ? 2 : F32 ? 8 : 4);        // store instructions of a whole tile (vec)
 
     Lane c = lane_of();
     const int lda = p.K;
-    const int tiles_n = (p.ncols + TNO - 1) / TNO;
-    fill_table(tab, p, c);
-    __syncthreads();
-    zero_rows(p, 0, tab.first[0]);
-    zero_rows(p, tab.first[p.E], p.M);
-    const int ntiles = count_tiles(tab, p.E, tiles_n);
-    const int nwg = spread(ntiles), self = first_of(nwg, ntiles);
-    if (self >= ntiles) return;
+    const Tiles<TM> tiles(tab, p, c, TNO);
+    const int nwg = spread(tiles.count), self = first_of(nwg, tiles.count);
+    if (self >= tiles.count) return;
     // at least three stages (the surplus reads zeros): the next tile's row
     // indices and scales land within a tile
     const int nk = max((p.K + kRowBytes - 1) / kRowBytes, 3);
-    auto find = [&](int round) {
-        return find_tile(tab, p.E, ntiles, tiles_n, TNO, snake(round, nwg, self),
-                         [&](const auto *at, int id) { return group_of(at, p.E, id, c); });
-    };
+    auto find = [&](int round) { return tiles(snake(round, nwg, self)); };
 
     // What the loads read: stage lk of the tile behind ra and rb.
     i32x4 ra, rb;
@@ -276,7 +296,7 @@ __global__ __launch_bounds__(512, 1) void i8_tiles(I8Gemm p)
         if (lk == first_k) aim(next, parity ^ 1);
     };
     fetch(cur);
-    turn_end<0>();
+    if (p.rows) turn_end<0>();
     aim(cur, 0);
     load(kALo, 0);
     load(kBLo, 0);
@@ -333,7 +353,7 @@ __global__ __launch_bounds__(512, 1) void i8_tiles(I8Gemm p)
                 }
             }
         }
-        stored = p.vec && NLO + NHI == 4;
+        stored = p.vec && NLO + NHI == TM / 64;
     };
     using I0 = std::integral_constant<int, 0>;
     using I1 = std::integral_constant<int, 1>;
@@ -407,24 +427,15 @@ __global__ __launch_bounds__(512, 1) void i8_tiles_deep(I8Gemm p)
     const Lane c = lane_of();
     const int wm = c.w / (S::WN * KS), wn = c.w / KS % S::WN, ks2 = KS == 2 ? c.w & 1 : 0, j = c.lane & 15, g = c.lane >> 4;
     const int lda = p.K;
-    const int tiles_n = (p.ncols + TNO - 1) / TNO;
-    fill_table(tab, p, c);
-    __syncthreads();
-    zero_rows(p, 0, tab.first[0]);
-    zero_rows(p, tab.first[p.E], p.M);
-    const int ntiles = count_tiles(tab, p.E, tiles_n);
-    const int nwg = spread(ntiles);
-    int tile = first_of(nwg, ntiles);
-    if (tile >= ntiles) return;
+    const Tiles<TM> find(tab, p, c, TNO);
+    const int nwg = spread(find.count);
+    int tile = first_of(nwg, find.count);
+    if (tile >= find.count) return;
     // more stages than the loads are ahead: they turn to the next tile behind a
     // barrier of this one, when the tile before's scales have been read.  (PIPE:
     // an even number, the two sets of registers take turns)
     int nk = max((p.K + S::kStageBytes - 1) / S::kStageBytes, S::kAhead + 1);
     if (S::PIPE) nk += nk & 1;
-    auto find = [&](int id) {
-        return find_tile(tab, p.E, ntiles, tiles_n, TNO, id,
-                         [&](const auto *at, int n) { return group_of(at, p.E, n, c); });
-    };
 
     // wave w loads rows 8 w .. (and 64 further down) of A; wave-load w + 8 q of W's: eight rows of one of the H parts
     i32x4 ra, rb;
@@ -498,10 +509,11 @@ __global__ __launch_bounds__(512, 1) void i8_tiles_deep(I8Gemm p)
     };
 
     int parity = 0;
-    RowTile cur = find(tile), next = find(tile + nwg);
+    RowTile cur = find(tile);
     fetch(cur, 0);
+    RowTile next = find(tile + nwg);
     fetch(next, 1);
-    turn_end<0>();
+    if (p.rows) turn_end<0>();
     aim(cur, 0);
 #pragma unroll
     for (int f = 0; f < S::kAhead; ++f) load(f, f);
@@ -649,19 +661,15 @@ __global__ __launch_bounds__(512, 4) void i8_rows(I8Gemm p)
     const int j = c.lane & 15, g = c.lane >> 4;
     const int tiles_n = (p.ncols + 15) / 16;
     auto tiles_of = [](int rows) { return (rows + 15) / 16; };
-    if (!p.offsets) {
-        if (threadIdx.x == 0) {
-            first[0] = at[0] = 0;
-            first[1] = p.M;
-            at[1] = tiles_of(p.M);
-        }
-    } else if (c.w == 0) {
-        group_table<true>(first, at, p.offsets, p.E, p.M, c, tiles_of);
+    int row_tiles = tiles_of(p.M);               // (of the dense product)
+    if (p.offsets) {
+        if (c.w == 0) group_table<true>(first, at, p.offsets, p.E, p.M, c, tiles_of);
+        __syncthreads();
+        zero_rows(p, 0, first[0]);
+        zero_rows(p, first[p.E], p.M);
+        row_tiles = same(at[p.E]);
     }
-    __syncthreads();
-    zero_rows(p, 0, first[0]);
-    zero_rows(p, first[p.E], p.M);
-    const int ntiles = same(at[p.E]) * tiles_n, nwg = spread(ntiles);
+    const int ntiles = row_tiles * tiles_n, nwg = spread(ntiles);
     int tile = first_of(nwg, ntiles);
     if (tile >= ntiles) return;
     // the wave's k-steps; the lane's end of them
@@ -677,9 +685,14 @@ __global__ __launch_bounds__(512, 4) void i8_rows(I8Gemm p)
         if (id >= ntiles) return t;
         const int row_tile = id / tiles_n;
         t.n0 = (id - row_tile * tiles_n) * 16;
-        t.grp = p.offsets ? group_of(at, p.E, row_tile, c) : 0;
-        t.m0 = same(first[t.grp]) + (row_tile - same(at[t.grp])) * 16;
-        t.left = min(same(first[t.grp + 1]) - t.m0, 16);
+        t.m0 = row_tile * 16;
+        int end = p.M;
+        if (p.offsets) {
+            t.grp = group_of(at, p.E, row_tile, c);
+            t.m0 = same(first[t.grp]) + (row_tile - same(at[t.grp])) * 16;
+            end = same(first[t.grp + 1]);
+        }
+        t.left = min(end - t.m0, 16);
         t.row = j < t.left ? (p.rows ? (uint32_t)p.rows[t.m0 + j] : (uint32_t)j) : ~0u;
         return t;
     };
