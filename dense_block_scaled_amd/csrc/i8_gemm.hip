@@ -488,24 +488,27 @@ __global__ __launch_bounds__(512, 1) void i8_tiles_deep(I8Gemm p)
                    (place * kScales + c.w * 64) * 4, e < TN && at < p.N ? (uint32_t)at * 4u : kRowOOB);
         }
     };
-    auto load = [&](int slot, int ks) {
-        ks += rot;
-        ks -= ks >= nk ? nk : 0;
+    // Wave-load q of the wave's kLoads of a stage at `k0` of the row: X's, then W's
+    auto load_one = [&](int q, int slot, int k0) {
         const uint32_t dst = slot * S::kSlot;
-        const int k0 = ks * S::kStageBytes;
-#pragma unroll
-        for (int h = 0; h < H; ++h) {
-            const int kc = (int)ax + k0 + h * kRowBytes;
-#pragma unroll
-            for (int q = 0; q < S::kLoadsA; ++q)
-                dma<16>(ra, lds, dst + h * S::kHalf + (c.w + 8 * q) * 1024, kc < lda ? aoff[q] + kc : kRowOOB);
-        }
-#pragma unroll
-        for (int q = 0; q < S::kLoadsW; ++q) {
+        if (q < H * S::kLoadsA) {
+            const int h = q / S::kLoadsA, r = q % S::kLoadsA, kc = (int)ax + k0 + h * kRowBytes;
+            dma<16>(ra, lds, dst + h * S::kHalf + (c.w + 8 * r) * 1024, kc < lda ? aoff[r] + kc : kRowOOB);
+        } else {
+            q -= H * S::kLoadsA;
             const int i = c.w + 8 * q, h = i / (TN / 8), kc = (int)bx + k0 + h * kRowBytes;
             dma<16>(rb, lds, dst + h * S::kHalf + S::kA + i % (TN / 8) * 1024,
                     kc < lda ? boff[S::kRowsW > 1 ? q : 0] + kc : kRowOOB);
         }
+    };
+    auto start_of = [&](int ks) {
+        ks += rot;
+        return (ks >= nk ? ks - nk : ks) * S::kStageBytes;
+    };
+    auto load = [&](int slot, int ks) {
+        const int k0 = start_of(ks);
+#pragma unroll
+        for (int q = 0; q < S::kLoads; ++q) load_one(q, slot, k0);
     };
 
     int parity = 0;
@@ -523,15 +526,17 @@ __global__ __launch_bounds__(512, 1) void i8_tiles_deep(I8Gemm p)
     struct Blocks {
         bf16x8 a[S::kSteps][RB], b[S::kSteps][NB];
     };
+    // read n of the kReads of a stage
+    constexpr int kReads = S::kSteps * (RB + NB);
+    auto read_one = [&](Blocks &f, int slot, int n) {
+        const int kk = n / (RB + NB), i = n % (RB + NB);
+        const uint32_t from = (uint32_t)(slot * S::kSlot + (KS * (kk >> 1) + ks2) * S::kHalf);
+        if (i < NB) f.b[kk][i] = deep_frag(lds, fb + from, kk & 1, i);
+        else f.a[kk][i - NB] = deep_frag(lds, fa + from, kk & 1, i - NB);
+    };
     auto read = [&](Blocks &f, int slot) {
 #pragma unroll
-        for (int kk = 0; kk < S::kSteps; ++kk) {
-            const uint32_t from = (uint32_t)(slot * S::kSlot + (KS * (kk >> 1) + ks2) * S::kHalf);
-#pragma unroll
-            for (int i = 0; i < RB; ++i) f.a[kk][i] = deep_frag(lds, fa + from, kk & 1, i);
-#pragma unroll
-            for (int u = 0; u < NB; ++u) f.b[kk][u] = deep_frag(lds, fb + from, kk & 1, u);
-        }
+        for (int n = 0; n < kReads; ++n) read_one(f, slot, n);
     };
     Blocks even, odd;
     if constexpr (S::PIPE) {
@@ -572,10 +577,19 @@ __global__ __launch_bounds__(512, 1) void i8_tiles_deep(I8Gemm p)
         if constexpr (S::PIPE) {
             auto stage = [&](const Blocks &now, Blocks &then, int s) {
                 const int ks = ahead(s), after_rs = rs + 1 == S::NS ? 0 : rs + 1;
-                read(then, after_rs);
-                load(rs, ks);
-                DBS_FENCE();
-                if (busy) multiply(now);
+                const int k0 = start_of(ks);
+                // reads and loads stand between the products, which they would hold back in front of them
+                constexpr int kAll = S::kSteps * RB * NB;
+#pragma unroll
+                for (int m = 0; m < kAll; ++m) {
+                    const int kk = m / (RB * NB), i = m / NB % RB, u = m % NB;
+                    acc[i][u] = MulI8::mul(now.b[kk][u], now.a[kk][i], acc[i][u]);
+                    DBS_FENCE();
+                    if (m < kReads) read_one(then, after_rs, m);
+                    if (m % (kAll / S::kLoads) == kAll / S::kLoads - 1) load_one(m / (kAll / S::kLoads), rs, k0);
+                    DBS_FENCE();
+                }
+                static_assert(kAll >= kReads && kAll % S::kLoads == 0, "a place for every read and load");
                 stage_barrier<S::kWait>();
                 rs = after_rs;
             };
