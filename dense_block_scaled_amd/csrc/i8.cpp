@@ -20,20 +20,21 @@ namespace dbs {
 // 5.5 TB/s where that is more.  Groups (E > 1) are known on the device only: M / E rows of
 // each, half a tile of each is waste, some may have none; tiles then even out,
 // and rounds are counted in parts.  us of the dense product with tiles of 16 x 16 /
-// 64 x 16 / 64 x 32 / 64 x 64 / 128 x 128 / 128 x 256 / 256 x 256:
+// 64 x 16 / 64 x 32 / 64 x 64 / 128 x 128 / 256 x 256:
 //
-//      1 x 4096 x 4096     5.0   7.5   8.9  10.6    23    35    38
+//      1 x 4096 x 4096     5.0   7.5   8.9  10.2    18    35
 //     16 x 8192 x 4096    10.2  12.4   9.5  11.0
 //     48 x 4096 x 4096    17.8   8.0   9.3  11.0
-//    128 x 8192 x 4096      63    22  15.7  11.9    24    36    39
-//    512 x 8192 x 1024     113    42    26  16.5  11.8  15.0  19.5
-//   1024 x 4096 x 4096                  54    36    25    35    46
-//   2048 x 4096 x 4096                  94    66    46    41    47
-//   4096 x 4096 x 4096                 180   127    85    75    57
+//    128 x 8192 x 4096      63    22  15.7  12.0    20    39
+//    512 x 8192 x 1024     113    42    26  16.3  10.6    20
+//   1024 x 4096 x 4096                  54    41    24    47
+//   2048 x 4096 x 4096                  94    71    42    48
+//   4096 x 4096 x 4096                 180   127    81    59
 //
-// and of 64 .. 8191 rows each to 4 of 32 experts of 2056 x 4096, with the last four, 57 / 71 /
-// 63 / 67 for 64 rows, 77 / 75 / 73 / 77 for 512, 110 / 95 / 85 / 83 for 1024, 563 / 401 / 361 / 282
-// for 8191.
+// and of 16 .. 8191 rows each to 4 of 32 experts of 2056 x 4096, with the last three, 40 / 54 /
+// 42 for 16 rows, 75 / 76 / 79 for 512, 105 / 95 / 84 for 1024, 586 / 377 / 293 for 8191.  (A tile of
+// 128 x 256 on the core of 256 x 256 was nowhere the fastest: 38 .. 79 us for the last three rows, 76
+// for 512 rows to the experts.)
 I8Tile i8_tile(int64_t M, int64_t E, int64_t N, int64_t ncols, int64_t K, bool gate, int cus)
 {
     const double k = K / 1024.0, n = cus;
@@ -67,9 +68,7 @@ I8Tile i8_tile(int64_t M, int64_t E, int64_t N, int64_t ncols, int64_t K, bool g
     deep(32, 0.95, 1.05);
     deep(64, 1.42, 1.55);
     double x = tiles(128, 128) / n;
-    offer(128, 128, 6.6 + 3.9 * k + more(x) * (3.2 + 4.4 * k));
-    x = tiles(128, 256) / n;
-    offer(128, 256, 7 + (7 + 1.3 * std::min(x, 1.0)) * k + more(x) * (4 + 7.9 * k));
+    offer(128, 128, 6.1 + (2.7 + 1.6 * std::min(x, 1.0)) * k + more(x) * (1.3 + 4.35 * k));
     x = tiles(256, 256) / n;
     offer(256, 256, 10 + (8.6 + 3.1 * std::min(x, 1.0)) * k + more(x) * (7 + 12.2 * k));
     return best;

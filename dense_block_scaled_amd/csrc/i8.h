@@ -28,7 +28,7 @@ struct I8Gemm {
 };
 
 // An output tile: 16 rows by 16 columns; 64 by the columns of 64, 32 or (without
-// the gate) 16 rows of W; 128 by those of 128; 128 or 256 by those of 256.
+// the gate) 16 rows of W; 128 by those of 128; 256 by those of 256.
 struct I8Tile {
     int rows, cols;
 };

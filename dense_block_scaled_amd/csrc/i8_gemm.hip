@@ -188,13 +188,12 @@ __device__ __forceinline__ void store_rows(uint8_t *buf, const I8Gemm &p, int r0
     }
 }
 
-// 256-row tiles, or of 128 rows (TM) where a call has too few of the large ones
-// for the CUs: the same stages, A's upper half filled with zeros and not
-// multiplied.  GATE, F32: see the head of the file.
-template <int TM, bool GATE, bool F32>
+// 256-row tiles by 256 rows of W; where a group has fewer rows left, the 64s of it that
+// it has are multiplied.  GATE, F32: see the head of the file.
+template <bool GATE, bool F32>
 __global__ __launch_bounds__(512, 1) void i8_tiles(I8Gemm p)
 {
-    constexpr int kBufs = kStage, kLds = kStage + 8 * 1024;
+    constexpr int TM = 256, kBufs = kStage, kLds = kStage + 8 * 1024;
     __shared__ __attribute__((aligned(1024))) uint8_t lds[kLds];
     __shared__ Table<TM> tab;
     __shared__ uint32_t rowbuf[256];
@@ -360,8 +359,8 @@ __global__ __launch_bounds__(512, 1) void i8_tiles(I8Gemm p)
     using I2 = std::integral_constant<int, 2>;
     for (;;) {
         next = find(++round);
-        if (TM == 256 && cur.blocks == 4) run(I2{}, std::integral_constant<int, TM == 256 ? 2 : 0>{});
-        else if (TM == 256 && cur.blocks == 3) run(I2{}, std::integral_constant<int, TM == 256>{});
+        if (cur.blocks == 4) run(I2{}, I2{});
+        else if (cur.blocks == 3) run(I2{}, I1{});
         else if (cur.blocks == 2) run(I2{}, I0{});
         else run(I1{}, I0{});
         if (next.blocks == 0) break;
@@ -383,7 +382,8 @@ __global__ __launch_bounds__(512, 1) void i8_tiles(I8Gemm p)
 // gate rows of W and the 16 up rows that meet them alternate, and a wave has
 // both.  Where the products count (PIPE) a wave reads a stage's blocks from LDS
 // while it multiplies those of the stage before, whose slot is refilled at once
-// (1024 x 4096 x 4096: one after the other 25.6 us).  A tile's row
+// (1024 x 4096 x 4096: one after the other 25.6 us, reads and loads in front
+// of the products 25.2, between them 21.8 .. 23.7).  A tile's row
 // indices are loaded two tiles ahead, its scales as in i8_tiles, all into LDS:
 // the loads of the ring are waited for by count, and a load into registers would
 // end that.
@@ -851,15 +851,10 @@ hipError_t launch_i8_tiles(const I8Gemm &p, I8Tile t, int cus, hipStream_t strea
         else if (t.cols == 32 || p.gate) go(I64{}, std::integral_constant<int, 32>{});
         else go(I64{}, std::integral_constant<int, 16>{});
     } else {
-        auto go = [&](auto tm) {
-            constexpr int TM = decltype(tm)::value;
-            const dim3 grid = tile_grid(p, TM, p.gate ? 128 : 256, cus);
-            if (p.gate) hipLaunchKernelGGL((i8_tiles<TM, true, false>), grid, block, 0, stream, p);
-            else if (p.f32) hipLaunchKernelGGL((i8_tiles<TM, false, true>), grid, block, 0, stream, p);
-            else hipLaunchKernelGGL((i8_tiles<TM, false, false>), grid, block, 0, stream, p);
-        };
-        if (t.rows == 256) go(std::integral_constant<int, 256>{});
-        else go(std::integral_constant<int, 128>{});
+        const dim3 grid = tile_grid(p, 256, p.gate ? 128 : 256, cus);
+        if (p.gate) hipLaunchKernelGGL((i8_tiles<true, false>), grid, block, 0, stream, p);
+        else if (p.f32) hipLaunchKernelGGL((i8_tiles<false, true>), grid, block, 0, stream, p);
+        else hipLaunchKernelGGL((i8_tiles<false, false>), grid, block, 0, stream, p);
     }
     return hipGetLastError();
 }

@@ -94,11 +94,12 @@ def test_quant_rows_on_odd_addresses():
 # ---------------------------------------------------------- the dense product
 
 # one row to several tiles, every number of 64-row blocks, widths and depths that
-# end inside a tile (a vector, a stage), the three tile heights, few and many stages
+# end inside a tile (a vector, a stage), every tile, few and many stages
 DENSE = [(1, 1, 16), (1, 64, 128), (1, 8192, 4096), (2, 33, 48), (5, 100, 144), (16, 256, 1024), (17, 1000, 2064),
          (48, 4096, 512), (63, 65, 912), (64, 2050, 1040), (65, 64, 16), (100, 300, 3200), (200, 4097, 272),
          (256, 256, 384), (300, 520, 4096), (513, 2047, 528), (1024, 1024, 1024), (700, 8200, 256), (2047, 4102, 400),
-         (4096, 4100, 128), (8192, 513, 160), (64, 8170, 528), (512, 8170, 512), (1030, 4099, 784)]
+         (4096, 4100, 128), (8192, 513, 160), (64, 8170, 528), (512, 8170, 512), (1030, 4099, 784),
+         (1030, 8170, 784), (2157, 6150, 1040), (2500, 4099, 1040)]
 
 
 @pytest.mark.parametrize("M,N,K", DENSE)
@@ -313,7 +314,8 @@ def test_other_streams_and_two_calls_at_once():
 
 
 # sizes that reach every kernel, with several tiles to a workgroup
-POISON = [(3, 70000, 200), (900, 33000, 640), (5000, 6000, 400), (9000, 9000, 130), (1500, 2500, 1024), (700, 30000, 260), (2047, 4102, 400), (1100, 9000, 768), (64, 30000, 512)]
+POISON = [(3, 70000, 200), (900, 33000, 640), (5000, 6000, 400), (9000, 9000, 130), (1500, 2500, 1024), (700, 30000, 260), (2047, 4102, 400), (1100, 9000, 768), (64, 30000, 512),
+          (64, 40000, 512), (2157, 6150, 1040)]
 
 
 @pytest.mark.parametrize("M,N,K", POISON)
