@@ -22,6 +22,7 @@ struct I8Gemm {
     int64_t T;                // rows of X
     int M, E, N, K;
     int ncols;                // columns of D: N, or N / 2 behind the gate
+    int ldd;                  // elements from one row of D to the next
     int gate;                 // 1: D = silu(first N/2 columns) * last N/2 columns
     int f32;                  // 1: D holds fp32 (without the gate)
     int vec;                  // 1 if D rows take 16-byte stores
@@ -34,7 +35,13 @@ struct I8Tile {
 };
 // The tile for M rows over E groups on `cus` compute units (the rule and what it
 // rests on: i8.cpp)
-I8Tile i8_tile(int64_t M, int64_t E, int64_t N, int64_t ncols, int64_t K, bool gate, int cus);
+I8Tile i8_tile(int64_t M, int64_t E, int64_t N, int64_t ncols, int64_t K, bool gate, int cus, double *us = nullptr);
+// The dense product's first launch: all M rows and N columns, or fewer of one where a
+// second one for the others pays
+struct I8Part {
+    int64_t rows, cols;
+};
+I8Part i8_part(int64_t M, int64_t N, int64_t K, int cus);
 hipError_t launch_i8_tiles(const I8Gemm &p, I8Tile tile, int cus, hipStream_t stream);
 
 // Row scales and codes of x (M x K, fp32 or bf16).
@@ -43,5 +50,7 @@ hipError_t launch_quant_i8(const void *x, int bf16, int64_t M, int64_t K, int8_t
 
 }  // namespace dbs
 
-// For the tests that say which kernel a size reaches (not in include/dbs.h): 1000 rows + cols of the tile
+// For the tests that say which kernel a size reaches (not in include/dbs.h): 1000 rows + cols of the tile; the
+// rows of the dense product's first launch, or -columns where it has all rows
 extern "C" int dbs_i8_tile(int64_t M, int64_t E, int64_t N, int64_t K, int gate, int cus);
+extern "C" int64_t dbs_i8_part(int64_t M, int64_t N, int64_t K, int cus);

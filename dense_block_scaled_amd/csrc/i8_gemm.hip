@@ -33,7 +33,7 @@ struct MulI8 {
 // Rows from .. to-1 of D are zero (those before the first group and behind the last).
 __device__ __forceinline__ void zero_rows(const I8Gemm &p, int64_t from, int64_t to)
 {
-    const int64_t row = (int64_t)p.ncols * (p.f32 ? 4 : 2), bytes = (to - from) * row;
+    const int64_t row = (int64_t)p.ldd * (p.f32 ? 4 : 2), bytes = (to - from) * row;
     uint8_t *z = p.D + from * row;
     const int64_t me = (int64_t)blockIdx.x * blockDim.x + threadIdx.x, all = (int64_t)gridDim.x * blockDim.x;
     if (p.vec)
@@ -145,14 +145,14 @@ __device__ __forceinline__ void store_rows(uint8_t *buf, const I8Gemm &p, int r0
     constexpr int SZ = F32 ? 4 : 2, kCols = 64 / SZ;
     asm volatile("" : "+v"(c.lane));
     const int left = __builtin_amdgcn_readfirstlane(max(0, min(16, mend - r0)));
-    const __amdgpu_buffer_rsrc_t rd = make_rsrc(p.D + (int64_t)r0 * p.ncols * SZ, (uint32_t)left * (uint32_t)p.ncols * (uint32_t)SZ);
+    const __amdgpu_buffer_rsrc_t rd = make_rsrc(p.D + (int64_t)r0 * p.ldd * SZ, (uint32_t)left * (uint32_t)p.ldd * (uint32_t)SZ);
     const int row = c.lane & 15, g = c.lane >> 4;
 #pragma unroll
     for (int h = 0; h < (F32 ? 2 : 1); ++h) {
         const int nh = n0 + 16 * h;
         if (F32 && p.vec) {
             const float w[4] = {value(h, 0), value(h, 1), value(h, 2), value(h, 3)};
-            store_four<true>(rd, w, nh + 4 * g, p.ncols, (uint32_t)(row * p.ncols + nh + 4 * g) * 4u, 1);
+            store_four<true>(rd, w, nh + 4 * g, p.ncols, (uint32_t)(row * p.ldd + nh + 4 * g) * 4u, 1);
             continue;
         }
         wave_handover();                     // (the rows before have been read)
@@ -171,14 +171,14 @@ __device__ __forceinline__ void store_rows(uint8_t *buf, const I8Gemm &p, int r0
         if (!F32 && p.vec) {
             const int r = c.lane >> 2, ch = c.lane & 3, n = nh + ch * 8;
             const i32x4 v = *reinterpret_cast<const i32x4 *>(buf + r * 64 + 16 * (ch ^ ((r >> 1) & 3)));
-            __builtin_amdgcn_raw_buffer_store_b128(v, rd, n < p.ncols ? (uint32_t)(r * p.ncols + n) * 2u : kOOB, 0, kStoreCached);
+            __builtin_amdgcn_raw_buffer_store_b128(v, rd, n < p.ncols ? (uint32_t)(r * p.ldd + n) * 2u : kOOB, 0, kStoreCached);
         } else {
             // lanes along the columns: 4 (fp32) or 2 (bf16) rows a store
             const int e = c.lane % kCols, n = nh + e;
 #pragma unroll
             for (int q = 0; q < kCols / 4; ++q) {
                 const int r = q * (64 / kCols) + c.lane / kCols, at = r * 64 + (((e * SZ >> 4) ^ ((r >> 1) & 3)) << 4) + (e * SZ & 15);
-                const uint32_t to = n < p.ncols ? (uint32_t)(r * p.ncols + n) * (uint32_t)SZ : kOOB;
+                const uint32_t to = n < p.ncols ? (uint32_t)(r * p.ldd + n) * (uint32_t)SZ : kOOB;
                 if constexpr (F32)
                     __builtin_amdgcn_raw_buffer_store_b32(*reinterpret_cast<const uint32_t *>(buf + at), rd, to, 0, kStoreCached);
                 else
@@ -635,14 +635,14 @@ __global__ __launch_bounds__(512, 1) void i8_tiles_deep(I8Gemm p)
                 } else {
                     const int left = __builtin_amdgcn_readfirstlane(max(0, min(16, cur.mend - r0)));
                     const __amdgpu_buffer_rsrc_t rd =
-                        make_rsrc(p.D + (int64_t)r0 * p.ncols * SZ, (uint32_t)left * (uint32_t)p.ncols * (uint32_t)SZ);
+                        make_rsrc(p.D + (int64_t)r0 * p.ldd * SZ, (uint32_t)left * (uint32_t)p.ldd * (uint32_t)SZ);
 #pragma unroll
                     for (int u = 0; u < (GATE ? 1 : NB); ++u) {
                         float v[4];
 #pragma unroll
                         for (int q = 0; q < 4; ++q) v[q] = GATE ? gated(scaled(0, q), scaled(NB - 1, q)) : scaled(u, q);
                         const int n = cur.n0 + (GATE ? 16 : 16 * NB) * wn + 16 * u + 4 * g;
-                        store_four<F32>(rd, v, n, p.ncols, (uint32_t)(j * p.ncols + n) * (uint32_t)SZ, p.vec);
+                        store_four<F32>(rd, v, n, p.ncols, (uint32_t)(j * p.ldd + n) * (uint32_t)SZ, p.vec);
                     }
                 }
             }
@@ -805,8 +805,8 @@ __global__ __launch_bounds__(512, 4) void i8_rows(I8Gemm p)
 #pragma unroll
             for (int q = 0; q < 4; ++q) v[q] = GATE ? gated(h[0][q], h[C - 1][q]) : h[0][q];
             const __amdgpu_buffer_rsrc_t rd =
-                make_rsrc(p.D + (int64_t)cur.m0 * p.ncols * SZ, (uint32_t)cur.left * (uint32_t)p.ncols * (uint32_t)SZ);
-            store_four<F32>(rd, v, n, p.ncols, (uint32_t)(j * p.ncols + n) * (uint32_t)SZ, p.vec);
+                make_rsrc(p.D + (int64_t)cur.m0 * p.ldd * SZ, (uint32_t)cur.left * (uint32_t)p.ldd * (uint32_t)SZ);
+            store_four<F32>(rd, v, n, p.ncols, (uint32_t)(j * p.ldd + n) * (uint32_t)SZ, p.vec);
         }
         if (!more) break;
         __syncthreads();                         // (the parts have been read)

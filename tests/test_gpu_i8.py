@@ -101,8 +101,11 @@ DENSE = [(1, 1, 16), (1, 64, 128), (1, 8192, 4096), (2, 33, 48), (5, 100, 144), 
          (4096, 4100, 128), (8192, 513, 160), (64, 8170, 528), (512, 8170, 512), (1030, 4099, 784),
          (1030, 8170, 784), (2157, 6150, 1040), (2500, 4099, 1040)]
 
+# in two launches, the second for the last rows or the last columns
+PARTS = [(2076, 2009, 1808), (411, 9523, 2592), (324, 11059, 1696), (3485, 1178, 2160), (992, 4108, 2320)]
 
-@pytest.mark.parametrize("M,N,K", DENSE)
+
+@pytest.mark.parametrize("M,N,K", DENSE + PARTS)
 @pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
 def test_gemm(M, N, K, dtype):
     g = _gen(M * 7 + N * 11 + K)

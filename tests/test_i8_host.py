@@ -232,6 +232,32 @@ def _tile(M, E, N, K, gate=0):
     return f(M, E, N, K, gate, 256)
 
 
+def _parts(M, N, K):
+    """The launches of a dense product."""
+    f = dbs.lib().dbs_i8_part
+    f.argtypes, f.restype = [ctypes.c_int64] * 3 + [ctypes.c_int], ctypes.c_int64
+    n = f(M, N, K, 256)
+    if n < 0:
+        return [(M, -n, K), (M, N + n, K)]
+    return [(n, N, K), (M - n, N, K)] if n < M else [(M, N, K)]
+
+
+def test_dense_products_in_two_launches():
+    assert all(len(_parts(*s)) == 1 for s in shapes.DENSE)
+    parts = [_parts(*s) for s in shapes.PARTS]
+    assert all(len(p) == 2 for p in parts)
+    assert {p[0][0] < s[0] for p, s in zip(parts, shapes.PARTS)} == {True, False}
+    rng = np.random.default_rng(6)
+    for _ in range(3000):
+        M, N, K = int(2 ** rng.uniform(0, 25)), int(2 ** rng.uniform(0, 21)), 16 * int(2 ** rng.uniform(0, 12.9))
+        parts = _parts(M, N, K)
+        assert sum(m * n for m, n, _ in parts) == M * N
+        if len(parts) == 2:
+            # whole tiles come first: what is behind them stays as aligned as the start
+            (m, n, _), (m2, n2, _) = parts
+            assert min(m, n, m2, n2) > 0 and ((m % 128 == 0 and n == N) or (n % 128 == 0 and m == M))
+
+
 def test_gpu_sizes_reach_every_kernel():
     """The rule that the products go by puts the sizes of the GPU tests in every kernel."""
     assert {_tile(M, 1, N, K) for M, N, K in shapes.DENSE} == TILES
