@@ -300,6 +300,27 @@ def test_graph_replays_on_new_inputs(T):
             assert torch.equal(a, b)
 
 
+@pytest.mark.parametrize("M,N,K", PARTS[:3])
+def test_graph_of_two_launches(M, N, K):
+    g = torch.Generator(device="cuda")
+    g.manual_seed(M)
+    codes = lambda *s: torch.randint(-128, 128, s, generator=g, device="cuda", dtype=torch.int8)
+    A, B, sA, sB = codes(M, K), codes(N, K), torch.rand(M, device="cuda"), torch.rand(N, device="cuda")
+    out = torch.full((M, N), float("nan"), device="cuda", dtype=torch.bfloat16)
+    dbs.gemm_i8(A, sA, B, sB)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        dbs.gemm_i8(A, sA, B, sB, out=out)
+    for _ in range(3):
+        A.copy_(codes(M, K))
+        graph.replay()
+        torch.cuda.synchronize()
+        got = out.clone()
+        assert torch.equal(got, dbs.gemm_i8(A, sA, B, sB))
+        assert bool(torch.isfinite(got).all())
+
+
 def test_other_streams_and_two_calls_at_once():
     args = _layer_inputs(700)
     other = _layer_inputs(900, seed=5)
