@@ -20,18 +20,19 @@ namespace dbs {
 // 5.5 TB/s where that is more.  Groups (E > 1) are known on the device only: M / E rows of
 // each, half a tile of each is waste, some may have none; tiles then even out,
 // and rounds are counted in parts.  us of the dense product with tiles of 16 x 16 /
-// 64 x 16 / 64 x 32 / 64 x 64 / 128 x 128 / 256 x 256:
+// 16 x 64 / 64 x 16 / 64 x 32 / 64 x 64 / 128 x 128 / 256 x 256:
 //
-//      1 x 4096 x 4096     5.0   7.5   8.9  10.2    18    35
-//     16 x 8192 x 4096    10.2  12.4   9.5  11.0
-//     48 x 4096 x 4096    17.8   8.0   9.3  11.0
-//    128 x 8192 x 4096      63    22  15.7  12.0    20    39
-//    512 x 8192 x 1024     113    42    26  16.3  10.6    20
-//   1024 x 4096 x 4096                  54    41    24    47
-//   2048 x 4096 x 4096                  94    71    42    48
-//   4096 x 4096 x 4096                 180   127    81    59
+//      1 x 4096 x 4096     4.8   8.2   7.3   8.5  10.2    18    35
+//     16 x 8192 x 4096     9.8   8.5  11.6   9.0  10.5
+//     48 x 4096 x 4096    17.1  10.6   7.5   8.7  10.6
+//    128 x 8192 x 4096      63          22  15.7  12.0    20    39
+//    512 x 8192 x 1024     113          42    26  16.3  10.6    20
+//   1024 x 4096 x 4096                        54    41    24    47
+//   2048 x 4096 x 4096                        94    71    42    48
+//   4096 x 4096 x 4096                       180   127    81    59
 //
-// and of 16 .. 8191 rows each to 4 of 32 experts of 2056 x 4096, with the last three, 40 / 54 /
+// of 1 / 4 / 16 / 48 tokens each to 8 of 64 experts of 2048 x 1408 with 16 x 64 9.0 / 16.8 / 26.6 / 35.3,
+// with 64 x 64 9.3 / 18.0 / 29.0 / 38.5, and of 16 .. 8191 rows each to 4 of 32 experts of 2056 x 4096, with the last three, 40 / 54 /
 // 42 for 16 rows, 75 / 76 / 79 for 512, 105 / 95 / 84 for 1024, 586 / 377 / 293 for 8191.  (A tile of
 // 128 x 256 on the core of 256 x 256 was nowhere the fastest: 38 .. 79 us for the last three rows, 76
 // for 512 rows to the experts.)
@@ -60,13 +61,14 @@ I8Tile i8_tile(int64_t M, int64_t E, int64_t N, int64_t ncols, int64_t K, bool g
         const double x = tiles(16, gate ? 32 : 16) / n, m = std::min(double(M) / met, 16.0) / 16, c = gate ? 1.6 : 1.0;
         if (x <= 2) offer(16, 16, 3.6 + c * k * (x <= 1 ? 0.36 + 0.37 * m : 0.95 + 0.7 * m));
     }
-    auto deep = [&](int cols, double first, double next) {
-        const double x = tiles(64, cols) / n;
-        offer(64, cols, 4.8 + first * k + more(x) * (1.9 + next * k));
+    auto deep = [&](int rows, int cols, double first, double next) {
+        const double x = tiles(rows, cols) / n;
+        offer(rows, cols, 4.8 + first * k + more(x) * (1.9 + next * k));
     };
-    if (!gate) deep(16, 0.6, 0.75);
-    deep(32, 0.95, 1.05);
-    deep(64, 1.42, 1.55);
+    if (!gate) deep(64, 16, 0.6, 0.75);
+    deep(64, 32, 0.95, 1.05);
+    deep(64, 64, 1.42, 1.55);
+    if (M <= 16 * met) deep(16, 64, 0.92, 1.0);    // (more rows read W again: 48 x 4096 x 4096 in 10.6 us)
     double x = tiles(128, 128) / n;
     offer(128, 128, 6.1 + (2.7 + 1.6 * std::min(x, 1.0)) * k + more(x) * (1.3 + 4.35 * k));
     x = tiles(256, 256) / n;

@@ -28,8 +28,8 @@ struct I8Gemm {
     int vec;                  // 1 if D rows take 16-byte stores
 };
 
-// An output tile: 16 rows by 16 columns; 64 by the columns of 64, 32 or (without
-// the gate) 16 rows of W; 128 by those of 128; 256 by those of 256.
+// An output tile: 16 rows by 16 columns; 16 by the columns of 64 rows of W; 64 by those of 64, 32 or (without
+// the gate) 16; 128 by those of 128; 256 by those of 256.
 struct I8Tile {
     int rows, cols;
 };

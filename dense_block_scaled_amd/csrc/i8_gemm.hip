@@ -59,6 +59,14 @@ struct Tiles {
             count = (p.M + TM - 1) / TM * tiles_n;
             return;
         }
+        if constexpr (TM == 16) {
+            if (c.w == 0) group_table<true>(tab.first, tab.whole, p.offsets, p.E, p.M, c, [](int rows) { return (rows + 15) / 16; });
+            __syncthreads();
+            zero_rows(p, 0, tab.first[0]);
+            zero_rows(p, tab.first[p.E], p.M);
+            count = same(tab.whole[p.E]) * tiles_n;
+            return;
+        }
         if (c.w == 0)
             group_table<true>(tab.first, tab.whole, p.offsets, p.E, p.M, c, [](int rows) { return Table<TM>::whole_of(rows); });
         else if (c.w < TM / 64)
@@ -72,6 +80,21 @@ struct Tiles {
 
     __device__ __forceinline__ RowTile operator()(int id) const
     {
+        if constexpr (TM == 16) {
+            RowTile r{};
+            if (id >= count) return r;
+            const int row_tile = id / tiles_n;
+            r.blocks = 1;
+            r.n0 = (id - row_tile * tiles_n) * tno;
+            r.m0 = row_tile * 16;
+            r.mend = p.M;
+            if (p.offsets) {
+                r.g = group_of(tab.whole, p.E, row_tile, c);
+                r.m0 = same(tab.first[r.g]) + (row_tile - same(tab.whole[r.g])) * 16;
+                r.mend = same(tab.first[r.g + 1]);
+            }
+            return r;
+        }
         if (p.offsets)
             return find_tile(tab, p.E, count, tiles_n, tno, id, [&](const auto *at, int n) { return group_of(at, p.E, n, c); });
         RowTile r{};
@@ -374,13 +397,15 @@ __global__ __launch_bounds__(512, 1) void i8_tiles(I8Gemm p)
 // a few rows per group, where the time is the reading of W: what a CU can have
 // under way is its LDS, over a latency of 1.2 us about 100 GB/s, so narrower
 // tiles pay where wide ones leave CUs idle, although each reads all of X's rows.
+// 16 rows by 64 where groups have no more: less of the ring goes to X, more to W (16 tokens
+// to 8 of 64 experts of 2048 x 1408: 26.6 us, by 64 rows 29.0).
 // 128 rows by 128 where the large tiles are too few for the CUs.
 //
 // A stage is H times 128 bytes of every row.  8 waves: WM along the rows, the others
-// along the columns or (KS = 2, where there are not enough of those to share
-// out) taking every second 128 bytes, to be added at the end.  With the gate 16
-// gate rows of W and the 16 up rows that meet them alternate, and a wave has
-// both.  Where the products count (PIPE) a wave reads a stage's blocks from LDS
+// along the columns or (KS = 2 or 4, where there are not enough of those to share
+// out) each taking its part of a stage's k-steps, to be added at the end.  With the
+// gate 16 gate rows of W and the 16 up rows that meet them alternate, and a wave
+// has both.  Where the products count (PIPE) a wave reads a stage's blocks from LDS
 // while it multiplies those of the stage before, whose slot is refilled at once
 // (1024 x 4096 x 4096: one after the other 25.6 us, reads and loads in front
 // of the products 25.2, between them 21.8 .. 23.7).  A tile's row
@@ -390,18 +415,20 @@ __global__ __launch_bounds__(512, 1) void i8_tiles(I8Gemm p)
 template <int TM_, int TN_, bool GATE>
 struct Deep {
     static constexpr int TM = TM_, TN = TN_, H = TM == 128 ? 1 : TN == 16 ? 4 : 2;
-    static constexpr int WM = TM == 128 ? 2 : 4, RB = TM / 16 / WM;            // waves along the rows, blocks of 16 of each
-    static constexpr int NB = TN >= 64 || GATE ? 2 : 1, WN = TN / 16 / NB, KS = 8 / WM / WN;
+    static constexpr int WM = TM == 16 ? 1 : TM == 128 ? 2 : 4, RB = TM / 16 / WM;   // waves along the rows, blocks of 16 of each
+    static constexpr int NB = (TM > 16 && TN >= 64) || GATE ? 2 : 1, WN = TN / 16 / NB, KS = 8 / WM / WN;
     static constexpr int kSteps = 2 * H / KS;                                  // k-steps of 64 bytes of a wave
     static constexpr int kA = TM * kRowBytes, kHalf = kA + TN * kRowBytes, kSlot = H * kHalf, kStageBytes = H * kRowBytes;
     static constexpr int NS = 131072 / kSlot;
     static constexpr bool PIPE = TM == 128;
     static constexpr int kAhead = PIPE ? NS : NS - 1;                          // stages that the loads are ahead
+    static constexpr int kRows = TM < 64 ? 64 : TM;                            // of the tile's row indices and scales in LDS
+    // wave-loads of a wave and 128 bytes of X's rows (TM = 16: the two of each go to four of the waves), of W's
     static constexpr int kLoadsA = TM / 64, kLoadsW = H * TN / 64, kLoads = H * kLoadsA + kLoadsW, kWait = (NS - 2) * kLoads;
     static constexpr int kRowsW = TN > 64 ? TN / 64 : 1;                       // wave-loads of W at rows of their own
     static constexpr int TNO = GATE ? TN / 2 : TN;
-    static_assert(KS == 1 || KS == 2, "one or two waves along K");
-    static_assert(KS * WN * WM == 8 && H % KS == 0 && NS >= 3, "");
+    static_assert(KS * WN * WM == 8 && 2 * H % KS == 0 && NS >= 3, "");
+    static_assert(TM > 16 || H == 2, "four waves load X's rows");
 };
 
 // k-step kk (64 bytes) of the 16 rows 16 i further down than the lane's base: those
@@ -418,14 +445,14 @@ __global__ __launch_bounds__(512, 1) void i8_tiles_deep(I8Gemm p)
     constexpr int RB = S::RB, NB = S::NB, KS = S::KS, H = S::H, TNO = S::TNO, SZ = F32 ? 4 : 2;
     __shared__ __attribute__((aligned(1024))) uint8_t lds[S::NS * S::kSlot];
     __shared__ Table<TM> tab;
-    __shared__ uint32_t rowbuf[2][TM];
+    __shared__ uint32_t rowbuf[2][S::kRows];
     // [parity of the tile]: rows' scales, then those of the tile's rows of W
-    constexpr int kScales = TM + (TN > 64 ? TN : 64);
+    constexpr int kScales = S::kRows + (TN > 64 ? TN : 64);
     __shared__ __attribute__((aligned(16))) float scales[2][kScales];
-    __shared__ __attribute__((aligned(16))) i32x4 part[TM == 128 ? 8 : KS == 2 ? 4 * NB : 1][64];
+    __shared__ __attribute__((aligned(16))) i32x4 part[TM == 128 ? 8 : KS > 1 ? (KS - 1) * S::WM * S::WN * NB : 1][64];
 
     const Lane c = lane_of();
-    const int wm = c.w / (S::WN * KS), wn = c.w / KS % S::WN, ks2 = KS == 2 ? c.w & 1 : 0, j = c.lane & 15, g = c.lane >> 4;
+    const int wm = c.w / (S::WN * KS), wn = c.w / KS % S::WN, ks = c.w % KS, j = c.lane & 15, g = c.lane >> 4;
     const int lda = p.K;
     const Tiles<TM> find(tab, p, c, TNO);
     const int nwg = spread(find.count);
@@ -439,15 +466,15 @@ __global__ __launch_bounds__(512, 1) void i8_tiles_deep(I8Gemm p)
 
     // wave w loads rows 8 w .. (and 64 further down) of A; wave-load w + 8 q of W's: eight rows of one of the H parts
     i32x4 ra, rb;
-    const int arow = 8 * c.w + (c.lane >> 3), wrow = 8 * (c.w % (TN / 8)) + (c.lane >> 3);
+    const int arow = 8 * (TM == 16 ? c.w & 1 : c.w) + (c.lane >> 3), wrow = 8 * (c.w % (TN / 8)) + (c.lane >> 3);
     int rot = 0;
-    uint32_t aoff[S::kLoadsA], boff[S::kRowsW];
+    uint32_t aoff[S::kRows / 64], boff[S::kRowsW];
     uint32_t ax = (uint32_t)(((c.lane & 7) ^ swz(arow)) << 4), bx = (uint32_t)(((c.lane & 7) ^ swz(wrow)) << 4);   // the lane's chunks
     // (64 rows a wave; that the other waves have a load less under way waits for no fewer)
     auto fetch = [&](const RowTile &r, int place) {
-        if (c.w >= TM / 64 || !p.rows) return;
+        if (c.w >= S::kRows / 64 || !p.rows) return;
         dma<4>(words_of(p.rows + r.m0, (uint32_t)max(min(r.mend - r.m0, TM), 0) * 4u), reinterpret_cast<uint8_t *>(rowbuf),
-               (place * TM + c.w * 64) * 4, (uint32_t)(c.w * 64 + c.lane) * 4u);
+               (place * S::kRows + c.w * 64) * 4, (uint32_t)(c.w * 64 + c.lane) * 4u);
     };
     auto aim = [&](const RowTile &r, int place) {
         if (r.blocks == 0) {
@@ -462,7 +489,7 @@ __global__ __launch_bounds__(512, 1) void i8_tiles_deep(I8Gemm p)
         const uint32_t have = p.rows ? (uint32_t)p.T : (uint32_t)left;
         ra = words_of(p.rows ? p.X : p.X + (int64_t)r.m0 * lda, have * (uint32_t)lda);
 #pragma unroll
-        for (int q = 0; q < S::kLoadsA; ++q) {
+        for (int q = 0; q < S::kRows / 64; ++q) {
             const int m = arow + 64 * q;
             const uint32_t row = p.rows ? rowbuf[place][m] : (uint32_t)m;
             aoff[q] = m < left && row < have ? row * (uint32_t)lda : kRowOOB;
@@ -477,13 +504,13 @@ __global__ __launch_bounds__(512, 1) void i8_tiles_deep(I8Gemm p)
             if constexpr (GATE) boff[q] = there(e) ? (uint32_t)(row_of_w(e) * lda) : kRowOOB;
             else boff[q] = (uint32_t)(e * lda);
         }
-        if (c.w < TM / 64) {
+        if (c.w < S::kRows / 64) {
             const int m = c.w * 64 + c.lane;
             const uint32_t at = p.rows ? rowbuf[place][m] : (uint32_t)m;
             dma<4>(words_of(p.rows ? p.sX : p.sX + r.m0, have * 4u), reinterpret_cast<uint8_t *>(scales),
                    (place * kScales + c.w * 64) * 4, at < have ? at * 4u : kRowOOB);
-        } else if (c.w < TM / 64 + (TN + 63) / 64) {
-            const int e = (c.w - TM / 64) * 64 + c.lane, at = GATE ? row_of_w(e) : r.n0 + e;
+        } else if (c.w < S::kRows / 64 + (TN + 63) / 64) {
+            const int e = (c.w - S::kRows / 64) * 64 + c.lane, at = GATE ? row_of_w(e) : r.n0 + e;
             dma<4>(words_of(p.sW + (int64_t)r.g * p.N, (uint32_t)p.N * 4u), reinterpret_cast<uint8_t *>(scales),
                    (place * kScales + c.w * 64) * 4, e < TN && at < p.N ? (uint32_t)at * 4u : kRowOOB);
         }
@@ -492,7 +519,8 @@ __global__ __launch_bounds__(512, 1) void i8_tiles_deep(I8Gemm p)
     auto load_one = [&](int q, int slot, int k0) {
         const uint32_t dst = slot * S::kSlot;
         if (q < H * S::kLoadsA) {
-            const int h = q / S::kLoadsA, r = q % S::kLoadsA, kc = (int)ax + k0 + h * kRowBytes;
+            constexpr int kEach = S::kLoadsA > 0 ? S::kLoadsA : 1;
+            const int h = q / kEach, r = q % kEach, kc = (int)ax + k0 + h * kRowBytes;
             dma<16>(ra, lds, dst + h * S::kHalf + (c.w + 8 * r) * 1024, kc < lda ? aoff[r] + kc : kRowOOB);
         } else {
             q -= H * S::kLoadsA;
@@ -509,6 +537,17 @@ __global__ __launch_bounds__(512, 1) void i8_tiles_deep(I8Gemm p)
         const int k0 = start_of(ks);
 #pragma unroll
         for (int q = 0; q < S::kLoads; ++q) load_one(q, slot, k0);
+        if constexpr (TM == 16) {
+            if (c.w < 4) {
+                const int kc = (int)ax + k0 + (c.w >> 1) * kRowBytes;
+                dma<16>(ra, lds, slot * S::kSlot + (c.w >> 1) * S::kHalf + (c.w & 1) * 1024, kc < lda ? aoff[0] + kc : kRowOOB);
+            }
+        }
+    };
+    // (every wave waits for its own loads: four of TM = 16's have one more in each stage)
+    auto barrier = [&] {
+        if (TM == 16 && c.w < 4) stage_barrier<S::kWait + (TM == 16 ? S::NS - 2 : 0)>();
+        else stage_barrier<S::kWait>();
     };
 
     int parity = 0;
@@ -530,9 +569,10 @@ __global__ __launch_bounds__(512, 1) void i8_tiles_deep(I8Gemm p)
     constexpr int kReads = S::kSteps * (RB + NB);
     auto read_one = [&](Blocks &f, int slot, int n) {
         const int kk = n / (RB + NB), i = n % (RB + NB);
-        const uint32_t from = (uint32_t)(slot * S::kSlot + (KS * (kk >> 1) + ks2) * S::kHalf);
-        if (i < NB) f.b[kk][i] = deep_frag(lds, fb + from, kk & 1, i);
-        else f.a[kk][i - NB] = deep_frag(lds, fa + from, kk & 1, i - NB);
+        const int step = ks * S::kSteps + kk;
+        const uint32_t from = (uint32_t)(slot * S::kSlot + (step >> 1) * S::kHalf);
+        if (i < NB) f.b[kk][i] = deep_frag(lds, fb + from, step & 1, i);
+        else f.a[kk][i - NB] = deep_frag(lds, fa + from, step & 1, i - NB);
     };
     auto read = [&](Blocks &f, int slot) {
 #pragma unroll
@@ -543,7 +583,7 @@ __global__ __launch_bounds__(512, 1) void i8_tiles_deep(I8Gemm p)
         stage_barrier<(S::NS - 1) * S::kLoads>();
         read(even, 0);
     }
-    stage_barrier<S::kWait>();
+    barrier();
 
     int rs = 0;               // slot of the stage
     for (;;) {
@@ -603,28 +643,32 @@ __global__ __launch_bounds__(512, 1) void i8_tiles_deep(I8Gemm p)
                 read(even, rs);
                 load(rs == 0 ? S::NS - 1 : rs - 1, ks);
                 multiply(even);
-                stage_barrier<S::kWait>();
+                barrier();
                 rs = rs + 1 == S::NS ? 0 : rs + 1;
             }
         }
-        if constexpr (KS == 2) {
+        if constexpr (KS > 1) {
             // (read before the next tile's stages end, written behind them)
-            if (ks2) {
+            const int at = (S::WN * wm + wn) * NB;
+            constexpr int kBlocks = S::WM * S::WN * NB;
+            if (ks) {
 #pragma unroll
-                for (int u = 0; u < NB; ++u) part[NB * wm + u][c.lane] = acc[0][u];
+                for (int u = 0; u < NB; ++u) part[(ks - 1) * kBlocks + at + u][c.lane] = acc[0][u];
             }
             asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory");
-            if (!ks2) {
+            if (!ks) {
 #pragma unroll
-                for (int u = 0; u < NB; ++u) acc[0][u] += part[NB * wm + u][c.lane];
+                for (int h = 0; h < KS - 1; ++h)
+#pragma unroll
+                    for (int u = 0; u < NB; ++u) acc[0][u] += part[h * kBlocks + at + u][c.lane];
             }
         }
-        if (!ks2 && busy) {
+        if (!ks && busy) {
             // lane: rows l % 16 of each block, four columns of each
             f32x4 sw[NB];
 #pragma unroll
             for (int u = 0; u < NB; ++u)
-                sw[u] = *reinterpret_cast<const f32x4 *>(&scales[parity][TM + 16 * NB * wn + 16 * u + 4 * g]);
+                sw[u] = *reinterpret_cast<const f32x4 *>(&scales[parity][S::kRows + 16 * NB * wn + 16 * u + 4 * g]);
 #pragma unroll
             for (int i = 0; i < RB; ++i) {
                 const int r0 = cur.m0 + 16 * (RB * wm + i);
@@ -826,7 +870,7 @@ dim3 tile_grid(const I8Gemm &p, int tm, int tno, int cus)
 hipError_t launch_i8_tiles(const I8Gemm &p, I8Tile t, int cus, hipStream_t stream)
 {
     const dim3 block(512);
-    if (t.rows == 16) {
+    if (t.cols == 16 && t.rows == 16) {
         const dim3 grid = tile_grid(p, 16, 16, 2 * cus);
         if (p.gate) hipLaunchKernelGGL((i8_rows<true, false>), grid, block, 0, stream, p);
         else if (p.f32) hipLaunchKernelGGL((i8_rows<false, true>), grid, block, 0, stream, p);
@@ -847,6 +891,7 @@ hipError_t launch_i8_tiles(const I8Gemm &p, I8Tile t, int cus, hipStream_t strea
         using I64 = std::integral_constant<int, 64>;
         using I128 = std::integral_constant<int, 128>;
         if (t.rows == 128) go(I128{}, I128{});
+        else if (t.rows == 16) go(std::integral_constant<int, 16>{}, I64{});
         else if (t.cols == 64) go(I64{}, I64{});
         else if (t.cols == 32 || p.gate) go(I64{}, std::integral_constant<int, 32>{});
         else go(I64{}, std::integral_constant<int, 16>{});

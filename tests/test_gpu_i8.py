@@ -99,7 +99,8 @@ DENSE = [(1, 1, 16), (1, 64, 128), (1, 8192, 4096), (2, 33, 48), (5, 100, 144), 
          (48, 4096, 512), (63, 65, 912), (64, 2050, 1040), (65, 64, 16), (100, 300, 3200), (200, 4097, 272),
          (256, 256, 384), (300, 520, 4096), (513, 2047, 528), (1024, 1024, 1024), (700, 8200, 256), (2047, 4102, 400),
          (4096, 4100, 128), (8192, 513, 160), (64, 8170, 528), (512, 8170, 512), (1030, 4099, 784),
-         (1030, 8170, 784), (2157, 6150, 1040), (2500, 4099, 1040)]
+         (1030, 8170, 784), (2157, 6150, 1040), (2500, 4099, 1040),
+         (16, 8200, 2064), (3, 20000, 528), (13, 17002, 400)]
 
 # in two launches, the second for the last rows or the last columns
 PARTS = [(2076, 2009, 1808), (411, 9523, 2592), (324, 11059, 1696), (3485, 1178, 2160), (992, 4108, 2320)]
@@ -214,7 +215,7 @@ def test_experts_rows_and_offsets_out_of_range():
 # Groups whose rows make more tiles than their number leads to expect, so that
 # workgroups of the small tiles take several: group sizes, N, K
 RAGGED = [([17, 1] * 4, 1024, 336), ([17, 0, 33, 2] * 4, 700, 1040), ([65] * 4, 640, 2048), ([65] * 4, 1300, 1040),
-          ([1, 129, 0, 70, 64, 3], 1500, 272)]
+          ([1, 129, 0, 70, 64, 3], 1500, 272), ([5, 16, 0, 20, 31, 1, 9] * 3, 2050, 400)]
 
 
 @pytest.mark.parametrize("sizes,N,K", RAGGED)
@@ -339,7 +340,7 @@ def test_other_streams_and_two_calls_at_once():
 
 # sizes that reach every kernel, with several tiles to a workgroup
 POISON = [(3, 70000, 200), (900, 33000, 640), (5000, 6000, 400), (9000, 9000, 130), (1500, 2500, 1024), (700, 30000, 260), (2047, 4102, 400), (1100, 9000, 768), (64, 30000, 512),
-          (64, 40000, 512), (2157, 6150, 1040)]
+          (64, 40000, 512), (2157, 6150, 1040), (16, 40000, 1024)]
 
 
 @pytest.mark.parametrize("M,N,K", POISON)
