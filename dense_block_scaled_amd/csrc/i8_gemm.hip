@@ -476,15 +476,33 @@ __global__ __launch_bounds__(512, 1) void i8_tiles_deep(I8Gemm p)
         dma<4>(words_of(p.rows + r.m0, (uint32_t)max(min(r.mend - r.m0, TM), 0) * 4u), reinterpret_cast<uint8_t *>(rowbuf),
                (place * S::kRows + c.w * 64) * 4, (uint32_t)(c.w * 64 + c.lane) * 4u);
     };
-    auto aim = [&](const RowTile &r, int place) {
+    auto row_of_w = [&](const RowTile &r, int e) { return ((e >> 4) & 1) * p.ncols + r.n0 + (e >> 5) * 16 + (e & 15); };
+    // What the loads of W read
+    auto aim_w = [&](const RowTile &r) {
         if (r.blocks == 0) {
-            ra = rb = words_of(nullptr, 0);
+            rb = words_of(nullptr, 0);
             return;
         }
         // (the walk along K starts elsewhere per tile, as in moe_tiles_64)
         rot = r.n0 / TNO % nk;
         const int64_t wbytes = (int64_t)p.N * p.K;
         const uint8_t *wg = p.W + r.g * wbytes;
+        rb = GATE ? words_of(wg, (uint32_t)wbytes) : words_of(wg + (int64_t)r.n0 * lda, (uint32_t)(min(p.N - r.n0, TN) * lda));
+        // rows 32 i + 16 u + q of the slot, with the gate: row n0 + 16 i + q of matrix u
+        auto there = [&](int e) { return r.n0 + (e >> 5) * 16 + (e & 15) < p.ncols; };
+#pragma unroll
+        for (int q = 0; q < S::kRowsW; ++q) {
+            const int e = wrow + 64 * q;
+            if constexpr (GATE) boff[q] = there(e) ? (uint32_t)(row_of_w(r, e) * lda) : kRowOOB;
+            else boff[q] = (uint32_t)(e * lda);
+        }
+    };
+    // Those of X, whose row indices are in rowbuf, and the scales
+    auto aim_x = [&](const RowTile &r, int place) {
+        if (r.blocks == 0) {
+            ra = words_of(nullptr, 0);
+            return;
+        }
         const int left = min(r.mend - r.m0, TM);
         const uint32_t have = p.rows ? (uint32_t)p.T : (uint32_t)left;
         ra = words_of(p.rows ? p.X : p.X + (int64_t)r.m0 * lda, have * (uint32_t)lda);
@@ -494,23 +512,13 @@ __global__ __launch_bounds__(512, 1) void i8_tiles_deep(I8Gemm p)
             const uint32_t row = p.rows ? rowbuf[place][m] : (uint32_t)m;
             aoff[q] = m < left && row < have ? row * (uint32_t)lda : kRowOOB;
         }
-        rb = GATE ? words_of(wg, (uint32_t)wbytes) : words_of(wg + (int64_t)r.n0 * lda, (uint32_t)(min(p.N - r.n0, TN) * lda));
-        // rows 32 i + 16 u + q of the slot, with the gate: row n0 + 16 i + q of matrix u
-        auto row_of_w = [&](int e) { return ((e >> 4) & 1) * p.ncols + r.n0 + (e >> 5) * 16 + (e & 15); };
-        auto there = [&](int e) { return r.n0 + (e >> 5) * 16 + (e & 15) < p.ncols; };
-#pragma unroll
-        for (int q = 0; q < S::kRowsW; ++q) {
-            const int e = wrow + 64 * q;
-            if constexpr (GATE) boff[q] = there(e) ? (uint32_t)(row_of_w(e) * lda) : kRowOOB;
-            else boff[q] = (uint32_t)(e * lda);
-        }
         if (c.w < S::kRows / 64) {
             const int m = c.w * 64 + c.lane;
             const uint32_t at = p.rows ? rowbuf[place][m] : (uint32_t)m;
             dma<4>(words_of(p.rows ? p.sX : p.sX + r.m0, have * 4u), reinterpret_cast<uint8_t *>(scales),
                    (place * kScales + c.w * 64) * 4, at < have ? at * 4u : kRowOOB);
         } else if (c.w < S::kRows / 64 + (TN + 63) / 64) {
-            const int e = (c.w - S::kRows / 64) * 64 + c.lane, at = GATE ? row_of_w(e) : r.n0 + e;
+            const int e = (c.w - S::kRows / 64) * 64 + c.lane, at = GATE ? row_of_w(r, e) : r.n0 + e;
             dma<4>(words_of(p.sW + (int64_t)r.g * p.N, (uint32_t)p.N * 4u), reinterpret_cast<uint8_t *>(scales),
                    (place * kScales + c.w * 64) * 4, e < TN && at < p.N ? (uint32_t)at * 4u : kRowOOB);
         }
@@ -533,10 +541,15 @@ __global__ __launch_bounds__(512, 1) void i8_tiles_deep(I8Gemm p)
         ks += rot;
         return (ks >= nk ? ks - nk : ks) * S::kStageBytes;
     };
-    auto load = [&](int slot, int ks) {
+    constexpr int kOfX = H * S::kLoadsA;
+    auto load_w = [&](int slot, int ks) {
+#pragma unroll
+        for (int q = kOfX; q < S::kLoads; ++q) load_one(q, slot, start_of(ks));
+    };
+    auto load_x = [&](int slot, int ks) {
         const int k0 = start_of(ks);
 #pragma unroll
-        for (int q = 0; q < S::kLoads; ++q) load_one(q, slot, k0);
+        for (int q = 0; q < kOfX; ++q) load_one(q, slot, k0);
         if constexpr (TM == 16) {
             if (c.w < 4) {
                 const int kc = (int)ax + k0 + (c.w >> 1) * kRowBytes;
@@ -544,21 +557,33 @@ __global__ __launch_bounds__(512, 1) void i8_tiles_deep(I8Gemm p)
             }
         }
     };
-    // (every wave waits for its own loads: four of TM = 16's have one more in each stage)
-    auto barrier = [&] {
-        if (TM == 16 && c.w < 4) stage_barrier<S::kWait + (TM == 16 ? S::NS - 2 : 0)>();
-        else stage_barrier<S::kWait>();
+    // Until all but the loads of the last `stages` stages have landed (every wave waits for
+    // its own: four of TM = 16's have one more in each stage)
+    auto barrier = [&](auto stages) {
+        constexpr int n = decltype(stages)::value;
+        if (TM == 16 && c.w < 4) stage_barrier<n * (S::kLoads + (TM == 16))>();
+        else stage_barrier<n * S::kLoads>();
     };
+    using Ring = std::integral_constant<int, S::NS - 2>;
 
     int parity = 0;
     RowTile cur = find(tile);
     fetch(cur, 0);
     RowTile next = find(tile + nwg);
     fetch(next, 1);
-    if (p.rows) turn_end<0>();
-    aim(cur, 0);
+    // (W's loads of two stages do not wait for the row indices)
+    aim_w(cur);
+    load_w(0, 0);
+    load_w(1, 1);
+    if (p.rows) turn_end<2 * S::kLoadsW>();
+    aim_x(cur, 0);
+    load_x(0, 0);
+    load_x(1, 1);
 #pragma unroll
-    for (int f = 0; f < S::kAhead; ++f) load(f, f);
+    for (int f = 2; f < S::kAhead; ++f) {
+        load_w(f, f);
+        load_x(f, f);
+    }
     const int ar = 16 * RB * wm + j, br = 16 * NB * wn + j;
     uint32_t fa = (uint32_t)(ar * kRowBytes + ((kgroup(g) ^ swz(ar)) << 4));
     uint32_t fb = (uint32_t)(S::kA + br * kRowBytes + ((kgroup(g) ^ swz(br)) << 4));
@@ -580,10 +605,12 @@ __global__ __launch_bounds__(512, 1) void i8_tiles_deep(I8Gemm p)
     };
     Blocks even, odd;
     if constexpr (S::PIPE) {
-        stage_barrier<(S::NS - 1) * S::kLoads>();
+        stage_barrier<S::kWait>();
         read(even, 0);
+        stage_barrier<S::kWait>();
+    } else {
+        barrier(std::integral_constant<int, S::NS - 3>{});   // (stage 1's W came before stage 0's X)
     }
-    barrier();
 
     int rs = 0;               // slot of the stage
     for (;;) {
@@ -609,7 +636,10 @@ __global__ __launch_bounds__(512, 1) void i8_tiles_deep(I8Gemm p)
             int ks = s + S::kAhead;
             if (ks >= nk) {
                 ks -= nk;
-                if (ks == 0) aim(next, parity ^ 1);
+                if (ks == 0) {
+                    aim_w(next);
+                    aim_x(next, parity ^ 1);
+                }
             }
             asm volatile("" : "+v"(ax), "+v"(bx), "+v"(fa), "+v"(fb));
             return ks;
@@ -641,9 +671,10 @@ __global__ __launch_bounds__(512, 1) void i8_tiles_deep(I8Gemm p)
             for (int s = 0; s < nk; ++s) {
                 const int ks = ahead(s);
                 read(even, rs);
-                load(rs == 0 ? S::NS - 1 : rs - 1, ks);
+                load_w(rs == 0 ? S::NS - 1 : rs - 1, ks);
+                load_x(rs == 0 ? S::NS - 1 : rs - 1, ks);
                 multiply(even);
-                barrier();
+                barrier(Ring{});
                 rs = rs + 1 == S::NS ? 0 : rs + 1;
             }
         }
