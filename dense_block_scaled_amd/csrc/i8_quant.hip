@@ -10,7 +10,9 @@
 // scale NaN and codes 0, so that every product with it is NaN.
 //
 // One pass: a row's pieces stay in registers between the maximum and the codes
-// (rows longer than LANES x 8 x P elements read the rest again).
+// (rows longer than LANES x 8 x P elements read the rest again).  Memory bounds it: 32768
+// rows of 4096 bf16 take 65 us, 6.2 TB/s read and written (a copy has 5.1 TB/s); 48 such
+// rows 3.4 us, the way into the kernel and two trips to memory.
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 
@@ -162,9 +164,19 @@ hipError_t launch_quant_i8(const void *x, int bf16, int64_t M, int64_t K, int8_t
     auto by_size = [&](auto b) {
         const bool whole = K % 8 == 0 && ((reinterpret_cast<uintptr_t>(x) & 15) | (reinterpret_cast<uintptr_t>(codes) & 7)) == 0;
         if (!whole) return go(b, I1{}, G{}, I8{});
+        // A workgroup a row has the row's pieces under way in one trip, a wave a row none of the
+        // waiting for the others: us of rows x K, wave / workgroup, bf16 then fp32:
+        //     48 x 1024    3.9 /  3.3    3.5 /  3.2        48 x 2048    4.7 /  3.3    4.4 /  3.2
+        //   4096 x 1024    5.7 /  6.7    6.5 /  6.9      8192 x 2048     15 /   14     19 /   17
+        //  32768 x 1024     21 /   36     31 /   35     32768 x 2048     38 /   46     60 /   57
+        //  32768 x  512     15 /   29     17 /   30     32768 x 4096     78 /   68    117 /  114
+        constexpr bool BF16 = decltype(b)::value;
         if (K <= 64 * 8) return go(b, I8{}, W{}, I1{});
-        if (K <= 64 * 8 * 2) return go(b, I8{}, W{}, I2{});
-        if (K <= 64 * 8 * 4) return go(b, I8{}, W{}, I4{});
+        if (K <= 64 * 8 * 2 && M >= 4096) return go(b, I8{}, W{}, I2{});
+        if constexpr (BF16) {
+            if (K <= 64 * 8 * 4 && M >= 16384) return go(b, I8{}, W{}, I4{});
+        }
+        if (K <= 256 * 8) return go(b, I8{}, G{}, I1{});
         if (K <= 256 * 8 * 2) return go(b, I8{}, G{}, I2{});
         if (K <= 256 * 8 * 4) return go(b, I8{}, G{}, I4{});
         return go(b, I8{}, G{}, I8{});

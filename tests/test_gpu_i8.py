@@ -32,7 +32,8 @@ def _say(*a):
 
 # both sides of every size of row a kernel holds, whole pieces and not
 QUANT = [(1, 1), (3, 7), (1, 16), (5, 8), (64, 512), (9, 520), (7, 1024), (6, 1032), (5, 2048), (4, 2056), (3, 4096),
-         (2, 4104), (3, 8192), (2, 8200), (2, 16384), (2, 16392), (1, 40000), (2, 2049), (1, 4101), (1000, 48), (257, 100)]
+         (2, 4104), (3, 8192), (2, 8200), (2, 16384), (2, 16392), (1, 40000), (2, 2049), (1, 4101), (1000, 48), (257, 100),
+         (4097, 520), (4096, 1024), (16385, 1032)]
 
 
 @pytest.mark.parametrize("M,K", QUANT)
