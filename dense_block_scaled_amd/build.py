@@ -6,9 +6,10 @@ hipcc compiles the kernel translation units (csrc/gemm_*.hip: one per group
 of formats, all instantiating the template in csrc/gemm_kernel.h), the
 launcher (csrc/gemm.hip), the quantisers (csrc/quant.hip), the
 mixture-of-experts kernels (csrc/moe_*.hip), the 8-bit integer kernels
-(csrc/i8_*.hip) and the ABI layer (csrc/dbs.cpp, csrc/moe.cpp, csrc/i8.cpp) to objects in parallel, then links them, in-tree; no GPU is
-needed to build.  Packed-fp32 VALU instructions are turned off for the
-device code.  build(poison=True) builds the same sources with
+(csrc/i8_*.hip) and the ABI layer (csrc/dbs.cpp, csrc/moe.cpp, csrc/i8.cpp) to
+objects in parallel, then links them, in-tree; no GPU is needed to build.
+Packed-fp32 VALU instructions are turned off for the device code.
+build(poison=True) builds the same sources with
 DBS_LDS_POISON=1 into libdbs_poison.so, a debug library whose direct-to-LDS
 loads first fill their destination with 0xFF (see gemm_kernel.h); the
 race-detection tests compare its results with libdbs.so's bit for bit.

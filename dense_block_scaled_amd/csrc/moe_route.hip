@@ -266,6 +266,11 @@ __global__ __launch_bounds__((select_threads<VPL, ONE>())) void route_select(Moe
 // over the 16 lanes' heads and one step of the winner's list, where
 // route_select goes through all of a lane's logits three times.
 //
+// One token of 256 experts: 6.6 us, the launch, two trips to memory and one wave's chain
+// of instructions.  16384 tokens, 8 of 256 experts in 4 of 8 groups, fp32: 16.3 us of choice, bound by its
+// vector instructions (1570 a wave of four tokens, a third of them the sigmoids'
+// exponentials; 10.5 us of issue on 1024 SIMDs), and 7.2 of order (route_place_bytes).
+//
 // Lanes.  The 16 lanes of a token are cut into as many runs as the groups'
 // count rounded up to a power of two, one run a group; a lane has Q experts in a
 // row (see launch_moe_route_grouped).
@@ -847,7 +852,8 @@ __global__ __launch_bounds__(kThreads) void route_bwd(const void *logits, int64_
 //     else:    u_j s_j (1 - s_j)
 //
 // with u the weights' gradients times `factor`.  Only the chosen logits are
-// read; a token's row of zeros and k values goes out through LDS.
+// read; a token's row of zeros and k values goes out through LDS.  (16384 tokens, 6 of 160
+// experts, bf16: 4.1 us, two trips to memory one after the other, the choice and its logits.)
 template <int VPL, int C, bool BF16>
 __global__ __launch_bounds__(kThreads) void route_sigmoid_bwd(const void *logits, int64_t T, int E, int k, int renorm,
                                                               float factor, const int32_t *experts, const float *dweights,
