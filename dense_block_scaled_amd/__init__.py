@@ -19,8 +19,9 @@ Operand encodings (contiguous; K-major unless la / lb say MN_MAJOR):
 MN-major operands (gemm_bf16, gemm_mx) are stored transposed: A (K, M), B
 (K, N), E2M1 packing two consecutive M (N) per byte, (K, M/2); scales keep
 their (M, K/32) layout.
-The mixture-of-experts operators (moe_route ... moe_combine_backward) are
-described at their functions.
+The mixture-of-experts operators (moe_route ... moe_combine_backward) and those
+in 8-bit integers (quant_i8 ... gemm_moe_swiglu_i8) are described at their
+functions.
 Each GEMM returns D: (M, N) torch.bfloat16 (or writes into ``out``).
 """
 from __future__ import annotations

@@ -160,12 +160,14 @@ __device__ __forceinline__ void place(const MoeRoute &p, int64_t t0, int64_t p0,
                                       const int32_t *base, const int32_t *before, const int32_t *experts)
 {
     const int total = base[p.E];
-    for (int64_t q = p0 + threadIdx.x; q < p1; q += blockDim.x) {
-        const int64_t t = q / p.k;
-        const int e = experts[q - p0];
+    // (a workgroup's pairs are few: 32 bits, whose division is short)
+    for (uint32_t i = threadIdx.x; i < (uint32_t)(p1 - p0); i += blockDim.x) {
+        const uint32_t tl = i / (uint32_t)p.k;
+        const int64_t q = p0 + i, t = t0 + tl;
+        const int e = experts[i];
         int slot = -1;
         if (e >= 0) {
-            const uint64_t below = ((uint64_t)1 << (t - t0)) - 1;
+            const uint64_t below = ((uint64_t)1 << tl) - 1;
             slot = base[e] + (before ? before[e] : 0) + __popcll(mask[e] & below);
             p.rows[slot] = (int32_t)t;
         }
@@ -260,16 +262,16 @@ __global__ __launch_bounds__((select_threads<VPL, ONE>())) void route_select(Moe
 // Choices must not hang on a rounding: c is computed in fp64 (vector fp64 runs at
 // fp32's rate here).  The expert's index lies in the ten lowest bits of
 // its c, so keys differ, ties go to the lower index, and sorting needs no second
-// register: two instructions for every exchange of a lane's network.  Scores that
-// agree to 2^-42 count as equal.  After the sort a lane's best are its
-// first, groups' sums come from neighbouring lanes, and a choice is one maximum
-// over the 16 lanes' heads and one step of the winner's list, where
-// route_select goes through all of a lane's logits three times.
+// register: two instructions for every exchange of a lane's network.  Scores
+// nearer than 2^-42 can count as equal.  After the sort a lane's best are its
+// first, groups' sums come from neighbouring lanes, and four merges of sorted
+// lists leave every lane the token's k best (one maximum over the lanes' heads for
+// every choice took 4 us more of 16384 tokens of 256 experts).
 //
 // One token of 256 experts: 6.6 us, the launch, two trips to memory and one wave's chain
-// of instructions.  16384 tokens, 8 of 256 experts in 4 of 8 groups, fp32: 16.3 us of choice, bound by its
-// vector instructions (1570 a wave of four tokens, a third of them the sigmoids'
-// exponentials; 10.5 us of issue on 1024 SIMDs), and 7.2 of order (route_place_bytes).
+// of instructions.  16384 tokens, 8 of 256 experts in 4 of 8 groups, fp32: 16 us of choice, bound by its
+// vector instructions (1500 a wave of four tokens, a third of them the sigmoids';
+// 10 us of issue on 1024 SIMDs), and 7.2 of order (route_place_bytes).
 //
 // Lanes.  The 16 lanes of a token are cut into as many runs as the groups'
 // count rounded up to a power of two, one run a group; a lane has Q experts in a
@@ -299,31 +301,32 @@ __device__ __forceinline__ double row_sum64(double v)
     return v + row_move64<3>(v);
 }
 
-// e^x for -708 <= x <= 708 to about 2^-46: x = (n + f) ln 2 with |f| <= 1 / 2, and the
-// series of e^(f ln 2) to its 11th power (the next term is 6.4e-15).  n is
+// e^x for -708 <= x <= 708 to about 2^-45: x = (n + f) ln 2 with |f| <= 1 / 2, and 2^f as
+// the polynomial of degree 9 that agrees with it at the Chebyshev nodes (off by 2^-45.6
+// at most; the series needs two terms more for that).  n is
 // taken from the low bits of a sum with 3 2^51, and put in by adding to the exponent
 // (the conversions, v_rndne_f64 and v_ldexp_f64 among them, issue more slowly).
 __device__ __forceinline__ double exp64(double x)
 {
-    constexpr double kLn2 = 0.6931471805599453, kRound = 6755399441055744.0;
+    constexpr double kRound = 6755399441055744.0;
     const double t = x * 1.4426950408889634, shifted = t + kRound;
-    const double r = (t - (shifted - kRound)) * kLn2;
-    double p = 1.0 / 39916800;
-    constexpr double inv[11] = {1.0 / 3628800, 1.0 / 362880, 1.0 / 40320, 1.0 / 5040, 1.0 / 720, 1.0 / 120,
-                                1.0 / 24,      1.0 / 6,      1.0 / 2,     1.0,        1.0};
+    const double f = t - (shifted - kRound);
+    double p = 1.0205905413765595e-07;
+    constexpr double c[9] = {1.325964524488711e-06, 1.5252672924850737e-05, 0.0001540343375125101,
+                             0.0013333558200794592, 0.009618129193934313,   0.05550410866465167,
+                             0.2402265069564034,    0.6931471805599462,     1.0000000000000135};
 #pragma unroll
-    for (int i = 0; i < 11; ++i) p = __builtin_fma(p, r, inv[i]);
+    for (int i = 0; i < 9; ++i) p = __builtin_fma(p, f, c[i]);
     const uint64_t b = __builtin_bit_cast(uint64_t, p);
     const uint32_t hi = (uint32_t)(b >> 32) + ((uint32_t)__builtin_bit_cast(uint64_t, shifted) << 20);
     return __builtin_bit_cast(double, (uint64_t)hi << 32 | (uint32_t)b);
 }
 
-// 1 / x, x a normal number: v_rcp_f64 and two Newton steps
+// 1 / x, x a normal number: y = v_rcp_f64 is off by a factor of 1 - d, d < 2^-20, and y (1 + d + d^2) by d^3
 __device__ __forceinline__ double inverse64(double x)
 {
-    double y = __builtin_amdgcn_rcp(x);
-    y = __builtin_fma(__builtin_fma(-x, y, 1.0), y, y);
-    return __builtin_fma(__builtin_fma(-x, y, 1.0), y, y);
+    const double y = __builtin_amdgcn_rcp(x), d = __builtin_fma(-x, y, 1.0);
+    return __builtin_fma(y, __builtin_fma(d, d, d), y);
 }
 
 constexpr uint64_t kIndexBits = 1023;           // kMoeMaxExperts - 1
@@ -410,15 +413,15 @@ __device__ __forceinline__ void best_of_row(double (&v)[VPL])
     best_of_both<3, N>(v);
 }
 
-// How many of the other 15 lanes have a larger value
-template <int BY = 1>
+// How many of the lanes BY, 2 BY .. further on in the row of 16 have a larger value
+template <int BY, int AT = BY>
 __device__ __forceinline__ int larger_in_row(double v)
 {
     const uint64_t b = __builtin_bit_cast(uint64_t, v);
-    const uint32_t lo = __builtin_amdgcn_mov_dpp((int)b, 0x120 + BY, 0xF, 0xF, true);               // row_ror
-    const uint32_t hi = __builtin_amdgcn_mov_dpp((int)(b >> 32), 0x120 + BY, 0xF, 0xF, true);
+    const uint32_t lo = __builtin_amdgcn_mov_dpp((int)b, 0x120 + AT, 0xF, 0xF, true);               // row_ror
+    const uint32_t hi = __builtin_amdgcn_mov_dpp((int)(b >> 32), 0x120 + AT, 0xF, 0xF, true);
     const int n = __builtin_bit_cast(double, (uint64_t)hi << 32 | lo) > v;
-    if constexpr (BY < 15) return n + larger_in_row<BY + 1>(v);
+    if constexpr (AT + BY < 16) return n + larger_in_row<BY, AT + BY>(v);
     return n;
 }
 
@@ -527,8 +530,10 @@ __device__ __forceinline__ void choose(const MoeRouteGrouped &p, int64_t tok, in
             if (p.best == 2 && two > -(double)INFINITY) score += unkeyed(two);
             score = keyed(score, group);
         }
-        // (a group's lanes all have its score)
-        const bool keep = larger_in_row(score) < p.kept * p.lanes && one > -(double)INFINITY;
+        // (a group's lanes all have its score; at most 16 groups, at least two: 1 .. 8 lanes)
+        const int rank = p.lanes == 1 ? larger_in_row<1>(score) : p.lanes == 2 ? larger_in_row<2>(score)
+                       : p.lanes == 4 ? larger_in_row<4>(score) : larger_in_row<8>(score);
+        const bool keep = rank < p.kept && one > -(double)INFINITY;
 #pragma unroll
         for (int i = 0; i < (VPL < kMoeMaxK ? VPL : kMoeMaxK); ++i) v[i] = keep ? v[i] : -(double)INFINITY;
     }
@@ -687,7 +692,7 @@ __global__ __launch_bounds__(kThreads) void route_place(MoeRoute p, int64_t nb)
     for (int64_t q = p0 + t; q < p1; q += kThreads) {
         const int e = p.experts[q];
         chosen[q - p0] = e;
-        if (e >= 0) atomicOr(reinterpret_cast<unsigned long long *>(&mask[e]), 1ull << (q / p.k - t0));
+        if (e >= 0) atomicOr(reinterpret_cast<unsigned long long *>(&mask[e]), 1ull << ((uint32_t)(q - p0) / (uint32_t)p.k));
     }
     __syncthreads();
     place(p, t0, p0, p1, mask, base, DIRECT ? before : p.counts + (int64_t)blockIdx.x * p.E, chosen);
