@@ -20,16 +20,18 @@ namespace dbs {
 // 5.5 TB/s where that is more.  Groups (E > 1) are known on the device only: M / E rows of
 // each, half a tile of each is waste, some may have none; tiles then even out,
 // and rounds are counted in parts.  us of the dense product with tiles of 16 x 16 /
-// 16 x 64 / 64 x 16 / 64 x 32 / 64 x 64 / 128 x 128 / 256 x 256:
+// 16 x 64 / 64 x 16 / 64 x 32 / 64 x 64 / 128 x 64 / 128 x 128 / 256 x 256:
 //
-//      1 x 4096 x 4096     4.8   8.2   7.3   8.5  10.2    18    35
+//      1 x 4096 x 4096     4.8   8.2   7.3   8.5  10.2          18    35
 //     16 x 8192 x 4096     9.8   8.5  11.6   9.0  10.5
-//     48 x 4096 x 4096    17.1  10.6   7.5   8.7  10.6
-//    128 x 8192 x 4096      63          22  15.7  12.0    20    39
-//    512 x 8192 x 1024     113          42    26  16.3  10.6    20
-//   1024 x 4096 x 4096                        54    41    24    47
-//   2048 x 4096 x 4096                        94    71    42    48
-//   4096 x 4096 x 4096                       180   127    81    59
+//     48 x 4096 x 4096    17.1  10.6   7.5   8.7  10.6  13.5    18
+//    128 x 8192 x 4096      63          22  15.7  12.2  15.0    19    39
+//    128 x 11008 x 8192                             31  23.5    30
+//    512 x 4096 x 4096                              20  16.3    20    46
+//    512 x 8192 x 1024     113          42    26  14.2  12.0  10.3    20
+//   1024 x 4096 x 4096                        54    34    27    22    47
+//   2048 x 4096 x 4096                        94    65    50    40    48
+//   4096 x 4096 x 4096                       180   127          80    59
 //
 // of 1 / 4 / 16 / 48 tokens each to 8 of 64 experts of 2048 x 1408 with 16 x 64 9.0 / 16.8 / 26.6 / 35.3,
 // with 64 x 64 9.3 / 18.0 / 29.0 / 38.5, and of 16 .. 8191 rows each to 4 of 32 experts of 2056 x 4096, with the last three, 40 / 54 /
@@ -69,7 +71,10 @@ I8Tile i8_tile(int64_t M, int64_t E, int64_t N, int64_t ncols, int64_t K, bool g
     deep(64, 32, 0.95, 1.05);
     deep(64, 64, 1.42, 1.55);
     if (M <= 16 * met) deep(16, 64, 0.92, 1.0);    // (more rows read W again: 48 x 4096 x 4096 in 10.6 us)
-    double x = tiles(128, 128) / n;
+    double x = tiles(128, 64) / n;
+    // (of groups, whose rows are not known, 128 x 128 or 64 x 64 tiles were as fast or up to 20 % faster)
+    if (E == 1 && !gate) offer(128, 64, 5.7 + (1.9 + 0.6 * std::min(x, 1.0)) * k + more(x) * (1.3 + 2.47 * k));
+    x = tiles(128, 128) / n;
     offer(128, 128, 6.1 + (2.7 + 1.6 * std::min(x, 1.0)) * k + more(x) * (1.3 + 4.35 * k));
     x = tiles(256, 256) / n;
     offer(256, 256, 10 + (8.6 + 3.1 * std::min(x, 1.0)) * k + more(x) * (7 + 12.2 * k));
@@ -80,9 +85,8 @@ I8Tile i8_tile(int64_t M, int64_t E, int64_t N, int64_t ncols, int64_t K, bool g
 // the one.  The rows (or columns) of the whole rounds then go by themselves and
 // the others behind them, where that saves more than 8 % and 2 us by the same
 // estimate: 4539 x 4096 x 4096 in 83 us, not 99, 4688 x 4096 x 8192 in 146, not 185, 1302 x 12205 x 3296
-// in 63, not 84, 268 x 14336 x 4096 in 34, not 38; with estimates nearer than that the two were
-// up to 8 % slower (543 x 7179 x 8160, whose rows do not start on cache lines, which the estimate
-// does not know: 74 us, not 69).
+// in 63, not 84, 992 x 4108 x 2320 in 23, not 29; with estimates nearer than that the two were up
+// to 5 % slower (2280 x 12836 x 4480: 129 us, not 123).
 I8Part i8_part(int64_t M, int64_t N, int64_t K, int cus)
 {
     I8Part best{M, N};

@@ -29,7 +29,7 @@ struct I8Gemm {
 };
 
 // An output tile: 16 rows by 16 columns; 16 by the columns of 64 rows of W; 64 by those of 64, 32 or (without
-// the gate) 16; 128 by those of 128; 256 by those of 256.
+// the gate) 16; 128 by those of 128 or 64; 256 by those of 256.
 struct I8Tile {
     int rows, cols;
 };

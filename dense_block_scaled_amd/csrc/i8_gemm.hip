@@ -21,6 +21,7 @@
 //   16 x 16    W's rows straight into registers: 1 x 8192 x 8192 in 11.8 us, 5.7 TB/s of W
 //   16 x 64, 64 x 16 .. 64    a deep ring in LDS: 48 tokens to 8 of 128 experts of 2 768 x 4096 in 104 us,
 //              7.4 TB/s of W; 48 x 8192 x 4096 in 9.0, the way into the kernel and 16 stages' latency
+//   128 x 64   128 x 11008 x 8192 in 23.5 us, 172 tiles
 //   128 x 128  1024 x 4096 x 4096 in 22 us, a round of tiles: LDS (96 KiB read and 32 written a
 //              stage, 1024 cycles at 128 bytes each, where the MFMAs take 512)
 //   256 x 256  8192 x 8192 x 8192 in 400 .. 410 us, 2.7 Pop/s: power (MFMAs busy 68 % of the time at
@@ -408,7 +409,7 @@ __global__ __launch_bounds__(512, 1) void i8_tiles(I8Gemm p)
 // tiles pay where wide ones leave CUs idle, although each reads all of X's rows.
 // 16 rows by 64 where groups have no more: less of the ring goes to X, more to W (16 tokens
 // to 8 of 64 experts of 2048 x 1408: 26.6 us, by 64 rows 29.0).
-// 128 rows by 128 where the large tiles are too few for the CUs.
+// 128 rows by 128, or by 64, where the large tiles are too few for the CUs.
 //
 // A stage is H times 128 bytes of every row.  8 waves: WM along the rows, the others
 // along the columns or (KS = 2 or 4, where there are not enough of those to share
@@ -424,7 +425,7 @@ __global__ __launch_bounds__(512, 1) void i8_tiles(I8Gemm p)
 template <int TM_, int TN_, bool GATE>
 struct Deep {
     static constexpr int TM = TM_, TN = TN_, H = TM == 128 ? 1 : TN == 16 ? 4 : 2;
-    static constexpr int WM = TM == 16 ? 1 : TM == 128 ? 2 : 4, RB = TM / 16 / WM;   // waves along the rows, blocks of 16 of each
+    static constexpr int WM = TM == 16 ? 1 : TM == 128 && TN == 128 ? 2 : 4, RB = TM / 16 / WM;   // waves along the rows, blocks of 16 of each
     static constexpr int NB = (TM > 16 && TN >= 64) || GATE ? 2 : 1, WN = TN / 16 / NB, KS = 8 / WM / WN;
     static constexpr int kSteps = 2 * H / KS;                                  // k-steps of 64 bytes of a wave
     static constexpr int kA = TM * kRowBytes, kHalf = kA + TN * kRowBytes, kSlot = H * kHalf, kStageBytes = H * kRowBytes;
@@ -492,8 +493,12 @@ __global__ __launch_bounds__(512, 1) void i8_tiles_deep(I8Gemm p)
             rb = words_of(nullptr, 0);
             return;
         }
-        // (the walk along K starts elsewhere per tile, as in moe_tiles_64)
-        rot = r.n0 / TNO % nk;
+        // The walk along K starts elsewhere per tile and group, or all read from few memory
+        // channels; but not a step further for each tile, which keeps them together where rows
+        // are 8 KiB apart (40 x 16384 x 8192 by 64 x 64: 39 us so, 30 all from the start, 27 like
+        // this; 128 tokens to 2 of 16 experts of 4096 x 8192: 120, 96 like this)
+        const int tn = r.n0 / TNO;
+        rot = (7 * tn + 3 * (tn >> 3) + 5 * r.g) % nk;
         const int64_t wbytes = (int64_t)p.N * p.K;
         const uint8_t *wg = p.W + r.g * wbytes;
         rb = GATE ? words_of(wg, (uint32_t)wbytes) : words_of(wg + (int64_t)r.n0 * lda, (uint32_t)(min(p.N - r.n0, TN) * lda));
@@ -664,11 +669,14 @@ __global__ __launch_bounds__(512, 1) void i8_tiles_deep(I8Gemm p)
                     const int kk = m / (RB * NB), i = m / NB % RB, u = m % NB;
                     acc[i][u] = MulI8::mul(now.b[kk][u], now.a[kk][i], acc[i][u]);
                     DBS_FENCE();
-                    if (m < kReads) read_one(then, after_rs, m);
-                    if (m % (kAll / S::kLoads) == kAll / S::kLoads - 1) load_one(m / (kAll / S::kLoads), rs, k0);
+#pragma unroll
+                    for (int n = 0; n < kReads; ++n)
+                        if (m == n * kAll / (kReads > kAll ? kReads : kAll)) read_one(then, after_rs, n);
+#pragma unroll
+                    for (int q = 0; q < S::kLoads; ++q)
+                        if (m == ((q + 1) * kAll - 1) / S::kLoads) load_one(q, rs, k0);
                     DBS_FENCE();
                 }
-                static_assert(kAll >= kReads && kAll % S::kLoads == 0, "a place for every read and load");
                 stage_barrier<S::kWait>();
                 rs = after_rs;
             };
@@ -919,7 +927,7 @@ hipError_t launch_i8_tiles(const I8Gemm &p, I8Tile t, int cus, hipStream_t strea
         auto go = [&](auto tm, auto tn) {
             constexpr int TM = decltype(tm)::value, TN = decltype(tn)::value;
             const dim3 grid = tile_grid(p, TM, p.gate ? TN / 2 : TN, cus);
-            if constexpr (TN >= 32) {
+            if constexpr (TN >= 32 && (TM < 128 || TN == 128)) {      // (the others are of the dense product)
                 if (p.gate) {
                     hipLaunchKernelGGL((i8_tiles_deep<TM, TN, true, false>), grid, block, 0, stream, p);
                     return;
@@ -930,7 +938,8 @@ hipError_t launch_i8_tiles(const I8Gemm &p, I8Tile t, int cus, hipStream_t strea
         };
         using I64 = std::integral_constant<int, 64>;
         using I128 = std::integral_constant<int, 128>;
-        if (t.rows == 128) go(I128{}, I128{});
+        if (t.rows == 128 && t.cols == 128) go(I128{}, I128{});
+        else if (t.rows == 128) go(I128{}, I64{});
         else if (t.rows == 16) go(std::integral_constant<int, 16>{}, I64{});
         else if (t.cols == 64) go(I64{}, I64{});
         else if (t.cols == 32 || p.gate) go(I64{}, std::integral_constant<int, 32>{});

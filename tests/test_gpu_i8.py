@@ -104,7 +104,7 @@ DENSE = [(1, 1, 16), (1, 64, 128), (1, 8192, 4096), (2, 33, 48), (5, 100, 144), 
          (16, 8200, 2064), (3, 20000, 528), (13, 17002, 400)]
 
 # in two launches, the second for the last rows or the last columns
-PARTS = [(2076, 2009, 1808), (411, 9523, 2592), (324, 11059, 1696), (3485, 1178, 2160), (992, 4108, 2320)]
+PARTS = [(1679, 2389, 2144), (2196, 1902, 3248), (330, 10932, 2208), (3104, 1298, 2848), (992, 4108, 2320)]
 
 
 @pytest.mark.parametrize("M,N,K", DENSE + PARTS)
@@ -173,7 +173,7 @@ def _split(M, E, seed, first=0, last=0):
 EXPERTS = [(1, 2, 4, 64, 128), (3, 9, 5, 33, 48), (7, 7, 1, 100, 16), (16, 64, 64, 130, 272), (48, 384, 128, 96, 512),
            (100, 600, 8, 513, 1040), (300, 900, 3, 264, 400), (500, 500, 40, 1000, 96), (600, 2400, 4, 1030, 160),
            (2000, 8000, 12, 520, 256), (4099, 4099, 6, 2050, 144), (40, 200, 1024, 40, 80),
-           (3000, 9000, 6, 2050, 528), (300, 1500, 6, 1030, 800)]
+           (3000, 9000, 6, 2050, 528), (300, 1500, 6, 1030, 800), (300, 250, 1, 8000, 1040)]
 
 
 @pytest.mark.parametrize("T,M,E,N,K", EXPERTS)
@@ -341,7 +341,7 @@ def test_other_streams_and_two_calls_at_once():
 
 # sizes that reach every kernel, with several tiles to a workgroup
 POISON = [(3, 70000, 200), (900, 33000, 640), (5000, 6000, 400), (9000, 9000, 130), (1500, 2500, 1024), (700, 30000, 260), (2047, 4102, 400), (1100, 9000, 768), (64, 30000, 512),
-          (64, 40000, 512), (2157, 6150, 1040), (16, 40000, 1024)]
+          (64, 40000, 512), (2157, 6150, 1040), (16, 40000, 1024), (250, 8000, 2064)]
 
 
 @pytest.mark.parametrize("M,N,K", POISON)
