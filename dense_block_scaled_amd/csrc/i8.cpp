@@ -34,10 +34,10 @@ namespace dbs {
 //   4096 x 4096 x 4096                       180   127          80    59
 //
 // of 1 / 4 / 16 / 48 tokens each to 8 of 64 experts of 2048 x 1408 with 16 x 64 9.0 / 16.8 / 26.6 / 35.3,
-// with 64 x 64 9.3 / 18.0 / 29.0 / 38.5, and of 16 .. 8191 rows each to 4 of 32 experts of 2056 x 4096, with the last three, 40 / 54 /
-// 42 for 16 rows, 75 / 76 / 79 for 512, 105 / 95 / 84 for 1024, 586 / 377 / 293 for 8191.  (A tile of
-// 128 x 256 on the core of 256 x 256 was nowhere the fastest: 38 .. 79 us for the last three rows, 76
-// for 512 rows to the experts.)
+// with 64 x 64 9.3 / 18.0 / 29.0 / 38.5, and of 16 .. 8191 rows each to 4 of 32 experts of 2056 x 4096 with
+// 64 x 64 / 128 x 128 / 256 x 256 40 / 54 / 42 for 16 rows, 75 / 76 / 79 for 512, 105 / 95 / 84 for 1024,
+// 586 / 377 / 293 for 8191.  (A tile of 128 x 256 on the core of 256 x 256 was nowhere the fastest: 38 .. 79 us
+// for the last three rows of the table, 76 for 512 rows to the experts.)
 I8Tile i8_tile(int64_t M, int64_t E, int64_t N, int64_t ncols, int64_t K, bool gate, int cus, double *us)
 {
     const double k = K / 1024.0, n = cus;
