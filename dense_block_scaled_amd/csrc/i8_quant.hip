@@ -144,9 +144,10 @@ __global__ __launch_bounds__(kThreads) void quant_i8_kernel(const void *x, int64
     }
 }
 
-}  // namespace
+// Rows of a launch: HIP takes grids of fewer than 2^32 threads, and a row has up to kThreads of them
+constexpr int64_t kLaunchRows = int64_t(1) << 23;
 
-hipError_t launch_quant_i8(const void *x, int bf16, int64_t M, int64_t K, int8_t *codes, float *scales, hipStream_t stream)
+hipError_t launch_rows(const void *x, int bf16, int64_t M, int64_t K, int8_t *codes, float *scales, hipStream_t stream)
 {
     auto go = [&](auto b, auto v, auto lanes, auto p) {
         constexpr int L = decltype(lanes)::value;
@@ -182,6 +183,18 @@ hipError_t launch_quant_i8(const void *x, int bf16, int64_t M, int64_t K, int8_t
         return go(b, I8{}, G{}, I8{});
     };
     return bf16 ? by_size(std::true_type{}) : by_size(std::false_type{});
+}
+
+}  // namespace
+
+hipError_t launch_quant_i8(const void *x, int bf16, int64_t M, int64_t K, int8_t *codes, float *scales, hipStream_t stream)
+{
+    for (int64_t m = 0; m < M; m += kLaunchRows) {
+        const hipError_t e = launch_rows(static_cast<const uint8_t *>(x) + m * K * (bf16 ? 2 : 4), bf16,
+                                         M - m < kLaunchRows ? M - m : kLaunchRows, K, codes + m * K, scales + m, stream);
+        if (e != hipSuccess) return e;
+    }
+    return hipSuccess;
 }
 
 }  // namespace dbs
