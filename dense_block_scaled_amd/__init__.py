@@ -586,10 +586,13 @@ def _given(out: torch.Tensor | None, shape, dtype, device: torch.device) -> torc
     return out
 
 
+_NO_WORKSPACE_TOKENS = 64                     # tokens up to which the library's routers need none
+
+
 def _routing(T: int, E: int, k: int, device: torch.device, workspace):
     """Outputs of a router, and its workspace (bytes, tensor or None)."""
     kk = min(max(k, 0), E)                    # (the library refuses other k; nothing is sized by them)
-    need = int(workspace(T, E, kk)) if T > 64 else 0          # (a decoding step's tokens need none)
+    need = int(workspace(T, E, kk)) if T > _NO_WORKSPACE_TOKENS else 0
     r = MoeRouting(_new((T, kk), torch.int32, device), _new((T, kk), torch.float32, device),
                    _new((E + 1,), torch.int32, device), _new((T * kk,), torch.int32, device),
                    _new((T, kk), torch.int32, device))

@@ -85,3 +85,12 @@ def test_deterministic_algorithms_fill_allocations(direct):
 def test_without_a_way_to_see_them_nothing_is_direct(monkeypatch):
     monkeypatch.setattr(dbs, "_empty_strided", None)
     _new(3, 4)
+
+
+def test_routers_need_no_workspace_where_the_binding_does_not_ask():
+    L = dbs.lib()
+    for workspace in (L.moe_route_workspace, L.moe_route_grouped_workspace):
+        for E in (1, 8, 160, 1024):
+            for T in range(1, dbs._NO_WORKSPACE_TOKENS + 1):
+                assert workspace(T, E, 1) == 0 and workspace(T, E, min(E, 16)) == 0
+            assert workspace(dbs._NO_WORKSPACE_TOKENS + 1, E, 1) > 0
