@@ -301,16 +301,18 @@ __device__ __forceinline__ double row_sum64(double v)
     return v + row_move64<3>(v);
 }
 
-// e^x for -708 <= x <= 708 to about 2^-45: x = (n + f) ln 2 with |f| <= 1 / 2, and 2^f as
+// e^x for -708 <= x <= 708, off by less than 2^-44.9 of it: x = (n + f) ln 2 with |f| <= 1 / 2, and 2^f as
 // the polynomial of degree 9 that agrees with it at the Chebyshev nodes (off by 2^-45.6
-// at most; the series needs two terms more for that).  n is
+// at most; the series needs two terms more for that).  log2(e)'s own rounding adds |x| 2^-55.9 (2^-46.5 at the
+// ends); the product with it is rounded nowhere, being part of an fma both times.  n is
 // taken from the low bits of a sum with 3 2^51, and put in by adding to the exponent
 // (the conversions, v_rndne_f64 and v_ldexp_f64 among them, issue more slowly).
 __device__ __forceinline__ double exp64(double x)
 {
     constexpr double kRound = 6755399441055744.0;
-    const double t = x * 1.4426950408889634, shifted = t + kRound;
-    const double f = t - (shifted - kRound);
+    constexpr double kLog2e = 1.4426950408889634;
+    const double shifted = __builtin_fma(x, kLog2e, kRound);
+    const double f = __builtin_fma(x, kLog2e, -(shifted - kRound));
     double p = 1.0205905413765595e-07;
     constexpr double c[9] = {1.325964524488711e-06, 1.5252672924850737e-05, 0.0001540343375125101,
                              0.0013333558200794592, 0.009618129193934313,   0.05550410866465167,
