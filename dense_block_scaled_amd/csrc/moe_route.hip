@@ -285,14 +285,6 @@ __device__ __forceinline__ double row_move64(double v)
     return __builtin_bit_cast(double, (uint64_t)hi << 32 | lo);
 }
 
-__device__ __forceinline__ double row_max64(double v)
-{
-    v = fmax(v, row_move64<0>(v));
-    v = fmax(v, row_move64<1>(v));
-    v = fmax(v, row_move64<2>(v));
-    return fmax(v, row_move64<3>(v));
-}
-
 __device__ __forceinline__ double row_sum64(double v)
 {
     v += row_move64<0>(v);
