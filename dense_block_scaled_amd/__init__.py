@@ -634,7 +634,9 @@ def moe_route_grouped(logits: torch.Tensor, k: int, bias: torch.Tensor | None = 
     kept, by the sum of their ``group_best`` (1 or 2) largest, and the k best
     experts of those chosen.  Weights are ``scale`` times the chosen scores,
     divided by their sum with renormalize=True; the bias is not in them.
-    Logits (or biases) of -inf or NaN close an expert; ties go to the lower one."""
+    Logits (or biases) of -inf or NaN close an expert.  Equal logits and biases go
+    by index; scores with bias that differ by less than 2**-39 of the larger of
+    score and |bias| (groups' sums: 2**-37) may come in either order."""
     k, groups = operator.index(k), operator.index(groups)
     kept = groups if kept_groups is None else operator.index(kept_groups)
     T, E = _dims(logits, "logits", 2)

@@ -262,11 +262,17 @@ __global__ __launch_bounds__((select_threads<VPL, ONE>())) void route_select(Moe
 // Choices must not hang on a rounding: c is computed in fp64 (vector fp64 runs at
 // fp32's rate here).  The expert's index lies in the ten lowest bits of
 // its c, so keys differ, ties go to the lower index, and sorting needs no second
-// register: two instructions for every exchange of a lane's network.  Scores
-// nearer than 2^-42 can count as equal.  After the sort a lane's best are its
+// register: two instructions for every exchange of a lane's network.  After the sort a lane's best are its
 // first, groups' sums come from neighbouring lanes, and four merges of sorted
 // lists leave every lane the token's k best (one maximum over the lanes' heads for
 // every choice took 4 us more of 16384 tokens of 256 experts).
+//
+// How near two c may lie and still be told apart, t the larger of s and |bias| of both: a sigmoid
+// is off by 2^-44.8 s (exp64), a softmax score by 2^-42 s (exp64 and the rounding of a difference of
+// logits up to 708, 2^-44, both a second time in the sum), and a key drops 2^-42 of c, which is
+// at most 2 t.  For two of them 2 2^-42 t + 2^-41 t = 2^-40 t, also where a bias near -s leaves little of c.
+// A group's score sums two c and is cut once more, at most 4 t: 4 (2^-42 + 2^-41) t + 2^-40 t = 2^-38 t.
+// (The callers are told twice as much.)
 //
 // One token of 256 experts: 6.6 us, the launch, two trips to memory and one wave's chain
 // of instructions.  16384 tokens, 8 of 256 experts in 4 of 8 groups, fp32: 16 us of choice, bound by its

@@ -397,9 +397,13 @@ dbs_status moe_route_bwd(dbs_real type, const void *logits, int64_t T, int64_t E
  * Closed experts are moe_route's (a logit of -inf or NaN); a bias of -inf or NaN
  * closes its expert to every token, +inf counts as the largest finite value.  A
  * closed expert adds nothing to its group; a group with none open is not kept.
- * c is computed in fp64; equal values go to the lower expert (group), and
- * values nearer than 2^-42 of their size may count as equal (sigmoid scores of
- * logits below -708 do).  Outputs are moe_route's; the
+ * c is computed in fp64, to about 42 bits of its terms: experts with the same
+ * logit and bias go in the order of their indices, and so do groups with the same
+ * best ones.  c that differ by less than 2^-39 of the larger of s and |bias|, and
+ * groups whose scores differ by less than 2^-37 of the largest s or |bias| in them,
+ * may come in either order (without a bias c is s, and 2^-39 of itself).  Sigmoid
+ * scores of logits below -708 count as equal, and softmax scores of logits
+ * more than 700 below the largest may.  Outputs are moe_route's; the
  * workspace is moe_route_grouped_workspace(T, E, k) bytes (0 up to 64 tokens) on
  * 16, and like moe_route's otherwise.  At most 16 groups, and at most 64
  * experts of a group to each of the 16 / (groups rounded up to a power of two)
