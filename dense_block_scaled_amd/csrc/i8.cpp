@@ -19,25 +19,26 @@ namespace dbs {
 // out of it), further rounds at what a busy machine takes, or the reading of W at
 // 5.5 TB/s where that is more.  Groups (E > 1) are known on the device only: M / E rows of
 // each, half a tile of each is waste, some may have none; tiles then even out,
-// and rounds are counted in parts.  us of the dense product with tiles of 16 x 16 /
-// 16 x 64 / 64 x 16 / 64 x 32 / 64 x 64 / 128 x 64 / 128 x 128 / 256 x 256:
+// and rounds are counted in parts.  (D's and X's bytes are not in it: 1075 x 28672 x 1024,
+// 62 MB of results, gets 128 x 128 tiles at 55 us where 256 x 256 take 45.)  us of the dense product, W from memory, with tiles of
 //
-//      1 x 4096 x 4096     4.8   8.2   7.3   8.5  10.2          18    35
-//     16 x 8192 x 4096     9.8   8.5  11.6   9.0  10.5
-//     48 x 4096 x 4096    17.1  10.6   7.5   8.7  10.6  13.5    18
-//    128 x 8192 x 4096      63          22  15.7  12.2  15.0    19    39
-//    128 x 11008 x 8192                             31  23.5    30
-//    512 x 4096 x 4096                              20  16.3    20    46
-//    512 x 8192 x 1024     113          42    26  14.2  12.0  10.3    20
-//   1024 x 4096 x 4096                        54    34    27    22    47
-//   2048 x 4096 x 4096                        94    65    50    40    48
-//   4096 x 4096 x 4096                       180   127          80    59
+//                        16 x 16  16 x 64  64 x 16  64 x 32  64 x 64  128 x 64  128 x 128  256 x 256
+//      1 x 4096 x 4096       5.8      9.3      9.0      9.6       11        14         19         36
+//     16 x 8192 x 4096        12       10       14       10       12        15         19         36
+//     48 x 4096 x 4096        18       11      9.5       11       13        15         20         36
+//    128 x 8192 x 4096        63       39       24       18       14        18         23         40
+//    128 x 11008 x 8192      169      110       62       45       41        32         43         72
+//    512 x 4096 x 4096       121       75       41       29       21        18         23         46
+//    512 x 8192 x 1024       111       43       40       24       15        13         11         19
+//   1024 x 4096 x 4096       237      146       75       51       35        30         24         48
+//   2048 x 4096 x 4096       477      289      142       95       64        55         42         52
+//   4096 x 4096 x 4096       956      581      274      182      123       104         78         59
 //
-// of 1 / 4 / 16 / 48 tokens each to 8 of 64 experts of 2048 x 1408 with 16 x 64 9.0 / 16.8 / 26.6 / 35.3,
-// with 64 x 64 9.3 / 18.0 / 29.0 / 38.5, and of 16 .. 8191 rows each to 4 of 32 experts of 2056 x 4096 with
-// 64 x 64 / 128 x 128 / 256 x 256 40 / 54 / 42 for 16 rows, 75 / 76 / 79 for 512, 105 / 95 / 84 for 1024,
-// 586 / 377 / 293 for 8191.  (A tile of 128 x 256 on the core of 256 x 256 was nowhere the fastest: 38 .. 79 us
-// for the last three rows of the table, 76 for 512 rows to the experts.)
+// of 1 / 4 / 16 / 48 tokens each to 8 of 64 experts of 2048 x 1408 with 16 x 64 8.7 / 17.0 / 26.4 / 34.6,
+// with 64 x 64 9.4 / 18.6 / 29.5 / 38.2, and of 16 .. 8191 tokens each to 4 of 32 experts of 2056 x 4096 with
+// 64 x 64 / 128 x 128 / 256 x 256 47 / 47 / 45 for 16 tokens (16 x 64: 44), 75 / 69 / 79 for 512, 102 / 94 / 86 for 1024,
+// 559 / 369 / 281 for 8191.  Over 80 dense sizes drawn at random the tile chosen takes 0.9 % longer than the fastest
+// (22 % at most), over 60 sizes of experts 2.6 % (23 %).
 I8Tile i8_tile(int64_t M, int64_t E, int64_t N, int64_t ncols, int64_t K, bool gate, int cus, double *us)
 {
     const double k = K / 1024.0, n = cus;
@@ -84,8 +85,8 @@ I8Tile i8_tile(int64_t M, int64_t E, int64_t N, int64_t ncols, int64_t K, bool g
 // Tiles that fill the CUs a whole number of times and one more cost a round for
 // the one.  The rows (or columns) of the whole rounds then go by themselves and
 // the others behind them, where that saves more than 8 % and 2 us by the same
-// estimate: 4539 x 4096 x 4096 in 83 us, not 99, 4688 x 4096 x 8192 in 146, not 185, 1302 x 12205 x 3296
-// in 63, not 84, 992 x 4108 x 2320 in 23, not 29; with estimates nearer than that the two were up
+// estimate: 4539 x 4096 x 4096 in 75 us, not 95, 4688 x 4096 x 8192 in 138, not 182, 1302 x 12205 x 3296
+// in 62, not 84, 992 x 4108 x 2320 in 22, not 28; with estimates nearer than that the two were up
 // to 5 % slower (2280 x 12836 x 4480: 129 us, not 123).
 I8Part i8_part(int64_t M, int64_t N, int64_t K, int cus)
 {

@@ -18,10 +18,12 @@
 // * Rows, bounds and the gate are the experts' products' (moe_gemm.hip).
 //
 // Tiles, from the fewest rows to the most (the rule is i8_tile in i8.cpp), and what bounds each:
-//   16 x 16    W's rows straight into registers: 1 x 8192 x 8192 in 11.8 us, 5.7 TB/s of W
-//   16 x 64, 64 x 16 .. 64    a deep ring in LDS: 48 tokens to 8 of 128 experts of 2 768 x 4096 in 104 us,
-//              7.4 TB/s of W; 48 x 8192 x 4096 in 9.0, the way into the kernel and 16 stages' latency
-//   128 x 64   128 x 11008 x 8192 in 23.5 us, 172 tiles
+//   16 x 16    W's rows straight into registers: 1 x 8192 x 8192 in 14.5 us, 4.6 TB/s of W from memory (11.9 and 5.6
+//              where the caches have it)
+//   16 x 64, 64 x 16 .. 64    a deep ring in LDS: 48 tokens to 8 of 128 experts of 2 768 x 4096, which meet 96 of
+//              them, in 102 us, 5.9 TB/s of W; 48 x 8192 x 4096 in 11.0 (caches: 9.5), the way into the kernel and 16
+//              stages' latency
+//   128 x 64   128 x 11008 x 8192 in 32 us (caches: 26), 172 tiles
 //   128 x 128  1024 x 4096 x 4096 in 22 us, a round of tiles: LDS (96 KiB read and 32 written a
 //              stage, 1024 cycles at 128 bytes each, where the MFMAs take 512)
 //   256 x 256  8192 x 8192 x 8192 in 400 .. 410 us, 2.7 Pop/s: power (MFMAs busy 68 % of the time at
